@@ -160,7 +160,8 @@ nt_status nt_ctx_create(nt_ctx** out, int device, size_t scratch_bytes) {
     return NT_ERR_CUDA;
   }
   c->err_flag = reinterpret_cast<unsigned*>(c->scratch + kScratchErr);
-  if (configure_gemv(c) != NT_OK || configure_ops(c) != NT_OK || configure_gemm(c) != NT_OK) {
+  if (configure_gemv(c) != NT_OK || configure_ops(c) != NT_OK || configure_gemm(c) != NT_OK ||
+      configure_kv8(c) != NT_OK) {
     g_create_error = c->last_error;
     cudaFree(c->scratch);
     delete c;
@@ -191,7 +192,9 @@ static nt_status take_device_flag(nt_ctx* ctx) {
     cudaMemset(ctx->err_flag, 0, sizeof(unsigned));
     if (flag & kErrWaitTimeout)
       return set_err(ctx, NT_ERR_TIMEOUT, "a device-side bounded wait ran out (flag 0x%x)", flag);
-    return set_err(ctx, NT_ERR_INVALID_ARG, "a device-side position ran past the KV cache (flag 0x%x)", flag);
+    if (flag & kErrPosRange)
+      return set_err(ctx, NT_ERR_INVALID_ARG, "a device-side position ran past the KV cache (flag 0x%x)", flag);
+    return set_err(ctx, NT_ERR_INVALID_ARG, "a NaN or an infinity was written to an 8-bit KV cache (flag 0x%x)", flag);
   }
   return NT_OK;
 }
@@ -468,6 +471,126 @@ nt_status nt_sample(nt_ctx* ctx, const float* z, int64_t n, float T, float P, ui
   DeviceGuard g(ctx->device);
   return launch_sample(ctx, z, n, 1, T, P, seed, nullptr, int64_t(counter), out, ctx->scratch + kScratchSample,
                        as_stream(stream));
+}
+
+namespace {
+nt_status check_kv8(nt_ctx* ctx, const nt_kv8* kv) {
+  NT_REQUIRE(kv, NT_ERR_INVALID_ARG, "null cache");
+  NT_REQUIRE(kv->fmt == NT_KV8_I8 || kv->fmt == NT_KV8_E4M3, NT_ERR_UNSUPPORTED_FMT, "unknown 8-bit cache format %d",
+             kv->fmt);
+  NT_REQUIRE(kv->head_dim == 64 || kv->head_dim == 128, NT_ERR_INVALID_ARG, "head_dim must be 64 or 128");
+  NT_REQUIRE(kv->n_kvh >= 1 && kv->n_kvh <= 64, NT_ERR_INVALID_ARG, "n_kvh must be 1..64");
+  NT_REQUIRE(kv->kv_stride >= 1 && kv->kv_stride <= (int64_t(1) << 30), NT_ERR_INVALID_ARG,
+             "kv_stride must be 1..2^30");
+  NT_REQUIRE(kv->k && kv->v && kv->kscale && kv->vscale, NT_ERR_INVALID_ARG, "null cache buffer");
+  NT_REQUIRE(!kv->kmin == !kv->kmax, NT_ERR_INVALID_ARG, "kmin and kmax: both or neither");
+  NT_REQUIRE(aligned(kv->k, 16) && aligned(kv->v, 16) && aligned(kv->kmin, 16) && aligned(kv->kmax, 16),
+             NT_ERR_ALIGNMENT, "k, v, kmin and kmax must be 16-byte aligned");
+  NT_REQUIRE(aligned(kv->kscale, 4) && aligned(kv->vscale, 4), NT_ERR_ALIGNMENT, "scales must be 4-byte aligned");
+  return NT_OK;
+}
+
+// the queries of an attention or selection over an 8-bit cache
+nt_status check_kv8_queries(nt_ctx* ctx, const nt_kv8* kv, const float* q, int n_qh, int64_t n_pos, int nq,
+                            const int64_t* pos_dev) {
+  NT_TRY(check_kv8(ctx, kv));
+  NT_TRY(check_vec(ctx, q, "q"));
+  NT_REQUIRE(n_qh >= 1 && n_qh % kv->n_kvh == 0 && n_qh / kv->n_kvh <= 16, NT_ERR_INVALID_ARG,
+             "n_qh must be 1..16 times n_kvh");
+  NT_REQUIRE(nq >= 1 && nq <= 16, NT_ERR_INVALID_ARG, "n_query must be 1..16");
+  NT_REQUIRE(nq - 1 <= kv->kv_stride, NT_ERR_INVALID_ARG, "more queries than positions");
+  NT_REQUIRE(pos_dev || (n_pos >= 0 && n_pos <= kv->kv_stride - (nq - 1)), NT_ERR_INVALID_ARG,
+             "need 0 <= n_pos and n_pos + n_query - 1 <= kv_stride");
+  NT_REQUIRE(aligned(pos_dev, 8), NT_ERR_ALIGNMENT, "pos_dev must be 8-byte aligned");
+  return NT_OK;
+}
+
+nt_status attn_kv8_entry(nt_ctx* ctx, const float* q, const nt_kv8* kv, float* out, int n_qh, int64_t n_pos, int nq,
+                         const int64_t* pos_dev, const int32_t* idx, int n_sel, void* stream) {
+  NT_TRY(check_vec(ctx, out, "out"));
+  const size_t need = size_t(n_qh) * nq * (kv->head_dim * sizeof(float) + sizeof(float2));
+  NT_REQUIRE(ctx->scratch_bytes >= kScratchGemm && ctx->scratch_bytes - kScratchGemm >= need, NT_ERR_OOM,
+             "the context scratch has no room for the attention's partials");
+  DeviceGuard g(ctx->device);
+  return launch_attn_kv8(ctx, *kv, q, out, n_qh, n_pos, nq, pos_dev, idx, n_sel, ctx->scratch + kScratchGemm,
+                         ctx->scratch_bytes - kScratchGemm, as_stream(stream));
+}
+}  // namespace
+
+nt_status nt_kv8_append(nt_ctx* ctx, const nt_kv8* kv, int src_fmt, const void* k, const void* v, int64_t n_tok,
+                        int64_t tok_stride, int64_t head_stride, int64_t pos, const int64_t* pos_dev, void* stream) {
+  NvtxRange nvtx_range("nt_kv8_append");
+  NT_TRY(pre_call(ctx));
+  NT_TRY(check_kv8(ctx, kv));
+  NT_REQUIRE(src_fmt == NT_F32 || src_fmt == NT_F16, NT_ERR_UNSUPPORTED_FMT, "rows must be NT_F32 or NT_F16");
+  NT_REQUIRE(n_tok >= 0 && n_tok <= kv->kv_stride, NT_ERR_INVALID_ARG, "n_tok outside 0..kv_stride");
+  NT_REQUIRE(pos_dev || (pos >= 0 && pos <= kv->kv_stride - n_tok), NT_ERR_INVALID_ARG,
+             "rows %lld .. + %lld outside the cache (stride %lld)", (long long)pos, (long long)n_tok,
+             (long long)kv->kv_stride);
+  if (n_tok == 0) return NT_OK;
+  NT_REQUIRE(k && v, NT_ERR_INVALID_ARG, "null rows");
+  const size_t wide = src_fmt == NT_F32 ? 16 : 8;  // bytes of four channels
+  NT_REQUIRE(aligned(k, wide) && aligned(v, wide) && tok_stride % 4 == 0 && head_stride % 4 == 0, NT_ERR_ALIGNMENT,
+             "rows must be %zu-byte aligned, strides multiples of 4", wide);
+  NT_REQUIRE(aligned(pos_dev, 8), NT_ERR_ALIGNMENT, "pos_dev must be 8-byte aligned");
+  DeviceGuard g(ctx->device);
+  return launch_kv8_append(ctx, *kv, src_fmt, k, v, n_tok, tok_stride, head_stride, pos, pos_dev, as_stream(stream));
+}
+
+nt_status nt_kv8_read(nt_ctx* ctx, const nt_kv8* kv, int64_t pos0, int64_t n, int dst_fmt, void* k, void* v,
+                      int64_t head_stride, void* stream) {
+  NvtxRange nvtx_range("nt_kv8_read");
+  NT_TRY(pre_call(ctx));
+  NT_TRY(check_kv8(ctx, kv));
+  NT_REQUIRE(dst_fmt == NT_F32 || dst_fmt == NT_F16, NT_ERR_UNSUPPORTED_FMT, "values must be NT_F32 or NT_F16");
+  NT_REQUIRE(n >= 0 && pos0 >= 0 && pos0 <= kv->kv_stride && n <= kv->kv_stride - pos0, NT_ERR_INVALID_ARG,
+             "rows %lld .. + %lld outside the cache (stride %lld)", (long long)pos0, (long long)n,
+             (long long)kv->kv_stride);
+  if (n == 0) return NT_OK;
+  NT_REQUIRE(k || v, NT_ERR_INVALID_ARG, "no output");
+  NT_REQUIRE(aligned(k, 16) && aligned(v, 16) && head_stride % (dst_fmt == NT_F32 ? 4 : 8) == 0, NT_ERR_ALIGNMENT,
+             "outputs and the stride between heads must be 16-byte aligned");
+  NT_REQUIRE(kv->n_kvh == 1 || head_stride >= n * kv->head_dim, NT_ERR_INVALID_ARG, "head_stride: the heads overlap");
+  DeviceGuard g(ctx->device);
+  return launch_kv8_read(ctx, *kv, pos0, n, dst_fmt, k, v, head_stride, as_stream(stream));
+}
+
+nt_status nt_attn_kv8(nt_ctx* ctx, const float* q, const nt_kv8* kv, float* out, int n_qh, int64_t n_pos, int n_query,
+                      const int64_t* pos_dev, void* stream) {
+  NvtxRange nvtx_range("nt_attn_kv8");
+  NT_TRY(pre_call(ctx));
+  NT_TRY(check_kv8_queries(ctx, kv, q, n_qh, n_pos, n_query, pos_dev));
+  return attn_kv8_entry(ctx, q, kv, out, n_qh, n_pos, n_query, pos_dev, nullptr, 0, stream);
+}
+
+nt_status nt_kv8_select(nt_ctx* ctx, const float* q, const nt_kv8* kv, int n_qh, int64_t n_pos, int n_query,
+                        const int64_t* pos_dev, int n_sel, int n_first, int n_last, int32_t* idx, void* stream) {
+  NvtxRange nvtx_range("nt_kv8_select");
+  NT_TRY(pre_call(ctx));
+  NT_TRY(check_kv8_queries(ctx, kv, q, n_qh, n_pos, n_query, pos_dev));
+  NT_REQUIRE(kv->kmin, NT_ERR_INVALID_ARG, "the cache has no block bounds (kmin, kmax)");
+  NT_REQUIRE(n_sel >= 1 && n_first >= 0 && n_last >= 0 && n_first <= n_sel && n_last <= n_sel - n_first,
+             NT_ERR_INVALID_ARG, "need n_sel >= 1 and n_first + n_last <= n_sel");
+  NT_REQUIRE(n_sel <= (1 << 24), NT_ERR_INVALID_ARG, "n_sel above 2^24");
+  NT_REQUIRE(idx, NT_ERR_INVALID_ARG, "idx is NULL");
+  NT_REQUIRE(aligned(idx, 4), NT_ERR_ALIGNMENT, "idx must be 4-byte aligned");
+  const size_t need = kv8_score_bytes(*kv, n_query);
+  NT_REQUIRE(ctx->scratch_bytes >= kScratchGemm && ctx->scratch_bytes - kScratchGemm >= need, NT_ERR_OOM,
+             "block scores need %zu scratch bytes beyond the first 32 MiB", need);
+  DeviceGuard g(ctx->device);
+  return launch_kv8_select(ctx, *kv, q, n_qh, n_pos, n_query, pos_dev, n_sel, n_first, n_last, idx,
+                           ctx->scratch + kScratchGemm, as_stream(stream));
+}
+
+nt_status nt_attn_kv8_blocks(nt_ctx* ctx, const float* q, const nt_kv8* kv, float* out, int n_qh, int64_t n_pos,
+                             int n_query, const int64_t* pos_dev, const int32_t* idx, int n_sel, void* stream) {
+  NvtxRange nvtx_range("nt_attn_kv8_blocks");
+  NT_TRY(pre_call(ctx));
+  NT_TRY(check_kv8_queries(ctx, kv, q, n_qh, n_pos, n_query, pos_dev));
+  NT_REQUIRE(idx, NT_ERR_INVALID_ARG, "idx is NULL");
+  NT_REQUIRE(aligned(idx, 4), NT_ERR_ALIGNMENT, "idx must be 4-byte aligned");
+  NT_REQUIRE(n_sel >= 1 && n_sel <= (1 << 24), NT_ERR_INVALID_ARG, "n_sel must be 1..2^24");
+  return attn_kv8_entry(ctx, q, kv, out, n_qh, n_pos, n_query, pos_dev, idx, n_sel, stream);
 }
 
 nt_status nt_host_register(nt_ctx* ctx, const void* p, size_t bytes, int read_only) {

@@ -1,0 +1,1022 @@
+// kv8.cu — the 8-bit KV cache: rows quantised as they are written and read
+// back, attention over the cache, and attention over the blocks that a bound on
+// their scores selects for each query.  It stands beside the F16 cache
+// ("Ntransformer", en.unwiki.net, roadmap) and the attention over it (ops.cu).
+//
+// Cache: bytes [n_kvh][kv_stride][HD]; one scale per 64 positions (a block) and
+// head, for K and for V.  A scale is a power of two, so dividing by it is exact:
+// what is stored depends only on the values, not on how the division rounds,
+// and a block whose scale has to grow while it fills (a later token is larger)
+// loses nothing but the low bits that the larger scale cannot hold.
+#include <cuda_fp16.h>
+
+#include "nt_internal.cuh"
+#include "ops.cuh"
+
+namespace nt {
+namespace {
+
+constexpr int kB = kKv8Block;
+
+// ---- scales and 8-bit values ---------------------------------------------------
+
+// the least power of two t >= 2^-100 with a <= QMAX t (a >= 0, finite).  QMAX =
+// 1.m * 2^E: t = 2^(e - E) when the mantissa of a (exponent e) is at most m, else
+// one more.
+template <int E, uint32_t MANT>
+__device__ __forceinline__ float pow2_scale(float a) {
+  const uint32_t u = __float_as_uint(a);
+  int e = int(u >> 23) - 127 - E + ((u & 0x7FFFFFu) > MANT ? 1 : 0);
+  e = e < -100 ? -100 : e;
+  return __uint_as_float(uint32_t(e + 127) << 23);
+}
+template <int FMT>
+__device__ __forceinline__ float kv8_scale(float a) {
+  if (FMT == NT_KV8_I8) return pow2_scale<6, 0x7E0000u>(a);  // QMAX 127 = 1.984375 * 2^6
+  return pow2_scale<8, 0x600000u>(a);                        // QMAX 448 = 1.75 * 2^8
+}
+__device__ __forceinline__ float pow2_inv(float t) { return __uint_as_float((254u << 23) - __float_as_uint(t)); }
+
+// four values over the scale -> four bytes (nearest, ties to even); values beyond
+// the largest 8-bit value (an infinity's) saturate
+template <int FMT>
+__device__ __forceinline__ uint32_t pack8(const float v[4]) {
+  if (FMT == NT_KV8_I8) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w |= (uint32_t(__float2int_rn(fminf(fmaxf(v[i], -127.f), 127.f))) & 0xFFu) << (8 * i);
+    return w;
+  }
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
+  return uint32_t(lo) | (uint32_t(hi) << 16);
+}
+
+// E4M3 bytes 0 and 1 of x (LO) or 2 and 3 as f16 times 2^-8: sign to bit 15,
+// exponent and mantissa to bits 13..7.  Exact for every byte (e4m3 subnormals
+// become f16 subnormals), and no byte gives a NaN or an infinity, so rows that a
+// mask hides cannot spoil a product with 0.
+template <bool LO>
+__device__ __forceinline__ uint32_t e4m3_to_h2(uint32_t x) {
+  const uint32_t s = __byte_perm(x, 0u, LO ? 0x1404 : 0x3424);
+  return (s & 0x80008000u) | ((s >> 1) & 0x3F803F80u);
+}
+// I8 bytes as f16: u = q + 128 in the mantissa of 1024 + u (exact), minus 1152
+template <bool LO>
+__device__ __forceinline__ uint32_t i8_to_h2(uint32_t x_biased) {
+  const uint32_t s = __byte_perm(x_biased, 0x64646464u, LO ? 0x4140 : 0x4342);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&s), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t bias8(uint32_t x) {
+  return FMT == NT_KV8_I8 ? x ^ 0x80808080u : x;
+}
+template <int FMT, bool LO>
+__device__ __forceinline__ uint32_t to_h2(uint32_t x) {  // x after bias8
+  return FMT == NT_KV8_I8 ? i8_to_h2<LO>(x) : e4m3_to_h2<LO>(x);
+}
+// what to_h2 leaves out of the value
+template <int FMT>
+__device__ __forceinline__ constexpr float h2_factor() { return FMT == NT_KV8_I8 ? 1.f : 256.f; }
+
+// four bytes -> values over the scale
+template <int FMT>
+__device__ __forceinline__ float4 unpack8(uint32_t x) {
+  const uint32_t b = bias8<FMT>(x);
+  const uint32_t lo = to_h2<FMT, true>(b), hi = to_h2<FMT, false>(b);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  constexpr float f = h2_factor<FMT>();
+  return make_float4(a.x * f, a.y * f, c.x * f, c.y * f);
+}
+
+// ---- write ---------------------------------------------------------------------
+constexpr int kAppendThreads = 256;
+
+struct AppendArgs {
+  const void* src[2];        // K, V rows
+  int64_t tok_stride, head_stride;
+  uint8_t* dst[2];
+  float* scale[2];
+  int8_t *kmin, *kmax;       // nullable
+  int64_t n, pos, kv_stride, nb;
+  const int64_t* pos_dev;
+  unsigned* err;
+};
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __half* p) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// One CTA per (block, head, K or V).  Its rows stay in registers from the load to
+// the store: the largest |x| is reduced over the CTA between them, so the source
+// is read once.  Rows the block already holds are loaded in the same round and
+// restated only when the scale grows.
+template <int FMT, int HD, typename T>
+__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendArgs a) {
+  constexpr int TR = HD / 4;                  // threads per row, four channels each
+  constexpr int RP = kAppendThreads / TR;     // rows per pass
+  constexpr int NP = kB / RP;
+  __shared__ float red[kAppendThreads / 32];
+  __shared__ float smin[RP][HD], smax[RP][HD];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t pos = a.pos_dev ? *a.pos_dev : a.pos;
+  if (pos < 0 || pos > a.kv_stride - a.n) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrPosRange);
+    return;
+  }
+  const int64_t blk = pos / kB + blockIdx.x, p0 = blk * kB;
+  const int r0 = int(max(pos, p0) - p0);
+  const int64_t end = min(pos + a.n, p0 + kB) - p0;
+  if (end <= r0) return;
+  const int r1 = int(end);
+  const int h = blockIdx.y, w = blockIdx.z;
+  const T* src = static_cast<const T*>(w ? a.src[1] : a.src[0]) + int64_t(h) * a.head_stride;
+  uint8_t* dst = (w ? a.dst[1] : a.dst[0]) + (int64_t(h) * a.kv_stride + p0) * HD;
+  float* scale = (w ? a.scale[1] : a.scale[0]) + int64_t(h) * a.nb + blk;
+  const int tr = threadIdx.x % TR, row = threadIdx.x / TR;
+
+  float4 v[NP];
+  float amax = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = row + i * RP;
+    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r >= r0 && r < r1) v[i] = load4(src + (p0 + r - pos) * a.tok_stride + 4 * tr);
+    else if (r < r0) v[i] = unpack8<FMT>(*reinterpret_cast<const uint32_t*>(dst + r * HD + 4 * tr));
+  }
+  const float t_old = r0 > 0 ? *scale : 0.f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = row + i * RP;
+    if (r < r0) continue;
+    float* x = &v[i].x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float m = fabsf(x[j]);
+      if (m <= 3.402823466e38f) {
+        amax = fmaxf(amax, m);
+      } else {  // NaN is stored as 0, an infinity as the largest value; neither moves the scale
+        bad = true;
+        if (x[j] != x[j]) x[j] = 0.f;
+      }
+    }
+  }
+  if (bad) flag_error(a.err, kErrNonFinite);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+  const float t = fmaxf(kv8_scale<FMT>(amax), t_old);
+  const float inv = pow2_inv(t), restate = t_old * inv;
+  if (threadIdx.x == 0) *scale = t;
+
+  const bool sums = w == 0 && a.kmin;
+  float lo[4] = {448.f, 448.f, 448.f, 448.f}, hi[4] = {-448.f, -448.f, -448.f, -448.f};
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = row + i * RP;
+    if (r >= r1) continue;
+    const float f = r < r0 ? restate : inv;
+    const float q[4] = {v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f};
+    const uint32_t packed = pack8<FMT>(q);
+    if (r >= r0 || restate != 1.f) *reinterpret_cast<uint32_t*>(dst + r * HD + 4 * tr) = packed;
+    if (sums) {
+      const float4 z = unpack8<FMT>(packed);
+      const float zz[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        lo[j] = fminf(lo[j], zz[j]);
+        hi[j] = fmaxf(hi[j], zz[j]);
+      }
+    }
+  }
+  if (!sums) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    smin[row][4 * tr + j] = lo[j];
+    smax[row][4 * tr + j] = hi[j];
+  }
+  __syncthreads();
+  if (threadIdx.x >= HD) return;
+  float l = smin[0][threadIdx.x], u = smax[0][threadIdx.x];
+#pragma unroll
+  for (int i = 1; i < RP; ++i) {
+    l = fminf(l, smin[i][threadIdx.x]);
+    u = fmaxf(u, smax[i][threadIdx.x]);
+  }
+  if (FMT == NT_KV8_E4M3) {  // whole numbers of 4 scale steps, rounded outwards: still bounds
+    l = floorf(l * 0.25f);
+    u = ceilf(u * 0.25f);
+  }
+  const int64_t at = (int64_t(h) * a.nb + blk) * HD + threadIdx.x;
+  a.kmin[at] = int8_t(__float2int_rn(l));
+  a.kmax[at] = int8_t(__float2int_rn(u));
+}
+
+// ---- read back -----------------------------------------------------------------
+constexpr int kReadThreads = 256;
+constexpr int kReadUnroll = 4;
+
+struct ReadArgs {
+  const uint8_t* src[2];
+  const float* scale[2];
+  void* dst[2];  // either may be null
+  int64_t pos, n, kv_stride, nb, head_stride;
+};
+
+// each thread turns VEC bytes into 16 bytes of values, kReadUnroll times
+template <int FMT, int HD, typename T>
+__global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a) {
+  constexpr int VEC = 16 / int(sizeof(T));
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.y, w = blockIdx.z;
+  void* out = w ? a.dst[1] : a.dst[0];
+  if (!out) return;
+  const uint8_t* src = (w ? a.src[1] : a.src[0]) + (int64_t(h) * a.kv_stride + a.pos) * HD;
+  const float* scale = (w ? a.scale[1] : a.scale[0]) + int64_t(h) * a.nb;
+  T* dst = static_cast<T*>(out) + int64_t(h) * a.head_stride;
+  const int64_t units = a.n * (HD / VEC);
+  const int64_t u0 = int64_t(blockIdx.x) * (kReadThreads * kReadUnroll) + threadIdx.x;
+  uint32_t x[kReadUnroll][VEC / 4];
+  float t[kReadUnroll];
+#pragma unroll
+  for (int i = 0; i < kReadUnroll; ++i) {
+    const int64_t u = u0 + i * kReadThreads;
+    if (u >= units) continue;
+    if (VEC == 4) {
+      x[i][0] = *reinterpret_cast<const uint32_t*>(src + u * VEC);
+    } else {
+      const uint2 r = *reinterpret_cast<const uint2*>(src + u * VEC);
+      x[i][0] = r.x;
+      x[i][VEC / 4 - 1] = r.y;
+    }
+    t[i] = scale[(a.pos + u / (HD / VEC)) / kB];
+  }
+#pragma unroll
+  for (int i = 0; i < kReadUnroll; ++i) {
+    const int64_t u = u0 + i * kReadThreads;
+    if (u >= units) continue;
+    const float4 f = unpack8<FMT>(x[i][0]);
+    uint4 o;
+    if (VEC == 4) {
+      o = make_uint4(__float_as_uint(f.x * t[i]), __float_as_uint(f.y * t[i]), __float_as_uint(f.z * t[i]),
+                     __float_as_uint(f.w * t[i]));
+    } else {
+      const float4 g = unpack8<FMT>(x[i][VEC / 4 - 1]);
+      const __half2 h0 = __floats2half2_rn(f.x * t[i], f.y * t[i]), h1 = __floats2half2_rn(f.z * t[i], f.w * t[i]);
+      const __half2 h2 = __floats2half2_rn(g.x * t[i], g.y * t[i]), h3 = __floats2half2_rn(g.z * t[i], g.w * t[i]);
+      o = make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                     *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
+    }
+    *reinterpret_cast<uint4*>(dst + u * VEC) = o;
+  }
+}
+
+// ---- attention -----------------------------------------------------------------
+// Scores and outputs on the tensor cores (mma.sync m16n8k16, f16 products, fp32
+// sums) with fp32-level operands.  The cached values are exact in f16.  A row of
+// q (and of the probabilities) is split into hi = f16(x), lo = f16(x - hi), which
+// carries 22 bits; the M = 16 rows of an MMA are the hi parts of 8 rows and, 8
+// below, their lo parts, so the two halves of a product meet in one thread:
+// accumulators c0 + c2 and c1 + c3.
+//
+// Fragments come straight from memory, without a transpose: MMA k and n indices
+// are ours to name.  Lane (n = lane / 4, c = lane % 4), a step of 16 tokens:
+//  - Q K^T: B column n of n-tile u (0, 1) is token 4 (n / 2) + 2 u + n % 2; the
+//    lane loads bytes 16 c .. 16 c + 15 (+ 64 for the upper half) of that row, and
+//    word w of a 16-byte piece is its k-slots of k-step w.
+//  - the scores of row n land in lane (n, c) for tokens 4 c .. 4 c + 3;
+//  - P V: those four tokens are the lane's k-slots; it loads bytes
+//    n HD/8 .. + HD/8 - 1 of their V rows, and byte i of them is B column n of
+//    n-tile i, i.e. output channel n HD/8 + i.
+constexpr int kAttnWarps = 8;
+constexpr int kStep = 16;  // tokens per warp step
+
+struct AttnKv8Args {
+  const float* q;
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  float* out;
+  float* part;         // [query * n_qh + head][S][HD], unnormalised outputs
+  float2* ml;          // [query * n_qh + head][S]: (max, sum)
+  const int32_t* idx;  // sparse: [query][n_kvh][n_sel]
+  int n_sel;
+  int n_qh, n_kvh, G, nq, S;
+  int chunks;          // row chunks of 8 R rows: per KV head (dense), per query and KV head (sparse)
+  int64_t n_pos, kv_stride, nb;
+  const int64_t* pos_dev;
+  unsigned* err;
+};
+
+// positions query 0 sees, held to the cache
+__device__ __forceinline__ int64_t seen_positions(const AttnKv8Args& a) {
+  int64_t n = a.pos_dev ? *a.pos_dev + 1 : a.n_pos;
+  if (n < 0 || n > a.kv_stride - (a.nq - 1)) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) flag_error(a.err, kErrPosRange);
+    n = n < 0 ? 0 : a.kv_stride - (a.nq - 1);
+  }
+  return n;
+}
+
+// steps per CTA and splits in use for `steps` 16-token steps: both launches
+// compute it, so an unused split is never read
+__device__ __forceinline__ int64_t split_steps(int64_t steps, int S) {
+  const int64_t even = (steps + S - 1) / S;
+  return even < kAttnWarps ? kAttnWarps : even;
+}
+
+__device__ __forceinline__ void mma16816(float c[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// hi and lo f16 parts of two values
+__device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+template <int HD, int R>
+constexpr size_t attn_kv8_smem() {
+  const size_t qa = size_t(R) * (HD / 16) * 32 * 16;
+  const size_t merge = size_t(kAttnWarps) * 8 * R * (HD + 2) * 4;
+  return qa > merge ? qa : merge;
+}
+
+template <int FMT, int HD, int R, bool SPARSE>
+__global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kernel(const AttnKv8Args a) {
+  constexpr int KS = HD / 16;        // k-steps of Q K^T
+  constexpr int NT = HD / 8;         // n-tiles of P V
+  constexpr int KP = HD / 64;        // 16-byte pieces of a K row per lane
+  constexpr int VW = HD / 32;        // words of a V row per lane
+  constexpr int ROWS = 8 * R;
+  extern __shared__ __align__(16) uint8_t sm8[];
+  uint4* qa = reinterpret_cast<uint4*>(sm8);  // [R][KS][32]: A fragments of q
+  __shared__ float s_amax[ROWS];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = lane >> 2, c = lane & 3;
+  const int g = blockIdx.x, s = blockIdx.y;
+  const int qi0 = SPARSE ? blockIdx.z / a.chunks : 0;
+  const int row0 = (SPARSE ? blockIdx.z % a.chunks : blockIdx.z) * ROWS;
+  const int rows = min(ROWS, (SPARSE ? a.G : a.nq * a.G) - row0);
+  const int64_t n_pos = seen_positions(a);
+  // row r of this chunk: query and head
+  const auto query_of = [&](int r) { return SPARSE ? qi0 : (row0 + r) / a.G; };
+  const auto vec_of = [&](int r) { return int64_t(query_of(r)) * a.n_qh + g * a.G + (SPARSE ? row0 + r : (row0 + r) % a.G); };
+  const int64_t tokens = n_pos + query_of(rows - 1);  // the last row sees the most
+  const int64_t steps = SPARSE ? int64_t(a.n_sel) * (kB / kStep) : (tokens + kStep - 1) / kStep;
+  const int64_t per = split_steps(steps, a.S);
+  const int64_t st0 = int64_t(s) * per, st1 = min(steps, st0 + per);
+  if (st0 >= st1 && s > 0) return;
+
+  // q: each row scaled by a power of two to amax in [2^13, 2^14), split, laid out as fragments
+  for (int r = warp; r < ROWS; r += kAttnWarps) {
+    float m = 0.f;
+    if (r < rows)
+      for (int d = lane; d < HD; d += 32) m = fmaxf(m, fabsf(a.q[vec_of(r) * HD + d]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) s_amax[r] = m;
+  }
+  __syncthreads();
+  const auto row_exp = [&](int r) {  // q times 2^row_exp
+    const int e = 140 - int(__float_as_uint(s_amax[r]) >> 23);
+    return e > 100 ? 100 : e;
+  };
+  for (int i = tid; i < R * KS * 32; i += kAttnWarps * 32) {
+    const int ln = i & 31, j = (i >> 5) % KS, rt = (i >> 5) / KS;
+    const int r = rt * 8 + (ln >> 2);
+    const int d = 64 * (j >> 2) + 16 * (ln & 3) + 4 * (j & 3);
+    uint4 f = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows) {
+      const float4 x = load4(a.q + vec_of(r) * HD + d);
+      const float sc = __uint_as_float(uint32_t(row_exp(r) + 127) << 23);
+      split_h2(x.x * sc, x.y * sc, f.x, f.y);
+      split_h2(x.z * sc, x.w * sc, f.z, f.w);
+    }
+    qa[i] = f;
+  }
+  __syncthreads();
+  float rscale[R];      // scores to the base-2 exponent
+  int64_t limit[R];     // positions row n sees
+  float m[R], l[R];
+  float o[R][NT][4];
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    const int r = t * 8 + n;
+    // log2(e) / sqrt(HD)
+    rscale[t] = __uint_as_float(uint32_t(127 - row_exp(r)) << 23) * (1.44269504088896f * rsqrtf(float(HD))) *
+                h2_factor<FMT>();
+    limit[t] = r < rows ? n_pos + query_of(r) : 0;
+    m[t] = -INFINITY;
+    l[t] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+  }
+  const uint8_t* kg = a.k + int64_t(g) * a.kv_stride * HD;
+  const uint8_t* vg = a.v + int64_t(g) * a.kv_stride * HD;
+  const float* ksg = a.ks + int64_t(g) * a.nb;
+  const float* vsg = a.vs + int64_t(g) * a.nb;
+  const int32_t* list = SPARSE ? a.idx + (int64_t(qi0) * a.n_kvh + g) * a.n_sel : nullptr;
+  const int64_t blocks_seen = (tokens + kB - 1) / kB;
+
+  for (int64_t st = st0 + warp; st < st1; st += kAttnWarps) {
+    int64_t t0, blk;
+    if (SPARSE) {
+      blk = list[st >> 2];
+      if (blk < 0 || blk >= blocks_seen) continue;
+      t0 = blk * kB + (st & 3) * kStep;
+      if (t0 >= tokens) continue;
+    } else {
+      t0 = st * kStep;
+      blk = t0 / kB;
+    }
+    const float ks = ksg[blk], vs = vsg[blk];
+    uint4 kw[2][KP];
+    uint32_t vw[4][VW];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t t = t0 + 4 * (n >> 1) + 2 * u + (n & 1);
+#pragma unroll
+      for (int p = 0; p < KP; ++p)
+        kw[u][p] = t < tokens ? __ldcs(reinterpret_cast<const uint4*>(kg + t * HD + 64 * p + 16 * c)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int64_t t = t0 + 4 * c + x;
+      const uint8_t* p = vg + t * HD + n * (HD / 8);
+      if (HD == 128) {
+        const uint4 r = t < tokens ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+        vw[x][0] = r.x;
+        vw[x][1] = r.y;
+        vw[x][VW - 2] = r.z;
+        vw[x][VW - 1] = r.w;
+      } else {
+        const uint2 r = t < tokens ? __ldcs(reinterpret_cast<const uint2*>(p)) : make_uint2(0u, 0u);
+        vw[x][0] = r.x;
+        vw[x][1] = r.y;
+      }
+    }
+    // ---- scores
+    float sc[R][2][4];
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) sc[t][u][0] = sc[t][u][1] = sc[t][u][2] = sc[t][u][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+      uint4 af[R];
+#pragma unroll
+      for (int t = 0; t < R; ++t) af[t] = qa[(t * KS + j) * 32 + lane];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4& k4 = kw[u][j >> 2];
+        const uint32_t raw = (j & 3) == 0 ? k4.x : (j & 3) == 1 ? k4.y : (j & 3) == 2 ? k4.z : k4.w;
+        const uint32_t x = bias8<FMT>(raw);
+        const uint32_t b0 = to_h2<FMT, true>(x), b1 = to_h2<FMT, false>(x);
+#pragma unroll
+        for (int t = 0; t < R; ++t) mma16816(sc[t][u], af[t], b0, b1);
+      }
+    }
+    // ---- online softmax: p = 2^(s - m); the f16 operand of P V is p times the
+    // block's V scale, so m follows s plus the exponent of that scale (which
+    // keeps the operand below 2^15), floored where a block's V is all but zero
+    const float lv = fmaxf(float(int(__float_as_uint(vs) >> 23) - 127), -64.f);
+    uint4 pf[R];
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      const float f = rscale[t] * ks;
+      float p[4];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float v = sc[t][x >> 1][x & 1] + sc[t][x >> 1][2 + (x & 1)];
+        p[x] = t0 + 4 * c + x < limit[t] ? v * f : -INFINITY;
+        mx = fmaxf(mx, p[x]);
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[t], mx + lv);
+      if (__any_sync(0xffffffffu, mn > m[t])) {
+        const float corr = m[t] == -INFINITY ? 0.f : ex2(m[t] - mn);
+        l[t] *= corr;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][i][e] *= corr;
+        m[t] = mn;
+      }
+      const float base = mn == -INFINITY ? 0.f : mn - 14.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        p[x] = ex2(p[x] - base);
+        l[t] += p[x];
+        p[x] *= vs;
+      }
+      split_h2(p[0], p[1], pf[t].x, pf[t].y);
+      split_h2(p[2], p[3], pf[t].z, pf[t].w);
+    }
+    // ---- P V: words of the lane's four tokens interleaved into (token, token + 1) pairs per channel
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      uint32_t y[2][2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        y[x][0] = bias8<FMT>(__byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x5140));
+        y[x][1] = bias8<FMT>(__byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x7362));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b0 = (i & 1) ? to_h2<FMT, false>(y[0][i >> 1]) : to_h2<FMT, true>(y[0][i >> 1]);
+        const uint32_t b1 = (i & 1) ? to_h2<FMT, false>(y[1][i >> 1]) : to_h2<FMT, true>(y[1][i >> 1]);
+#pragma unroll
+        for (int t = 0; t < R; ++t) mma16816(o[t][4 * w + i], pf[t], b0, b1);
+      }
+    }
+  }
+
+  // ---- merge the warps: (m, l, o) of every row in shared memory
+  __syncthreads();
+  float* mo = reinterpret_cast<float*>(sm8);                 // [warps][ROWS][HD]
+  float* mm = mo + size_t(kAttnWarps) * ROWS * HD;           // [warps][ROWS] max
+  float* mll = mm + kAttnWarps * ROWS;                       // [warps][ROWS] sum
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    const int r = t * 8 + n;
+    l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
+    l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
+    if (c == 0) {
+      mm[warp * ROWS + r] = m[t];
+      mll[warp * ROWS + r] = l[t];
+    }
+    float* w = mo + (size_t(warp) * ROWS + r) * HD;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      w[(HD / 8) * (2 * c) + i] = o[t][i][0] + o[t][i][2];
+      w[(HD / 8) * (2 * c + 1) + i] = o[t][i][1] + o[t][i][3];
+    }
+  }
+  __syncthreads();
+  const bool whole = per >= steps;  // one split: the output itself
+  for (int i = tid; i < rows * HD; i += kAttnWarps * 32) {
+    const int r = i / HD, d = i % HD;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, mm[w * ROWS + r]);
+    float acc = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      const float mw = mm[w * ROWS + r];
+      const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
+      acc = fmaf(mo[(size_t(w) * ROWS + r) * HD + d], f, acc);
+      sum = fmaf(mll[w * ROWS + r], f, sum);
+    }
+    const int64_t vec = vec_of(r);
+    acc *= h2_factor<FMT>();
+    if (whole) {
+      a.out[vec * HD + d] = sum > 0.f ? acc / sum : (sum == 0.f ? 0.f : sum);
+    } else {
+      a.part[(vec * a.S + s) * HD + d] = acc;
+      if (d == 0) a.ml[vec * a.S + s] = make_float2(M, sum);
+    }
+  }
+}
+
+// the splits' partials of one row into the output: one thread per channel
+template <int HD, bool SPARSE>
+__global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args a, int rows_per_chunk) {
+  pdl_wait();
+  pdl_trigger();
+  const int qh = blockIdx.x, qi = blockIdx.y, d = threadIdx.x;
+  const int64_t n_pos = seen_positions(a);
+  int64_t tokens = n_pos + qi;
+  if (!SPARSE) {  // the chunk of this row ends at its last row's query
+    const int r = qi * a.G + qh % a.G, last = min(a.nq * a.G, (r / rows_per_chunk + 1) * rows_per_chunk) - 1;
+    tokens = n_pos + last / a.G;
+  }
+  const int64_t steps = SPARSE ? int64_t(a.n_sel) * (kB / kStep) : (tokens + kStep - 1) / kStep;
+  const int64_t per = split_steps(steps, a.S);
+  if (per >= steps) return;
+  const int used = int((steps + per - 1) / per);
+  const int64_t vec = int64_t(qi) * a.n_qh + qh;
+  const float2* ml = a.ml + vec * a.S;
+  const float* part = a.part + vec * a.S * HD + d;
+  float M = -INFINITY;
+  for (int i = 0; i < used; ++i) M = fmaxf(M, __ldcg(ml + i).x);
+  float acc = 0.f, sum = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < used; ++i) {
+    const float2 x = __ldcg(ml + i);
+    const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+    acc = fmaf(__ldcg(part + int64_t(i) * HD), f, acc);
+    sum = fmaf(x.y, f, sum);
+  }
+  a.out[vec * HD + d] = sum > 0.f ? acc / sum : (sum == 0.f ? 0.f : sum);
+}
+
+using AttnKv8Kernel = void (*)(AttnKv8Args);
+template <int FMT, int HD, bool SPARSE>
+AttnKv8Kernel attn_kv8_pick(int R, size_t* smem) {
+  *smem = R == 1 ? attn_kv8_smem<HD, 1>() : attn_kv8_smem<HD, 2>();
+  return R == 1 ? attn_kv8_kernel<FMT, HD, 1, SPARSE> : attn_kv8_kernel<FMT, HD, 2, SPARSE>;
+}
+template <bool SPARSE>
+AttnKv8Kernel attn_kv8_for(int fmt, int hd, int R, size_t* smem) {
+  if (fmt == NT_KV8_I8)
+    return hd == 128 ? attn_kv8_pick<NT_KV8_I8, 128, SPARSE>(R, smem) : attn_kv8_pick<NT_KV8_I8, 64, SPARSE>(R, smem);
+  return hd == 128 ? attn_kv8_pick<NT_KV8_E4M3, 128, SPARSE>(R, smem)
+                   : attn_kv8_pick<NT_KV8_E4M3, 64, SPARSE>(R, smem);
+}
+
+// ---- block selection -----------------------------------------------------------
+// The largest score that any key within a block's channel bounds could have with
+// head h is sum_d max(q_d kmin_d, q_d kmax_d) = sum_d max(q_d, 0) kmax_d +
+// min(q_d, 0) kmin_d: linear in the two halves of q, so the group's heads are
+// added first and a block costs 2 HD products whatever the group size.  With q as
+// 12-bit integers every sum is a whole number below 2^31: the scores, and with
+// them the choice, do not depend on the order of additions.
+constexpr int kScoreThreads = 256;
+constexpr int kSelThreads = 1024;
+
+struct SelectArgs {
+  const float* q;
+  const int8_t *kmin, *kmax;
+  const float* ks;
+  float* score;      // [query][n_kvh][nb]
+  int32_t* idx;      // [query][n_kvh][n_sel]
+  int n_qh, n_kvh, G, nq, n_sel, n_first, n_last;
+  int64_t n_pos, kv_stride, nb;
+  const int64_t* pos_dev;
+  unsigned* err;
+};
+
+__device__ __forceinline__ int64_t seen_positions(const SelectArgs& a) {
+  AttnKv8Args t{};
+  t.pos_dev = a.pos_dev;
+  t.n_pos = a.n_pos;
+  t.nq = a.nq;
+  t.kv_stride = a.kv_stride;
+  t.err = a.err;
+  return seen_positions(t);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const SelectArgs a) {
+  constexpr int LB = HD / 16;            // lanes per block, 16 channels each
+  constexpr int BW = 32 / LB;            // blocks per warp
+  __shared__ float red[kScoreThreads / 32];
+  __shared__ __align__(16) int16_t qp[HD], qn[HD];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = blockIdx.y, qi = blockIdx.z;
+  const int64_t blocks = (seen_positions(a) + qi + kB - 1) / kB;
+  const float* q = a.q + (int64_t(qi) * a.n_qh + g * a.G) * HD;
+  float m = 0.f;
+  for (int i = tid; i < a.G * HD; i += kScoreThreads) {
+    const float v = fabsf(q[i]);
+    if (v <= 3.402823466e38f) m = fmaxf(m, v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kScoreThreads / 32; ++w) m = fmaxf(m, red[w]);
+  const float inv = pow2_inv(pow2_scale<10, 0x7FE000u>(m));  // 2047 = 1.99902 * 2^10
+  for (int d = tid; d < HD; d += kScoreThreads) {
+    int p = 0, n = 0;
+    for (int h = 0; h < a.G; ++h) {
+      const float x = q[h * HD + d];
+      const int v = x != x ? 0 : __float2int_rn(fminf(fmaxf(x * inv, -2047.f), 2047.f));
+      p += max(v, 0);
+      n += min(v, 0);
+    }
+    qp[d] = int16_t(p);
+    qn[d] = int16_t(n);
+  }
+  __syncthreads();
+  const int part = lane % LB;
+  int p2[8], n2[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    p2[i] = reinterpret_cast<const int*>(qp)[part * 8 + i];
+    n2[i] = reinterpret_cast<const int*>(qn)[part * 8 + i];
+  }
+  float* score = a.score + (int64_t(qi) * a.n_kvh + g) * a.nb;
+  for (int64_t b0 = (int64_t(blockIdx.x) * (kScoreThreads / 32) + warp) * BW; b0 < blocks;
+       b0 += int64_t(gridDim.x) * (kScoreThreads / 32) * BW) {
+    const int64_t b = b0 + lane / LB;
+    int acc = 0;
+    if (b < blocks) {
+      const int64_t at = (int64_t(g) * a.nb + b) * HD + part * 16;
+      const uint4 hi = *reinterpret_cast<const uint4*>(a.kmax + at), lo = *reinterpret_cast<const uint4*>(a.kmin + at);
+      const int hw[4] = {int(hi.x), int(hi.y), int(hi.z), int(hi.w)}, lw[4] = {int(lo.x), int(lo.y), int(lo.z), int(lo.w)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc = __dp2a_lo(p2[2 * i], hw[i], acc);
+        acc = __dp2a_hi(p2[2 * i + 1], hw[i], acc);
+        acc = __dp2a_lo(n2[2 * i], lw[i], acc);
+        acc = __dp2a_hi(n2[2 * i + 1], lw[i], acc);
+      }
+    }
+#pragma unroll
+    for (int o = LB / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (b < blocks && part == 0) score[b] = __int2float_rn(acc) * a.ks[int64_t(g) * a.nb + b];
+  }
+}
+
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0u;
+  const uint32_t b = __float_as_uint(v);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// One CTA per (KV head, query): the key of the n_sel-th largest by four 8-bit
+// radix rounds, then the blocks at or above it in index order (of those at the
+// key itself, the lowest indices).
+__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const SelectArgs a) {
+  __shared__ int hist[256];
+  __shared__ int s_digit, s_need, wsum[2][32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = blockIdx.x, qi = blockIdx.y;
+  const int64_t blocks = (seen_positions(a) + qi + kB - 1) / kB;
+  const float* score = a.score + (int64_t(qi) * a.n_kvh + g) * a.nb;
+  int32_t* idx = a.idx + (int64_t(qi) * a.n_kvh + g) * a.n_sel;
+  if (blocks <= a.n_sel) {
+    for (int i = tid; i < a.n_sel; i += kSelThreads) idx[i] = i < blocks ? i : -1;
+    return;
+  }
+  const auto key_of = [&](int64_t b) {
+    return b < a.n_first || b >= blocks - a.n_last ? 0xFFFFFFFFu : order_key(__ldcg(score + b));
+  };
+  uint32_t prefix = 0;
+  int need = a.n_sel;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < 256) hist[tid] = 0;
+    __syncthreads();
+    for (int64_t b = tid; b < blocks; b += kSelThreads) {
+      const uint32_t k = key_of(b);
+      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane L holds bins 255 - 8 L .. 248 - 8 L, highest first
+      int h[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += h[i] = hist[255 - 8 * lane - i];
+      int incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      int before = incl - sum;
+      if (before < need && incl >= need) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (before < need && before + h[i] >= need) {
+            s_digit = 255 - 8 * lane - i;
+            s_need = need - before;
+          }
+          before += h[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= uint32_t(s_digit) << shift;
+    need = s_need;
+    __syncthreads();
+  }
+  // `need` blocks are taken at the key itself
+  int out = 0, ties = 0;
+  for (int64_t b0 = 0; b0 < blocks; b0 += kSelThreads) {
+    const int64_t b = b0 + tid;
+    const uint32_t k = b < blocks ? key_of(b) : 0u;
+    const bool tie = b < blocks && k == prefix;
+    const unsigned tm = __ballot_sync(0xffffffffu, tie);
+    if (lane == 0) wsum[0][warp] = __popc(tm);
+    __syncthreads();
+    int tr = ties, tt = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) tr += wsum[0][w];
+      tt += wsum[0][w];
+    }
+    tr += __popc(tm & ((1u << lane) - 1u));
+    const bool take = (b < blocks && k > prefix) || (tie && tr < need);
+    const unsigned km = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) wsum[1][warp] = __popc(km);
+    __syncthreads();
+    int at = out, kt = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) at += wsum[1][w];
+      kt += wsum[1][w];
+    }
+    at += __popc(km & ((1u << lane) - 1u));
+    if (take) idx[at] = int32_t(b);
+    out += kt;
+    ties += tt;
+  }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------------
+// launchers (arguments already validated by the C ABI layer)
+
+nt_status launch_kv8_append(Ctx* c, const nt_kv8& kv, int src_fmt, const void* k, const void* v, int64_t n,
+                            int64_t tok_stride, int64_t head_stride, int64_t pos, const int64_t* pos_dev,
+                            cudaStream_t st) {
+  AppendArgs a{};
+  a.src[0] = k;
+  a.src[1] = v;
+  a.tok_stride = tok_stride;
+  a.head_stride = head_stride;
+  a.dst[0] = static_cast<uint8_t*>(kv.k);
+  a.dst[1] = static_cast<uint8_t*>(kv.v);
+  a.scale[0] = kv.kscale;
+  a.scale[1] = kv.vscale;
+  a.kmin = kv.kmin;
+  a.kmax = kv.kmax;
+  a.n = n;
+  a.pos = pos;
+  a.pos_dev = pos_dev;
+  a.kv_stride = kv.kv_stride;
+  a.nb = kv8_blocks(kv.kv_stride);
+  a.err = c->err_flag;
+  // blocks the rows can touch: exact for a host position, the worst offset for a device one
+  const int64_t o0 = pos_dev ? kB - 1 : pos % kB;
+  const dim3 grid(unsigned((o0 + n + kB - 1) / kB), kv.n_kvh, 2), block(kAppendThreads);
+  using K = void (*)(AppendArgs);
+  const bool i8 = kv.fmt == NT_KV8_I8, h128 = kv.head_dim == 128;
+  K kern;
+  if (src_fmt == NT_F32)
+    kern = i8 ? (h128 ? kv8_append_kernel<NT_KV8_I8, 128, float> : kv8_append_kernel<NT_KV8_I8, 64, float>)
+              : (h128 ? kv8_append_kernel<NT_KV8_E4M3, 128, float> : kv8_append_kernel<NT_KV8_E4M3, 64, float>);
+  else
+    kern = i8 ? (h128 ? kv8_append_kernel<NT_KV8_I8, 128, __half> : kv8_append_kernel<NT_KV8_I8, 64, __half>)
+              : (h128 ? kv8_append_kernel<NT_KV8_E4M3, 128, __half> : kv8_append_kernel<NT_KV8_E4M3, 64, __half>);
+  return cuda_check(c, launch_k(c, kern, grid, block, 0, st, a), "8-bit cache write launch");
+}
+
+nt_status launch_kv8_read(Ctx* c, const nt_kv8& kv, int64_t pos, int64_t n, int dst_fmt, void* k, void* v,
+                          int64_t head_stride, cudaStream_t st) {
+  ReadArgs a{};
+  a.src[0] = static_cast<const uint8_t*>(kv.k);
+  a.src[1] = static_cast<const uint8_t*>(kv.v);
+  a.scale[0] = kv.kscale;
+  a.scale[1] = kv.vscale;
+  a.dst[0] = k;
+  a.dst[1] = v;
+  a.pos = pos;
+  a.n = n;
+  a.kv_stride = kv.kv_stride;
+  a.nb = kv8_blocks(kv.kv_stride);
+  a.head_stride = head_stride;
+  const int vec = dst_fmt == NT_F32 ? 4 : 8;
+  const int64_t units = n * (kv.head_dim / vec), per = kReadThreads * kReadUnroll;
+  const dim3 grid(unsigned((units + per - 1) / per), kv.n_kvh, 2), block(kReadThreads);
+  using K = void (*)(ReadArgs);
+  const bool i8 = kv.fmt == NT_KV8_I8, h128 = kv.head_dim == 128;
+  K kern;
+  if (dst_fmt == NT_F32)
+    kern = i8 ? (h128 ? kv8_read_kernel<NT_KV8_I8, 128, float> : kv8_read_kernel<NT_KV8_I8, 64, float>)
+              : (h128 ? kv8_read_kernel<NT_KV8_E4M3, 128, float> : kv8_read_kernel<NT_KV8_E4M3, 64, float>);
+  else
+    kern = i8 ? (h128 ? kv8_read_kernel<NT_KV8_I8, 128, __half> : kv8_read_kernel<NT_KV8_I8, 64, __half>)
+              : (h128 ? kv8_read_kernel<NT_KV8_E4M3, 128, __half> : kv8_read_kernel<NT_KV8_E4M3, 64, __half>);
+  return cuda_check(c, launch_k(c, kern, grid, block, 0, st, a), "8-bit cache read launch");
+}
+
+nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, int n_qh, int64_t n_pos, int nq,
+                          const int64_t* pos_dev, const int32_t* idx, int n_sel, char* scratch, size_t scratch_bytes,
+                          cudaStream_t st) {
+  AttnKv8Args a{};
+  a.q = q;
+  a.k = static_cast<const uint8_t*>(kv.k);
+  a.v = static_cast<const uint8_t*>(kv.v);
+  a.ks = kv.kscale;
+  a.vs = kv.vscale;
+  a.out = out;
+  a.idx = idx;
+  a.n_sel = n_sel;
+  a.n_qh = n_qh;
+  a.n_kvh = kv.n_kvh;
+  a.G = n_qh / kv.n_kvh;
+  a.nq = nq;
+  a.n_pos = n_pos;
+  a.kv_stride = kv.kv_stride;
+  a.nb = kv8_blocks(kv.kv_stride);
+  a.pos_dev = pos_dev;
+  a.err = c->err_flag;
+  const bool sparse = idx != nullptr;
+  const int rows = sparse ? a.G : a.G * nq;
+  const int R = rows > 8 ? 2 : 1;
+  a.chunks = (rows + 8 * R - 1) / (8 * R);
+  const int z = sparse ? a.chunks * nq : a.chunks;
+  // splits: the grid fills the SMs once (two CTAs each, one with R = 2), no more
+  // than the longest sequence has work for, and what the scratch holds
+  const int64_t most = sparse ? int64_t(n_sel) * kB : (pos_dev ? kv.kv_stride : n_pos + nq - 1);
+  const int64_t steps = (most + kStep - 1) / kStep;
+  int64_t S = int64_t(c->num_sms) * (R == 1 ? 2 : 1) / (int64_t(kv.n_kvh) * z);
+  const int64_t useful = (steps + kAttnWarps - 1) / kAttnWarps;
+  const size_t vecs = size_t(n_qh) * nq, row = vecs * (kv.head_dim * 4 + 8);
+  if (S > useful) S = useful;
+  if (S * int64_t(row) > int64_t(scratch_bytes)) S = int64_t(scratch_bytes / row);
+  if (S < 1) S = 1;
+  a.S = int(S);
+  a.part = reinterpret_cast<float*>(scratch);
+  a.ml = reinterpret_cast<float2*>(scratch + vecs * S * kv.head_dim * 4);
+  size_t smem = 0;
+  AttnKv8Kernel kern = sparse ? attn_kv8_for<true>(kv.fmt, kv.head_dim, R, &smem)
+                              : attn_kv8_for<false>(kv.fmt, kv.head_dim, R, &smem);
+  nt_status s = cuda_check(c, launch_k(c, kern, dim3(kv.n_kvh, a.S, z), dim3(kAttnWarps * 32), smem, st, a),
+                           "8-bit attention launch");
+  if (s || a.S == 1) return s;  // one split wrote the output
+  using C = void (*)(AttnKv8Args, int);
+  C comb = kv.head_dim == 128 ? (sparse ? attn_kv8_combine_kernel<128, true> : attn_kv8_combine_kernel<128, false>)
+                              : (sparse ? attn_kv8_combine_kernel<64, true> : attn_kv8_combine_kernel<64, false>);
+  return cuda_check(c, launch_k(c, comb, dim3(n_qh, nq), dim3(kv.head_dim), 0, st, a, 8 * R),
+                    "8-bit attention combine launch");
+}
+
+size_t kv8_score_bytes(const nt_kv8& kv, int nq) {
+  return size_t(nq) * kv.n_kvh * size_t(kv8_blocks(kv.kv_stride)) * sizeof(float);
+}
+
+nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, int64_t n_pos, int nq,
+                            const int64_t* pos_dev, int n_sel, int n_first, int n_last, int32_t* idx, char* scratch,
+                            cudaStream_t st) {
+  SelectArgs a{};
+  a.q = q;
+  a.kmin = kv.kmin;
+  a.kmax = kv.kmax;
+  a.ks = kv.kscale;
+  a.score = reinterpret_cast<float*>(scratch);
+  a.idx = idx;
+  a.n_qh = n_qh;
+  a.n_kvh = kv.n_kvh;
+  a.G = n_qh / kv.n_kvh;
+  a.nq = nq;
+  a.n_sel = n_sel;
+  a.n_first = n_first;
+  a.n_last = n_last;
+  a.n_pos = n_pos;
+  a.kv_stride = kv.kv_stride;
+  a.nb = kv8_blocks(kv.kv_stride);
+  a.pos_dev = pos_dev;
+  a.err = c->err_flag;
+  const int64_t blocks = pos_dev ? a.nb : kv8_blocks(n_pos + nq - 1);
+  const int bw = 32 / (kv.head_dim / 16) * (kScoreThreads / 32);  // blocks per CTA and pass
+  int64_t gx = (blocks + bw - 1) / bw;
+  const int64_t fill = (int64_t(c->num_sms) * 8 + int64_t(kv.n_kvh) * nq - 1) / (int64_t(kv.n_kvh) * nq);
+  gx = gx < 1 ? 1 : (gx > fill ? fill : gx);
+  nt_status s = cuda_check(c, launch_k(c, kv.head_dim == 128 ? kv8_score_kernel<128> : kv8_score_kernel<64>,
+                                       dim3(unsigned(gx), kv.n_kvh, nq), dim3(kScoreThreads), 0, st, a),
+                           "block score launch");
+  if (s) return s;
+  return cuda_check(c, launch_k(c, kv8_select_kernel, dim3(kv.n_kvh, nq), dim3(kSelThreads), 0, st, a),
+                    "block select launch");
+}
+
+nt_status configure_kv8(Ctx* c) {
+  for (int fmt : {NT_KV8_I8, NT_KV8_E4M3})
+    for (int hd : {64, 128})
+      for (int R : {1, 2})
+        for (bool sparse : {false, true}) {
+          size_t smem = 0;
+          AttnKv8Kernel k = sparse ? attn_kv8_for<true>(fmt, hd, R, &smem) : attn_kv8_for<false>(fmt, hd, R, &smem);
+          nt_status s = cuda_check(c, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)),
+                                   "8-bit attention shared-memory attribute");
+          if (s) return s;
+        }
+  return NT_OK;
+}
+
+}  // namespace nt

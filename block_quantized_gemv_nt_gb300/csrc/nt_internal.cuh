@@ -23,6 +23,7 @@ constexpr int kStallSpin = 8;       // the cap of a launch armed by nt_debug_sta
 constexpr unsigned kWaitHintNs = 50000;  // each try_wait may sleep this long (cap ~3 s in all)
 constexpr unsigned kErrWaitTimeout = 1u;
 constexpr unsigned kErrPosRange = 2u;  // a device-side position fell outside the KV cache: nothing written there
+constexpr unsigned kErrNonFinite = 4u;  // a NaN or an infinity was written to an 8-bit cache
 
 // a GEMV launch configuration: warps per CTA and stage-size cap (what the
 // tuner chooses), and, for the record, the shape's arithmetic: column parts
@@ -89,7 +90,13 @@ constexpr size_t kScratchSample = size_t(20) << 20;  // sampler state (one row o
 constexpr size_t kSampRowBytes = 32768;             // sampler state per logits row
 constexpr int64_t kSampMaxN = 256 * 4000;           // longest row the sampler takes
 constexpr size_t kScratchTune = size_t(24) << 20;  // GEMV plan tuning outputs (8 MiB)
-constexpr size_t kScratchGemm = size_t(32) << 20;  // verify-GEMM partial sums, to the end of the scratch
+constexpr size_t kScratchGemm = size_t(32) << 20;  // verify-GEMM partial sums and the 8-bit cache's partials and block scores, to the end of the scratch
+
+// 8-bit KV cache: positions per scale
+constexpr int kKv8Block = NT_KV8_BLOCK;
+__host__ __device__ constexpr int64_t kv8_blocks(int64_t positions) {
+  return (positions + kKv8Block - 1) / kKv8Block;
+}
 
 // format geometry ---------------------------------------------------------------
 __host__ __device__ constexpr int block_elems(int fmt) {

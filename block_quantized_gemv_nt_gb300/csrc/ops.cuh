@@ -57,4 +57,20 @@ nt_status launch_inv_freq(Ctx* c, double* out, int head_dim, float theta, cudaSt
 nt_status configure_ops(Ctx* c);
 nt_status launch_cos(Ctx* c, const float* a, const float* b, int64_t n, float* out, cudaStream_t st);
 
+// 8-bit KV cache (kv8.cu)
+nt_status launch_kv8_append(Ctx* c, const nt_kv8& kv, int src_fmt, const void* k, const void* v, int64_t n,
+                            int64_t tok_stride, int64_t head_stride, int64_t pos, const int64_t* pos_dev,
+                            cudaStream_t st);
+nt_status launch_kv8_read(Ctx* c, const nt_kv8& kv, int64_t pos, int64_t n, int dst_fmt, void* k, void* v,
+                          int64_t head_stride, cudaStream_t st);
+// idx null: every position; else attention over the listed blocks of each query and KV head
+nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, int n_qh, int64_t n_pos, int nq,
+                          const int64_t* pos_dev, const int32_t* idx, int n_sel, char* scratch, size_t scratch_bytes,
+                          cudaStream_t st);
+size_t kv8_score_bytes(const nt_kv8& kv, int nq);
+nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, int64_t n_pos, int nq,
+                            const int64_t* pos_dev, int n_sel, int n_first, int n_last, int32_t* idx, char* scratch,
+                            cudaStream_t st);
+nt_status configure_kv8(Ctx* c);
+
 }  // namespace nt

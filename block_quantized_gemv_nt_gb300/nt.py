@@ -16,6 +16,9 @@ from . import build as _build
 Q8_0, Q4_0, Q4_K, Q5_K, Q6_K, F16, F32 = 0, 1, 2, 3, 4, 5, 6
 FMT_NAMES = {Q8_0: "Q8_0", Q4_0: "Q4_0", Q4_K: "Q4_K", Q5_K: "Q5_K", Q6_K: "Q6_K", F16: "F16", F32: "F32"}
 
+KV8_I8, KV8_E4M3 = 0, 1
+KV8_BLOCK = 64
+
 NT_OK, NT_ERR_INVALID_ARG, NT_ERR_UNSUPPORTED_FMT, NT_ERR_ALIGNMENT, NT_ERR_CUDA, NT_ERR_OOM, NT_ERR_TIMEOUT = range(7)
 STATUS_NAMES = ["NT_OK", "NT_ERR_INVALID_ARG", "NT_ERR_UNSUPPORTED_FMT", "NT_ERR_ALIGNMENT", "NT_ERR_CUDA",
                 "NT_ERR_OOM", "NT_ERR_TIMEOUT"]
@@ -72,6 +75,18 @@ _sig("nt_softmax", [_vp, _vp, _vp, _i64, _vp])
 _sig("nt_swiglu", [_vp, _vp, _vp, _vp, _i64, _vp])
 _sig("nt_argmax", [_vp, _vp, _i64, _vp, _vp])
 _sig("nt_cos_sim", [_vp, _vp, _vp, _i64, _vp, _vp])
+
+
+class nt_kv8(ctypes.Structure):
+    _fields_ = [("fmt", _ci), ("n_kvh", _ci), ("head_dim", _ci), ("kv_stride", _i64)] + [
+        (n, _vp) for n in ("k", "v", "kscale", "vscale", "kmin", "kmax")]
+
+
+_sig("nt_kv8_append", [_vp, ctypes.POINTER(nt_kv8), _ci, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp])
+_sig("nt_kv8_read", [_vp, ctypes.POINTER(nt_kv8), _i64, _i64, _ci, _vp, _vp, _i64, _vp])
+_sig("nt_attn_kv8", [_vp, _vp, ctypes.POINTER(nt_kv8), _vp, _ci, _i64, _ci, _vp, _vp])
+_sig("nt_kv8_select", [_vp, _vp, ctypes.POINTER(nt_kv8), _ci, _i64, _ci, _vp, _ci, _ci, _ci, _vp, _vp])
+_sig("nt_attn_kv8_blocks", [_vp, _vp, ctypes.POINTER(nt_kv8), _vp, _ci, _i64, _ci, _vp, _vp, _ci, _vp])
 
 
 class nt_model_desc(ctypes.Structure):
@@ -135,6 +150,7 @@ EXPORTED = ["nt_ctx_create", "nt_ctx_destroy", "nt_ctx_sync", "nt_last_error", "
             "nt_gemm_q", "nt_attn_verify", "nt_plan_residency", "nt_prefill", "nt_sample", "nt_model_set_sampler",
             "nt_host_register", "nt_host_unregister", "nt_stream_sync", "nt_debug_fail_copy", "nt_debug_host_delay",
             "nt_debug_stall_waits", "nt_ctx_gemv_plans", "nt_model_graph_count", "nt_model_prefill_chunk",
+            "nt_kv8_append", "nt_kv8_read", "nt_attn_kv8", "nt_kv8_select", "nt_attn_kv8_blocks",
             "nt_file_open", "nt_file_close", "nt_file_desc", "nt_file_header", "nt_file_entry", "nt_file_lock",
             "nt_file_unlock", "nt_debug_file_refuse_in_place"]
 
@@ -281,6 +297,31 @@ def nt_gemm_q(ctx, fmt, W, X, Y, rows, cols, M, residual=None, norm_g=None, eps=
 def nt_attn_verify(ctx, q, kcache, vcache, out, n_qh, n_kvh, head_dim, n_pos0, n_query, kv_stride, stream=None):
     return ctx.check(_lib.nt_attn_verify(ctx.handle, _ptr(q), _ptr(kcache), _ptr(vcache), _ptr(out), n_qh, n_kvh,
                                          head_dim, n_pos0, n_query, kv_stride, _stream(stream, out)))
+
+
+def nt_kv8_append(ctx, cache: nt_kv8, src_fmt, k, v, n_tok, tok_stride, head_stride, pos, pos_dev=None, stream=None):
+    return ctx.check(_lib.nt_kv8_append(ctx.handle, ctypes.byref(cache), src_fmt, _ptr(k), _ptr(v), n_tok, tok_stride,
+                                        head_stride, pos, _ptr(pos_dev), _stream(stream, k)))
+
+
+def nt_kv8_read(ctx, cache: nt_kv8, pos0, n, dst_fmt, k, v, head_stride, stream=None):
+    return ctx.check(_lib.nt_kv8_read(ctx.handle, ctypes.byref(cache), pos0, n, dst_fmt, _ptr(k), _ptr(v), head_stride,
+                                      _stream(stream, v if k is None else k)))
+
+
+def nt_attn_kv8(ctx, q, cache: nt_kv8, out, n_qh, n_pos, n_query=1, pos_dev=None, stream=None):
+    return ctx.check(_lib.nt_attn_kv8(ctx.handle, _ptr(q), ctypes.byref(cache), _ptr(out), n_qh, n_pos, n_query,
+                                      _ptr(pos_dev), _stream(stream, out)))
+
+
+def nt_kv8_select(ctx, q, cache: nt_kv8, n_qh, n_pos, n_query, n_sel, n_first, n_last, idx, pos_dev=None, stream=None):
+    return ctx.check(_lib.nt_kv8_select(ctx.handle, _ptr(q), ctypes.byref(cache), n_qh, n_pos, n_query, _ptr(pos_dev),
+                                        n_sel, n_first, n_last, _ptr(idx), _stream(stream, idx)))
+
+
+def nt_attn_kv8_blocks(ctx, q, cache: nt_kv8, out, n_qh, n_pos, n_query, idx, n_sel, pos_dev=None, stream=None):
+    return ctx.check(_lib.nt_attn_kv8_blocks(ctx.handle, _ptr(q), ctypes.byref(cache), _ptr(out), n_qh, n_pos, n_query,
+                                             _ptr(pos_dev), _ptr(idx), n_sel, _stream(stream, out)))
 
 
 def nt_host_register(ctx, host_ptr: int, nbytes: int, read_only: bool = True):

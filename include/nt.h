@@ -262,6 +262,112 @@ nt_status nt_sample(nt_ctx* ctx, const float* logits_dev, int64_t n, float tempe
 nt_status nt_cos_sim(nt_ctx* ctx, const float* a_dev, const float* b_dev, int64_t n, float* out_dev,
                      void* stream);
 
+/* ---- 8-bit KV cache --------------------------------------------------------- */
+
+/* Formats of an 8-bit KV cache, beside the F16 one of [road]: whole numbers
+ * -127..127, or E4M3 floating point (4 exponent and 3 mantissa bits, no
+ * infinities, largest 448). */
+enum { NT_KV8_I8 = 0, NT_KV8_E4M3 = 1 };
+/* Positions that share a scale (a block). */
+#define NT_KV8_BLOCK 64
+
+/* One layer's 8-bit KV cache, in buffers of the caller.  The value at position p
+ * of head h is byte value * scale[h][p / 64].  Scales are powers of two, at
+ * least 2^-100.  kmin / kmax (both or neither) bound each block's k per channel
+ * in units of its scale (I8) or of 4 times its scale (E4M3, rounded outwards);
+ * nt_kv8_append keeps them and nt_kv8_select reads them.  k, v, kmin and kmax
+ * 16-byte aligned, scales 4-byte.  Nothing needs to be initialised: a block is
+ * begun by the append that writes its first position. */
+typedef struct {
+  int fmt;              /* NT_KV8_I8 or NT_KV8_E4M3 */
+  int n_kvh, head_dim;  /* 1..64 heads of 64 or 128 channels */
+  int64_t kv_stride;    /* positions per head, 1..2^30 */
+  void *k, *v;          /* [n_kvh][kv_stride][head_dim] bytes */
+  float *kscale, *vscale; /* [n_kvh][ceil(kv_stride / 64)] */
+  int8_t *kmin, *kmax;  /* [n_kvh][ceil(kv_stride / 64)][head_dim], or NULL */
+} nt_kv8;
+
+/* Append to an 8-bit KV cache, the quantising form of the F16 append of [road]:
+ * n_tok rows of k and v (after RoPE) to positions pos .. pos + n_tok - 1 of every
+ * head.  Row t of head h is at k + t * tok_stride + h * head_stride elements of
+ * src_fmt (NT_F32 or NT_F16): a step's rows [n_tok][n_kvh][head_dim] have
+ * tok_stride = n_kvh * head_dim, head_stride = head_dim; an F16 cache
+ * [n_kvh][kv_stride][head_dim] is converted with tok_stride = head_dim,
+ * head_stride = kv_stride * head_dim.  For each block touched, head, and K and V:
+ *   need = the least power of two >= 2^-100 with max |x| <= 127 (I8) or 448
+ *   (E4M3) times it, over the block's new rows;  scale = need when the rows
+ *   begin the block, else max(old scale, need);
+ *   new rows are x / scale rounded to nearest, ties to even; when the scale
+ *   grows, the block's earlier rows are rounded the same way to the new scale.
+ * Rows of the block behind the last one written no longer count: a shorter
+ * sequence is continued by appending at its end (a speculative step that was
+ * cut back), and kmin / kmax then bound the block's rows up to the last written.
+ * The scale of a block never shrinks until its first position is written again.
+ * A NaN is stored as 0 and an infinity as the largest 8-bit value; both set the
+ * device flag that nt_ctx_sync reports (NT_ERR_INVALID_ARG).
+ * pos_dev (nullable): the position is read from the device (8-byte aligned) and
+ * pos is ignored, so a captured call can be replayed; rows that would leave the
+ * cache are then not written and set the device flag.
+ * Rows 16-byte (F32) or 8-byte (F16) aligned, strides multiples of 4.  One
+ * launch, no scratch. */
+nt_status nt_kv8_append(nt_ctx* ctx, const nt_kv8* cache, int src_fmt, const void* k_dev, const void* v_dev,
+                        int64_t n_tok, int64_t tok_stride, int64_t head_stride, int64_t pos,
+                        const int64_t* pos_dev, void* stream);
+
+/* Read back positions pos0 .. pos0 + n - 1 of an 8-bit KV cache ([road] has the
+ * F16 cache this converts to): byte value * scale as dst_fmt (NT_F32, or NT_F16
+ * rounded to nearest), head h's rows [n][head_dim] at k_dev + h * head_stride
+ * elements.  k_dev or v_dev may be NULL.  Outputs 16-byte aligned, head_stride
+ * a multiple of 4 (F32) or 8 (F16) and, with several heads, at least
+ * n * head_dim. */
+nt_status nt_kv8_read(nt_ctx* ctx, const nt_kv8* cache, int64_t pos0, int64_t n, int dst_fmt, void* k_dev,
+                      void* v_dev, int64_t head_stride, void* stream);
+
+/* Attention with grouped KV heads [feat] over an 8-bit KV cache: n_query (1..16)
+ * consecutive tokens whose K/V are already in the cache; query i attends to
+ * positions 0 .. n_pos - 1 + i (the rule of nt_attn_verify; n_query = 1 is a
+ * decode step).  For q head h, KV head g = h / (n_qh / n_kvh):
+ *   out_h = softmax_j(q_h . K_g[j] / sqrt(head_dim)) . V_g[j].
+ * q_dev, out_dev fp32 [n_query][n_qh][head_dim], 16-byte aligned; n_qh is 1..16
+ * times n_kvh.  A query with no positions (n_pos = 0) gives zeros.  Positions
+ * the query does not see may hold anything.  Scales may be any normal positive
+ * floats.  Scores, probabilities and sums are fp32-accurate: q and the
+ * probabilities enter the tensor cores as two f16 parts each.
+ * pos_dev (nullable): n_pos = *pos_dev + 1 is read from the device and the
+ * argument ignored (a captured call can be replayed); a value outside the cache
+ * sets the device flag and is held to the cache.
+ * Uses the context scratch beyond its first 32 MiB for split partials:
+ * NT_ERR_OOM when n_query * n_qh * (4 head_dim + 8) bytes do not fit. */
+nt_status nt_attn_kv8(nt_ctx* ctx, const float* q_dev, const nt_kv8* cache, float* out_dev, int n_qh, int64_t n_pos,
+                      int n_query, const int64_t* pos_dev, void* stream);
+
+/* Choose the blocks of an 8-bit KV cache [road] that each query reads, by a
+ * bound on their attention scores.  With query i seeing B = ceil((n_pos + i) /
+ * 64) blocks, and per KV head the group's q rounded to whole numbers
+ *   qi = rint(q / tq), tq the least power of two >= 2^-100 with max |q| <= 2047 tq
+ * over the group (a NaN counts as 0, an infinity as 2047 tq), block b scores
+ *   fp32(sum_h sum_d max(qi kmin[b][d], qi kmax[b][d])) * kscale[b]:
+ * up to q's rounding, an upper bound on sum_h q_h . k of any key in the block
+ * (per channel bounds: Tang et al. 2024).  idx_dev int32 [n_query][n_kvh][n_sel]
+ * receives the first n_first and the last n_last of the B blocks and, of the
+ * others, the highest scores (ties: lower index), n_sel in all, in ascending
+ * order; all B and then -1 when B <= n_sel.  The whole-number sums make the
+ * choice independent of the order of additions.  Needs kmin / kmax;
+ * n_first + n_last <= n_sel <= 2^24; q, n_pos, n_query and pos_dev as
+ * nt_attn_kv8.  Uses the context scratch beyond its first 32 MiB: NT_ERR_OOM
+ * when 4 * n_query * n_kvh * ceil(kv_stride / 64) bytes do not fit. */
+nt_status nt_kv8_select(nt_ctx* ctx, const float* q_dev, const nt_kv8* cache, int n_qh, int64_t n_pos, int n_query,
+                        const int64_t* pos_dev, int n_sel, int n_first, int n_last, int32_t* idx_dev, void* stream);
+
+/* nt_attn_kv8 ([feat] GQA) over the blocks listed for each query and KV head:
+ * idx_dev int32 [n_query][n_kvh][n_sel], as nt_kv8_select writes them.  Query i
+ * attends to the positions of its blocks below n_pos + i.  The order of a list
+ * does not matter; an entry that is negative or past the query's last block is
+ * skipped, and a block listed twice counts twice.  A query left without
+ * positions gives zeros.  Scratch as nt_attn_kv8. */
+nt_status nt_attn_kv8_blocks(nt_ctx* ctx, const float* q_dev, const nt_kv8* cache, float* out_dev, int n_qh,
+                             int64_t n_pos, int n_query, const int64_t* pos_dev, const int32_t* idx_dev, int n_sel,
+                             void* stream);
 
 /* ---- whole decode step ------------------------------------------------------ */
 
