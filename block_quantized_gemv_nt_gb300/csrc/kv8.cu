@@ -302,15 +302,21 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 //  - P V: those four tokens are the lane's k-slots; it loads bytes
 //    n HD/8 .. + HD/8 - 1 of their V rows, and byte i of them is B column n of
 //    n-tile i, i.e. output channel n HD/8 + i.
+//
+// Each lane copies exactly the bytes it will use into its own slots of a ring in
+// shared memory (cp.async), kStages steps ahead: no barrier joins the lanes, no
+// slot has a bank conflict, and what is in flight costs no registers.
 constexpr int kAttnWarps = 8;
 constexpr int kStep = 16;  // tokens per warp step
+constexpr int kStages = 2;
+constexpr int kFlush = 16;
 
 struct AttnKv8Args {
   const float* q;
   const uint8_t *k, *v;
   const float *ks, *vs;
   float* out;
-  float* part;         // [query * n_qh + head][S][HD], unnormalised outputs
+  float* part;         // [query * n_qh + head][S][HD], unnormalised outputs in fragment order
   float2* ml;          // [query * n_qh + head][S]: (max, sum)
   const int32_t* idx;  // sparse: [query][n_kvh][n_sel]
   int n_sel;
@@ -331,8 +337,8 @@ __device__ __forceinline__ int64_t seen_positions(const AttnKv8Args& a) {
   return n;
 }
 
-// steps per CTA and splits in use for `steps` 16-token steps: both launches
-// compute it, so an unused split is never read
+// steps per CTA for `steps` 16-token steps over S splits: both launches compute
+// it, so an unused split is never read
 __device__ __forceinline__ int64_t split_steps(int64_t steps, int S) {
   const int64_t even = (steps + S - 1) / S;
   return even < kAttnWarps ? kAttnWarps : even;
@@ -360,22 +366,43 @@ __device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-template <int HD, int R>
-constexpr size_t attn_kv8_smem() {
-  const size_t qa = size_t(R) * (HD / 16) * 32 * 16;
-  const size_t merge = size_t(kAttnWarps) * 8 * R * (HD + 2) * 4;
-  return qa > merge ? qa : merge;
+// BYTES (16 or 8) global -> shared; `live` false fills with zeros and reads nothing
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live) {
+  const int n = live ? BYTES : 0;
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// shared memory: q fragments [R][HD / 16][32] x 16, totals [warps][R][HD / 8][32] x 8,
+// (max, sum) [2][warps][8 R], the ring [warps][kStages][32 tokens' bytes]
+template <int HD, int R>
+struct AttnKv8Smem {
+  static constexpr size_t q = 0;
+  static constexpr size_t tot = q + size_t(R) * (HD / 16) * 512;
+  static constexpr size_t ml = tot + size_t(kAttnWarps) * R * (HD / 8) * 256;
+  static constexpr size_t ring = ml + size_t(2) * kAttnWarps * 8 * R * 4;
+  static constexpr size_t stage = size_t(kStep) * HD * 2;
+  static constexpr size_t bytes = ring + kAttnWarps * kStages * stage;
+};
 
 template <int FMT, int HD, int R, bool SPARSE>
 __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kernel(const AttnKv8Args a) {
+  using L = AttnKv8Smem<HD, R>;
   constexpr int KS = HD / 16;        // k-steps of Q K^T
   constexpr int NT = HD / 8;         // n-tiles of P V
   constexpr int KP = HD / 64;        // 16-byte pieces of a K row per lane
   constexpr int VW = HD / 32;        // words of a V row per lane
   constexpr int ROWS = 8 * R;
   extern __shared__ __align__(16) uint8_t sm8[];
-  uint4* qa = reinterpret_cast<uint4*>(sm8);  // [R][KS][32]: A fragments of q
+  uint4* qa = reinterpret_cast<uint4*>(sm8 + L::q);
   __shared__ float s_amax[ROWS];
   pdl_wait();
   pdl_trigger();
@@ -394,11 +421,65 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const int64_t st0 = int64_t(s) * per, st1 = min(steps, st0 + per);
   if (st0 >= st1 && s > 0) return;
 
+  const uint8_t* kg = a.k + int64_t(g) * a.kv_stride * HD;
+  const uint8_t* vg = a.v + int64_t(g) * a.kv_stride * HD;
+  const float* ksg = a.ks + int64_t(g) * a.nb;
+  const float* vsg = a.vs + int64_t(g) * a.nb;
+  const int32_t* list = SPARSE ? a.idx + (int64_t(qi0) * a.n_kvh + g) * a.n_sel : nullptr;
+  const int64_t blocks_seen = (tokens + kB - 1) / kB;
+  const uint32_t ring = smem_u32(sm8 + L::ring + size_t(warp) * kStages * L::stage);
+
+  // first token of step st (tokens: nothing to do), and its copies into `slot`
+  const auto step_token = [&](int64_t st) -> int64_t {
+    if (st >= st1) return tokens;
+    if (!SPARSE) return st * kStep;
+    const int64_t b = __ldg(list + (st >> 2));
+    return b < 0 || b >= blocks_seen ? tokens : min(tokens, b * kB + (st & 3) * kStep);
+  };
+  const auto issue = [&](int64_t t0, int slot, float& ks, float& vs) {
+    ks = vs = 0.f;
+    if (t0 < tokens) {
+      const uint32_t at = ring + slot * uint32_t(L::stage);
+      const int left = int(min(tokens - t0, int64_t(kStep)));
+      const uint8_t* kr = kg + t0 * HD;
+      const uint8_t* vr = vg + t0 * HD;
+      ks = __ldg(ksg + t0 / kB);
+      vs = __ldg(vsg + t0 / kB);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = 4 * (n >> 1) + 2 * u + (n & 1);
+        const bool live = t < left;
+#pragma unroll
+        for (int p = 0; p < KP; ++p)
+          cp_async<16>(at + (u * KP + p) * 512 + lane * 16, kr + (live ? t * HD + 64 * p + 16 * c : 0), live);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int t = 4 * c + x;
+        const bool live = t < left;
+        cp_async<HD / 8>(at + 2 * KP * 512 + x * (HD / 8) * 32 + lane * (HD / 8), vr + (live ? t * HD + n * (HD / 8) : 0),
+                         live);
+      }
+    }
+    cp_commit();
+  };
+  int64_t tq[kStages + 1];            // first tokens of the next steps
+  float ksq[kStages], vsq[kStages];
+  int64_t st = st0 + warp;
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) tq[i] = step_token(st + i * kAttnWarps);
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) issue(tq[i], i, ksq[i], vsq[i]);
+  tq[kStages] = step_token(st + kStages * kAttnWarps);
+
   // q: each row scaled by a power of two to amax in [2^13, 2^14), split, laid out as fragments
   for (int r = warp; r < ROWS; r += kAttnWarps) {
     float m = 0.f;
-    if (r < rows)
-      for (int d = lane; d < HD; d += 32) m = fmaxf(m, fabsf(a.q[vec_of(r) * HD + d]));
+    if (r < rows) {
+      const float* qr = a.q + vec_of(r) * HD;
+#pragma unroll
+      for (int d = 0; d < HD; d += 32) m = fmaxf(m, fabsf(qr[d + lane]));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) s_amax[r] = m;
@@ -424,7 +505,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   __syncthreads();
   float rscale[R];      // scores to the base-2 exponent
   int64_t limit[R];     // positions row n sees
-  float m[R], l[R];
+  float m[R], l[R], mf[R];
   float o[R][NT][4];
 #pragma unroll
   for (int t = 0; t < R; ++t) {
@@ -433,186 +514,217 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     rscale[t] = __uint_as_float(uint32_t(127 - row_exp(r)) << 23) * (1.44269504088896f * rsqrtf(float(HD))) *
                 h2_factor<FMT>();
     limit[t] = r < rows ? n_pos + query_of(r) : 0;
-    m[t] = -INFINITY;
+    m[t] = mf[t] = -INFINITY;
     l[t] = 0.f;
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
   }
-  const uint8_t* kg = a.k + int64_t(g) * a.kv_stride * HD;
-  const uint8_t* vg = a.v + int64_t(g) * a.kv_stride * HD;
-  const float* ksg = a.ks + int64_t(g) * a.nb;
-  const float* vsg = a.vs + int64_t(g) * a.nb;
-  const int32_t* list = SPARSE ? a.idx + (int64_t(qi0) * a.n_kvh + g) * a.n_sel : nullptr;
-  const int64_t blocks_seen = (tokens + kB - 1) / kB;
-
-  for (int64_t st = st0 + warp; st < st1; st += kAttnWarps) {
-    int64_t t0, blk;
-    if (SPARSE) {
-      blk = list[st >> 2];
-      if (blk < 0 || blk >= blocks_seen) continue;
-      t0 = blk * kB + (st & 3) * kStep;
-      if (t0 >= tokens) continue;
-    } else {
-      t0 = st * kStep;
-      blk = t0 / kB;
-    }
-    const float ks = ksg[blk], vs = vsg[blk];
-    uint4 kw[2][KP];
-    uint32_t vw[4][VW];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t t = t0 + 4 * (n >> 1) + 2 * u + (n & 1);
-#pragma unroll
-      for (int p = 0; p < KP; ++p)
-        kw[u][p] = t < tokens ? __ldcs(reinterpret_cast<const uint4*>(kg + t * HD + 64 * p + 16 * c)) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int64_t t = t0 + 4 * c + x;
-      const uint8_t* p = vg + t * HD + n * (HD / 8);
-      if (HD == 128) {
-        const uint4 r = t < tokens ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-        vw[x][0] = r.x;
-        vw[x][1] = r.y;
-        vw[x][VW - 2] = r.z;
-        vw[x][VW - 1] = r.w;
-      } else {
-        const uint2 r = t < tokens ? __ldcs(reinterpret_cast<const uint2*>(p)) : make_uint2(0u, 0u);
-        vw[x][0] = r.x;
-        vw[x][1] = r.y;
-      }
-    }
-    // ---- scores
-    float sc[R][2][4];
-#pragma unroll
-    for (int t = 0; t < R; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) sc[t][u][0] = sc[t][u][1] = sc[t][u][2] = sc[t][u][3] = 0.f;
-#pragma unroll
-    for (int j = 0; j < KS; ++j) {
-      uint4 af[R];
-#pragma unroll
-      for (int t = 0; t < R; ++t) af[t] = qa[(t * KS + j) * 32 + lane];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint4& k4 = kw[u][j >> 2];
-        const uint32_t raw = (j & 3) == 0 ? k4.x : (j & 3) == 1 ? k4.y : (j & 3) == 2 ? k4.z : k4.w;
-        const uint32_t x = bias8<FMT>(raw);
-        const uint32_t b0 = to_h2<FMT, true>(x), b1 = to_h2<FMT, false>(x);
-#pragma unroll
-        for (int t = 0; t < R; ++t) mma16816(sc[t][u], af[t], b0, b1);
-      }
-    }
-    // ---- online softmax: p = 2^(s - m); the f16 operand of P V is p times the
-    // block's V scale, so m follows s plus the exponent of that scale (which
-    // keeps the operand below 2^15), floored where a block's V is all but zero
-    const float lv = fmaxf(float(int(__float_as_uint(vs) >> 23) - 127), -64.f);
-    uint4 pf[R];
+  float2* tot = reinterpret_cast<float2*>(sm8 + L::tot) + size_t(warp) * R * NT * 32 + lane;  // [R][NT], lane's own
+  // add the accumulators into the totals (both held relative to their maxima, mf and m)
+  const auto flush = [&](bool first) {
 #pragma unroll
     for (int t = 0; t < R; ++t) {
-      const float f = rscale[t] * ks;
-      float p[4];
-      float mx = -INFINITY;
+      const float f = mf[t] == -INFINITY ? 0.f : ex2(mf[t] - m[t]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float v = sc[t][x >> 1][x & 1] + sc[t][x >> 1][2 + (x & 1)];
-        p[x] = t0 + 4 * c + x < limit[t] ? v * f : -INFINITY;
-        mx = fmaxf(mx, p[x]);
+      for (int i = 0; i < NT; ++i) {
+        float2 x = make_float2(o[t][i][0] + o[t][i][2], o[t][i][1] + o[t][i][3]);
+        if (!first) {
+          const float2 y = tot[(t * NT + i) * 32];
+          x.x = fmaf(y.x, f, x.x);
+          x.y = fmaf(y.y, f, x.y);
+        }
+        tot[(t * NT + i) * 32] = x;
+        o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[t], mx + lv);
-      if (__any_sync(0xffffffffu, mn > m[t])) {
-        const float corr = m[t] == -INFINITY ? 0.f : ex2(m[t] - mn);
-        l[t] *= corr;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[t][i][e] *= corr;
-        m[t] = mn;
-      }
-      const float base = mn == -INFINITY ? 0.f : mn - 14.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        p[x] = ex2(p[x] - base);
-        l[t] += p[x];
-        p[x] *= vs;
-      }
-      split_h2(p[0], p[1], pf[t].x, pf[t].y);
-      split_h2(p[2], p[3], pf[t].z, pf[t].w);
+      mf[t] = m[t];
     }
-    // ---- P V: words of the lane's four tokens interleaved into (token, token + 1) pairs per channel
-#pragma unroll
-    for (int w = 0; w < VW; ++w) {
-      uint32_t y[2][2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        y[x][0] = bias8<FMT>(__byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x5140));
-        y[x][1] = bias8<FMT>(__byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x7362));
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t b0 = (i & 1) ? to_h2<FMT, false>(y[0][i >> 1]) : to_h2<FMT, true>(y[0][i >> 1]);
-        const uint32_t b1 = (i & 1) ? to_h2<FMT, false>(y[1][i >> 1]) : to_h2<FMT, true>(y[1][i >> 1]);
-#pragma unroll
-        for (int t = 0; t < R; ++t) mma16816(o[t][4 * w + i], pf[t], b0, b1);
-      }
-    }
-  }
+  };
 
-  // ---- merge the warps: (m, l, o) of every row in shared memory
-  __syncthreads();
-  float* mo = reinterpret_cast<float*>(sm8);                 // [warps][ROWS][HD]
-  float* mm = mo + size_t(kAttnWarps) * ROWS * HD;           // [warps][ROWS] max
-  float* mll = mm + kAttnWarps * ROWS;                       // [warps][ROWS] sum
+  int slot = 0, since = 0;
+  bool first = true;
+  for (; st < st1; st += kAttnWarps) {
+    const int64_t t0 = tq[0];
+    const float ks = ksq[0], vs = vsq[0];
+    const uint8_t* sb = sm8 + L::ring + (size_t(warp) * kStages + slot) * L::stage;
+    cp_wait<kStages - 1>();
+    if (t0 < tokens) {
+      // ---- scores
+      float sc[R][2][4];
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) sc[t][u][0] = sc[t][u][1] = sc[t][u][2] = sc[t][u][3] = 0.f;
+      uint4 kw[2][KP];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int p = 0; p < KP; ++p) kw[u][p] = *reinterpret_cast<const uint4*>(sb + (u * KP + p) * 512 + lane * 16);
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        uint4 af[R];
+#pragma unroll
+        for (int t = 0; t < R; ++t) af[t] = qa[(t * KS + j) * 32 + lane];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint4& k4 = kw[u][j >> 2];
+          const uint32_t raw = (j & 3) == 0 ? k4.x : (j & 3) == 1 ? k4.y : (j & 3) == 2 ? k4.z : k4.w;
+          const uint32_t x = bias8<FMT>(raw);
+          const uint32_t b0 = to_h2<FMT, true>(x), b1 = to_h2<FMT, false>(x);
+#pragma unroll
+          for (int t = 0; t < R; ++t) mma16816(sc[t][u], af[t], b0, b1);
+        }
+      }
+      // ---- online softmax: p = 2^(s - m); the f16 operand of P V is p times the
+      // block's V scale, so m follows s plus the exponent of that scale (which
+      // keeps the operand below 2^15), floored where a block's V is all but zero
+      const float lv = fmaxf(float(int(__float_as_uint(vs) >> 23) - 127), -64.f);
+      uint4 pf[R];
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        const float f = rscale[t] * ks;
+        const int left = int(max(int64_t(-1), min(limit[t] - t0, int64_t(kStep)))) - 4 * c;
+        float p[4];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float v = sc[t][x >> 1][x & 1] + sc[t][x >> 1][2 + (x & 1)];
+          p[x] = x < left ? v * f : -INFINITY;
+          mx = fmaxf(mx, p[x]);
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[t], mx + lv);
+        if (__any_sync(0xffffffffu, mn > m[t])) {
+          const float corr = m[t] == -INFINITY ? 0.f : ex2(m[t] - mn);
+          l[t] *= corr;
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][i][e] *= corr;
+          m[t] = mn;
+        }
+        const float base = mn == -INFINITY ? 0.f : mn - 14.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          p[x] = ex2(p[x] - base);
+          l[t] += p[x];
+          p[x] *= vs;
+        }
+        split_h2(p[0], p[1], pf[t].x, pf[t].y);
+        split_h2(p[2], p[3], pf[t].z, pf[t].w);
+      }
+      // ---- P V: words of the lane's four tokens interleaved into (token, token + 1) pairs per channel
+      uint32_t vw[4][VW];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint8_t* p = sb + 2 * KP * 512 + x * (HD / 8) * 32 + lane * (HD / 8);
+        if (HD == 128) {
+          const uint4 r = *reinterpret_cast<const uint4*>(p);
+          vw[x][0] = r.x;
+          vw[x][1] = r.y;
+          vw[x][VW - 2] = r.z;
+          vw[x][VW - 1] = r.w;
+        } else {
+          const uint2 r = *reinterpret_cast<const uint2*>(p);
+          vw[x][0] = r.x;
+          vw[x][1] = r.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        uint32_t y[2][2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          y[x][0] = bias8<FMT>(__byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x5140));
+          y[x][1] = bias8<FMT>(__byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x7362));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t b0 = (i & 1) ? to_h2<FMT, false>(y[0][i >> 1]) : to_h2<FMT, true>(y[0][i >> 1]);
+          const uint32_t b1 = (i & 1) ? to_h2<FMT, false>(y[1][i >> 1]) : to_h2<FMT, true>(y[1][i >> 1]);
+#pragma unroll
+          for (int t = 0; t < R; ++t) mma16816(o[t][4 * w + i], pf[t], b0, b1);
+        }
+      }
+      // the tensor cores round sums towards zero: after kFlush of them the
+      // accumulators go into fp32 totals, rounded to nearest, so that the bias
+      // does not grow with the length (1,000,003 positions: 4.3e-6 without)
+      if (++since == kFlush) {
+        flush(first);
+        first = false;
+        since = 0;
+      }
+    }
+    // the slot's bytes are in registers and used: copy the step after next into it
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) tq[i] = tq[i + 1];
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) {
+      ksq[i] = ksq[i + 1];
+      vsq[i] = vsq[i + 1];
+    }
+    issue(tq[kStages - 1], slot, ksq[kStages - 1], vsq[kStages - 1]);
+    tq[kStages] = step_token(st + (kStages + 1) * kAttnWarps);
+    slot = slot + 1 == kStages ? 0 : slot + 1;
+  }
+  cp_wait<0>();
+  flush(first);
+
+  // ---- merge the warps
+  float* mm = reinterpret_cast<float*>(sm8 + L::ml);  // [warps][ROWS] max
+  float* mll = mm + kAttnWarps * ROWS;                // [warps][ROWS] sum
 #pragma unroll
   for (int t = 0; t < R; ++t) {
-    const int r = t * 8 + n;
     l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
     l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
     if (c == 0) {
-      mm[warp * ROWS + r] = m[t];
-      mll[warp * ROWS + r] = l[t];
-    }
-    float* w = mo + (size_t(warp) * ROWS + r) * HD;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      w[(HD / 8) * (2 * c) + i] = o[t][i][0] + o[t][i][2];
-      w[(HD / 8) * (2 * c + 1) + i] = o[t][i][1] + o[t][i][3];
+      mm[warp * ROWS + t * 8 + n] = m[t];
+      mll[warp * ROWS + t * 8 + n] = l[t];
     }
   }
   __syncthreads();
   const bool whole = per >= steps;  // one split: the output itself
-  for (int i = tid; i < rows * HD; i += kAttnWarps * 32) {
-    const int r = i / HD, d = i % HD;
+  const float2* all = reinterpret_cast<const float2*>(sm8 + L::tot);
+  for (int i = tid; i < R * NT * 32; i += kAttnWarps * 32) {
+    const int ln = i & 31, nt = (i >> 5) % NT, r = (i >> 5) / NT * 8 + (ln >> 2), cc = ln & 3;
+    if (r >= rows) continue;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, mm[w * ROWS + r]);
-    float acc = 0.f, sum = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+    float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
       const float mw = mm[w * ROWS + r];
       const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-      acc = fmaf(mo[(size_t(w) * ROWS + r) * HD + d], f, acc);
+      const float2 x = all[size_t(w) * R * NT * 32 + i];
+      acc.x = fmaf(x.x, f, acc.x);
+      acc.y = fmaf(x.y, f, acc.y);
       sum = fmaf(mll[w * ROWS + r], f, sum);
     }
     const int64_t vec = vec_of(r);
-    acc *= h2_factor<FMT>();
+    acc.x *= h2_factor<FMT>();
+    acc.y *= h2_factor<FMT>();
     if (whole) {
-      a.out[vec * HD + d] = sum > 0.f ? acc / sum : (sum == 0.f ? 0.f : sum);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      a.out[vec * HD + (HD / 8) * (2 * cc) + nt] = acc.x * inv;
+      a.out[vec * HD + (HD / 8) * (2 * cc + 1) + nt] = acc.y * inv;
     } else {
-      a.part[(vec * a.S + s) * HD + d] = acc;
-      if (d == 0) a.ml[vec * a.S + s] = make_float2(M, sum);
+      *reinterpret_cast<float2*>(a.part + (vec * a.S + s) * HD + (nt * 4 + cc) * 2) = acc;
+      if (nt == 0 && cc == 0) a.ml[vec * a.S + s] = make_float2(M, sum);
     }
   }
 }
 
 // the splits' partials of one row into the output: one thread per channel
+constexpr int kMaxSplits = 512;
 template <int HD, bool SPARSE>
 __global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args a, int rows_per_chunk) {
+  __shared__ float wts[kMaxSplits];
+  __shared__ float red[HD / 32];
   pdl_wait();
   pdl_trigger();
-  const int qh = blockIdx.x, qi = blockIdx.y, d = threadIdx.x;
+  const int qh = blockIdx.x, qi = blockIdx.y, d = threadIdx.x, lane = d & 31, warp = d >> 5;
   const int64_t n_pos = seen_positions(a);
   int64_t tokens = n_pos + qi;
   if (!SPARSE) {  // the chunk of this row ends at its last row's query
@@ -626,23 +738,58 @@ __global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args 
   const int64_t vec = int64_t(qi) * a.n_qh + qh;
   const float2* ml = a.ml + vec * a.S;
   const float* part = a.part + vec * a.S * HD + d;
+  // this channel of the first 16 splits and the splits' (max, sum), all in flight together
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = i < used ? __ldcg(part + int64_t(i) * HD) : 0.f;
+  float2 x[kMaxSplits / HD];
   float M = -INFINITY;
-  for (int i = 0; i < used; ++i) M = fmaxf(M, __ldcg(ml + i).x);
-  float acc = 0.f, sum = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < used; ++i) {
-    const float2 x = __ldcg(ml + i);
-    const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
-    acc = fmaf(__ldcg(part + int64_t(i) * HD), f, acc);
-    sum = fmaf(x.y, f, sum);
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / HD; ++i) {
+    x[i] = d + i * HD < used ? __ldcg(ml + d + i * HD) : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, x[i].x);
   }
-  a.out[vec * HD + d] = sum > 0.f ? acc / sum : (sum == 0.f ? 0.f : sum);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+  M = red[0];
+#pragma unroll
+  for (int w = 1; w < HD / 32; ++w) M = fmaxf(M, red[w]);
+  __syncthreads();
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / HD; ++i) {
+    const float f = x[i].x == -INFINITY ? 0.f : ex2(x[i].x - M);
+    if (d + i * HD < used) wts[d + i * HD] = f;
+    sum = fmaf(x[i].y, f, sum);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  sum = red[0];
+#pragma unroll
+  for (int w = 1; w < HD / 32; ++w) sum += red[w];
+  float acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < used) acc = fmaf(v[i], wts[i], acc);
+  for (int i0 = 16; i0 < used; i0 += 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i0 + i < used ? __ldcg(part + int64_t(i0 + i) * HD) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i0 + i < used) acc = fmaf(v[i], wts[i0 + i], acc);
+  }
+  // fragment order (n-tile, lane pair, column) -> channel
+  const int ch = (HD / 8) * (d & 7) + (d >> 3);
+  a.out[vec * HD + ch] = acc * (sum == 0.f ? 0.f : 1.f / sum);
 }
 
 using AttnKv8Kernel = void (*)(AttnKv8Args);
 template <int FMT, int HD, bool SPARSE>
 AttnKv8Kernel attn_kv8_pick(int R, size_t* smem) {
-  *smem = R == 1 ? attn_kv8_smem<HD, 1>() : attn_kv8_smem<HD, 2>();
+  *smem = R == 1 ? AttnKv8Smem<HD, 1>::bytes : AttnKv8Smem<HD, 2>::bytes;
   return R == 1 ? attn_kv8_kernel<FMT, HD, 1, SPARSE> : attn_kv8_kernel<FMT, HD, 2, SPARSE>;
 }
 template <bool SPARSE>
@@ -949,6 +1096,7 @@ nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, 
   const size_t vecs = size_t(n_qh) * nq, row = vecs * (kv.head_dim * 4 + 8);
   if (S > useful) S = useful;
   if (S * int64_t(row) > int64_t(scratch_bytes)) S = int64_t(scratch_bytes / row);
+  if (S > kMaxSplits) S = kMaxSplits;
   if (S < 1) S = 1;
   a.S = int(S);
   a.part = reinterpret_cast<float*>(scratch);
