@@ -54,43 +54,42 @@ __device__ __forceinline__ uint32_t pack8(const float v[4]) {
   return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
-// E4M3 bytes 0 and 1 of x (LO) or 2 and 3 as f16 times 2^-8: sign to bit 15,
-// exponent and mantissa to bits 13..7.  Exact for every byte (e4m3 subnormals
-// become f16 subnormals), and no byte gives a NaN or an infinity, so rows that a
-// mask hides cannot spoil a product with 0.
-template <bool LO>
-__device__ __forceinline__ uint32_t e4m3_to_h2(uint32_t x) {
-  const uint32_t s = __byte_perm(x, 0u, LO ? 0x1404 : 0x3424);
-  return (s & 0x80008000u) | ((s >> 1) & 0x3F803F80u);
-}
-// I8 bytes as f16: u = q + 128 in the mantissa of 1024 + u (exact), minus 1152
-template <bool LO>
-__device__ __forceinline__ uint32_t i8_to_h2(uint32_t x_biased) {
-  const uint32_t s = __byte_perm(x_biased, 0x64646464u, LO ? 0x4140 : 0x4342);
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&s), __half2half2(__ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+// Four bytes as two f16 pairs, exact.
+//  I8: bytes (0, 2) and (1, 3): q + 128 in the mantissa of 1024 + (q + 128), minus
+//  1152.  Masking, the sign bias and the exponent are one three-input operation.
+//  E4M3: bytes (0, 1) and (2, 3) through the hardware's conversion.
 template <int FMT>
-__device__ __forceinline__ uint32_t bias8(uint32_t x) {
-  return FMT == NT_KV8_I8 ? x ^ 0x80808080u : x;
+__device__ __forceinline__ void to_h2(uint32_t x, uint32_t& a, uint32_t& b) {
+  if (FMT == NT_KV8_I8) {
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+    const uint32_t even = (x & 0x00FF00FFu) ^ 0x64806480u, odd = ((x >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+    const __half2 h0 = __hsub2(*reinterpret_cast<const __half2*>(&even), bias);
+    const __half2 h1 = __hsub2(*reinterpret_cast<const __half2*>(&odd), bias);
+    a = *reinterpret_cast<const uint32_t*>(&h0);
+    b = *reinterpret_cast<const uint32_t*>(&h1);
+  } else {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"(uint16_t(x & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(uint16_t(x >> 16)));
+  }
 }
-template <int FMT, bool LO>
-__device__ __forceinline__ uint32_t to_h2(uint32_t x) {  // x after bias8
-  return FMT == NT_KV8_I8 ? i8_to_h2<LO>(x) : e4m3_to_h2<LO>(x);
-}
-// what to_h2 leaves out of the value
+// the byte of the first pair's second value (the other pair holds the other two)
 template <int FMT>
-__device__ __forceinline__ constexpr float h2_factor() { return FMT == NT_KV8_I8 ? 1.f : 256.f; }
+constexpr int kPairStep = FMT == NT_KV8_I8 ? 2 : 1;
+// words of two rows -> two words whose to_h2 pairs are (row 0, row 1) of bytes 0, 1 and of bytes 2, 3
+template <int FMT>
+__device__ __forceinline__ void interleave8(uint32_t r0, uint32_t r1, uint32_t& lo, uint32_t& hi) {
+  lo = __byte_perm(r0, r1, FMT == NT_KV8_I8 ? 0x5410 : 0x5140);
+  hi = __byte_perm(r0, r1, FMT == NT_KV8_I8 ? 0x7632 : 0x7362);
+}
 
 // four bytes -> values over the scale
 template <int FMT>
 __device__ __forceinline__ float4 unpack8(uint32_t x) {
-  const uint32_t b = bias8<FMT>(x);
-  const uint32_t lo = to_h2<FMT, true>(b), hi = to_h2<FMT, false>(b);
+  uint32_t lo, hi;
+  to_h2<FMT>(x, lo, hi);
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  constexpr float f = h2_factor<FMT>();
-  return make_float4(a.x * f, a.y * f, c.x * f, c.y * f);
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return FMT == NT_KV8_I8 ? make_float4(a.x, b.x, a.y, b.y) : make_float4(a.x, a.y, b.x, b.y);
 }
 
 // ---- write ---------------------------------------------------------------------
@@ -310,6 +309,7 @@ constexpr int kAttnWarps = 8;
 constexpr int kStep = 16;  // tokens per warp step
 constexpr int kStages = 2;
 constexpr int kFlush = 16;
+constexpr float kPTop = 8.f, kSlack = 6.f;
 
 struct AttnKv8Args {
   const float* q;
@@ -339,8 +339,8 @@ __device__ __forceinline__ int64_t seen_positions(const AttnKv8Args& a) {
 
 // steps per CTA for `steps` 16-token steps over S splits: both launches compute
 // it, so an unused split is never read
-__device__ __forceinline__ int64_t split_steps(int64_t steps, int S) {
-  const int64_t even = (steps + S - 1) / S;
+__device__ __forceinline__ int split_steps(int steps, int S) {
+  const int even = (steps + S - 1) / S;
   return even < kAttnWarps ? kAttnWarps : even;
 }
 
@@ -366,14 +366,23 @@ __device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// BYTES (16 or 8) global -> shared; `live` false fills with zeros and reads nothing
+// BYTES (16 or 8) global -> shared
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live) {
-  const int n = live ? BYTES : 0;
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
   if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// the same, or zeros (nothing is read; `safe` stands in for the address) when not `live`
+template <int BYTES>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, const void* safe, bool live) {
+  const int n = live ? BYTES : 0;
+  const void* from = live ? src : safe;
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -411,14 +420,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const int qi0 = SPARSE ? blockIdx.z / a.chunks : 0;
   const int row0 = (SPARSE ? blockIdx.z % a.chunks : blockIdx.z) * ROWS;
   const int rows = min(ROWS, (SPARSE ? a.G : a.nq * a.G) - row0);
-  const int64_t n_pos = seen_positions(a);
+  const int n_pos = int(seen_positions(a));  // positions fit 30 bits
   // row r of this chunk: query and head
   const auto query_of = [&](int r) { return SPARSE ? qi0 : (row0 + r) / a.G; };
   const auto vec_of = [&](int r) { return int64_t(query_of(r)) * a.n_qh + g * a.G + (SPARSE ? row0 + r : (row0 + r) % a.G); };
-  const int64_t tokens = n_pos + query_of(rows - 1);  // the last row sees the most
-  const int64_t steps = SPARSE ? int64_t(a.n_sel) * (kB / kStep) : (tokens + kStep - 1) / kStep;
-  const int64_t per = split_steps(steps, a.S);
-  const int64_t st0 = int64_t(s) * per, st1 = min(steps, st0 + per);
+  const int tokens = n_pos + query_of(rows - 1);  // the last row sees the most
+  const int steps = SPARSE ? a.n_sel * (kB / kStep) : (tokens + kStep - 1) / kStep;
+  const int per = split_steps(steps, a.S);
+  const int st0 = s * per, st1 = min(steps, st0 + per);
   if (st0 >= st1 && s > 0) return;
 
   const uint8_t* kg = a.k + int64_t(g) * a.kv_stride * HD;
@@ -426,46 +435,53 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const float* ksg = a.ks + int64_t(g) * a.nb;
   const float* vsg = a.vs + int64_t(g) * a.nb;
   const int32_t* list = SPARSE ? a.idx + (int64_t(qi0) * a.n_kvh + g) * a.n_sel : nullptr;
-  const int64_t blocks_seen = (tokens + kB - 1) / kB;
+  const int blocks_seen = (tokens + kB - 1) / kB;
+  // this lane's first K and V bytes within a step, and its slots
+  const uint8_t* klane = kg + (4 * (n >> 1) + (n & 1)) * HD + 16 * c;
+  const uint8_t* vlane = vg + 4 * c * HD + n * (HD / 8);
   const uint32_t ring = smem_u32(sm8 + L::ring + size_t(warp) * kStages * L::stage);
+  const uint32_t kslot = ring + lane * 16, vslot = ring + 2 * KP * 512 + lane * (HD / 8);
 
   // first token of step st (tokens: nothing to do), and its copies into `slot`
-  const auto step_token = [&](int64_t st) -> int64_t {
+  const auto step_token = [&](int st) {
     if (st >= st1) return tokens;
     if (!SPARSE) return st * kStep;
-    const int64_t b = __ldg(list + (st >> 2));
+    const int b = __ldg(list + (st >> 2));
     return b < 0 || b >= blocks_seen ? tokens : min(tokens, b * kB + (st & 3) * kStep);
   };
-  const auto issue = [&](int64_t t0, int slot, float& ks, float& vs) {
+  const auto issue = [&](int t0, int slot, float& ks, float& vs) {
     ks = vs = 0.f;
     if (t0 < tokens) {
-      const uint32_t at = ring + slot * uint32_t(L::stage);
-      const int left = int(min(tokens - t0, int64_t(kStep)));
-      const uint8_t* kr = kg + t0 * HD;
-      const uint8_t* vr = vg + t0 * HD;
+      const uint32_t at = slot * uint32_t(L::stage);
+      const uint8_t* kr = klane + int64_t(t0) * HD;
+      const uint8_t* vr = vlane + int64_t(t0) * HD;
       ks = __ldg(ksg + t0 / kB);
       vs = __ldg(vsg + t0 / kB);
+      const int left = tokens - t0;
+      if (left >= kStep) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int t = 4 * (n >> 1) + 2 * u + (n & 1);
-        const bool live = t < left;
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int p = 0; p < KP; ++p)
-          cp_async<16>(at + (u * KP + p) * 512 + lane * 16, kr + (live ? t * HD + 64 * p + 16 * c : 0), live);
-      }
+          for (int p = 0; p < KP; ++p) cp_async<16>(kslot + at + (u * KP + p) * 512, kr + 2 * u * HD + 64 * p);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int t = 4 * c + x;
-        const bool live = t < left;
-        cp_async<HD / 8>(at + 2 * KP * 512 + x * (HD / 8) * 32 + lane * (HD / 8), vr + (live ? t * HD + n * (HD / 8) : 0),
-                         live);
+        for (int x = 0; x < 4; ++x) cp_async<HD / 8>(vslot + at + x * HD * 4, vr + x * HD);
+      } else {  // the last step of a sequence: rows past its end read as zeros
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int p = 0; p < KP; ++p)
+            cp_async_zfill<16>(kslot + at + (u * KP + p) * 512, kr + 2 * u * HD + 64 * p, kg,
+                               4 * (n >> 1) + 2 * u + (n & 1) < left);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          cp_async_zfill<HD / 8>(vslot + at + x * HD * 4, vr + x * HD, vg, 4 * c + x < left);
       }
     }
     cp_commit();
   };
-  int64_t tq[kStages + 1];            // first tokens of the next steps
+  int tq[kStages + 1];                // first tokens of the next steps
   float ksq[kStages], vsq[kStages];
-  int64_t st = st0 + warp;
+  int st = st0 + warp;
 #pragma unroll
   for (int i = 0; i < kStages; ++i) tq[i] = step_token(st + i * kAttnWarps);
 #pragma unroll
@@ -497,22 +513,21 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     if (r < rows) {
       const float4 x = load4(a.q + vec_of(r) * HD + d);
       const float sc = __uint_as_float(uint32_t(row_exp(r) + 127) << 23);
-      split_h2(x.x * sc, x.y * sc, f.x, f.y);
-      split_h2(x.z * sc, x.w * sc, f.z, f.w);
+      split_h2(x.x * sc, (kPairStep<FMT> == 2 ? x.z : x.y) * sc, f.x, f.y);
+      split_h2((kPairStep<FMT> == 2 ? x.y : x.z) * sc, x.w * sc, f.z, f.w);
     }
     qa[i] = f;
   }
   __syncthreads();
   float rscale[R];      // scores to the base-2 exponent
-  int64_t limit[R];     // positions row n sees
+  int limit[R];         // positions row n sees
   float m[R], l[R], mf[R];
   float o[R][NT][4];
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     const int r = t * 8 + n;
     // log2(e) / sqrt(HD)
-    rscale[t] = __uint_as_float(uint32_t(127 - row_exp(r)) << 23) * (1.44269504088896f * rsqrtf(float(HD))) *
-                h2_factor<FMT>();
+    rscale[t] = __uint_as_float(uint32_t(127 - row_exp(r)) << 23) * (1.44269504088896f * rsqrtf(float(HD)));
     limit[t] = r < rows ? n_pos + query_of(r) : 0;
     m[t] = mf[t] = -INFINITY;
     l[t] = 0.f;
@@ -540,10 +555,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     }
   };
 
+  const int fewest = SPARSE ? tokens : n_pos + query_of(0);  // positions every row sees
   int slot = 0, since = 0;
   bool first = true;
   for (; st < st1; st += kAttnWarps) {
-    const int64_t t0 = tq[0];
+    const int t0 = tq[0];
     const float ks = ksq[0], vs = vsq[0];
     const uint8_t* sb = sm8 + L::ring + (size_t(warp) * kStages + slot) * L::stage;
     cp_wait<kStages - 1>();
@@ -567,34 +583,36 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint4& k4 = kw[u][j >> 2];
-          const uint32_t raw = (j & 3) == 0 ? k4.x : (j & 3) == 1 ? k4.y : (j & 3) == 2 ? k4.z : k4.w;
-          const uint32_t x = bias8<FMT>(raw);
-          const uint32_t b0 = to_h2<FMT, true>(x), b1 = to_h2<FMT, false>(x);
+          uint32_t b0, b1;
+          to_h2<FMT>((j & 3) == 0 ? k4.x : (j & 3) == 1 ? k4.y : (j & 3) == 2 ? k4.z : k4.w, b0, b1);
 #pragma unroll
           for (int t = 0; t < R; ++t) mma16816(sc[t][u], af[t], b0, b1);
         }
       }
-      // ---- online softmax: p = 2^(s - m); the f16 operand of P V is p times the
-      // block's V scale, so m follows s plus the exponent of that scale (which
-      // keeps the operand below 2^15), floored where a block's V is all but zero
+      // ---- online softmax: p = 2^(s - m + kPTop).  The f16 operand of P V is p
+      // times the block's V scale, so m follows s plus the exponent of that scale
+      // (floored where a block's V is all but zero).  m is left behind by up to
+      // kSlack before the accumulators are rescaled to a new one: the operand
+      // then stays below 2^(kPTop + kSlack + 1), the largest f16 exponent, and a
+      // warp rescales once or twice in a sequence instead of at every new maximum.
       const float lv = fmaxf(float(int(__float_as_uint(vs) >> 23) - 127), -64.f);
       uint4 pf[R];
 #pragma unroll
       for (int t = 0; t < R; ++t) {
         const float f = rscale[t] * ks;
-        const int left = int(max(int64_t(-1), min(limit[t] - t0, int64_t(kStep)))) - 4 * c;
         float p[4];
-        float mx = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float v = sc[t][x >> 1][x & 1] + sc[t][x >> 1][2 + (x & 1)];
-          p[x] = x < left ? v * f : -INFINITY;
-          mx = fmaxf(mx, p[x]);
+        for (int x = 0; x < 4; ++x) p[x] = (sc[t][x >> 1][x & 1] + sc[t][x >> 1][2 + (x & 1)]) * f;
+        if (t0 + kStep > fewest) {
+          const int left = limit[t] - t0 - 4 * c;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) p[x] = x < left ? p[x] : -INFINITY;
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[t], mx + lv);
-        if (__any_sync(0xffffffffu, mn > m[t])) {
+        const float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) + lv;
+        if (__any_sync(0xffffffffu, mx > m[t] + kSlack)) {
+          float mn = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
+          mn = fmaxf(m[t], mn);
           const float corr = m[t] == -INFINITY ? 0.f : ex2(m[t] - mn);
           l[t] *= corr;
 #pragma unroll
@@ -603,7 +621,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
             for (int e = 0; e < 4; ++e) o[t][i][e] *= corr;
           m[t] = mn;
         }
-        const float base = mn == -INFINITY ? 0.f : mn - 14.f;
+        const float base = m[t] == -INFINITY ? 0.f : m[t] - kPTop;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           p[x] = ex2(p[x] - base);
@@ -634,16 +652,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       for (int w = 0; w < VW; ++w) {
         uint32_t y[2][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          y[x][0] = bias8<FMT>(__byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x5140));
-          y[x][1] = bias8<FMT>(__byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x7362));
-        }
+        for (int x = 0; x < 2; ++x) interleave8<FMT>(vw[2 * x][w], vw[2 * x + 1][w], y[x][0], y[x][1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t b0 = (i & 1) ? to_h2<FMT, false>(y[0][i >> 1]) : to_h2<FMT, true>(y[0][i >> 1]);
-          const uint32_t b1 = (i & 1) ? to_h2<FMT, false>(y[1][i >> 1]) : to_h2<FMT, true>(y[1][i >> 1]);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t b0[2], b1[2];
+          to_h2<FMT>(y[0][i], b0[0], b0[1]);
+          to_h2<FMT>(y[1][i], b1[0], b1[1]);
 #pragma unroll
-          for (int t = 0; t < R; ++t) mma16816(o[t][4 * w + i], pf[t], b0, b1);
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int t = 0; t < R; ++t) mma16816(o[t][4 * w + 2 * i + e], pf[t], b0[e], b1[e]);
         }
       }
       // the tensor cores round sums towards zero: after kFlush of them the
@@ -703,8 +721,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       sum = fmaf(mll[w * ROWS + r], f, sum);
     }
     const int64_t vec = vec_of(r);
-    acc.x *= h2_factor<FMT>();
-    acc.y *= h2_factor<FMT>();
     if (whole) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       a.out[vec * HD + (HD / 8) * (2 * cc) + nt] = acc.x * inv;
@@ -725,16 +741,16 @@ __global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args 
   pdl_wait();
   pdl_trigger();
   const int qh = blockIdx.x, qi = blockIdx.y, d = threadIdx.x, lane = d & 31, warp = d >> 5;
-  const int64_t n_pos = seen_positions(a);
-  int64_t tokens = n_pos + qi;
+  const int n_pos = int(seen_positions(a));
+  int tokens = n_pos + qi;
   if (!SPARSE) {  // the chunk of this row ends at its last row's query
     const int r = qi * a.G + qh % a.G, last = min(a.nq * a.G, (r / rows_per_chunk + 1) * rows_per_chunk) - 1;
     tokens = n_pos + last / a.G;
   }
-  const int64_t steps = SPARSE ? int64_t(a.n_sel) * (kB / kStep) : (tokens + kStep - 1) / kStep;
-  const int64_t per = split_steps(steps, a.S);
+  const int steps = SPARSE ? a.n_sel * (kB / kStep) : (tokens + kStep - 1) / kStep;
+  const int per = split_steps(steps, a.S);
   if (per >= steps) return;
-  const int used = int((steps + per - 1) / per);
+  const int used = (steps + per - 1) / per;
   const int64_t vec = int64_t(qi) * a.n_qh + qh;
   const float2* ml = a.ml + vec * a.S;
   const float* part = a.part + vec * a.S * HD + d;
