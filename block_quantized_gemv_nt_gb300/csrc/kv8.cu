@@ -9,6 +9,7 @@
 // and a block whose scale has to grow while it fills (a later token is larger)
 // loses nothing but the low bits that the larger scale cannot hold.
 #include <cuda_fp16.h>
+#include <cstdlib>
 
 #include "nt_internal.cuh"
 #include "ops.cuh"
@@ -292,23 +293,21 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 // below, their lo parts, so the two halves of a product meet in one thread:
 // accumulators c0 + c2 and c1 + c3.
 //
-// Fragments come straight from memory, without a transpose: MMA k and n indices
-// are ours to name.  Lane (n = lane / 4, c = lane % 4), a step of 16 tokens:
-//  - Q K^T: B column n of n-tile u (0, 1) is token 4 (n / 2) + 2 u + n % 2; the
-//    lane loads bytes 16 c .. 16 c + 15 (+ 64 for the upper half) of that row, and
+// Fragments come without a transpose: MMA k and n indices are ours to name.  Lane
+// (n = lane / 4, c = lane % 4), a step of 16 U tokens:
+//  - Q K^T: B column n of n-tile u (0 .. 2 U - 1) is token 4 U (n / 2) + 2 u + n % 2;
+//    the lane reads bytes 16 c .. 16 c + 15 (+ 64 for the upper half) of that row, and
 //    word w of a 16-byte piece is its k-slots of k-step w.
-//  - the scores of row n land in lane (n, c) for tokens 4 c .. 4 c + 3;
-//  - P V: those four tokens are the lane's k-slots; it loads bytes
-//    n HD/8 .. + HD/8 - 1 of their V rows, and byte i of them is B column n of
-//    n-tile i, i.e. output channel n HD/8 + i.
+//  - the scores of row n land in lane (n, c) for tokens 4 U c .. 4 U c + 4 U - 1;
+//  - P V: those tokens are the lane's k-slots; it reads bytes n HD/8 .. + HD/8 - 1 of
+//    their V rows, and byte i of them is B column n of n-tile i, i.e. output channel
+//    n HD/8 + i.
 //
-// Each lane copies exactly the bytes it will use into its own slots of a ring in
-// shared memory (cp.async), kStages steps ahead: no barrier joins the lanes, no
-// slot has a bank conflict, and what is in flight costs no registers.
+// Each warp walks its own steps: one bulk copy brings a step's K, four its V (the
+// rows of each c, 32 bytes apart from the next, so that a warp's V reads meet no
+// bank twice).  The next step's K is copied while the warp works on the probabilities
+// and V, the next V while it works on K; no barrier joins the warps.
 constexpr int kAttnWarps = 8;
-constexpr int kStep = 16;  // tokens per warp step
-constexpr int kStages = 2;
-constexpr int kFlush = 16;
 constexpr float kPTop = 8.f, kSlack = 6.f;
 
 struct AttnKv8Args {
@@ -325,6 +324,7 @@ struct AttnKv8Args {
   int64_t n_pos, kv_stride, nb;
   const int64_t* pos_dev;
   unsigned* err;
+  int stall;           // test hook: issue no bulk copies; the waits give up after kStallSpin tries
 };
 
 // positions query 0 sees, held to the cache
@@ -366,53 +366,34 @@ __device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// BYTES (16 or 8) global -> shared
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-// the same, or zeros (nothing is read; `safe` stands in for the address) when not `live`
-template <int BYTES>
-__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, const void* safe, bool live) {
-  const int n = live ? BYTES : 0;
-  const void* from = live ? src : safe;
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // shared memory: q fragments [R][HD / 16][32] x 16, totals [warps][R][HD / 8][32] x 8,
-// (max, sum) [2][warps][8 R], the ring [warps][kStages][32 tokens' bytes]
-template <int HD, int R>
+// (max, sum) [2][warps][8 R], each warp's slots for one step's K and V
+template <int HD, int R, int U>
 struct AttnKv8Smem {
   static constexpr size_t q = 0;
   static constexpr size_t tot = q + size_t(R) * (HD / 16) * 512;
   static constexpr size_t ml = tot + size_t(kAttnWarps) * R * (HD / 8) * 256;
   static constexpr size_t ring = ml + size_t(2) * kAttnWarps * 8 * R * 4;
-  static constexpr size_t stage = size_t(kStep) * HD * 2;
-  static constexpr size_t bytes = ring + kAttnWarps * kStages * stage;
+  static constexpr size_t group = size_t(4 * U) * HD + 32;           // V rows of one c
+  static constexpr size_t stage = size_t(16 * U) * HD + 4 * group;   // K, then V
+  static constexpr size_t bytes = ring + kAttnWarps * stage;
 };
 
-template <int FMT, int HD, int R, bool SPARSE>
+template <int FMT, int HD, int R, int U, bool SPARSE>
 __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kernel(const AttnKv8Args a) {
-  using L = AttnKv8Smem<HD, R>;
+  using L = AttnKv8Smem<HD, R, U>;
+  constexpr int kStep = 16 * U;      // tokens per warp step
   constexpr int KS = HD / 16;        // k-steps of Q K^T
   constexpr int NT = HD / 8;         // n-tiles of P V
   constexpr int KP = HD / 64;        // 16-byte pieces of a K row per lane
   constexpr int VW = HD / 32;        // words of a V row per lane
   constexpr int ROWS = 8 * R;
+  constexpr int CH = U == 1 ? 2 : 1; // accumulators per score tile: at least four chains of MMAs
+  constexpr int kFlush = 16 / U;
   extern __shared__ __align__(16) uint8_t sm8[];
   uint4* qa = reinterpret_cast<uint4*>(sm8 + L::q);
   __shared__ float s_amax[ROWS];
+  __shared__ __align__(8) uint64_t bars[kAttnWarps][2];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = lane >> 2, c = lane & 3;
@@ -436,57 +417,53 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const float* vsg = a.vs + int64_t(g) * a.nb;
   const int32_t* list = SPARSE ? a.idx + (int64_t(qi0) * a.n_kvh + g) * a.n_sel : nullptr;
   const int blocks_seen = (tokens + kB - 1) / kB;
-  // this lane's first K and V bytes within a step, and its slots
-  const uint8_t* klane = kg + (4 * (n >> 1) + (n & 1)) * HD + 16 * c;
-  const uint8_t* vlane = vg + 4 * c * HD + n * (HD / 8);
-  const uint32_t ring = smem_u32(sm8 + L::ring + size_t(warp) * kStages * L::stage);
-  const uint32_t kslot = ring + lane * 16, vslot = ring + 2 * KP * 512 + lane * (HD / 8);
+  const uint8_t* sk = sm8 + L::ring + size_t(warp) * L::stage;  // this warp's K rows, then its V groups
+  const uint8_t* sv = sk + kStep * HD;
+  const uint32_t bar_k = smem_u32(&bars[warp][0]), bar_v = smem_u32(&bars[warp][1]);
+  const uint64_t pol = policy_evict_first();
+  if (lane == 0) {
+    mbar_init(bar_k, 1);
+    mbar_init(bar_v, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
 
-  // first token of step st (tokens: nothing to do), and its copies into `slot`
+  // first token of step st (tokens: nothing to do)
   const auto step_token = [&](int st) {
     if (st >= st1) return tokens;
     if (!SPARSE) return st * kStep;
-    const int b = __ldg(list + (st >> 2));
-    return b < 0 || b >= blocks_seen ? tokens : min(tokens, b * kB + (st & 3) * kStep);
+    const int b = __ldg(list + st / (kB / kStep));
+    return b < 0 || b >= blocks_seen ? tokens : min(tokens, b * kB + st % (kB / kStep) * kStep);
   };
-  const auto issue = [&](int t0, int slot, float& ks, float& vs) {
-    ks = vs = 0.f;
-    if (t0 < tokens) {
-      const uint32_t at = slot * uint32_t(L::stage);
-      const uint8_t* kr = klane + int64_t(t0) * HD;
-      const uint8_t* vr = vlane + int64_t(t0) * HD;
-      ks = __ldg(ksg + t0 / kB);
-      vs = __ldg(vsg + t0 / kB);
-      const int left = tokens - t0;
-      if (left >= kStep) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int p = 0; p < KP; ++p) cp_async<16>(kslot + at + (u * KP + p) * 512, kr + 2 * u * HD + 64 * p);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) cp_async<HD / 8>(vslot + at + x * HD * 4, vr + x * HD);
-      } else {  // the last step of a sequence: rows past its end read as zeros
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int p = 0; p < KP; ++p)
-            cp_async_zfill<16>(kslot + at + (u * KP + p) * 512, kr + 2 * u * HD + 64 * p, kg,
-                               4 * (n >> 1) + 2 * u + (n & 1) < left);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          cp_async_zfill<HD / 8>(vslot + at + x * HD * 4, vr + x * HD, vg, 4 * c + x < left);
-      }
+  // the copies of one step's K and V, rows below `tokens` only
+  const auto copy_k = [&](int t0) {
+    if (t0 < tokens && lane == 0) {
+      const uint32_t bytes = min(kStep, tokens - t0) * HD;
+      mbar_arrive_expect_tx(bar_k, bytes);
+      if (!a.stall) bulk_g2s(smem_u32(sk), kg + int64_t(t0) * HD, bytes, bar_k, pol);
     }
-    cp_commit();
   };
-  int tq[kStages + 1];                // first tokens of the next steps
-  float ksq[kStages], vsq[kStages];
+  const auto copy_v = [&](int t0) {
+    if (t0 < tokens && lane < 4) {
+      const int left = tokens - t0, mine = max(0, min(4 * U, left - 4 * U * lane));
+      if (lane == 0) mbar_arrive_expect_tx(bar_v, min(kStep, left) * HD);
+      if (mine && !a.stall)
+        bulk_g2s(smem_u32(sv + lane * L::group), vg + int64_t(t0 + 4 * U * lane) * HD, mine * HD, bar_v, pol);
+    }
+  };
+  const auto wait = [&](uint32_t bar, uint32_t phase) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, a.stall ? kStallSpin : kMaxSpin));
+    if (!ok && lane == 0) flag_error(a.err, kErrWaitTimeout);
+    return ok;
+  };
+  const auto scales = [&](int t0) {
+    return t0 < tokens ? make_float2(__ldg(ksg + t0 / kB), __ldg(vsg + t0 / kB)) : make_float2(0.f, 0.f);
+  };
   int st = st0 + warp;
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) tq[i] = step_token(st + i * kAttnWarps);
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) issue(tq[i], i, ksq[i], vsq[i]);
-  tq[kStages] = step_token(st + kStages * kAttnWarps);
+  int t0 = step_token(st), t1 = step_token(st + kAttnWarps);  // this step's first token, the next one's
+  copy_k(t0);
+  copy_v(t0);
+  float2 kvs = scales(t0);
 
   // q: each row scaled by a power of two to amax in [2^13, 2^14), split, laid out as fragments
   for (int r = warp; r < ROWS; r += kAttnWarps) {
@@ -556,59 +533,74 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   };
 
   const int fewest = SPARSE ? tokens : n_pos + query_of(0);  // positions every row sees
-  int slot = 0, since = 0;
+  int since = 0;
+  uint32_t phase = 0;
   bool first = true;
   for (; st < st1; st += kAttnWarps) {
-    const int t0 = tq[0];
-    const float ks = ksq[0], vs = vsq[0];
-    const uint8_t* sb = sm8 + L::ring + (size_t(warp) * kStages + slot) * L::stage;
-    cp_wait<kStages - 1>();
+    const int t2 = step_token(st + 2 * kAttnWarps);
+    const float2 kvs1 = scales(t1);
+    // ---- scores
+    float sc[R][2 * U][CH][4];
     if (t0 < tokens) {
-      // ---- scores
-      float sc[R][2][4];
+      if (!wait(bar_k, phase)) break;
 #pragma unroll
       for (int t = 0; t < R; ++t)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) sc[t][u][0] = sc[t][u][1] = sc[t][u][2] = sc[t][u][3] = 0.f;
-      uint4 kw[2][KP];
+        for (int u = 0; u < 2 * U; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+          for (int e = 0; e < CH; ++e) sc[t][u][e][0] = sc[t][u][e][1] = sc[t][u][e][2] = sc[t][u][e][3] = 0.f;
 #pragma unroll
-        for (int p = 0; p < KP; ++p) kw[u][p] = *reinterpret_cast<const uint4*>(sb + (u * KP + p) * 512 + lane * 16);
+      for (int p = 0; p < KP; ++p) {
+        uint4 kw[2 * U];
 #pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        uint4 af[R];
+        for (int u = 0; u < 2 * U; ++u) 
+          kw[u] = *reinterpret_cast<const uint4*>(sk + (4 * U * (n >> 1) + 2 * u + (n & 1)) * HD + 64 * p + 16 * c);
 #pragma unroll
-        for (int t = 0; t < R; ++t) af[t] = qa[(t * KS + j) * 32 + lane];
+        for (int j = 0; j < 4; ++j) {
+          uint4 af[R];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint4& k4 = kw[u][j >> 2];
-          uint32_t b0, b1;
-          to_h2<FMT>((j & 3) == 0 ? k4.x : (j & 3) == 1 ? k4.y : (j & 3) == 2 ? k4.z : k4.w, b0, b1);
+          for (int t = 0; t < R; ++t) af[t] = qa[(t * KS + 4 * p + j) * 32 + lane];
 #pragma unroll
-          for (int t = 0; t < R; ++t) mma16816(sc[t][u], af[t], b0, b1);
+          for (int u = 0; u < 2 * U; ++u) {
+            uint32_t b0, b1;
+            to_h2<FMT>(j == 0 ? kw[u].x : j == 1 ? kw[u].y : j == 2 ? kw[u].z : kw[u].w, b0, b1);
+#pragma unroll
+            for (int t = 0; t < R; ++t) mma16816(sc[t][u][j % CH], af[t], b0, b1);
+          }
         }
       }
+    }
+    __syncwarp();  // this step's K is in registers and used
+    copy_k(t1);
+    uint4 pf[R][U];
+    if (t0 < tokens) {
       // ---- online softmax: p = 2^(s - m + kPTop).  The f16 operand of P V is p
       // times the block's V scale, so m follows s plus the exponent of that scale
       // (floored where a block's V is all but zero).  m is left behind by up to
       // kSlack before the accumulators are rescaled to a new one: the operand
       // then stays below 2^(kPTop + kSlack + 1), the largest f16 exponent, and a
       // warp rescales once or twice in a sequence instead of at every new maximum.
+      const float vs = kvs.y;
       const float lv = fmaxf(float(int(__float_as_uint(vs) >> 23) - 127), -64.f);
-      uint4 pf[R];
 #pragma unroll
       for (int t = 0; t < R; ++t) {
-        const float f = rscale[t] * ks;
-        float p[4];
+        const float f = rscale[t] * kvs.x;
+        float p[4 * U];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) p[x] = (sc[t][x >> 1][x & 1] + sc[t][x >> 1][2 + (x & 1)]) * f;
-        if (t0 + kStep > fewest) {
-          const int left = limit[t] - t0 - 4 * c;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) p[x] = x < left ? p[x] : -INFINITY;
+        for (int x = 0; x < 4 * U; ++x) {
+          float v = sc[t][x >> 1][0][x & 1] + sc[t][x >> 1][0][2 + (x & 1)];
+          if (CH == 2) v += sc[t][x >> 1][CH - 1][x & 1] + sc[t][x >> 1][CH - 1][2 + (x & 1)];
+          p[x] = v * f;
         }
-        const float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) + lv;
+        if (t0 + kStep > fewest) {
+          const int left = limit[t] - t0 - 4 * U * c;
+#pragma unroll
+          for (int x = 0; x < 4 * U; ++x) p[x] = x < left ? p[x] : -INFINITY;
+        }
+        float mx = p[0];
+#pragma unroll
+        for (int x = 1; x < 4 * U; ++x) mx = fmaxf(mx, p[x]);
+        mx += lv;
         if (__any_sync(0xffffffffu, mx > m[t] + kSlack)) {
           float mn = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
@@ -623,48 +615,65 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
         }
         const float base = m[t] == -INFINITY ? 0.f : m[t] - kPTop;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 4 * U; ++x) {
           p[x] = ex2(p[x] - base);
           l[t] += p[x];
           p[x] *= vs;
         }
-        split_h2(p[0], p[1], pf[t].x, pf[t].y);
-        split_h2(p[2], p[3], pf[t].z, pf[t].w);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          split_h2(p[4 * u], p[4 * u + 1], pf[t][u].x, pf[t][u].y);
+          split_h2(p[4 * u + 2], p[4 * u + 3], pf[t][u].z, pf[t][u].w);
+        }
       }
+    }
+    if (t0 < tokens) {
+      if (!wait(bar_v, phase)) break;
+      phase ^= 1;
       // ---- P V: words of the lane's four tokens interleaved into (token, token + 1) pairs per channel
-      uint32_t vw[4][VW];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint8_t* p = sb + 2 * KP * 512 + x * (HD / 8) * 32 + lane * (HD / 8);
-        if (HD == 128) {
-          const uint4 r = *reinterpret_cast<const uint4*>(p);
-          vw[x][0] = r.x;
-          vw[x][1] = r.y;
-          vw[x][VW - 2] = r.z;
-          vw[x][VW - 1] = r.w;
-        } else {
-          const uint2 r = *reinterpret_cast<const uint2*>(p);
-          vw[x][0] = r.x;
-          vw[x][1] = r.y;
+      for (int u = 0; u < U; ++u) {
+        uint32_t vw[4][VW];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint8_t* p = sv + c * L::group + (4 * u + x) * HD + n * (HD / 8);
+          if (HD == 128) {
+            const uint4 r = *reinterpret_cast<const uint4*>(p);
+            vw[x][0] = r.x;
+            vw[x][1] = r.y;
+            vw[x][VW - 2] = r.z;
+            vw[x][VW - 1] = r.w;
+          } else {
+            const uint2 r = *reinterpret_cast<const uint2*>(p);
+            vw[x][0] = r.x;
+            vw[x][1] = r.y;
+          }
+        }
+        if (t0 + kStep > tokens) {  // rows past the end were not copied: their bytes must not meet the zeros of p
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+              if (t0 + 4 * U * c + 4 * u + x >= tokens) vw[x][w] = 0u;
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          uint32_t y[2][2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) interleave8<FMT>(vw[2 * x][w], vw[2 * x + 1][w], y[x][0], y[x][1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t b0[2], b1[2];
+            to_h2<FMT>(y[0][i], b0[0], b0[1]);
+            to_h2<FMT>(y[1][i], b1[0], b1[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int t = 0; t < R; ++t) mma16816(o[t][4 * w + 2 * i + e], pf[t][u], b0[e], b1[e]);
+          }
         }
       }
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        uint32_t y[2][2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) interleave8<FMT>(vw[2 * x][w], vw[2 * x + 1][w], y[x][0], y[x][1]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t b0[2], b1[2];
-          to_h2<FMT>(y[0][i], b0[0], b0[1]);
-          to_h2<FMT>(y[1][i], b1[0], b1[1]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int t = 0; t < R; ++t) mma16816(o[t][4 * w + 2 * i + e], pf[t], b0[e], b1[e]);
-        }
-      }
-      // the tensor cores round sums towards zero: after kFlush of them the
+      // the tensor cores round sums towards zero: after 16 of them the
       // accumulators go into fp32 totals, rounded to nearest, so that the bias
       // does not grow with the length (1,000,003 positions: 4.3e-6 without)
       if (++since == kFlush) {
@@ -673,19 +682,12 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
         since = 0;
       }
     }
-    // the slot's bytes are in registers and used: copy the step after next into it
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) tq[i] = tq[i + 1];
-#pragma unroll
-    for (int i = 0; i + 1 < kStages; ++i) {
-      ksq[i] = ksq[i + 1];
-      vsq[i] = vsq[i + 1];
-    }
-    issue(tq[kStages - 1], slot, ksq[kStages - 1], vsq[kStages - 1]);
-    tq[kStages] = step_token(st + (kStages + 1) * kAttnWarps);
-    slot = slot + 1 == kStages ? 0 : slot + 1;
+    __syncwarp();  // and its V
+    copy_v(t1);
+    t0 = t1;
+    t1 = t2;
+    kvs = kvs1;
   }
-  cp_wait<0>();
   flush(first);
 
   // ---- merge the warps
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
 // the splits' partials of one row into the output: one thread per channel
 constexpr int kMaxSplits = 512;
 template <int HD, bool SPARSE>
-__global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args a, int rows_per_chunk) {
+__global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args a, int rows_per_chunk, int step) {
   __shared__ float wts[kMaxSplits];
   __shared__ float red[HD / 32];
   pdl_wait();
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args 
     const int r = qi * a.G + qh % a.G, last = min(a.nq * a.G, (r / rows_per_chunk + 1) * rows_per_chunk) - 1;
     tokens = n_pos + last / a.G;
   }
-  const int steps = SPARSE ? a.n_sel * (kB / kStep) : (tokens + kStep - 1) / kStep;
+  const int steps = SPARSE ? a.n_sel * (kB / step) : (tokens + step - 1) / step;
   const int per = split_steps(steps, a.S);
   if (per >= steps) return;
   const int used = (steps + per - 1) / per;
@@ -803,17 +805,21 @@ __global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args 
 }
 
 using AttnKv8Kernel = void (*)(AttnKv8Args);
+struct AttnKv8Variant {
+  AttnKv8Kernel kernel;
+  size_t smem;
+};
 template <int FMT, int HD, bool SPARSE>
-AttnKv8Kernel attn_kv8_pick(int R, size_t* smem) {
-  *smem = R == 1 ? AttnKv8Smem<HD, 1>::bytes : AttnKv8Smem<HD, 2>::bytes;
-  return R == 1 ? attn_kv8_kernel<FMT, HD, 1, SPARSE> : attn_kv8_kernel<FMT, HD, 2, SPARSE>;
+AttnKv8Variant attn_kv8_pick(int R, int U) {
+  if (R == 1 && U == 1) return {attn_kv8_kernel<FMT, HD, 1, 1, SPARSE>, AttnKv8Smem<HD, 1, 1>::bytes};
+  if (R == 1) return {attn_kv8_kernel<FMT, HD, 1, 2, SPARSE>, AttnKv8Smem<HD, 1, 2>::bytes};
+  return {attn_kv8_kernel<FMT, HD, 2, 2, SPARSE>, AttnKv8Smem<HD, 2, 2>::bytes};
 }
 template <bool SPARSE>
-AttnKv8Kernel attn_kv8_for(int fmt, int hd, int R, size_t* smem) {
+AttnKv8Variant attn_kv8_for(int fmt, int hd, int R, int U) {
   if (fmt == NT_KV8_I8)
-    return hd == 128 ? attn_kv8_pick<NT_KV8_I8, 128, SPARSE>(R, smem) : attn_kv8_pick<NT_KV8_I8, 64, SPARSE>(R, smem);
-  return hd == 128 ? attn_kv8_pick<NT_KV8_E4M3, 128, SPARSE>(R, smem)
-                   : attn_kv8_pick<NT_KV8_E4M3, 64, SPARSE>(R, smem);
+    return hd == 128 ? attn_kv8_pick<NT_KV8_I8, 128, SPARSE>(R, U) : attn_kv8_pick<NT_KV8_I8, 64, SPARSE>(R, U);
+  return hd == 128 ? attn_kv8_pick<NT_KV8_E4M3, 128, SPARSE>(R, U) : attn_kv8_pick<NT_KV8_E4M3, 64, SPARSE>(R, U);
 }
 
 // ---- block selection -----------------------------------------------------------
@@ -1077,6 +1083,11 @@ nt_status launch_kv8_read(Ctx* c, const nt_kv8& kv, int64_t pos, int64_t n, int 
   return cuda_check(c, launch_k(c, kern, grid, block, 0, st, a), "8-bit cache read launch");
 }
 
+static int kv8_u2_tokens() {
+  const char* e = getenv("KV8_U2");
+  return e ? atoi(e) : 32;
+}
+
 nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, int n_qh, int64_t n_pos, int nq,
                           const int64_t* pos_dev, const int32_t* idx, int n_sel, char* scratch, size_t scratch_bytes,
                           cudaStream_t st) {
@@ -1106,27 +1117,29 @@ nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, 
   // splits: the grid fills the SMs once (two CTAs each, one with R = 2), no more
   // than the longest sequence has work for, and what the scratch holds
   const int64_t most = sparse ? int64_t(n_sel) * kB : (pos_dev ? kv.kv_stride : n_pos + nq - 1);
-  const int64_t steps = (most + kStep - 1) / kStep;
   int64_t S = int64_t(c->num_sms) * (R == 1 ? 2 : 1) / (int64_t(kv.n_kvh) * z);
+  if (S > kMaxSplits) S = kMaxSplits;
+  if (S < 1) S = 1;
+  const int U = R == 2 || most >= S * kAttnWarps * kv8_u2_tokens() ? 2 : 1;
+  const int64_t steps = (most + 16 * U - 1) / (16 * U);
   const int64_t useful = (steps + kAttnWarps - 1) / kAttnWarps;
   const size_t vecs = size_t(n_qh) * nq, row = vecs * (kv.head_dim * 4 + 8);
   if (S > useful) S = useful;
   if (S * int64_t(row) > int64_t(scratch_bytes)) S = int64_t(scratch_bytes / row);
-  if (S > kMaxSplits) S = kMaxSplits;
   if (S < 1) S = 1;
   a.S = int(S);
   a.part = reinterpret_cast<float*>(scratch);
   a.ml = reinterpret_cast<float2*>(scratch + vecs * S * kv.head_dim * 4);
-  size_t smem = 0;
-  AttnKv8Kernel kern = sparse ? attn_kv8_for<true>(kv.fmt, kv.head_dim, R, &smem)
-                              : attn_kv8_for<false>(kv.fmt, kv.head_dim, R, &smem);
-  nt_status s = cuda_check(c, launch_k(c, kern, dim3(kv.n_kvh, a.S, z), dim3(kAttnWarps * 32), smem, st, a),
+  a.stall = take_stall(st);
+  const AttnKv8Variant kern = sparse ? attn_kv8_for<true>(kv.fmt, kv.head_dim, R, U)
+                                     : attn_kv8_for<false>(kv.fmt, kv.head_dim, R, U);
+  nt_status s = cuda_check(c, launch_k(c, kern.kernel, dim3(kv.n_kvh, a.S, z), dim3(kAttnWarps * 32), kern.smem, st, a),
                            "8-bit attention launch");
   if (s || a.S == 1) return s;  // one split wrote the output
-  using C = void (*)(AttnKv8Args, int);
+  using C = void (*)(AttnKv8Args, int, int);
   C comb = kv.head_dim == 128 ? (sparse ? attn_kv8_combine_kernel<128, true> : attn_kv8_combine_kernel<128, false>)
                               : (sparse ? attn_kv8_combine_kernel<64, true> : attn_kv8_combine_kernel<64, false>);
-  return cuda_check(c, launch_k(c, comb, dim3(n_qh, nq), dim3(kv.head_dim), 0, st, a, 8 * R),
+  return cuda_check(c, launch_k(c, comb, dim3(n_qh, nq), dim3(kv.head_dim), 0, st, a, 8 * R, 16 * U),
                     "8-bit attention combine launch");
 }
 
@@ -1172,14 +1185,14 @@ nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, 
 nt_status configure_kv8(Ctx* c) {
   for (int fmt : {NT_KV8_I8, NT_KV8_E4M3})
     for (int hd : {64, 128})
-      for (int R : {1, 2})
-        for (bool sparse : {false, true}) {
-          size_t smem = 0;
-          AttnKv8Kernel k = sparse ? attn_kv8_for<true>(fmt, hd, R, &smem) : attn_kv8_for<false>(fmt, hd, R, &smem);
-          nt_status s = cuda_check(c, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)),
-                                   "8-bit attention shared-memory attribute");
-          if (s) return s;
-        }
+      for (int v = 0; v < 6; ++v) {
+        const int R = v < 4 ? 1 : 2, U = v < 2 ? 1 : 2;
+        const AttnKv8Variant k = v & 1 ? attn_kv8_for<true>(fmt, hd, R, U) : attn_kv8_for<false>(fmt, hd, R, U);
+        nt_status s = cuda_check(
+            c, cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.smem)),
+            "8-bit attention shared-memory attribute");
+        if (s) return s;
+      }
   return NT_OK;
 }
 
