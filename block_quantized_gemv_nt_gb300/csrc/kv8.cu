@@ -351,6 +351,14 @@ __device__ __forceinline__ void mma16816(float c[4], const uint4& a, uint32_t b0
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
+// the same from zero
+__device__ __forceinline__ void mma16816_zero(float c[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -366,17 +374,18 @@ __device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// shared memory: q fragments [R][HD / 16][32] x 16, totals [warps][R][HD / 8][32] x 8,
-// (max, sum) [2][warps][8 R], each warp's slots for one step's K and V
+// shared memory: q fragments [R][HD / 16][32] x 16, (max, sum) [2][warps][8 R], each
+// warp's slots for one step's K and V; at the end, in place of the slots, the warps'
+// outputs [warps][R][HD / 8][32] x 8
 template <int HD, int R, int U>
 struct AttnKv8Smem {
   static constexpr size_t q = 0;
-  static constexpr size_t tot = q + size_t(R) * (HD / 16) * 512;
-  static constexpr size_t ml = tot + size_t(kAttnWarps) * R * (HD / 8) * 256;
+  static constexpr size_t ml = q + size_t(R) * (HD / 16) * 512;
   static constexpr size_t ring = ml + size_t(2) * kAttnWarps * 8 * R * 4;
   static constexpr size_t group = size_t(4 * U) * HD + 32;           // V rows of one c
   static constexpr size_t stage = size_t(16 * U) * HD + 4 * group;   // K, then V
-  static constexpr size_t bytes = ring + kAttnWarps * stage;
+  static constexpr size_t outs = size_t(R) * (HD / 8) * 256;         // one warp's outputs
+  static constexpr size_t bytes = ring + kAttnWarps * (stage > outs ? stage : outs);
 };
 
 template <int FMT, int HD, int R, int U, bool SPARSE>
@@ -389,7 +398,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   constexpr int VW = HD / 32;        // words of a V row per lane
   constexpr int ROWS = 8 * R;
   constexpr int CH = U == 1 ? 2 : 1; // accumulators per score tile: at least four chains of MMAs
-  constexpr int kFlush = 16 / U;
   extern __shared__ __align__(16) uint8_t sm8[];
   uint4* qa = reinterpret_cast<uint4*>(sm8 + L::q);
   __shared__ float s_amax[ROWS];
@@ -498,44 +506,21 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   __syncthreads();
   float rscale[R];      // scores to the base-2 exponent
   int limit[R];         // positions row n sees
-  float m[R], l[R], mf[R];
-  float o[R][NT][4];
+  float m[R], l[R];
+  float2 o[R][NT];      // row n, channels 2 c (HD / 8) + i and (2 c + 1) (HD / 8) + i
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     const int r = t * 8 + n;
     // log2(e) / sqrt(HD)
     rscale[t] = __uint_as_float(uint32_t(127 - row_exp(r)) << 23) * (1.44269504088896f * rsqrtf(float(HD)));
     limit[t] = r < rows ? n_pos + query_of(r) : 0;
-    m[t] = mf[t] = -INFINITY;
+    m[t] = -INFINITY;
     l[t] = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+    for (int i = 0; i < NT; ++i) o[t][i] = make_float2(0.f, 0.f);
   }
-  float2* tot = reinterpret_cast<float2*>(sm8 + L::tot) + size_t(warp) * R * NT * 32 + lane;  // [R][NT], lane's own
-  // add the accumulators into the totals (both held relative to their maxima, mf and m)
-  const auto flush = [&](bool first) {
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      const float f = mf[t] == -INFINITY ? 0.f : ex2(mf[t] - m[t]);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        float2 x = make_float2(o[t][i][0] + o[t][i][2], o[t][i][1] + o[t][i][3]);
-        if (!first) {
-          const float2 y = tot[(t * NT + i) * 32];
-          x.x = fmaf(y.x, f, x.x);
-          x.y = fmaf(y.y, f, x.y);
-        }
-        tot[(t * NT + i) * 32] = x;
-        o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
-      }
-      mf[t] = m[t];
-    }
-  };
-
   const int fewest = SPARSE ? tokens : n_pos + query_of(0);  // positions every row sees
-  int since = 0;
   uint32_t phase = 0;
-  bool first = true;
   for (; st < st1; st += kAttnWarps) {
     const int t2 = step_token(st + 2 * kAttnWarps);
     const float2 kvs1 = scales(t1);
@@ -608,9 +593,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
           const float corr = m[t] == -INFINITY ? 0.f : ex2(m[t] - mn);
           l[t] *= corr;
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][i][e] *= corr;
+          for (int i = 0; i < NT; ++i) {
+            o[t][i].x *= corr;
+            o[t][i].y *= corr;
+          }
           m[t] = mn;
         }
         const float base = m[t] == -INFINITY ? 0.f : m[t] - kPTop;
@@ -630,56 +616,58 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     if (t0 < tokens) {
       if (!wait(bar_v, phase)) break;
       phase ^= 1;
-      // ---- P V: words of the lane's four tokens interleaved into (token, token + 1) pairs per channel
+      // ---- P V: words of two tokens interleaved into (token, token + 1) pairs per
+      // channel.  Each step's products start from zero and are added to the output
+      // in fp32: the tensor cores round their sums towards zero, and a bias of one
+      // such rounding per step would grow with the length (1,000,003 positions:
+      // error 4.3e-6 with one running accumulator).
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t vw[4][VW];
+      for (int w = 0; w < VW; w += 2) {
+        uint32_t vw[4 * U][2];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint8_t* p = sv + c * L::group + (4 * u + x) * HD + n * (HD / 8);
-          if (HD == 128) {
-            const uint4 r = *reinterpret_cast<const uint4*>(p);
-            vw[x][0] = r.x;
-            vw[x][1] = r.y;
-            vw[x][VW - 2] = r.z;
-            vw[x][VW - 1] = r.w;
-          } else {
-            const uint2 r = *reinterpret_cast<const uint2*>(p);
-            vw[x][0] = r.x;
-            vw[x][1] = r.y;
-          }
+        for (int x = 0; x < 4 * U; ++x) {
+          const uint2 r = *reinterpret_cast<const uint2*>(sv + c * L::group + x * HD + n * (HD / 8) + 4 * w);
+          vw[x][0] = r.x;
+          vw[x][1] = r.y;
         }
         if (t0 + kStep > tokens) {  // rows past the end were not copied: their bytes must not meet the zeros of p
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int w = 0; w < VW; ++w)
-              if (t0 + 4 * U * c + 4 * u + x >= tokens) vw[x][w] = 0u;
+          for (int x = 0; x < 4 * U; ++x)
+            if (t0 + 4 * U * c + x >= tokens) vw[x][0] = vw[x][1] = 0u;
         }
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          uint32_t y[2][2];
+        for (int h = 0; h < 2; ++h) {
+          float acc[R][4][4];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) interleave8<FMT>(vw[2 * x][w], vw[2 * x + 1][w], y[x][0], y[x][1]);
+          for (int u = 0; u < U; ++u) {
+            uint32_t y[2][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t b0[2], b1[2];
-            to_h2<FMT>(y[0][i], b0[0], b0[1]);
-            to_h2<FMT>(y[1][i], b1[0], b1[1]);
+            for (int x = 0; x < 2; ++x) interleave8<FMT>(vw[4 * u + 2 * x][h], vw[4 * u + 2 * x + 1][h], y[x][0], y[x][1]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int i = 0; i < 2; ++i) {
+              uint32_t b0[2], b1[2];
+              to_h2<FMT>(y[0][i], b0[0], b0[1]);
+              to_h2<FMT>(y[1][i], b1[0], b1[1]);
 #pragma unroll
-              for (int t = 0; t < R; ++t) mma16816(o[t][4 * w + 2 * i + e], pf[t][u], b0[e], b1[e]);
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int t = 0; t < R; ++t) {
+                  if (u == 0)
+                    mma16816_zero(acc[t][2 * i + e], pf[t][u], b0[e], b1[e]);
+                  else
+                    mma16816(acc[t][2 * i + e], pf[t][u], b0[e], b1[e]);
+                }
+            }
           }
+#pragma unroll
+          for (int t = 0; t < R; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2& x = o[t][4 * (w + h) + i];
+              x.x += acc[t][i][0] + acc[t][i][2];
+              x.y += acc[t][i][1] + acc[t][i][3];
+            }
         }
-      }
-      // the tensor cores round sums towards zero: after 16 of them the
-      // accumulators go into fp32 totals, rounded to nearest, so that the bias
-      // does not grow with the length (1,000,003 positions: 4.3e-6 without)
-      if (++since == kFlush) {
-        flush(first);
-        first = false;
-        since = 0;
       }
     }
     __syncwarp();  // and its V
@@ -688,11 +676,12 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     t1 = t2;
     kvs = kvs1;
   }
-  flush(first);
 
   // ---- merge the warps
+  __syncthreads();  // every warp is done with its slots
   float* mm = reinterpret_cast<float*>(sm8 + L::ml);  // [warps][ROWS] max
   float* mll = mm + kAttnWarps * ROWS;                // [warps][ROWS] sum
+  float2* outs = reinterpret_cast<float2*>(sm8 + L::ring);
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
@@ -701,10 +690,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       mm[warp * ROWS + t * 8 + n] = m[t];
       mll[warp * ROWS + t * 8 + n] = l[t];
     }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) outs[(size_t(warp) * R * NT + t * NT + i) * 32 + lane] = o[t][i];
   }
   __syncthreads();
   const bool whole = per >= steps;  // one split: the output itself
-  const float2* all = reinterpret_cast<const float2*>(sm8 + L::tot);
   for (int i = tid; i < R * NT * 32; i += kAttnWarps * 32) {
     const int ln = i & 31, nt = (i >> 5) % NT, r = (i >> 5) / NT * 8 + (ln >> 2), cc = ln & 3;
     if (r >= rows) continue;
@@ -717,7 +707,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     for (int w = 0; w < kAttnWarps; ++w) {
       const float mw = mm[w * ROWS + r];
       const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-      const float2 x = all[size_t(w) * R * NT * 32 + i];
+      const float2 x = outs[size_t(w) * R * NT * 32 + i];
       acc.x = fmaf(x.x, f, acc.x);
       acc.y = fmaf(x.y, f, acc.y);
       sum = fmaf(mll[w * ROWS + r], f, sum);
