@@ -574,8 +574,8 @@ nt_status nt_kv8_select(nt_ctx* ctx, const float* q, const nt_kv8* kv, int n_qh,
   NT_REQUIRE(n_sel <= (1 << 24), NT_ERR_INVALID_ARG, "n_sel above 2^24");
   NT_REQUIRE(idx, NT_ERR_INVALID_ARG, "idx is NULL");
   NT_REQUIRE(aligned(idx, 4), NT_ERR_ALIGNMENT, "idx must be 4-byte aligned");
-  const size_t need = kv8_score_bytes(*kv, n_query);
-  NT_REQUIRE(ctx->scratch_bytes >= kScratchGemm && ctx->scratch_bytes - kScratchGemm >= need, NT_ERR_OOM,
+  const size_t need = kv8_score_bytes(ctx, *kv, n_pos, n_query, pos_dev != nullptr);
+  NT_REQUIRE(!need || (ctx->scratch_bytes >= kScratchGemm && ctx->scratch_bytes - kScratchGemm >= need), NT_ERR_OOM,
              "block scores need %zu scratch bytes beyond the first 32 MiB", need);
   DeviceGuard g(ctx->device);
   return launch_kv8_select(ctx, *kv, q, n_qh, n_pos, n_query, pos_dev, n_sel, n_first, n_last, idx,

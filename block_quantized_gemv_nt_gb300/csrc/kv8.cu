@@ -819,14 +819,16 @@ AttnKv8Variant attn_kv8_for(int fmt, int hd, int R, int U) {
 // added first and a block costs 2 HD products whatever the group size.  With q as
 // 12-bit integers every sum is a whole number below 2^31: the scores, and with
 // them the choice, do not depend on the order of additions.
-constexpr int kScoreThreads = 256;
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 1024;
+constexpr uint32_t kForced = 0xFFFFFFFFu;  // key of a block that is taken whatever its score
 
 struct SelectArgs {
   const float* q;
   const int8_t *kmin, *kmax;
   const float* ks;
-  float* score;      // [query][n_kvh][nb]
+  uint32_t* keys;    // [query][n_kvh][nb]: scratch, when the keys of a head do not fit in shared memory
   int32_t* idx;      // [query][n_kvh][n_sel]
   int n_qh, n_kvh, G, nq, n_sel, n_first, n_last;
   int64_t n_pos, kv_stride, nb;
@@ -844,164 +846,247 @@ __device__ __forceinline__ int64_t seen_positions(const SelectArgs& a) {
   return seen_positions(t);
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const SelectArgs a) {
-  constexpr int LB = HD / 16;            // lanes per block, 16 channels each
-  constexpr int BW = 32 / LB;            // blocks per warp
-  __shared__ float red[kScoreThreads / 32];
-  __shared__ __align__(16) int16_t qp[HD], qn[HD];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = blockIdx.y, qi = blockIdx.z;
-  const int64_t blocks = (seen_positions(a) + qi + kB - 1) / kB;
-  const float* q = a.q + (int64_t(qi) * a.n_qh + g * a.G) * HD;
-  float m = 0.f;
-  for (int i = tid; i < a.G * HD; i += kScoreThreads) {
-    const float v = fabsf(q[i]);
-    if (v <= 3.402823466e38f) m = fmaxf(m, v);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kScoreThreads / 32; ++w) m = fmaxf(m, red[w]);
-  const float inv = pow2_inv(pow2_scale<10, 0x7FE000u>(m));  // 2047 = 1.99902 * 2^10
-  for (int d = tid; d < HD; d += kScoreThreads) {
-    int p = 0, n = 0;
-    for (int h = 0; h < a.G; ++h) {
-      const float x = q[h * HD + d];
-      const int v = x != x ? 0 : __float2int_rn(fminf(fmaxf(x * inv, -2047.f), 2047.f));
-      p += max(v, 0);
-      n += min(v, 0);
-    }
-    qp[d] = int16_t(p);
-    qn[d] = int16_t(n);
-  }
-  __syncthreads();
-  const int part = lane % LB;
-  int p2[8], n2[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    p2[i] = reinterpret_cast<const int*>(qp)[part * 8 + i];
-    n2[i] = reinterpret_cast<const int*>(qn)[part * 8 + i];
-  }
-  float* score = a.score + (int64_t(qi) * a.n_kvh + g) * a.nb;
-  for (int64_t b0 = (int64_t(blockIdx.x) * (kScoreThreads / 32) + warp) * BW; b0 < blocks;
-       b0 += int64_t(gridDim.x) * (kScoreThreads / 32) * BW) {
-    const int64_t b = b0 + lane / LB;
-    int acc = 0;
-    if (b < blocks) {
-      const int64_t at = (int64_t(g) * a.nb + b) * HD + part * 16;
-      const uint4 hi = *reinterpret_cast<const uint4*>(a.kmax + at), lo = *reinterpret_cast<const uint4*>(a.kmin + at);
-      const int hw[4] = {int(hi.x), int(hi.y), int(hi.z), int(hi.w)}, lw[4] = {int(lo.x), int(lo.y), int(lo.z), int(lo.w)};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc = __dp2a_lo(p2[2 * i], hw[i], acc);
-        acc = __dp2a_hi(p2[2 * i + 1], hw[i], acc);
-        acc = __dp2a_lo(n2[2 * i], lw[i], acc);
-        acc = __dp2a_hi(n2[2 * i + 1], lw[i], acc);
-      }
-    }
-#pragma unroll
-    for (int o = LB / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (b < blocks && part == 0) score[b] = __int2float_rn(acc) * a.ks[int64_t(g) * a.nb + b];
-  }
-}
-
+// order-preserving key of a score; NaN ranks below everything
 __device__ __forceinline__ uint32_t order_key(float v) {
   if (v != v) return 0u;
   const uint32_t b = __float_as_uint(v);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// One CTA per (KV head, query): the key of the n_sel-th largest by four 8-bit
-// radix rounds, then the blocks at or above it in index order (of those at the
-// key itself, the lowest indices).
-__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const SelectArgs a) {
-  __shared__ int hist[256];
-  __shared__ int s_digit, s_need, wsum[2][32];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = blockIdx.x, qi = blockIdx.y;
-  const int64_t blocks = (seen_positions(a) + qi + kB - 1) / kB;
-  const float* score = a.score + (int64_t(qi) * a.n_kvh + g) * a.nb;
-  int32_t* idx = a.idx + (int64_t(qi) * a.n_kvh + g) * a.n_sel;
-  if (blocks <= a.n_sel) {
-    for (int i = tid; i < a.n_sel; i += kSelThreads) idx[i] = i < blocks ? i : -1;
-    return;
-  }
-  const auto key_of = [&](int64_t b) {
-    return b < a.n_first || b >= blocks - a.n_last ? 0xFFFFFFFFu : order_key(__ldcg(score + b));
+// The keys of one head's blocks for one query, by CTA `rank` of `ranks`, each to
+// put(block, key).  HD / 16 lanes share a block.
+template <int HD, typename Put>
+__device__ __forceinline__ void score_blocks(const SelectArgs& a, int g, int qi, int blocks, int rank, int ranks,
+                                             Put put) {
+  constexpr int LB = HD / 16;            // lanes per block, 16 channels each
+  constexpr int BW = 32 / LB;            // blocks per warp
+  __shared__ float red[kSelWarps];
+  __shared__ int sums[2][HD];            // group sums of max(qi, 0) and min(qi, 0)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = lane % LB;
+  const int stride = ranks * kSelWarps * BW;
+  const int64_t head = int64_t(g) * a.nb;
+  int b = (rank * kSelWarps + warp) * BW + lane / LB;
+  uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+  float ks = 0.f;
+  const auto load = [&](int at) {  // this warp's bounds, in flight while q is prepared or the last ones are summed
+    if (at >= blocks) return;
+    hi = *reinterpret_cast<const uint4*>(a.kmax + (head + at) * HD + part * 16);
+    lo = *reinterpret_cast<const uint4*>(a.kmin + (head + at) * HD + part * 16);
+    ks = a.ks[head + at];
   };
-  uint32_t prefix = 0;
-  int need = a.n_sel;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int64_t b = tid; b < blocks; b += kSelThreads) {
-      const uint32_t k = key_of(b);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {  // lane L holds bins 255 - 8 L .. 248 - 8 L, highest first
-      int h[8], sum = 0;
+  load(b);
+  const float* q = a.q + (int64_t(qi) * a.n_qh + g * a.G) * HD;
+  constexpr int QR = 16 * HD / kSelThreads;  // q values per thread, at most
+  float x[QR];
+  float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += h[i] = hist[255 - 8 * lane - i];
-      int incl = sum;
+  for (int i = 0; i < QR; ++i) {
+    const int at = tid + i * kSelThreads;
+    x[i] = at < a.G * HD ? q[at] : 0.f;
+    const float v = fabsf(x[i]);
+    if (v <= 3.402823466e38f) m = fmaxf(m, v);
+  }
+  if (tid < 2 * HD) (&sums[0][0])[tid] = 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = red[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float inv = pow2_inv(pow2_scale<10, 0x7FE000u>(m));  // 2047 = 1.99902 * 2^10
+#pragma unroll
+  for (int i = 0; i < QR; ++i) {
+    const int v = x[i] != x[i] ? 0 : __float2int_rn(fminf(fmaxf(x[i] * inv, -2047.f), 2047.f));
+    if (v) atomicAdd(&sums[v < 0][(tid + i * kSelThreads) % HD], v);
+  }
+  __syncthreads();
+  int p2[8], n2[8];  // pairs of 16-bit sums (16 heads of 2047 fit)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int d = part * 16 + 2 * i;
+    p2[i] = (sums[0][d] & 0xFFFF) | (sums[0][d + 1] << 16);
+    n2[i] = (sums[1][d] & 0xFFFF) | (sums[1][d + 1] << 16);
+  }
+  for (int b0 = b - lane / LB; b0 < blocks; b0 += stride, b += stride) {
+    const int hw[4] = {int(hi.x), int(hi.y), int(hi.z), int(hi.w)}, lw[4] = {int(lo.x), int(lo.y), int(lo.z), int(lo.w)};
+    const float t = ks;
+    load(b + stride);
+    int acc = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc = __dp2a_lo(p2[2 * i], hw[i], acc);
+      acc = __dp2a_hi(p2[2 * i + 1], hw[i], acc);
+      acc = __dp2a_lo(n2[2 * i], lw[i], acc);
+      acc = __dp2a_hi(n2[2 * i + 1], lw[i], acc);
+    }
+#pragma unroll
+    for (int o = LB / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (b < blocks && part == 0)
+      put(b, b < a.n_first || b >= blocks - a.n_last ? kForced : order_key(__int2float_rn(acc) * t));
+  }
+}
+
+// The n_sel largest of `blocks` keys, as ascending indices: radix rounds of up to
+// ten bits below the keys' common prefix, ending as soon as the chosen bin is taken
+// whole; then one scan in index order (thread t holds blocks t chunk .. ; chunk odd,
+// so that the threads of a warp read different banks).  key(b): the key of block b.
+template <typename Key>
+__device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, int32_t* idx, Key key) {
+  __shared__ int hist[kSelBins];
+  __shared__ int wsum[kSelWarps];
+  __shared__ unsigned long long wscan[kSelWarps];
+  __shared__ uint32_t wmin[kSelWarps], wmax[kSelWarps];
+  __shared__ int s_bin, s_above, s_count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunk = ((blocks + kSelThreads - 1) / kSelThreads) | 1;
+  const int i0 = min(blocks, tid * chunk), i1 = min(blocks, i0 + chunk);
+  int need = a.n_sel - a.n_first - a.n_last;
+  uint32_t mn = kForced, mx = 0u;
+  for (int b = i0; b < i1; ++b) {
+    const uint32_t k = key(b);
+    if (k != kForced) {
+      mn = min(mn, k);
+      mx = max(mx, k);
+    }
+  }
+  mn = __reduce_min_sync(0xffffffffu, mn);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if (lane == 0) {
+    wmin[warp] = mn;
+    wmax[warp] = mx;
+  }
+  __syncthreads();
+  mn = __reduce_min_sync(0xffffffffu, wmin[lane]);
+  mx = __reduce_max_sync(0xffffffffu, wmax[lane]);
+  uint32_t cut = kForced;  // keys above it are taken, and the first `need` at it
+  if (need > 0) {
+    int bits = mx == mn ? 0 : 32 - __clz(mx ^ mn);
+    cut = bits == 32 ? 0u : (mx >> bits) << bits;
+    while (bits > 0) {
+      const int dig = min(10, bits), shift = bits - dig;
+      hist[tid] = 0;
+      __syncthreads();
+      for (int b = i0; b < i1; ++b) {
+        const uint32_t k = key(b);
+        if (k != kForced && (bits == 32 || (k >> bits) == (cut >> bits)))
+          atomicAdd(&hist[(k >> shift) & ((1u << dig) - 1u)], 1);
+      }
+      __syncthreads();
+      const int bin = kSelBins - 1 - tid;  // thread 0 holds the highest bin
+      const int h = hist[bin];
+      int incl = h;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int t = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += t;
       }
-      int before = incl - sum;
-      if (before < need && incl >= need) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (before < need && before + h[i] >= need) {
-            s_digit = 255 - 8 * lane - i;
-            s_need = need - before;
-          }
-          before += h[i];
-        }
+      if (lane == 31) wsum[warp] = incl;
+      __syncthreads();
+      const int below = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0);
+      incl += below;
+      if (incl - h < need && incl >= need) {
+        s_bin = bin;
+        s_above = incl - h;
+        s_count = h;
+      }
+      __syncthreads();
+      cut |= uint32_t(s_bin) << shift;
+      need -= s_above;
+      bits = shift;
+      if (s_count == need) {  // the whole bin: every key from here up (never all keys: n_sel < blocks)
+        cut -= 1u;
+        need = 0;
+        break;
       }
     }
-    __syncthreads();
-    prefix |= uint32_t(s_digit) << shift;
-    need = s_need;
-    __syncthreads();
   }
-  // `need` blocks are taken at the key itself
-  int out = 0, ties = 0;
-  for (int64_t b0 = 0; b0 < blocks; b0 += kSelThreads) {
-    const int64_t b = b0 + tid;
-    const uint32_t k = b < blocks ? key_of(b) : 0u;
-    const bool tie = b < blocks && k == prefix;
-    const unsigned tm = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) wsum[0][warp] = __popc(tm);
-    __syncthreads();
-    int tr = ties, tt = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) tr += wsum[0][w];
-      tt += wsum[0][w];
-    }
-    tr += __popc(tm & ((1u << lane) - 1u));
-    const bool take = (b < blocks && k > prefix) || (tie && tr < need);
-    const unsigned km = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) wsum[1][warp] = __popc(km);
-    __syncthreads();
-    int at = out, kt = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) at += wsum[1][w];
-      kt += wsum[1][w];
-    }
-    at += __popc(km & ((1u << lane) - 1u));
-    if (take) idx[at] = int32_t(b);
-    out += kt;
-    ties += tt;
+  unsigned long long cnt = 0;  // blocks taken above the cut, and (high half) blocks at it
+  for (int b = i0; b < i1; ++b) {
+    const uint32_t k = key(b);
+    cnt += k == kForced || k > cut ? 1ull : (k == cut ? 1ull << 32 : 0ull);
   }
+  unsigned long long incl = cnt;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) wscan[warp] = incl;
+  __syncthreads();
+  unsigned long long base = lane < warp ? wscan[lane] : 0ull;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+  base += incl - cnt;
+  int above = int(base & 0xFFFFFFFFull), ties = int(base >> 32);
+  for (int b = i0; b < i1; ++b) {
+    const uint32_t k = key(b);
+    if (k == kForced || k > cut) {
+      idx[above + min(ties, need)] = b;
+      ++above;
+    } else if (k == cut) {
+      if (ties < need) idx[above + ties] = b;
+      ++ties;
+    }
+  }
+}
+
+// One cluster per (KV head, query): its CTAs score the head's blocks and put the
+// keys into the first CTA's shared memory, which selects.  Bound by the latency of
+// its phases for short sequences and by reading the bounds for long ones.
+template <int HD>
+__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const SelectArgs a) {
+  extern __shared__ uint32_t keys[];
+  pdl_wait();
+  pdl_trigger();
+  const int ranks = gridDim.x, rank = blockIdx.x;  // the grid is one cluster wide
+  const int g = blockIdx.y, qi = blockIdx.z;
+  const int blocks = int(kv8_blocks(seen_positions(a) + qi));
+  int32_t* idx = a.idx + (int64_t(qi) * a.n_kvh + g) * a.n_sel;
+  if (blocks <= a.n_sel) {  // uniform over the cluster
+    for (int i = rank * kSelThreads + threadIdx.x; i < a.n_sel; i += ranks * kSelThreads) idx[i] = i < blocks ? i : -1;
+    return;
+  }
+  if (ranks == 1) {
+    score_blocks<HD>(a, g, qi, blocks, 0, 1, [&](int b, uint32_t k) { keys[b] = k; });
+    __syncthreads();
+  } else {
+    uint32_t first;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(first) : "r"(smem_u32(keys)));
+    // no CTA writes into the first one before it runs
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    score_blocks<HD>(a, g, qi, blocks, rank, ranks, [&](int b, uint32_t k) {
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first + 4u * uint32_t(b)), "r"(k) : "memory");
+    });
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank) return;
+  }
+  select_blocks(a, blocks, idx, [&](int b) { return keys[b]; });
+}
+
+// the same in two launches with the keys in scratch, for heads whose keys do not
+// fit in shared memory
+template <int HD>
+__global__ void __launch_bounds__(kSelThreads) kv8_score_kernel(const SelectArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.y, qi = blockIdx.z;
+  const int blocks = int(kv8_blocks(seen_positions(a) + qi));
+  uint32_t* out = a.keys + (int64_t(qi) * a.n_kvh + g) * a.nb;
+  score_blocks<HD>(a, g, qi, blocks, blockIdx.x, gridDim.x, [&](int b, uint32_t k) { out[b] = k; });
+}
+__global__ void __launch_bounds__(kSelThreads) kv8_select_scratch_kernel(const SelectArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.y, qi = blockIdx.z;
+  const int blocks = int(kv8_blocks(seen_positions(a) + qi));
+  int32_t* idx = a.idx + (int64_t(qi) * a.n_kvh + g) * a.n_sel;
+  if (blocks <= a.n_sel) {
+    for (int i = threadIdx.x; i < a.n_sel; i += kSelThreads) idx[i] = i < blocks ? i : -1;
+    return;
+  }
+  const uint32_t* keys = a.keys + (int64_t(qi) * a.n_kvh + g) * a.nb;
+  select_blocks(a, blocks, idx, [&](int b) { return __ldcg(keys + b); });
 }
 
 }  // namespace
@@ -1133,8 +1218,17 @@ nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, 
                     "8-bit attention combine launch");
 }
 
-size_t kv8_score_bytes(const nt_kv8& kv, int nq) {
-  return size_t(nq) * kv.n_kvh * size_t(kv8_blocks(kv.kv_stride)) * sizeof(float);
+// dynamic shared memory of a selection, its static part held back
+constexpr size_t kSelStatic = 8192;
+
+static bool kv8_select_fits(const Ctx* c, int64_t blocks) {
+  return size_t(blocks) * sizeof(uint32_t) + kSelStatic <= c->smem_optin;
+}
+
+size_t kv8_score_bytes(const Ctx* c, const nt_kv8& kv, int64_t n_pos, int nq, bool pos_on_device) {
+  const int64_t nb = kv8_blocks(kv.kv_stride);
+  const int64_t most = pos_on_device ? nb : kv8_blocks(n_pos + nq - 1);
+  return kv8_select_fits(c, most) ? 0 : size_t(nq) * kv.n_kvh * size_t(nb) * sizeof(uint32_t);
 }
 
 nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, int64_t n_pos, int nq,
@@ -1145,7 +1239,7 @@ nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, 
   a.kmin = kv.kmin;
   a.kmax = kv.kmax;
   a.ks = kv.kscale;
-  a.score = reinterpret_cast<float*>(scratch);
+  a.keys = reinterpret_cast<uint32_t*>(scratch);
   a.idx = idx;
   a.n_qh = n_qh;
   a.n_kvh = kv.n_kvh;
@@ -1160,19 +1254,49 @@ nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, 
   a.pos_dev = pos_dev;
   a.err = c->err_flag;
   const int64_t blocks = pos_dev ? a.nb : kv8_blocks(n_pos + nq - 1);
-  const int bw = 32 / (kv.head_dim / 16) * (kScoreThreads / 32);  // blocks per CTA and pass
-  int64_t gx = (blocks + bw - 1) / bw;
-  const int64_t fill = (int64_t(c->num_sms) * 8 + int64_t(kv.n_kvh) * nq - 1) / (int64_t(kv.n_kvh) * nq);
-  gx = gx < 1 ? 1 : (gx > fill ? fill : gx);
+  const int64_t pass = int64_t(kSelWarps) * 32 / (kv.head_dim / 16);  // blocks a CTA scores at a time
+  const int64_t groups = int64_t(kv.n_kvh) * nq;
+  if (kv8_select_fits(c, blocks)) {
+    // CTAs per cluster: a pass of work for each, and the grid within the SMs
+    int ranks = 1;
+    while (ranks < 16 && ranks * pass < blocks && 2 * ranks * groups <= c->num_sms) ranks *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ranks, kv.n_kvh, nq);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = size_t(blocks) * sizeof(uint32_t);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = c->pdl && !c->pdl_hold ? 2 : 1;
+    c->pdl_hold = false;
+    return cuda_check(c, cudaLaunchKernelEx(&cfg, kv.head_dim == 128 ? kv8_select_kernel<128> : kv8_select_kernel<64>, a),
+                      "block select launch");
+  }
+  int64_t gx = (blocks + pass - 1) / pass;
+  const int64_t fill = (int64_t(c->num_sms) * 2 + groups - 1) / groups;
+  gx = gx > fill ? fill : gx;
   nt_status s = cuda_check(c, launch_k(c, kv.head_dim == 128 ? kv8_score_kernel<128> : kv8_score_kernel<64>,
-                                       dim3(unsigned(gx), kv.n_kvh, nq), dim3(kScoreThreads), 0, st, a),
+                                       dim3(unsigned(gx), kv.n_kvh, nq), dim3(kSelThreads), 0, st, a),
                            "block score launch");
   if (s) return s;
-  return cuda_check(c, launch_k(c, kv8_select_kernel, dim3(kv.n_kvh, nq), dim3(kSelThreads), 0, st, a),
+  return cuda_check(c, launch_k(c, kv8_select_scratch_kernel, dim3(1, kv.n_kvh, nq), dim3(kSelThreads), 0, st, a),
                     "block select launch");
 }
 
 nt_status configure_kv8(Ctx* c) {
+  for (const auto k : {kv8_select_kernel<64>, kv8_select_kernel<128>}) {
+    nt_status s = cuda_check(c, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     int(c->smem_optin - kSelStatic)),
+                             "block select shared-memory attribute");
+    if (!s) s = cuda_check(c, cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
+                           "block select cluster attribute");
+    if (s) return s;
+  }
   for (int fmt : {NT_KV8_I8, NT_KV8_E4M3})
     for (int hd : {64, 128})
       for (int v = 0; v < 6; ++v) {

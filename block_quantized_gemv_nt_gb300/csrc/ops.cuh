@@ -67,7 +67,8 @@ nt_status launch_kv8_read(Ctx* c, const nt_kv8& kv, int64_t pos, int64_t n, int 
 nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, int n_qh, int64_t n_pos, int nq,
                           const int64_t* pos_dev, const int32_t* idx, int n_sel, char* scratch, size_t scratch_bytes,
                           cudaStream_t st);
-size_t kv8_score_bytes(const nt_kv8& kv, int nq);
+// scratch of a selection: none while the keys of a head fit in shared memory
+size_t kv8_score_bytes(const Ctx* c, const nt_kv8& kv, int64_t n_pos, int nq, bool pos_on_device);
 nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, int64_t n_pos, int nq,
                             const int64_t* pos_dev, int n_sel, int n_first, int n_last, int32_t* idx, char* scratch,
                             cudaStream_t st);

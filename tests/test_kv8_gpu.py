@@ -122,8 +122,8 @@ def test_refusals(ctx):
         with pytest.raises(nt.NtError) as e:
             nt.nt_attn_kv8(small, f, g.desc, f, 4, 1)
         assert e.value.status == oom
-        with pytest.raises(nt.NtError) as e:
-            nt.nt_kv8_select(small, f, g.desc, 4, 1, 1, 4, 0, 1, i)
+        with pytest.raises(nt.NtError) as e:  # 2^22 blocks: their keys go to scratch
+            nt.nt_kv8_select(small, f, desc(kv_stride=2 ** 28), 4, 2 ** 28, 1, 4, 0, 1, i)
         assert e.value.status == oom
     finally:
         small.close()
@@ -359,6 +359,28 @@ def test_select(ctx, fmt, H, G, hd, n_pos, nq, n_sel, first, last):
     out = torch.empty((nq, H * G, hd), device="cuda")
     g.attend_blocks(dev(q), out, n_pos, idx)
     _check(host(out), *ref.attend_cache(c, q, n_pos, want))
+
+
+@pytest.mark.parametrize("nq", [1, 3])
+@pytest.mark.parametrize("n_blocks", [130, 2047, 15626, 60000])
+def test_select_many_blocks(ctx, n_blocks, nq):
+    """Random bounds and scales for up to 60,000 blocks (their keys no longer fit in shared memory), many equal
+    scores, lists from one block to nearly all."""
+    H, G, hd, n = 1, 3, 64, 64 * n_blocks - 5
+    g, c = _cache(ctx, I8, H, hd, n + nq)
+    rng = np.random.default_rng(n_blocks)
+    a, b = rng.integers(-127, 128, size=(2, H, n_blocks, hd))
+    c.kmin[:], c.kmax[:] = np.minimum(a, b), np.maximum(a, b)
+    c.kmin[:, 40:90], c.kmax[:, 40:90] = c.kmin[:, 40:41], c.kmax[:, 40:41]
+    c.scale["k"][:] = 2.0 ** rng.integers(-6, 3, size=(H, n_blocks))
+    c.scale["k"][:, 40:90] = 4.0
+    for name, v in (("kmin", c.kmin), ("kmax", c.kmax), ("kscale", c.scale["k"].astype(np.float32))):
+        g.buffers[name].copy_(torch.from_numpy(v))
+    q = rng.normal(size=(nq, H * G, hd)).astype(np.float32)
+    for n_sel, first, last in ((1, 0, 0), (1, 1, 0), (17, 1, 4), (60, 0, 0), (n_blocks - 1, 2, 1), (128, 64, 64)):
+        idx = torch.full((nq, H, n_sel), -9, dtype=torch.int32, device="cuda")
+        g.select(dev(q), idx, n, n_first=first, n_last=last)
+        assert np.array_equal(host(idx), ref.select(c, q, n, n_sel, first, last)), (n_sel, first, last)
 
 
 def test_select_ties_and_odd_queries(ctx):
