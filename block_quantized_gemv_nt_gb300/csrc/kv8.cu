@@ -55,6 +55,14 @@ __device__ __forceinline__ uint32_t pack8(const float v[4]) {
   return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
+// (x & m) ^ b as one operation (written as two, the compiler keeps both constants as
+// immediates and spends two)
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t m, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "r"(m), "r"(b));
+  return r;
+}
+
 // Four bytes as two f16 pairs, exact.
 //  I8: bytes (0, 2) and (1, 3): q + 128 in the mantissa of 1024 + (q + 128), minus
 //  1152.  Masking, the sign bias and the exponent are one three-input operation.
@@ -63,7 +71,7 @@ template <int FMT>
 __device__ __forceinline__ void to_h2(uint32_t x, uint32_t& a, uint32_t& b) {
   if (FMT == NT_KV8_I8) {
     const __half2 bias = __half2half2(__ushort_as_half(0x6480));
-    const uint32_t even = (x & 0x00FF00FFu) ^ 0x64806480u, odd = ((x >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+    const uint32_t even = and_xor(x, 0x00FF00FFu, 0x64806480u), odd = and_xor(x >> 8, 0x00FF00FFu, 0x64806480u);
     const __half2 h0 = __hsub2(*reinterpret_cast<const __half2*>(&even), bias);
     const __half2 h1 = __hsub2(*reinterpret_cast<const __half2*>(&odd), bias);
     a = *reinterpret_cast<const uint32_t*>(&h0);
@@ -365,6 +373,24 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// a + b on two floats at once
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // hi and lo f16 parts of two values
 __device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -438,8 +464,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
 
   // first token of step st (tokens: nothing to do)
   const auto step_token = [&](int st) {
+    if (!SPARSE) return st < st1 ? st * kStep : tokens;
     if (st >= st1) return tokens;
-    if (!SPARSE) return st * kStep;
     const int b = __ldg(list + st / (kB / kStep));
     return b < 0 || b >= blocks_seen ? tokens : min(tokens, b * kB + st % (kB / kStep) * kStep);
   };
@@ -572,10 +598,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
         const float f = rscale[t] * kvs.x;
         float p[4 * U];
 #pragma unroll
-        for (int x = 0; x < 4 * U; ++x) {
-          float v = sc[t][x >> 1][0][x & 1] + sc[t][x >> 1][0][2 + (x & 1)];
-          if (CH == 2) v += sc[t][x >> 1][CH - 1][x & 1] + sc[t][x >> 1][CH - 1][2 + (x & 1)];
-          p[x] = v * f;
+        for (int x = 0; x < 2 * U; ++x) {
+          const float* v = sc[t][x][0];
+          float2 y = add2(make_float2(v[0], v[1]), make_float2(v[2], v[3]));
+          if (CH == 2) {
+            const float* z = sc[t][x][CH - 1];
+            y = add2(y, add2(make_float2(z[0], z[1]), make_float2(z[2], z[3])));
+          }
+          y = mul2(y, make_float2(f, f));
+          p[2 * x] = y.x;
+          p[2 * x + 1] = y.y;
         }
         if (t0 + kStep > fewest) {
           const int left = limit[t] - t0 - 4 * U * c;
@@ -599,18 +631,22 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
           }
           m[t] = mn;
         }
-        const float base = m[t] == -INFINITY ? 0.f : m[t] - kPTop;
-#pragma unroll
-        for (int x = 0; x < 4 * U; ++x) {
-          p[x] = ex2(p[x] - base);
-          l[t] += p[x];
-          p[x] *= vs;
-        }
+        const float base = m[t] == -INFINITY ? 0.f : kPTop - m[t];
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          split_h2(p[4 * u], p[4 * u + 1], pf[t][u].x, pf[t][u].y);
-          split_h2(p[4 * u + 2], p[4 * u + 3], pf[t][u].z, pf[t][u].w);
+          float2 y[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            y[x] = add2(make_float2(p[4 * u + 2 * x], p[4 * u + 2 * x + 1]), make_float2(base, base));
+            y[x] = make_float2(ex2(y[x].x), ex2(y[x].y));
+            sum = add2(sum, y[x]);
+            y[x] = mul2(y[x], make_float2(vs, vs));
+          }
+          split_h2(y[0].x, y[0].y, pf[t][u].x, pf[t][u].y);
+          split_h2(y[1].x, y[1].y, pf[t][u].z, pf[t][u].w);
         }
+        l[t] += sum.x + sum.y;
       }
     }
     if (t0 < tokens) {
@@ -663,9 +699,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
           for (int t = 0; t < R; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float2& x = o[t][4 * (w + h) + i];
-              x.x += acc[t][i][0] + acc[t][i][2];
-              x.y += acc[t][i][1] + acc[t][i][3];
+              const float* x = acc[t][i];
+              o[t][4 * (w + h) + i] =
+                  add2(o[t][4 * (w + h) + i], add2(make_float2(x[0], x[1]), make_float2(x[2], x[3])));
             }
         }
       }
