@@ -84,11 +84,10 @@ __device__ __forceinline__ void to_h2(uint32_t x, uint32_t& a, uint32_t& b) {
 // the byte of the first pair's second value (the other pair holds the other two)
 template <int FMT>
 constexpr int kPairStep = FMT == NT_KV8_I8 ? 2 : 1;
-// words of two rows -> two words whose to_h2 pairs are (row 0, row 1) of bytes 0, 1 and of bytes 2, 3
+// words of two rows -> a word whose to_h2 pairs are (row 0, row 1) of bytes 0 and 1 (half 0) or 2 and 3
 template <int FMT>
-__device__ __forceinline__ void interleave8(uint32_t r0, uint32_t r1, uint32_t& lo, uint32_t& hi) {
-  lo = __byte_perm(r0, r1, FMT == NT_KV8_I8 ? 0x5410 : 0x5140);
-  hi = __byte_perm(r0, r1, FMT == NT_KV8_I8 ? 0x7632 : 0x7362);
+__device__ __forceinline__ uint32_t interleave8(uint32_t r0, uint32_t r1, int half) {
+  return FMT == NT_KV8_I8 ? __byte_perm(r0, r1, half ? 0x7632 : 0x5410) : __byte_perm(r0, r1, half ? 0x7362 : 0x5140);
 }
 
 // four bytes -> values over the scale
@@ -329,6 +328,7 @@ struct AttnKv8Args {
   int n_sel;
   int n_qh, n_kvh, G, nq, S;
   int chunks;          // row chunks of 8 R rows: per KV head (dense), per query and KV head (sparse)
+  int inv_g;           // ceil(2^16 / G): r / G = r inv_g >> 16 for the rows (at most 256) of a call
   int64_t n_pos, kv_stride, nb;
   const int64_t* pos_dev;
   unsigned* err;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   constexpr int CH = U == 1 ? 2 : 1; // accumulators per score tile: at least four chains of MMAs
   extern __shared__ __align__(16) uint8_t sm8[];
   uint4* qa = reinterpret_cast<uint4*>(sm8 + L::q);
-  __shared__ float s_amax[ROWS];
+  __shared__ float s_amax[R * KS][8];  // by k-step and row
   __shared__ __align__(8) uint64_t bars[kAttnWarps][2];
   pdl_wait();
   pdl_trigger();
@@ -437,8 +437,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const int rows = min(ROWS, (SPARSE ? a.G : a.nq * a.G) - row0);
   const int n_pos = int(seen_positions(a));  // positions fit 30 bits
   // row r of this chunk: query and head
-  const auto query_of = [&](int r) { return SPARSE ? qi0 : (row0 + r) / a.G; };
-  const auto vec_of = [&](int r) { return int64_t(query_of(r)) * a.n_qh + g * a.G + (SPARSE ? row0 + r : (row0 + r) % a.G); };
+  const auto query_of = [&](int r) { return SPARSE ? qi0 : ((row0 + r) * a.inv_g) >> 16; };
+  const auto vec_of = [&](int r) {
+    const int qi = query_of(r);
+    return int64_t(qi) * a.n_qh + g * a.G + (SPARSE ? row0 + r : row0 + r - qi * a.G);
+  };
   const int tokens = n_pos + query_of(rows - 1);  // the last row sees the most
   const int steps = SPARSE ? a.n_sel * (kB / kStep) : (tokens + kStep - 1) / kStep;
   const int per = split_steps(steps, a.S);
@@ -499,35 +502,40 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   copy_v(t0);
   float2 kvs = scales(t0);
 
-  // q: each row scaled by a power of two to amax in [2^13, 2^14), split, laid out as fragments
-  for (int r = warp; r < ROWS; r += kAttnWarps) {
-    float m = 0.f;
-    if (r < rows) {
-      const float* qr = a.q + vec_of(r) * HD;
+  // q: each row scaled by a power of two to amax in [2^13, 2^14), split, laid out as
+  // fragments: warp w holds k-step w % KS of every row
+  constexpr int QI = (R * KS + kAttnWarps - 1) / kAttnWarps;  // fragments per thread
+  float4 qv[QI];
 #pragma unroll
-      for (int d = 0; d < HD; d += 32) m = fmaxf(m, fabsf(qr[d + lane]));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) s_amax[r] = m;
+  for (int i = 0; i < QI; ++i) {
+    const int f = warp + i * kAttnWarps, j = f % KS, r = f / KS * 8 + n;
+    qv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (f >= R * KS) continue;
+    if (r < rows) qv[i] = load4(a.q + vec_of(r) * HD + 64 * (j >> 2) + 16 * c + 4 * (j & 3));
+    float x = fmaxf(fmaxf(fabsf(qv[i].x), fabsf(qv[i].y)), fmaxf(fabsf(qv[i].z), fabsf(qv[i].w)));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    if (c == 0) s_amax[f][n] = x;
   }
   __syncthreads();
-  const auto row_exp = [&](int r) {  // q times 2^row_exp
-    const int e = 140 - int(__float_as_uint(s_amax[r]) >> 23);
-    return e > 100 ? 100 : e;
-  };
-  for (int i = tid; i < R * KS * 32; i += kAttnWarps * 32) {
-    const int ln = i & 31, j = (i >> 5) % KS, rt = (i >> 5) / KS;
-    const int r = rt * 8 + (ln >> 2);
-    const int d = 64 * (j >> 2) + 16 * (ln & 3) + 4 * (j & 3);
-    uint4 f = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows) {
-      const float4 x = load4(a.q + vec_of(r) * HD + d);
-      const float sc = __uint_as_float(uint32_t(row_exp(r) + 127) << 23);
-      split_h2(x.x * sc, (kPairStep<FMT> == 2 ? x.z : x.y) * sc, f.x, f.y);
-      split_h2((kPairStep<FMT> == 2 ? x.y : x.z) * sc, x.w * sc, f.z, f.w);
-    }
-    qa[i] = f;
+  int qe[R];  // q of row 8 t + n times 2^qe
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    float x = s_amax[t * KS][n];
+#pragma unroll
+    for (int j = 1; j < KS; ++j) x = fmaxf(x, s_amax[t * KS + j][n]);
+    qe[t] = min(100, 140 - int(__float_as_uint(x) >> 23));
+  }
+#pragma unroll
+  for (int i = 0; i < QI; ++i) {
+    const int f = warp + i * kAttnWarps;
+    if (f >= R * KS) continue;
+    const float sc = __uint_as_float(uint32_t((R == 1 || f < KS ? qe[0] : qe[R - 1]) + 127) << 23);
+    const float4 x = qv[i];
+    uint4 y;
+    split_h2(x.x * sc, (kPairStep<FMT> == 2 ? x.z : x.y) * sc, y.x, y.y);
+    split_h2((kPairStep<FMT> == 2 ? x.y : x.z) * sc, x.w * sc, y.z, y.w);
+    qa[f * 32 + lane] = y;
   }
   __syncthreads();
   float rscale[R];      // scores to the base-2 exponent
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   for (int t = 0; t < R; ++t) {
     const int r = t * 8 + n;
     // log2(e) / sqrt(HD)
-    rscale[t] = __uint_as_float(uint32_t(127 - row_exp(r)) << 23) * (1.44269504088896f * rsqrtf(float(HD)));
+    rscale[t] = __uint_as_float(uint32_t(127 - qe[t]) << 23) * (1.44269504088896f * rsqrtf(float(HD)));
     limit[t] = r < rows ? n_pos + query_of(r) : 0;
     m[t] = -INFINITY;
     l[t] = 0.f;
@@ -672,36 +680,30 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
             if (t0 + 4 * U * c + x >= tokens) vw[x][0] = vw[x][1] = 0u;
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float acc[R][4][4];
+        for (int h = 0; h < 4; ++h) {  // half (h % 2) of word h / 2: two channels
+          float acc[R][2][4];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            uint32_t y[2][2];
+            uint32_t b0[2], b1[2];
+            to_h2<FMT>(interleave8<FMT>(vw[4 * u][h >> 1], vw[4 * u + 1][h >> 1], h & 1), b0[0], b0[1]);
+            to_h2<FMT>(interleave8<FMT>(vw[4 * u + 2][h >> 1], vw[4 * u + 3][h >> 1], h & 1), b1[0], b1[1]);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) interleave8<FMT>(vw[4 * u + 2 * x][h], vw[4 * u + 2 * x + 1][h], y[x][0], y[x][1]);
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t b0[2], b1[2];
-              to_h2<FMT>(y[0][i], b0[0], b0[1]);
-              to_h2<FMT>(y[1][i], b1[0], b1[1]);
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int t = 0; t < R; ++t) {
-                  if (u == 0)
-                    mma16816_zero(acc[t][2 * i + e], pf[t][u], b0[e], b1[e]);
-                  else
-                    mma16816(acc[t][2 * i + e], pf[t][u], b0[e], b1[e]);
-                }
-            }
+              for (int t = 0; t < R; ++t) {
+                if (u == 0)
+                  mma16816_zero(acc[t][e], pf[t][u], b0[e], b1[e]);
+                else
+                  mma16816(acc[t][e], pf[t][u], b0[e], b1[e]);
+              }
           }
 #pragma unroll
           for (int t = 0; t < R; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* x = acc[t][i];
-              o[t][4 * (w + h) + i] =
-                  add2(o[t][4 * (w + h) + i], add2(make_float2(x[0], x[1]), make_float2(x[2], x[3])));
+            for (int e = 0; e < 2; ++e) {
+              const float* x = acc[t][e];
+              float2& y = o[t][4 * w + 2 * h + e];
+              y = add2(y, add2(make_float2(x[0], x[1]), make_float2(x[2], x[3])));
             }
         }
       }
@@ -731,32 +733,39 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   }
   __syncthreads();
   const bool whole = per >= steps;  // one split: the output itself
-  for (int i = tid; i < R * NT * 32; i += kAttnWarps * 32) {
-    const int ln = i & 31, nt = (i >> 5) % NT, r = (i >> 5) / NT * 8 + (ln >> 2), cc = ln & 3;
-    if (r >= rows) continue;
-    float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, mm[w * ROWS + r]);
-    float2 acc = make_float2(0.f, 0.f);
-    float sum = 0.f;
+  for (int t = 0; t < R; ++t) {
+    const int r = t * 8 + n;
+    if (r >= rows) continue;
+    float f[kAttnWarps], M = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
-      const float mw = mm[w * ROWS + r];
-      const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-      const float2 x = outs[size_t(w) * R * NT * 32 + i];
-      acc.x = fmaf(x.x, f, acc.x);
-      acc.y = fmaf(x.y, f, acc.y);
-      sum = fmaf(mll[w * ROWS + r], f, sum);
+      f[w] = mm[w * ROWS + r];
+      M = fmaxf(M, f[w]);
+    }
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      f[w] = f[w] == -INFINITY ? 0.f : ex2(f[w] - M);
+      sum = fmaf(mll[w * ROWS + r], f[w], sum);
     }
     const int64_t vec = vec_of(r);
-    if (whole) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      a.out[vec * HD + (HD / 8) * (2 * cc) + nt] = acc.x * inv;
-      a.out[vec * HD + (HD / 8) * (2 * cc + 1) + nt] = acc.y * inv;
-    } else {
-      *reinterpret_cast<float2*>(a.part + (vec * a.S + s) * HD + (nt * 4 + cc) * 2) = acc;
-      if (nt == 0 && cc == 0) a.ml[vec * a.S + s] = make_float2(M, sum);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int i = warp; i < NT; i += kAttnWarps) {
+      float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float2 x = outs[(size_t(w) * R * NT + t * NT + i) * 32 + lane];
+        acc.x = fmaf(x.x, f[w], acc.x);
+        acc.y = fmaf(x.y, f[w], acc.y);
+      }
+      if (whole) {
+        a.out[vec * HD + (HD / 8) * (2 * c) + i] = acc.x * inv;
+        a.out[vec * HD + (HD / 8) * (2 * c + 1) + i] = acc.y * inv;
+      } else {
+        *reinterpret_cast<float2*>(a.part + (vec * a.S + s) * HD + (i * 4 + c) * 2) = acc;
+      }
     }
+    if (!whole && warp == 0 && c == 0) a.ml[vec * a.S + s] = make_float2(M, sum);
   }
 }
 
@@ -1214,6 +1223,7 @@ nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, 
   a.n_qh = n_qh;
   a.n_kvh = kv.n_kvh;
   a.G = n_qh / kv.n_kvh;
+  a.inv_g = (65536 + a.G - 1) / a.G;
   a.nq = nq;
   a.n_pos = n_pos;
   a.kv_stride = kv.kv_stride;
