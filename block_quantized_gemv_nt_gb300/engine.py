@@ -80,51 +80,52 @@ class KV8Cache:
         self.desc = nt.nt_kv8(fmt, n_kvh, head_dim, kv_stride,
                               *[nt._ptr(buffers.get(n)) for n in ("k", "v", "kscale", "vscale", "kmin", "kmax")])
 
-    @staticmethod
-    def _fmt(t):
-        if t.dtype not in (torch.float32, torch.float16):
-            raise ValueError("rows must be float32 or float16")
-        return nt.F32 if t.dtype == torch.float32 else nt.F16
-
     def _rows(self, k, v, tok, head):
-        if (k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(2) != 1
-                or k.shape[head] != self.n_kvh or k.shape[2] != self.head_dim):
+        shape, stride, dtype = k.shape, k.stride(), k.dtype
+        if (len(shape) != 3 or shape != v.shape or dtype != v.dtype or stride != v.stride() or stride[2] != 1
+                or shape[head] != self.n_kvh or shape[2] != self.head_dim):
             raise ValueError("k and v: rows of n_kvh heads of head_dim channels, alike in layout")
-        return k.shape[tok], k.stride(tok), k.stride(head)
+        fmt = nt.F32 if dtype is torch.float32 else nt.F16 if dtype is torch.float16 else None
+        if fmt is None:
+            raise ValueError("rows must be float32 or float16")
+        return fmt, shape[tok], stride[tok], stride[head]
 
     def append(self, k, v, pos: int, pos_dev=None, stream=None):
         """Rows [n][n_kvh][head_dim] (fp32 or f16, any strides between rows and heads) to positions pos .."""
-        n, ts, hs = self._rows(k, v, 0, 1)
-        nt.nt_kv8_append(self.ctx, self.desc, self._fmt(k), k, v, n, ts, hs, pos, pos_dev, stream)
+        fmt, n, ts, hs = self._rows(k, v, 0, 1)
+        nt.nt_kv8_append(self.ctx, self.desc, fmt, k, v, n, ts, hs, pos, pos_dev, stream)
 
     def append_from_heads(self, k, v, pos: int, pos_dev=None, stream=None):
         """Rows [n_kvh][n][head_dim], the layout of an F16 cache (a slice of its positions), to positions pos .."""
-        n, ts, hs = self._rows(k, v, 1, 0)
-        nt.nt_kv8_append(self.ctx, self.desc, self._fmt(k), k, v, n, ts, hs, pos, pos_dev, stream)
+        fmt, n, ts, hs = self._rows(k, v, 1, 0)
+        nt.nt_kv8_append(self.ctx, self.desc, fmt, k, v, n, ts, hs, pos, pos_dev, stream)
 
     def read(self, pos0: int, k, v, stream=None):
         """Positions pos0 .. into k and v [n_kvh][n][head_dim] (fp32 or f16; rows of a head contiguous)."""
-        n, ts, hs = self._rows(k, v, 1, 0)
+        fmt, n, ts, hs = self._rows(k, v, 1, 0)
         if n > 1 and ts != self.head_dim:
             raise ValueError("the rows of a head must be contiguous")
-        nt.nt_kv8_read(self.ctx, self.desc, pos0, n, self._fmt(k), k, v, hs, stream)
+        nt.nt_kv8_read(self.ctx, self.desc, pos0, n, fmt, k, v, hs, stream)
 
-    def _queries(self, q):
-        if q.dim() != 3 or q.shape[2] != self.head_dim or q.dtype != torch.float32 or not q.is_contiguous():
-            raise ValueError("q and out: contiguous float32 [n_query][n_qh][head_dim]")
-        return q.shape[0], q.shape[1]
+    def _queries(self, q, out=None):
+        shape = q.shape
+        if len(shape) != 3 or shape[2] != self.head_dim or q.dtype is not torch.float32 or not q.is_contiguous():
+            raise ValueError("q: contiguous float32 [n_query][n_qh][head_dim]")
+        if out is not None and (out.shape != shape or out.dtype is not torch.float32 or not out.is_contiguous()):
+            raise ValueError("out: like q")
+        return shape[0], shape[1]
 
     def attend(self, q, out, n_pos: int, pos_dev=None, stream=None):
         """Attention of q [n_query][n_qh][head_dim] into out; query i sees n_pos + i positions."""
-        nq, n_qh = self._queries(q)
-        if self._queries(out) != (nq, n_qh):
-            raise ValueError("out: the shape of q")
+        nq, n_qh = self._queries(q, out)
         nt.nt_attn_kv8(self.ctx, q, self.desc, out, n_qh, n_pos, nq, pos_dev, stream)
 
     def _list(self, idx, nq):
-        if idx.dim() != 3 or idx.shape[:2] != (nq, self.n_kvh) or idx.dtype != torch.int32 or not idx.is_contiguous():
+        shape = idx.shape
+        if (len(shape) != 3 or shape[0] != nq or shape[1] != self.n_kvh or idx.dtype is not torch.int32
+                or not idx.is_contiguous()):
             raise ValueError("idx: contiguous int32 [n_query][n_kvh][n_sel]")
-        return idx.shape[2]
+        return shape[2]
 
     def select(self, q, idx, n_pos: int, n_first: int = 0, n_last: int = 1, pos_dev=None, stream=None):
         """The blocks each query reads into idx [n_query][n_kvh][n_sel]."""
@@ -134,9 +135,7 @@ class KV8Cache:
 
     def attend_blocks(self, q, out, n_pos: int, idx, pos_dev=None, stream=None):
         """Attention over the listed blocks only."""
-        nq, n_qh = self._queries(q)
-        if self._queries(out) != (nq, n_qh):
-            raise ValueError("out: the shape of q")
+        nq, n_qh = self._queries(q, out)
         nt.nt_attn_kv8_blocks(self.ctx, q, self.desc, out, n_qh, n_pos, nq, idx, self._list(idx, nq), pos_dev, stream)
 
 

@@ -168,12 +168,23 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's current stream of a device index as an integer, looked up once
+
+
 def _stream(stream, like=None):
+    global _raw_stream
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    dev = like.device if like is not None and hasattr(like, "device") else None
-    return torch.cuda.current_stream(dev).cuda_stream
+    if _raw_stream is None:
+        import torch
+        # the handle without a Stream object around it (about 2 us a call) where torch has that call
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    dev = getattr(like, "device", None)
+    if dev is None or dev.index is None:
+        import torch
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
 
 
 class Context:
