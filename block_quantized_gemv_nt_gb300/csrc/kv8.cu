@@ -9,6 +9,7 @@
 // and a block whose scale has to grow while it fills (a later token is larger)
 // loses nothing but the low bits that the larger scale cannot hold.
 #include <cuda_fp16.h>
+#include <algorithm>
 #include <cstdlib>
 
 #include "nt_internal.cuh"
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 // and V, the next V while it works on K; no barrier joins the warps.
 constexpr int kAttnWarps = 8;
 constexpr float kPTop = 8.f, kSlack = 6.f;
+constexpr int kMaxCluster = 16;
 
 struct AttnKv8Args {
   const float* q;
@@ -332,6 +334,7 @@ struct AttnKv8Args {
   int64_t n_pos, kv_stride, nb;
   const int64_t* pos_dev;
   unsigned* err;
+  int cluster;         // the splits of a head are one cluster and join in shared memory
   int stall;           // test hook: issue no bulk copies; the waits give up after kStallSpin tries
 };
 
@@ -400,14 +403,23 @@ __device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// shared memory: q fragments [R][HD / 16][32] x 16, (max, sum) [2][warps][8 R], each
-// warp's slots for one step's K and V; at the end, in place of the slots, the warps'
+// two floats into the shared memory of CTA `rank` of this cluster, at this CTA's address `at`
+__device__ __forceinline__ void st_cluster(uint32_t at, int rank, float2 v) {
+  uint32_t to;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// shared memory: q fragments [R][HD / 16][32] x 16, (max, sum) [2][warps][8 R], what
+// the other CTAs of a cluster send, each warp's slots for one step's K and V; at the end, in place of the slots, the warps'
 // outputs [warps][R][HD / 8][32] x 8
 template <int HD, int R, int U>
 struct AttnKv8Smem {
   static constexpr size_t q = 0;
   static constexpr size_t ml = q + size_t(R) * (HD / 16) * 512;
-  static constexpr size_t ring = ml + size_t(2) * kAttnWarps * 8 * R * 4;
+  static constexpr size_t push = ml + size_t(2) * kAttnWarps * 8 * R * 4;           // from the cluster: outputs
+  static constexpr size_t push_ml = push + size_t(R) * (HD / 8) * 256;               // and (max, sum) [splits][8 R]
+  static constexpr size_t ring = push_ml + size_t(kMaxCluster) * 8 * R * 8;
   static constexpr size_t group = size_t(4 * U) * HD + 32;           // V rows of one c
   static constexpr size_t stage = size_t(16 * U) * HD + 4 * group;   // K, then V
   static constexpr size_t outs = size_t(R) * (HD / 8) * 256;         // one warp's outputs
@@ -446,7 +458,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const int steps = SPARSE ? a.n_sel * (kB / kStep) : (tokens + kStep - 1) / kStep;
   const int per = split_steps(steps, a.S);
   const int st0 = s * per, st1 = min(steps, st0 + per);
-  if (st0 >= st1 && s > 0) return;
+  if (a.cluster)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA's shared memory may be written
+  else if (st0 >= st1 && s > 0)
+    return;
 
   const uint8_t* kg = a.k + int64_t(g) * a.kv_stride * HD;
   const uint8_t* vg = a.v + int64_t(g) * a.kv_stride * HD;
@@ -732,11 +747,15 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     for (int i = 0; i < NT; ++i) outs[(size_t(warp) * R * NT + t * NT + i) * 32 + lane] = o[t][i];
   }
   __syncthreads();
-  const bool whole = per >= steps;  // one split: the output itself
+  const bool whole = a.S == 1 || (per >= steps && !a.cluster);  // one split: the output itself
+  // of the R NT fragment tiles, `own` belong to each CTA of a cluster
+  const int own = a.cluster ? R * NT / a.S : 1;
+  const uint32_t push = smem_u32(sm8 + L::push), push_ml = smem_u32(sm8 + L::push_ml);
+  if (a.cluster) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     const int r = t * 8 + n;
-    if (r >= rows) continue;
+    if (r >= rows && !a.cluster) continue;
     float f[kAttnWarps], M = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
@@ -758,14 +777,45 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
         acc.x = fmaf(x.x, f[w], acc.x);
         acc.y = fmaf(x.y, f[w], acc.y);
       }
-      if (whole) {
+      if (a.cluster) {
+        const int tile = t * NT + i;
+        st_cluster(push + ((s * own + tile % own) * 32 + lane) * 8, tile / own, acc);
+      } else if (whole) {
         a.out[vec * HD + (HD / 8) * (2 * c) + i] = acc.x * inv;
         a.out[vec * HD + (HD / 8) * (2 * c + 1) + i] = acc.y * inv;
       } else {
         *reinterpret_cast<float2*>(a.part + (vec * a.S + s) * HD + (i * 4 + c) * 2) = acc;
       }
     }
-    if (!whole && warp == 0 && c == 0) a.ml[vec * a.S + s] = make_float2(M, sum);
+    if (a.cluster) {
+      for (int d = c + 4 * warp; d < a.S; d += 4 * kAttnWarps)
+        st_cluster(push_ml + (s * ROWS + r) * 8, d, make_float2(M, sum));
+    } else if (!whole && warp == 0 && c == 0) {
+      a.ml[vec * a.S + s] = make_float2(M, sum);
+    }
+  }
+  if (!a.cluster) return;
+  // ---- merge the cluster's splits: this CTA's tiles of every split have arrived
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const float2* pushed = reinterpret_cast<const float2*>(sm8 + L::push);
+  const float2* pushed_ml = reinterpret_cast<const float2*>(sm8 + L::push_ml);
+  for (int k = warp; k < own; k += kAttnWarps) {
+    const int tile = s * own + k, r = tile / NT * 8 + n, i = tile % NT;
+    if (r >= rows) continue;
+    float M = -INFINITY, sum = 0.f;
+    for (int x = 0; x < a.S; ++x) M = fmaxf(M, pushed_ml[x * ROWS + r].x);
+    float2 acc = make_float2(0.f, 0.f);
+    for (int x = 0; x < a.S; ++x) {
+      const float2 y = pushed_ml[x * ROWS + r], z = pushed[(x * own + k) * 32 + lane];
+      const float f = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+      sum = fmaf(y.y, f, sum);
+      acc.x = fmaf(z.x, f, acc.x);
+      acc.y = fmaf(z.y, f, acc.y);
+    }
+    const int64_t vec = vec_of(r);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    a.out[vec * HD + (HD / 8) * (2 * c) + i] = acc.x * inv;
+    a.out[vec * HD + (HD / 8) * (2 * c + 1) + i] = acc.y * inv;
   }
 }
 
@@ -864,8 +914,6 @@ AttnKv8Variant attn_kv8_for(int fmt, int hd, int R, int U) {
 // added first and a block costs 2 HD products whatever the group size.  With q as
 // 12-bit integers every sum is a whole number below 2^31: the scores, and with
 // them the choice, do not depend on the order of additions.
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 1024;
 constexpr uint32_t kForced = 0xFFFFFFFFu;  // key of a block that is taken whatever its score
 
@@ -898,148 +946,192 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// blocks a warp scores per pass: HD / 8 lanes share a block, four blocks at a time each
+template <int HD>
+constexpr int kScorePass = 4 * 32 / (HD / 8);
+
 // The keys of one head's blocks for one query, by CTA `rank` of `ranks`, each to
-// put(block, key).  HD / 16 lanes share a block.
-template <int HD, typename Put>
+// put(block, key).  A lane holds 8 channels of a block; four blocks are loaded and
+// summed together: their lanes' sums are exchanged so that lane j (mod 4) of a group
+// ends with block j, in 5 or 4 shuffles for the four.
+template <int NT, int HD, typename Put>
 __device__ __forceinline__ void score_blocks(const SelectArgs& a, int g, int qi, int blocks, int rank, int ranks,
                                              Put put) {
-  constexpr int LB = HD / 16;            // lanes per block, 16 channels each
-  constexpr int BW = 32 / LB;            // blocks per warp
-  __shared__ float red[kSelWarps];
+  constexpr int LB = HD / 8, BW = 32 / LB;
+  constexpr int W = NT / 32;
+  __shared__ float red[W];
   __shared__ int sums[2][HD];            // group sums of max(qi, 0) and min(qi, 0)
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = lane % LB;
-  const int stride = ranks * kSelWarps * BW;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = lane % LB, sub = lane / LB;
+  const int stride = ranks * W * kScorePass<HD>;
   const int64_t head = int64_t(g) * a.nb;
-  int b = (rank * kSelWarps + warp) * BW + lane / LB;
-  uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-  float ks = 0.f;
-  const auto load = [&](int at) {  // this warp's bounds, in flight while q is prepared or the last ones are summed
-    if (at >= blocks) return;
-    hi = *reinterpret_cast<const uint4*>(a.kmax + (head + at) * HD + part * 16);
-    lo = *reinterpret_cast<const uint4*>(a.kmin + (head + at) * HD + part * 16);
-    ks = a.ks[head + at];
+  const int8_t* pmax = a.kmax + head * HD + part * 8;
+  const int8_t* pmin = a.kmin + head * HD + part * 8;
+  int b0 = (rank * W + warp) * kScorePass<HD>;  // the warp's blocks b0 + j BW + sub, j < 4
+  uint2 hi[4], lo[4];
+  float ks;
+  const auto load = [&](int at) {  // in flight while q is prepared or the last four are summed
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t b = min(at + j * BW + sub, blocks - 1);
+      hi[j] = *reinterpret_cast<const uint2*>(pmax + b * HD);
+      lo[j] = *reinterpret_cast<const uint2*>(pmin + b * HD);
+    }
+    ks = a.ks[head + min(at + (part & 3) * BW + sub, blocks - 1)];
   };
-  load(b);
+  load(b0);
   const float* q = a.q + (int64_t(qi) * a.n_qh + g * a.G) * HD;
-  constexpr int QR = 16 * HD / kSelThreads;  // q values per thread, at most
+  constexpr int QR = 16 * HD / NT;  // q values per thread, at most
   float x[QR];
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < QR; ++i) {
-    const int at = tid + i * kSelThreads;
+    const int at = tid + i * NT;
     x[i] = at < a.G * HD ? q[at] : 0.f;
     const float v = fabsf(x[i]);
     if (v <= 3.402823466e38f) m = fmaxf(m, v);
   }
-  if (tid < 2 * HD) (&sums[0][0])[tid] = 0;
+  for (int i = tid; i < 2 * HD; i += NT) (&sums[0][0])[i] = 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red[warp] = m;
   __syncthreads();
-  m = red[lane];
+  m = red[lane % W];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float inv = pow2_inv(pow2_scale<10, 0x7FE000u>(m));  // 2047 = 1.99902 * 2^10
 #pragma unroll
   for (int i = 0; i < QR; ++i) {
     const int v = x[i] != x[i] ? 0 : __float2int_rn(fminf(fmaxf(x[i] * inv, -2047.f), 2047.f));
-    if (v) atomicAdd(&sums[v < 0][(tid + i * kSelThreads) % HD], v);
+    if (v) atomicAdd(&sums[v < 0][(tid + i * NT) % HD], v);
   }
   __syncthreads();
-  int p2[8], n2[8];  // pairs of 16-bit sums (16 heads of 2047 fit)
+  int p2[4], n2[4];  // pairs of 16-bit sums (16 heads of 2047 fit)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int d = part * 16 + 2 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int d = part * 8 + 2 * i;
     p2[i] = (sums[0][d] & 0xFFFF) | (sums[0][d + 1] << 16);
     n2[i] = (sums[1][d] & 0xFFFF) | (sums[1][d + 1] << 16);
   }
-  for (int b0 = b - lane / LB; b0 < blocks; b0 += stride, b += stride) {
-    const int hw[4] = {int(hi.x), int(hi.y), int(hi.z), int(hi.w)}, lw[4] = {int(lo.x), int(lo.y), int(lo.z), int(lo.w)};
-    const float t = ks;
-    load(b + stride);
-    int acc = 0;
+  for (; b0 < blocks; b0 += stride) {
+    int v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc = __dp2a_lo(p2[2 * i], hw[i], acc);
-      acc = __dp2a_hi(p2[2 * i + 1], hw[i], acc);
-      acc = __dp2a_lo(n2[2 * i], lw[i], acc);
-      acc = __dp2a_hi(n2[2 * i + 1], lw[i], acc);
+    for (int j = 0; j < 4; ++j) {
+      int acc = __dp2a_lo(p2[0], int(hi[j].x), 0);
+      acc = __dp2a_hi(p2[1], int(hi[j].x), acc);
+      acc = __dp2a_lo(p2[2], int(hi[j].y), acc);
+      acc = __dp2a_hi(p2[3], int(hi[j].y), acc);
+      acc = __dp2a_lo(n2[0], int(lo[j].x), acc);
+      acc = __dp2a_hi(n2[1], int(lo[j].x), acc);
+      acc = __dp2a_lo(n2[2], int(lo[j].y), acc);
+      v[j] = __dp2a_hi(n2[3], int(lo[j].y), acc);
     }
+    const float t = ks;
+    load(b0 + stride);
+    // odd lanes keep blocks 1 and 3, then lanes with bit 1 the upper of the two
+    const bool o1 = part & 1, o2 = part & 2;
+    const int k0 = (o1 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, o1 ? v[0] : v[1], 1);
+    const int k1 = (o1 ? v[3] : v[2]) + __shfl_xor_sync(0xffffffffu, o1 ? v[2] : v[3], 1);
+    int acc = (o2 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, o2 ? k0 : k1, 2);
 #pragma unroll
-    for (int o = LB / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (b < blocks && part == 0)
+    for (int o = 4; o < LB; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    const int b = b0 + (part & 3) * BW + sub;
+    if (b < blocks && part < 4)
       put(b, b < a.n_first || b >= blocks - a.n_last ? kForced : order_key(__int2float_rn(acc) * t));
   }
 }
 
 // The n_sel largest of `blocks` keys, as ascending indices: radix rounds of up to
 // ten bits below the keys' common prefix, ending as soon as the chosen bin is taken
-// whole; then one scan in index order (thread t holds blocks t chunk .. ; chunk odd,
-// so that the threads of a warp read different banks).  key(b): the key of block b.
-template <typename Key>
-__device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, int32_t* idx, Key key) {
-  __shared__ int hist[kSelBins];
-  __shared__ int wsum[kSelWarps];
-  __shared__ unsigned long long wscan[kSelWarps];
-  __shared__ uint32_t wmin[kSelWarps], wmax[kSelWarps];
-  __shared__ int s_bin, s_above, s_count;
+// whole; then one scan in index order.  Thread t holds blocks t K .. t K + K - 1 in
+// registers (K odd, so that the threads of a warp read different banks), or re-reads
+// them every time (K = 0).  key(b): the key of block b.
+template <int NT>
+struct SelShared {
+  unsigned long long wscan[NT / 32];
+  int hist[kSelBins];
+  int wsum[NT / 32];
+  uint32_t wmin[NT / 32], wmax[NT / 32];
+  int bin, above, count;
+};
+template <int NT, int K, typename Key>
+__device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, int32_t* idx, SelShared<NT>& sh, Key key) {
+  constexpr int W = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunk = ((blocks + kSelThreads - 1) / kSelThreads) | 1;
-  const int i0 = min(blocks, tid * chunk), i1 = min(blocks, i0 + chunk);
-  int need = a.n_sel - a.n_first - a.n_last;
-  uint32_t mn = kForced, mx = 0u;
-  for (int b = i0; b < i1; ++b) {
-    const uint32_t k = key(b);
-    if (k != kForced) {
-      mn = min(mn, k);
-      mx = max(mx, k);
+  const int chunk = K ? K : ((blocks + NT - 1) / NT) | 1;
+  const int i0 = min(blocks, tid * chunk), have = min(blocks - i0, chunk);
+  uint32_t own[K ? K : 1];
+#pragma unroll
+  for (int j = 0; j < K; ++j) own[j] = j < have ? key(i0 + j) : 0u;
+  const auto each = [&](auto fn) {
+    if (K) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (j < have) fn(i0 + j, own[j]);
+    } else {
+      for (int j = 0; j < have; ++j) fn(i0 + j, key(i0 + j));
     }
-  }
-  mn = __reduce_min_sync(0xffffffffu, mn);
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if (lane == 0) {
-    wmin[warp] = mn;
-    wmax[warp] = mx;
-  }
-  __syncthreads();
-  mn = __reduce_min_sync(0xffffffffu, wmin[lane]);
-  mx = __reduce_max_sync(0xffffffffu, wmax[lane]);
+  };
+  int need = a.n_sel - a.n_first - a.n_last;
   uint32_t cut = kForced;  // keys above it are taken, and the first `need` at it
   if (need > 0) {
+    uint32_t mn = kForced, mx = 0u;
+    each([&](int, uint32_t k) {
+      if (k != kForced) {
+        mn = min(mn, k);
+        mx = max(mx, k);
+      }
+    });
+    mn = __reduce_min_sync(0xffffffffu, mn);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (lane == 0) {
+      sh.wmin[warp] = mn;
+      sh.wmax[warp] = mx;
+    }
+    for (int i = tid; i < kSelBins; i += NT) sh.hist[i] = 0;
+    __syncthreads();
+    mn = __reduce_min_sync(0xffffffffu, sh.wmin[lane % W]);
+    mx = __reduce_max_sync(0xffffffffu, sh.wmax[lane % W]);
     int bits = mx == mn ? 0 : 32 - __clz(mx ^ mn);
     cut = bits == 32 ? 0u : (mx >> bits) << bits;
     while (bits > 0) {
       const int dig = min(10, bits), shift = bits - dig;
-      hist[tid] = 0;
-      __syncthreads();
-      for (int b = i0; b < i1; ++b) {
-        const uint32_t k = key(b);
+      each([&](int, uint32_t k) {
         if (k != kForced && (bits == 32 || (k >> bits) == (cut >> bits)))
-          atomicAdd(&hist[(k >> shift) & ((1u << dig) - 1u)], 1);
-      }
+          atomicAdd(&sh.hist[(k >> shift) & ((1u << dig) - 1u)], 1);
+      });
       __syncthreads();
-      const int bin = kSelBins - 1 - tid;  // thread 0 holds the highest bin
-      const int h = hist[bin];
-      int incl = h;
+      // thread 0 holds the highest bins
+      constexpr int HB = kSelBins / NT;
+      int h[HB], sum = 0;
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        h[j] = sh.hist[kSelBins - 1 - tid * HB - j];
+        sum += h[j];
+      }
+      int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int t = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += t;
       }
-      if (lane == 31) wsum[warp] = incl;
+      if (lane == 31) sh.wsum[warp] = incl;
       __syncthreads();
-      const int below = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0);
-      incl += below;
-      if (incl - h < need && incl >= need) {
-        s_bin = bin;
-        s_above = incl - h;
-        s_count = h;
+      int before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.wsum[lane % W] : 0) + incl - sum;
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        if (before < need && before + h[j] >= need) {
+          sh.bin = kSelBins - 1 - tid * HB - j;
+          sh.above = before;
+          sh.count = h[j];
+        }
+        before += h[j];
+        sh.hist[kSelBins - 1 - tid * HB - j] = 0;  // for the next round
       }
       __syncthreads();
-      cut |= uint32_t(s_bin) << shift;
-      need -= s_above;
+      cut |= uint32_t(sh.bin) << shift;
+      need -= sh.above;
       bits = shift;
-      if (s_count == need) {  // the whole bin: every key from here up (never all keys: n_sel < blocks)
+      if (sh.count == need) {  // the whole bin: every key from here up (never all keys: n_sel < blocks)
         cut -= 1u;
         need = 0;
         break;
@@ -1047,25 +1139,21 @@ __device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, i
     }
   }
   unsigned long long cnt = 0;  // blocks taken above the cut, and (high half) blocks at it
-  for (int b = i0; b < i1; ++b) {
-    const uint32_t k = key(b);
-    cnt += k == kForced || k > cut ? 1ull : (k == cut ? 1ull << 32 : 0ull);
-  }
+  each([&](int, uint32_t k) { cnt += k == kForced || k > cut ? 1ull : (k == cut ? 1ull << 32 : 0ull); });
   unsigned long long incl = cnt;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
-  if (lane == 31) wscan[warp] = incl;
+  if (lane == 31) sh.wscan[warp] = incl;
   __syncthreads();
-  unsigned long long base = lane < warp ? wscan[lane] : 0ull;
+  unsigned long long base = lane < warp ? sh.wscan[lane % W] : 0ull;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
   base += incl - cnt;
   int above = int(base & 0xFFFFFFFFull), ties = int(base >> 32);
-  for (int b = i0; b < i1; ++b) {
-    const uint32_t k = key(b);
+  each([&](int b, uint32_t k) {
     if (k == kForced || k > cut) {
       idx[above + min(ties, need)] = b;
       ++above;
@@ -1073,15 +1161,16 @@ __device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, i
       if (ties < need) idx[above + ties] = b;
       ++ties;
     }
-  }
+  });
 }
 
 // One cluster per (KV head, query): its CTAs score the head's blocks and put the
 // keys into the first CTA's shared memory, which selects.  Bound by the latency of
 // its phases for short sequences and by reading the bounds for long ones.
-template <int HD>
-__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const SelectArgs a) {
+template <int NT, int HD>
+__global__ void __launch_bounds__(NT) kv8_select_kernel(const SelectArgs a) {
   extern __shared__ uint32_t keys[];
+  __shared__ SelShared<NT> sh;
   pdl_wait();
   pdl_trigger();
   const int ranks = gridDim.x, rank = blockIdx.x;  // the grid is one cluster wide
@@ -1089,50 +1178,60 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const SelectArg
   const int blocks = int(kv8_blocks(seen_positions(a) + qi));
   int32_t* idx = a.idx + (int64_t(qi) * a.n_kvh + g) * a.n_sel;
   if (blocks <= a.n_sel) {  // uniform over the cluster
-    for (int i = rank * kSelThreads + threadIdx.x; i < a.n_sel; i += ranks * kSelThreads) idx[i] = i < blocks ? i : -1;
+    for (int i = rank * NT + threadIdx.x; i < a.n_sel; i += ranks * NT) idx[i] = i < blocks ? i : -1;
     return;
   }
   if (ranks == 1) {
-    score_blocks<HD>(a, g, qi, blocks, 0, 1, [&](int b, uint32_t k) { keys[b] = k; });
+    score_blocks<NT, HD>(a, g, qi, blocks, 0, 1, [&](int b, uint32_t k) { keys[b] = k; });
     __syncthreads();
   } else {
     uint32_t first;
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(first) : "r"(smem_u32(keys)));
     // no CTA writes into the first one before it runs
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    score_blocks<HD>(a, g, qi, blocks, rank, ranks, [&](int b, uint32_t k) {
+    score_blocks<NT, HD>(a, g, qi, blocks, rank, ranks, [&](int b, uint32_t k) {
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first + 4u * uint32_t(b)), "r"(k) : "memory");
     });
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank) return;
   }
-  select_blocks(a, blocks, idx, [&](int b) { return keys[b]; });
+  const auto key = [&](int b) { return keys[b]; };
+  if (blocks <= NT) select_blocks<NT, 1>(a, blocks, idx, sh, key);
+  else if (blocks <= 5 * NT) select_blocks<NT, 5>(a, blocks, idx, sh, key);
+  else if (blocks <= 17 * NT) select_blocks<NT, 17>(a, blocks, idx, sh, key);
+  else select_blocks<NT, 0>(a, blocks, idx, sh, key);
 }
 
 // the same in two launches with the keys in scratch, for heads whose keys do not
 // fit in shared memory
-template <int HD>
-__global__ void __launch_bounds__(kSelThreads) kv8_score_kernel(const SelectArgs a) {
+template <int NT, int HD>
+__global__ void __launch_bounds__(NT) kv8_score_kernel(const SelectArgs a) {
   pdl_wait();
   pdl_trigger();
   const int g = blockIdx.y, qi = blockIdx.z;
   const int blocks = int(kv8_blocks(seen_positions(a) + qi));
+  if (blocks == 0) return;
   uint32_t* out = a.keys + (int64_t(qi) * a.n_kvh + g) * a.nb;
-  score_blocks<HD>(a, g, qi, blocks, blockIdx.x, gridDim.x, [&](int b, uint32_t k) { out[b] = k; });
+  score_blocks<NT, HD>(a, g, qi, blocks, blockIdx.x, gridDim.x, [&](int b, uint32_t k) { out[b] = k; });
 }
-__global__ void __launch_bounds__(kSelThreads) kv8_select_scratch_kernel(const SelectArgs a) {
+template <int NT>
+__global__ void __launch_bounds__(NT) kv8_select_scratch_kernel(const SelectArgs a) {
+  __shared__ SelShared<NT> sh;
   pdl_wait();
   pdl_trigger();
   const int g = blockIdx.y, qi = blockIdx.z;
   const int blocks = int(kv8_blocks(seen_positions(a) + qi));
   int32_t* idx = a.idx + (int64_t(qi) * a.n_kvh + g) * a.n_sel;
   if (blocks <= a.n_sel) {
-    for (int i = threadIdx.x; i < a.n_sel; i += kSelThreads) idx[i] = i < blocks ? i : -1;
+    for (int i = threadIdx.x; i < a.n_sel; i += NT) idx[i] = i < blocks ? i : -1;
     return;
   }
   const uint32_t* keys = a.keys + (int64_t(qi) * a.n_kvh + g) * a.nb;
-  select_blocks(a, blocks, idx, [&](int b) { return __ldcg(keys + b); });
+  select_blocks<NT, 0>(a, blocks, idx, sh, [&](int b) { return __ldcg(keys + b); });
 }
+
+constexpr int kSelWide = 1024, kSelNarrow = 256;  // threads of a selection
+constexpr int kSelNarrowBlocks = 256;             // most blocks of the narrow one
 
 }  // namespace
 
@@ -1208,6 +1307,34 @@ static int kv8_u2_tokens() {
   return e ? atoi(e) : 32;
 }
 
+static int64_t kv8_cluster_tokens() {
+  const char* e = getenv("KV8_CL");
+  return e ? atoi(e) : 512;
+}
+
+// launch_k with a cluster shape (1, 1, 1: none)
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(const Ctx* c, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                           dim3 cluster, Args&&... args) {
+  if (cluster.x * cluster.y * cluster.z == 1) return launch_k(c, kernel, grid, block, smem, st, std::forward<Args>(args)...);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster.x;
+  attr[0].val.clusterDim.y = cluster.y;
+  attr[0].val.clusterDim.z = cluster.z;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = (c->pdl && !c->pdl_hold) ? 2 : 1;
+  c->pdl_hold = false;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, int n_qh, int64_t n_pos, int nq,
                           const int64_t* pos_dev, const int32_t* idx, int n_sel, char* scratch, size_t scratch_bytes,
                           cudaStream_t st) {
@@ -1241,24 +1368,34 @@ nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, 
   int64_t S = int64_t(c->num_sms) * (R == 1 ? 2 : 1) / (int64_t(kv.n_kvh) * z);
   if (S > kMaxSplits) S = kMaxSplits;
   if (S < 1) S = 1;
-  const int U = R == 2 || most >= S * kAttnWarps * kv8_u2_tokens() ? 2 : 1;
-  const int64_t steps = (most + 16 * U - 1) / (16 * U);
-  const int64_t useful = (steps + kAttnWarps - 1) / kAttnWarps;
+  int U = R == 2 || most >= S * kAttnWarps * kv8_u2_tokens() ? 2 : 1;
+  const int64_t useful = (most + 16 * kAttnWarps * U - 1) / (16 * kAttnWarps * U);
   const size_t vecs = size_t(n_qh) * nq, row = vecs * (kv.head_dim * 4 + 8);
-  if (S > useful) S = useful;
-  if (S * int64_t(row) > int64_t(scratch_bytes)) S = int64_t(scratch_bytes / row);
-  if (S < 1) S = 1;
+  // short sequences: the splits of a head as one cluster, which saves the second launch
+  int64_t C = 1;
+  const int64_t widest = std::min<int64_t>(std::min(kMaxCluster, R * kv.head_dim / 8), S);
+  while (C < (most + 16 * kAttnWarps * R - 1) / (16 * kAttnWarps * R) && 2 * C <= widest) C *= 2;
+  a.cluster = C > 1 && most <= kv8_cluster_tokens() * C;
+  if (a.cluster) {
+    S = C;
+    U = R == 2 || most >= S * kAttnWarps * kv8_u2_tokens() ? 2 : 1;
+  } else {
+    if (S > useful) S = useful;
+    if (S * int64_t(row) > int64_t(scratch_bytes)) S = int64_t(scratch_bytes / row);
+    if (S < 1) S = 1;
+  }
   a.S = int(S);
   a.part = reinterpret_cast<float*>(scratch);
   a.ml = reinterpret_cast<float2*>(scratch + vecs * S * kv.head_dim * 4);
   a.stall = take_stall(st);
   const AttnKv8Variant kern = sparse ? attn_kv8_for<true>(kv.fmt, kv.head_dim, R, U)
                                      : attn_kv8_for<false>(kv.fmt, kv.head_dim, R, U);
-  nt_status s = cuda_check(c, launch_k(c, kern.kernel, dim3(kv.n_kvh, a.S, z), dim3(kAttnWarps * 32), kern.smem, st, a),
+  nt_status s = cuda_check(c, launch_cluster(c, kern.kernel, dim3(kv.n_kvh, a.S, z), dim3(kAttnWarps * 32), kern.smem,
+                                             st, dim3(1, a.cluster ? a.S : 1, 1), a),
                            "8-bit attention launch");
-  if (s || a.S == 1) return s;  // one split wrote the output
-  using C = void (*)(AttnKv8Args, int, int);
-  C comb = kv.head_dim == 128 ? (sparse ? attn_kv8_combine_kernel<128, true> : attn_kv8_combine_kernel<128, false>)
+  if (s || a.S == 1 || a.cluster) return s;  // the output is written
+  using Combine = void (*)(AttnKv8Args, int, int);
+  Combine comb = kv.head_dim == 128 ? (sparse ? attn_kv8_combine_kernel<128, true> : attn_kv8_combine_kernel<128, false>)
                               : (sparse ? attn_kv8_combine_kernel<64, true> : attn_kv8_combine_kernel<64, false>);
   return cuda_check(c, launch_k(c, comb, dim3(n_qh, nq), dim3(kv.head_dim), 0, st, a, 8 * R, 16 * U),
                     "8-bit attention combine launch");
@@ -1300,42 +1437,35 @@ nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, 
   a.pos_dev = pos_dev;
   a.err = c->err_flag;
   const int64_t blocks = pos_dev ? a.nb : kv8_blocks(n_pos + nq - 1);
-  const int64_t pass = int64_t(kSelWarps) * 32 / (kv.head_dim / 16);  // blocks a CTA scores at a time
+  const bool h128 = kv.head_dim == 128;
+  const int64_t pass = int64_t(kSelWide / 32) * (h128 ? kScorePass<128> : kScorePass<64>);  // blocks a CTA scores at a time
   const int64_t groups = int64_t(kv.n_kvh) * nq;
+  if (blocks <= kSelNarrowBlocks)
+    return cuda_check(c, launch_k(c, h128 ? kv8_select_kernel<kSelNarrow, 128> : kv8_select_kernel<kSelNarrow, 64>,
+                                  dim3(1, kv.n_kvh, nq), dim3(kSelNarrow), size_t(blocks) * sizeof(uint32_t), st, a),
+                      "block select launch");
   if (kv8_select_fits(c, blocks)) {
     // CTAs per cluster: a pass of work for each, and the grid within the SMs
     int ranks = 1;
-    while (ranks < 16 && ranks * pass < blocks && 2 * ranks * groups <= c->num_sms) ranks *= 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ranks, kv.n_kvh, nq);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = size_t(blocks) * sizeof(uint32_t);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = c->pdl && !c->pdl_hold ? 2 : 1;
-    c->pdl_hold = false;
-    return cuda_check(c, cudaLaunchKernelEx(&cfg, kv.head_dim == 128 ? kv8_select_kernel<128> : kv8_select_kernel<64>, a),
+    while (ranks < kMaxCluster && ranks * pass < blocks && 2 * ranks * groups <= c->num_sms) ranks *= 2;
+    return cuda_check(c, launch_cluster(c, h128 ? kv8_select_kernel<kSelWide, 128> : kv8_select_kernel<kSelWide, 64>,
+                                        dim3(ranks, kv.n_kvh, nq), dim3(kSelWide), size_t(blocks) * sizeof(uint32_t),
+                                        st, dim3(ranks, 1, 1), a),
                       "block select launch");
   }
   int64_t gx = (blocks + pass - 1) / pass;
   const int64_t fill = (int64_t(c->num_sms) * 2 + groups - 1) / groups;
   gx = gx > fill ? fill : gx;
-  nt_status s = cuda_check(c, launch_k(c, kv.head_dim == 128 ? kv8_score_kernel<128> : kv8_score_kernel<64>,
-                                       dim3(unsigned(gx), kv.n_kvh, nq), dim3(kSelThreads), 0, st, a),
+  nt_status s = cuda_check(c, launch_k(c, h128 ? kv8_score_kernel<kSelWide, 128> : kv8_score_kernel<kSelWide, 64>,
+                                       dim3(unsigned(gx), kv.n_kvh, nq), dim3(kSelWide), 0, st, a),
                            "block score launch");
   if (s) return s;
-  return cuda_check(c, launch_k(c, kv8_select_scratch_kernel, dim3(1, kv.n_kvh, nq), dim3(kSelThreads), 0, st, a),
+  return cuda_check(c, launch_k(c, kv8_select_scratch_kernel<kSelWide>, dim3(1, kv.n_kvh, nq), dim3(kSelWide), 0, st, a),
                     "block select launch");
 }
 
 nt_status configure_kv8(Ctx* c) {
-  for (const auto k : {kv8_select_kernel<64>, kv8_select_kernel<128>}) {
+  for (const auto k : {kv8_select_kernel<kSelWide, 64>, kv8_select_kernel<kSelWide, 128>}) {
     nt_status s = cuda_check(c, cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      int(c->smem_optin - kSelStatic)),
                              "block select shared-memory attribute");
@@ -1351,6 +1481,9 @@ nt_status configure_kv8(Ctx* c) {
         nt_status s = cuda_check(
             c, cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.smem)),
             "8-bit attention shared-memory attribute");
+        if (!s)
+          s = cuda_check(c, cudaFuncSetAttribute(k.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
+                         "8-bit attention cluster attribute");
         if (s) return s;
       }
   return NT_OK;
