@@ -529,9 +529,9 @@ nt_status nt_kv8_append(nt_ctx* ctx, const nt_kv8* kv, int src_fmt, const void* 
              (long long)kv->kv_stride);
   if (n_tok == 0) return NT_OK;
   NT_REQUIRE(k && v, NT_ERR_INVALID_ARG, "null rows");
-  const size_t wide = src_fmt == NT_F32 ? 16 : 8;  // bytes of four channels
-  NT_REQUIRE(aligned(k, wide) && aligned(v, wide) && tok_stride % 4 == 0 && head_stride % 4 == 0, NT_ERR_ALIGNMENT,
-             "rows must be %zu-byte aligned, strides multiples of 4", wide);
+  const int vec = src_fmt == NT_F32 ? 4 : 8;
+  NT_REQUIRE(aligned(k, 16) && aligned(v, 16) && tok_stride % vec == 0 && head_stride % vec == 0, NT_ERR_ALIGNMENT,
+             "rows must be 16-byte aligned, strides multiples of %d", vec);
   NT_REQUIRE(aligned(pos_dev, 8), NT_ERR_ALIGNMENT, "pos_dev must be 8-byte aligned");
   DeviceGuard g(ctx->device);
   return launch_kv8_append(ctx, *kv, src_fmt, k, v, n_tok, tok_stride, head_stride, pos, pos_dev, as_stream(stream));

@@ -39,20 +39,22 @@ __device__ __forceinline__ float kv8_scale(float a) {
 }
 __device__ __forceinline__ float pow2_inv(float t) { return __uint_as_float((254u << 23) - __float_as_uint(t)); }
 
-// four values over the scale -> four bytes (nearest, ties to even); values beyond
-// the largest 8-bit value (an infinity's) saturate
+// four finite values times inv (1 / scale) -> four bytes, nearest, ties to even.  I8:
+// one fused step adds 1.5 * 2^23, which leaves the rounded number in the low byte;
+// q receives the results as floats that order like them (offset by 1.5 * 2^23).
+constexpr float kMagic = 12582912.f;
 template <int FMT>
-__device__ __forceinline__ uint32_t pack8(const float v[4]) {
+__device__ __forceinline__ uint32_t pack8(const float v[4], float inv, float q[4]) {
   if (FMT == NT_KV8_I8) {
-    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w |= (uint32_t(__float2int_rn(fminf(fmaxf(v[i], -127.f), 127.f))) & 0xFFu) << (8 * i);
-    return w;
+    for (int i = 0; i < 4; ++i) q[i] = fmaf(v[i], inv, kMagic);
+    const uint32_t lo = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(q[2]), __float_as_uint(q[3]), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
   }
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1] * inv), "f"(v[0] * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3] * inv), "f"(v[2] * inv));
   return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
@@ -116,24 +118,27 @@ struct AppendArgs {
 };
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __half* p) {
-  const uint2 r = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
-  return make_float4(a.x, a.y, b.x, b.y);
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // the larger; NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
+__device__ __forceinline__ float2 h2f(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 
 // One CTA per (block, head, K or V).  Its rows stay in registers from the load to
 // the store: the largest |x| is reduced over the CTA between them, so the source
 // is read once.  Rows the block already holds are loaded in the same round and
-// restated only when the scale grows.
+// restated only when the scale grows.  Bound by HBM; about four operations a value.
 template <int FMT, int HD, typename T>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendArgs a) {
-  constexpr int TR = HD / 4;                  // threads per row, four channels each
+  constexpr int VEC = 16 / int(sizeof(T));    // channels per thread: 16 bytes of the source
+  constexpr int TR = HD / VEC;                // threads per row
   constexpr int RP = kAppendThreads / TR;     // rows per pass
   constexpr int NP = kB / RP;
-  __shared__ float red[kAppendThreads / 32];
-  __shared__ float smin[RP][HD], smax[RP][HD];
+  constexpr int W = kAppendThreads / 32;
+  __shared__ float red[W];
+  __shared__ float smin[W][HD], smax[W][HD];
   pdl_wait();
   pdl_trigger();
   const int64_t pos = a.pos_dev ? *a.pos_dev : a.pos;
@@ -147,84 +152,158 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   if (end <= r0) return;
   const int r1 = int(end);
   const int h = blockIdx.y, w = blockIdx.z;
-  const T* src = static_cast<const T*>(w ? a.src[1] : a.src[0]) + int64_t(h) * a.head_stride;
-  uint8_t* dst = (w ? a.dst[1] : a.dst[0]) + (int64_t(h) * a.kv_stride + p0) * HD;
+  const int tr = threadIdx.x % TR, row = threadIdx.x / TR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T* src = static_cast<const T*>(w ? a.src[1] : a.src[0]) + int64_t(h) * a.head_stride +
+                 (p0 - pos) * a.tok_stride + VEC * tr;
+  uint8_t* dst = (w ? a.dst[1] : a.dst[0]) + (int64_t(h) * a.kv_stride + p0) * HD + VEC * tr;
   float* scale = (w ? a.scale[1] : a.scale[0]) + int64_t(h) * a.nb + blk;
-  const int tr = threadIdx.x % TR, row = threadIdx.x / TR;
 
-  float4 v[NP];
-  float amax = 0.f;
-  bool bad = false;
+  uint4 raw[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int r = row + i * RP;
-    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r >= r0 && r < r1) v[i] = load4(src + (p0 + r - pos) * a.tok_stride + 4 * tr);
-    else if (r < r0) v[i] = unpack8<FMT>(*reinterpret_cast<const uint32_t*>(dst + r * HD + 4 * tr));
-  }
-  const float t_old = r0 > 0 ? *scale : 0.f;
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = row + i * RP;
-    if (r < r0) continue;
-    float* x = &v[i].x;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float m = fabsf(x[j]);
-      if (m <= 3.402823466e38f) {
-        amax = fmaxf(amax, m);
-      } else {  // NaN is stored as 0, an infinity as the largest value; neither moves the scale
-        bad = true;
-        if (x[j] != x[j]) x[j] = 0.f;
-      }
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r >= r0 && r < r1) {
+      raw[i] = *reinterpret_cast<const uint4*>(src + r * a.tok_stride);
+    } else if (r < r0) {
+      raw[i].x = *reinterpret_cast<const uint32_t*>(dst + r * HD);
+      if (VEC == 8) raw[i].y = *reinterpret_cast<const uint32_t*>(dst + r * HD + 4);
     }
   }
-  if (bad) flag_error(a.err, kErrNonFinite);
+  const float t_old = r0 > 0 ? *scale : 0.f;
+  // channels 4 k .. 4 k + 3 of pass i: the source's values, or over the old scale the cache's
+  const auto values = [&](int i, int k, float v[4]) {
+    if (row + i * RP < r0) {
+      const float4 f = unpack8<FMT>(k ? raw[i].y : raw[i].x);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else if (VEC == 4) {
+      v[0] = __uint_as_float(raw[i].x), v[1] = __uint_as_float(raw[i].y);
+      v[2] = __uint_as_float(raw[i].z), v[3] = __uint_as_float(raw[i].w);
+    } else {
+      const float2 x = h2f(k ? raw[i].z : raw[i].x), y = h2f(k ? raw[i].w : raw[i].y);
+      v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
+    }
+  };
+  float amax = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  for (int i = 0; i < NP; ++i) {
+    if (row + i * RP < r0) continue;
+    if (VEC == 4) {
+      float v[4];
+      values(i, 0, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = max_nan(amax, fabsf(v[j]));
+    } else {
+      const __half2* x = reinterpret_cast<const __half2*>(&raw[i]);
+      const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(x[0]), __habs2(x[1])), __hmax2_nan(__habs2(x[2]), __habs2(x[3])));
+      const float2 f = __half22float2(m);
+      amax = max_nan(amax, max_nan(f.x, f.y));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (lane == 0) red[warp] = amax;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+  for (int i = 0; i < W; ++i) amax = max_nan(amax, red[i]);
+  const bool clean = amax <= 3.402823466e38f;
+  if (!clean) {
+    // a NaN or an infinity: the scale follows the finite values
+    if (threadIdx.x == 0) flag_error(a.err, kErrNonFinite);
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC / 4; ++k) {
+        float v[4];
+        values(i, k, v);
+        if (row + i * RP >= r0)
+          for (int j = 0; j < 4; ++j)
+            if (fabsf(v[j]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(v[j]));
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    __syncthreads();
+    if (lane == 0) red[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) amax = fmaxf(amax, red[i]);
+  }
   const float t = fmaxf(kv8_scale<FMT>(amax), t_old);
   const float inv = pow2_inv(t), restate = t_old * inv;
   if (threadIdx.x == 0) *scale = t;
 
   const bool sums = w == 0 && a.kmin;
-  float lo[4] = {448.f, 448.f, 448.f, 448.f}, hi[4] = {-448.f, -448.f, -448.f, -448.f};
+  float lo[VEC], hi[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    lo[j] = INFINITY;
+    hi[j] = -INFINITY;
+  }
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int r = row + i * RP;
     if (r >= r1) continue;
     const float f = r < r0 ? restate : inv;
-    const float q[4] = {v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f};
-    const uint32_t packed = pack8<FMT>(q);
-    if (r >= r0 || restate != 1.f) *reinterpret_cast<uint32_t*>(dst + r * HD + 4 * tr) = packed;
-    if (sums) {
-      const float4 z = unpack8<FMT>(packed);
-      const float zz[4] = {z.x, z.y, z.z, z.w};
+    uint32_t packed[VEC / 4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        lo[j] = fminf(lo[j], zz[j]);
-        hi[j] = fmaxf(hi[j], zz[j]);
+    for (int k = 0; k < VEC / 4; ++k) {
+      float v[4], q[4];
+      values(i, k, v);
+      if (!clean && r >= r0) {  // NaN is stored as 0, an infinity as the largest value
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float top = (FMT == NT_KV8_I8 ? 127.f : 448.f) * t;
+          v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j], -top), top);
+        }
       }
+      packed[k] = pack8<FMT>(v, f, q);
+      if (sums) {
+        if (FMT == NT_KV8_E4M3) {
+          const float4 z = unpack8<FMT>(packed[k]);
+          q[0] = z.x, q[1] = z.y, q[2] = z.z, q[3] = z.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          lo[4 * k + j] = fminf(lo[4 * k + j], q[j]);
+          hi[4 * k + j] = fmaxf(hi[4 * k + j], q[j]);
+        }
+      }
+    }
+    if (r >= r0 || restate != 1.f) {
+      if (VEC == 4)
+        *reinterpret_cast<uint32_t*>(dst + r * HD) = packed[0];
+      else
+        *reinterpret_cast<uint2*>(dst + r * HD) = make_uint2(packed[0], packed[VEC / 4 - 1]);
     }
   }
   if (!sums) return;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    smin[row][4 * tr + j] = lo[j];
-    smax[row][4 * tr + j] = hi[j];
+  for (int o = TR; o < 32; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      lo[j] = fminf(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
+      hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
+    }
+  if (lane < TR) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      smin[warp][VEC * tr + j] = lo[j];
+      smax[warp][VEC * tr + j] = hi[j];
+    }
   }
   __syncthreads();
   if (threadIdx.x >= HD) return;
   float l = smin[0][threadIdx.x], u = smax[0][threadIdx.x];
 #pragma unroll
-  for (int i = 1; i < RP; ++i) {
+  for (int i = 1; i < W; ++i) {
     l = fminf(l, smin[i][threadIdx.x]);
     u = fmaxf(u, smax[i][threadIdx.x]);
   }
-  if (FMT == NT_KV8_E4M3) {  // whole numbers of 4 scale steps, rounded outwards: still bounds
+  if (FMT == NT_KV8_I8) {
+    l -= kMagic;
+    u -= kMagic;
+  } else {  // whole numbers of 4 scale steps, rounded outwards: still bounds
     l = floorf(l * 0.25f);
     u = ceilf(u * 0.25f);
   }
@@ -1232,6 +1311,7 @@ __global__ void __launch_bounds__(NT) kv8_select_scratch_kernel(const SelectArgs
 
 constexpr int kSelWide = 1024, kSelNarrow = 256;  // threads of a selection
 constexpr int kSelNarrowBlocks = 256;             // most blocks of the narrow one
+constexpr int kSelCluster = 8;  // clusters of 16 CTAs of this size do not all fit at once (15,626 blocks: 22 us, 18 with 8)
 
 }  // namespace
 
@@ -1447,7 +1527,7 @@ nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, 
   if (kv8_select_fits(c, blocks)) {
     // CTAs per cluster: a pass of work for each, and the grid within the SMs
     int ranks = 1;
-    while (ranks < kMaxCluster && ranks * pass < blocks && 2 * ranks * groups <= c->num_sms) ranks *= 2;
+    while (ranks < kSelCluster && ranks * pass < blocks && 2 * ranks * groups <= c->num_sms) ranks *= 2;
     return cuda_check(c, launch_cluster(c, h128 ? kv8_select_kernel<kSelWide, 128> : kv8_select_kernel<kSelWide, 64>,
                                         dim3(ranks, kv.n_kvh, nq), dim3(kSelWide), size_t(blocks) * sizeof(uint32_t),
                                         st, dim3(ranks, 1, 1), a),

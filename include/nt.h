@@ -308,8 +308,8 @@ typedef struct {
  * pos_dev (nullable): the position is read from the device (8-byte aligned) and
  * pos is ignored, so a captured call can be replayed; rows that would leave the
  * cache are then not written and set the device flag.
- * Rows 16-byte (F32) or 8-byte (F16) aligned, strides multiples of 4.  One
- * launch, no scratch. */
+ * Rows 16-byte aligned: strides multiples of 4 (F32) or 8 (F16).  One launch, no
+ * scratch. */
 nt_status nt_kv8_append(nt_ctx* ctx, const nt_kv8* cache, int src_fmt, const void* k_dev, const void* v_dev,
                         int64_t n_tok, int64_t tok_stride, int64_t head_stride, int64_t pos,
                         const int64_t* pos_dev, void* stream);

@@ -89,7 +89,8 @@ def test_refusals(ctx):
     refuse(fmt, lambda: app(src=nt.Q8_0))
     for kw in [dict(n=-1), dict(n=101), dict(pos=-1), dict(pos=100), dict(n=2, pos=99), dict(k=None), dict(v=None)]:
         refuse(bad, lambda: app(**kw))
-    for kw in [dict(k=p + 8), dict(v=p + 4), dict(ts=130), dict(hs=2), dict(pd=p + 4), dict(src=nt.F16, k=p + 4)]:
+    for kw in [dict(k=p + 8), dict(v=p + 4), dict(ts=130), dict(hs=2), dict(pd=p + 4), dict(src=nt.F16, k=p + 8),
+               dict(src=nt.F16, ts=260), dict(src=nt.F16, hs=132)]:
         refuse(align, lambda: app(**kw))
     rd = lambda pos=0, n=1, t=nt.F32, k=f, v=f, hs=128: nt.nt_kv8_read(ctx, g.desc, pos, n, t, k, v, hs, stream=0)  # noqa: E731
     refuse(fmt, lambda: rd(t=nt.Q4_0))
