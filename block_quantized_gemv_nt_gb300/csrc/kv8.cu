@@ -40,14 +40,13 @@ __device__ __forceinline__ float kv8_scale(float a) {
 __device__ __forceinline__ float pow2_inv(float t) { return __uint_as_float((254u << 23) - __float_as_uint(t)); }
 
 // four finite values times inv (1 / scale) -> four bytes, nearest, ties to even.  I8:
-// one fused step adds 1.5 * 2^23, which leaves the rounded number in the low byte;
-// q receives the results as floats that order like them (offset by 1.5 * 2^23).
-constexpr float kMagic = 12582912.f;
+// one fused step adds 1.5 * 2^23, which leaves the rounded number in the low byte.
 template <int FMT>
-__device__ __forceinline__ uint32_t pack8(const float v[4], float inv, float q[4]) {
+__device__ __forceinline__ uint32_t pack8(const float v[4], float inv) {
   if (FMT == NT_KV8_I8) {
+    float q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = fmaf(v[i], inv, kMagic);
+    for (int i = 0; i < 4; ++i) q[i] = fmaf(v[i], inv, 12582912.f);
     const uint32_t lo = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x0040);
     const uint32_t hi = __byte_perm(__float_as_uint(q[2]), __float_as_uint(q[3]), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
@@ -234,11 +233,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   if (threadIdx.x == 0) *scale = t;
 
   const bool sums = w == 0 && a.kmin;
-  float lo[VEC], hi[VEC];
+  __half2 lo[VEC / 2], hi[VEC / 2];  // the stored values' bounds, in the order of to_h2; exact in f16
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    lo[j] = INFINITY;
-    hi[j] = -INFINITY;
+  for (int j = 0; j < VEC / 2; ++j) {
+    lo[j] = __half2half2(__ushort_as_half(0x7C00));  // +inf
+    hi[j] = __half2half2(__ushort_as_half(0xFC00));
   }
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     uint32_t packed[VEC / 4];
 #pragma unroll
     for (int k = 0; k < VEC / 4; ++k) {
-      float v[4], q[4];
+      float v[4];
       values(i, k, v);
       if (!clean && r >= r0) {  // NaN is stored as 0, an infinity as the largest value
 #pragma unroll
@@ -257,16 +256,15 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
           v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j], -top), top);
         }
       }
-      packed[k] = pack8<FMT>(v, f, q);
+      packed[k] = pack8<FMT>(v, f);
       if (sums) {
-        if (FMT == NT_KV8_E4M3) {
-          const float4 z = unpack8<FMT>(packed[k]);
-          q[0] = z.x, q[1] = z.y, q[2] = z.z, q[3] = z.w;
-        }
+        uint32_t z[2];
+        to_h2<FMT>(packed[k], z[0], z[1]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          lo[4 * k + j] = fminf(lo[4 * k + j], q[j]);
-          hi[4 * k + j] = fmaxf(hi[4 * k + j], q[j]);
+        for (int j = 0; j < 2; ++j) {
+          const __half2 y = *reinterpret_cast<const __half2*>(&z[j]);
+          lo[2 * k + j] = __hmin2(lo[2 * k + j], y);
+          hi[2 * k + j] = __hmax2(hi[2 * k + j], y);
         }
       }
     }
@@ -281,15 +279,20 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
 #pragma unroll
   for (int o = TR; o < 32; o <<= 1)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      lo[j] = fminf(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
-      hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
+    for (int j = 0; j < VEC / 2; ++j) {
+      lo[j] = __hmin2(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
+      hi[j] = __hmax2(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
     }
   if (lane < TR) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      smin[warp][VEC * tr + j] = lo[j];
-      smax[warp][VEC * tr + j] = hi[j];
+    for (int j = 0; j < VEC / 2; ++j) {
+      // pair j of to_h2 holds bytes b and b + kPairStep
+      const int ch = VEC * tr + 4 * (j / 2) + (j & 1) * (3 - kPairStep<FMT>);
+      const float2 l = __half22float2(lo[j]), u = __half22float2(hi[j]);
+      smin[warp][ch] = l.x;
+      smin[warp][ch + kPairStep<FMT>] = l.y;
+      smax[warp][ch] = u.x;
+      smax[warp][ch + kPairStep<FMT>] = u.y;
     }
   }
   __syncthreads();
@@ -300,10 +303,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     l = fminf(l, smin[i][threadIdx.x]);
     u = fmaxf(u, smax[i][threadIdx.x]);
   }
-  if (FMT == NT_KV8_I8) {
-    l -= kMagic;
-    u -= kMagic;
-  } else {  // whole numbers of 4 scale steps, rounded outwards: still bounds
+  if (FMT == NT_KV8_E4M3) {  // whole numbers of 4 scale steps, rounded outwards: still bounds
     l = floorf(l * 0.25f);
     u = ceilf(u * 0.25f);
   }
