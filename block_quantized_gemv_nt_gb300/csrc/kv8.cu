@@ -129,27 +129,21 @@ __device__ __forceinline__ float2 h2f(uint32_t h) { return __half22float2(*reint
 // the store: the largest |x| is reduced over the CTA between them, so the source
 // is read once.  Rows the block already holds are loaded in the same round and
 // restated only when the scale grows.  Bound by HBM; about four operations a value.
-template <int FMT, int HD, typename T>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendArgs a) {
+struct AppendShared {
+  float red[kAppendThreads / 32];
+  float smin[kAppendThreads / 32][128], smax[kAppendThreads / 32][128];
+};
+
+// FULL: the rows are the whole block (no test by row)
+template <int FMT, int HD, typename T, bool FULL>
+__device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& sh, int64_t pos, int64_t blk, int r0,
+                                             int r1) {
   constexpr int VEC = 16 / int(sizeof(T));    // channels per thread: 16 bytes of the source
   constexpr int TR = HD / VEC;                // threads per row
   constexpr int RP = kAppendThreads / TR;     // rows per pass
   constexpr int NP = kB / RP;
   constexpr int W = kAppendThreads / 32;
-  __shared__ float red[W];
-  __shared__ float smin[W][HD], smax[W][HD];
-  pdl_wait();
-  pdl_trigger();
-  const int64_t pos = a.pos_dev ? *a.pos_dev : a.pos;
-  if (pos < 0 || pos > a.kv_stride - a.n) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrPosRange);
-    return;
-  }
-  const int64_t blk = pos / kB + blockIdx.x, p0 = blk * kB;
-  const int r0 = int(max(pos, p0) - p0);
-  const int64_t end = min(pos + a.n, p0 + kB) - p0;
-  if (end <= r0) return;
-  const int r1 = int(end);
+  const int64_t p0 = blk * kB;
   const int h = blockIdx.y, w = blockIdx.z;
   const int tr = threadIdx.x % TR, row = threadIdx.x / TR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* src = static_cast<const T*>(w ? a.src[1] : a.src[0]) + int64_t(h) * a.head_stride +
@@ -162,17 +156,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   for (int i = 0; i < NP; ++i) {
     const int r = row + i * RP;
     raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= r0 && r < r1) {
+    if (FULL || (r >= r0 && r < r1)) {
       raw[i] = *reinterpret_cast<const uint4*>(src + r * a.tok_stride);
     } else if (r < r0) {
       raw[i].x = *reinterpret_cast<const uint32_t*>(dst + r * HD);
       if (VEC == 8) raw[i].y = *reinterpret_cast<const uint32_t*>(dst + r * HD + 4);
     }
   }
-  const float t_old = r0 > 0 ? *scale : 0.f;
+  const float t_old = !FULL && r0 > 0 ? *scale : 0.f;
   // channels 4 k .. 4 k + 3 of pass i: the source's values, or over the old scale the cache's
   const auto values = [&](int i, int k, float v[4]) {
-    if (row + i * RP < r0) {
+    if (!FULL && row + i * RP < r0) {
       const float4 f = unpack8<FMT>(k ? raw[i].y : raw[i].x);
       v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
     } else if (VEC == 4) {
@@ -186,7 +180,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    if (row + i * RP < r0) continue;
+    if (!FULL && row + i * RP < r0) continue;
     if (VEC == 4) {
       float v[4];
       values(i, 0, v);
@@ -201,10 +195,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) red[warp] = amax;
+  if (lane == 0) sh.red[warp] = amax;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < W; ++i) amax = max_nan(amax, red[i]);
+  for (int i = 0; i < W; ++i) amax = max_nan(amax, sh.red[i]);
   const bool clean = amax <= 3.402823466e38f;
   if (!clean) {
     // a NaN or an infinity: the scale follows the finite values
@@ -216,17 +210,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
       for (int k = 0; k < VEC / 4; ++k) {
         float v[4];
         values(i, k, v);
-        if (row + i * RP >= r0)
+        if (FULL || row + i * RP >= r0)
           for (int j = 0; j < 4; ++j)
             if (fabsf(v[j]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(v[j]));
       }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     __syncthreads();
-    if (lane == 0) red[warp] = amax;
+    if (lane == 0) sh.red[warp] = amax;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < W; ++i) amax = fmaxf(amax, red[i]);
+    for (int i = 0; i < W; ++i) amax = fmaxf(amax, sh.red[i]);
   }
   const float t = fmaxf(kv8_scale<FMT>(amax), t_old);
   const float inv = pow2_inv(t), restate = t_old * inv;
@@ -242,14 +236,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int r = row + i * RP;
-    if (r >= r1) continue;
-    const float f = r < r0 ? restate : inv;
+    if (!FULL && r >= r1) continue;
+    const float f = !FULL && r < r0 ? restate : inv;
     uint32_t packed[VEC / 4];
 #pragma unroll
     for (int k = 0; k < VEC / 4; ++k) {
       float v[4];
       values(i, k, v);
-      if (!clean && r >= r0) {  // NaN is stored as 0, an infinity as the largest value
+      if (!clean && (FULL || r >= r0)) {  // NaN is stored as 0, an infinity as the largest value
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float top = (FMT == NT_KV8_I8 ? 127.f : 448.f) * t;
@@ -268,7 +262,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
         }
       }
     }
-    if (r >= r0 || restate != 1.f) {
+    if (FULL || r >= r0 || restate != 1.f) {
       if (VEC == 4)
         *reinterpret_cast<uint32_t*>(dst + r * HD) = packed[0];
       else
@@ -289,19 +283,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
       // pair j of to_h2 holds bytes b and b + kPairStep
       const int ch = VEC * tr + 4 * (j / 2) + (j & 1) * (3 - kPairStep<FMT>);
       const float2 l = __half22float2(lo[j]), u = __half22float2(hi[j]);
-      smin[warp][ch] = l.x;
-      smin[warp][ch + kPairStep<FMT>] = l.y;
-      smax[warp][ch] = u.x;
-      smax[warp][ch + kPairStep<FMT>] = u.y;
+      sh.smin[warp][ch] = l.x;
+      sh.smin[warp][ch + kPairStep<FMT>] = l.y;
+      sh.smax[warp][ch] = u.x;
+      sh.smax[warp][ch + kPairStep<FMT>] = u.y;
     }
   }
   __syncthreads();
   if (threadIdx.x >= HD) return;
-  float l = smin[0][threadIdx.x], u = smax[0][threadIdx.x];
+  float l = sh.smin[0][threadIdx.x], u = sh.smax[0][threadIdx.x];
 #pragma unroll
   for (int i = 1; i < W; ++i) {
-    l = fminf(l, smin[i][threadIdx.x]);
-    u = fmaxf(u, smax[i][threadIdx.x]);
+    l = fminf(l, sh.smin[i][threadIdx.x]);
+    u = fmaxf(u, sh.smax[i][threadIdx.x]);
   }
   if (FMT == NT_KV8_E4M3) {  // whole numbers of 4 scale steps, rounded outwards: still bounds
     l = floorf(l * 0.25f);
@@ -310,6 +304,26 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   const int64_t at = (int64_t(h) * a.nb + blk) * HD + threadIdx.x;
   a.kmin[at] = int8_t(__float2int_rn(l));
   a.kmax[at] = int8_t(__float2int_rn(u));
+}
+
+template <int FMT, int HD, typename T>
+__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendArgs a) {
+  __shared__ AppendShared sh;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t pos = a.pos_dev ? *a.pos_dev : a.pos;
+  if (pos < 0 || pos > a.kv_stride - a.n) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrPosRange);
+    return;
+  }
+  const int64_t blk = pos / kB + blockIdx.x, p0 = blk * kB;
+  const int r0 = int(max(pos, p0) - p0);
+  const int64_t end = min(pos + a.n, p0 + kB) - p0;
+  if (end <= r0) return;
+  if (r0 == 0 && end == kB)
+    append_block<FMT, HD, T, true>(a, sh, pos, blk, 0, kB);
+  else
+    append_block<FMT, HD, T, false>(a, sh, pos, blk, r0, int(end));
 }
 
 // ---- read back -----------------------------------------------------------------
