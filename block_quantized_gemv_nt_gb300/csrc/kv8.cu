@@ -404,10 +404,9 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 //    their V rows, and byte i of them is B column n of n-tile i, i.e. output channel
 //    n HD/8 + i.
 //
-// Each warp walks its own steps: one bulk copy brings a step's K, four its V (the
-// rows of each c, 32 bytes apart from the next, so that a warp's V reads meet no
-// bank twice).  The next step's K is copied while the warp works on the probabilities
-// and V, the next V while it works on K; no barrier joins the warps.
+// Each warp walks its own steps: one bulk copy brings a step's K and one its V.  The
+// next step's K is copied while the warp works on the probabilities and V, the next V
+// while it works on K; no barrier joins the warps.
 constexpr int kAttnWarps = 8;
 constexpr float kPTop = 8.f, kSlack = 6.f;
 constexpr int kMaxCluster = 16;
@@ -463,6 +462,19 @@ __device__ __forceinline__ void mma16816_zero(float c[4], const uint4& a, uint32
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// whether phase `parity` of an mbarrier has completed, without waiting
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -508,15 +520,17 @@ __device__ __forceinline__ void st_cluster(uint32_t at, int rank, float2 v) {
 // outputs [warps][R][HD / 8][32] x 8
 template <int HD, int R, int U>
 struct AttnKv8Smem {
+  // steps in flight per warp: one of 32 tokens with 16 warps on an SM keeps HBM busy;
+  // short steps, and the 8 warps of R = 2, take two
+  static constexpr int stages = R == 2 || U == 1 ? 2 : 1;
   static constexpr size_t q = 0;
   static constexpr size_t ml = q + size_t(R) * (HD / 16) * 512;
   static constexpr size_t push = ml + size_t(2) * kAttnWarps * 8 * R * 4;           // from the cluster: outputs
   static constexpr size_t push_ml = push + size_t(R) * (HD / 8) * 256;               // and (max, sum) [splits][8 R]
   static constexpr size_t ring = push_ml + size_t(kMaxCluster) * 8 * R * 8;
-  static constexpr size_t group = size_t(4 * U) * HD + 32;           // V rows of one c
-  static constexpr size_t stage = size_t(16 * U) * HD + 4 * group;   // K, then V
+  static constexpr size_t stage = size_t(16 * U) * HD * 2;           // K, then V
   static constexpr size_t outs = size_t(R) * (HD / 8) * 256;         // one warp's outputs
-  static constexpr size_t bytes = ring + kAttnWarps * (stage > outs ? stage : outs);
+  static constexpr size_t bytes = ring + kAttnWarps * (stages * stage > outs ? stages * stage : outs);
 };
 
 template <int FMT, int HD, int R, int U, bool SPARSE>
@@ -532,7 +546,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   extern __shared__ __align__(16) uint8_t sm8[];
   uint4* qa = reinterpret_cast<uint4*>(sm8 + L::q);
   __shared__ float s_amax[R * KS][8];  // by k-step and row
-  __shared__ __align__(8) uint64_t bars[kAttnWarps][2];
+  constexpr int ST = L::stages;
+  __shared__ __align__(8) uint64_t bars[kAttnWarps][2 * ST];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = lane >> 2, c = lane & 3;
@@ -556,19 +571,26 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   else if (st0 >= st1 && s > 0)
     return;
 
+  // this thread's q values, requested before the copies of K and V fill the memory system
+  constexpr int QI = (R * KS + kAttnWarps - 1) / kAttnWarps;  // fragments per thread
+  float4 qv[QI];
+#pragma unroll
+  for (int i = 0; i < QI; ++i) {
+    const int f = warp + i * kAttnWarps, j = f % KS, r = f / KS * 8 + n;
+    qv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (f < R * KS && r < rows) qv[i] = load4(a.q + vec_of(r) * HD + 64 * (j >> 2) + 16 * c + 4 * (j & 3));
+  }
   const uint8_t* kg = a.k + int64_t(g) * a.kv_stride * HD;
   const uint8_t* vg = a.v + int64_t(g) * a.kv_stride * HD;
   const float* ksg = a.ks + int64_t(g) * a.nb;
   const float* vsg = a.vs + int64_t(g) * a.nb;
   const int32_t* list = SPARSE ? a.idx + (int64_t(qi0) * a.n_kvh + g) * a.n_sel : nullptr;
   const int blocks_seen = (tokens + kB - 1) / kB;
-  const uint8_t* sk = sm8 + L::ring + size_t(warp) * L::stage;  // this warp's K rows, then its V groups
-  const uint8_t* sv = sk + kStep * HD;
-  const uint32_t bar_k = smem_u32(&bars[warp][0]), bar_v = smem_u32(&bars[warp][1]);
+  const uint8_t* ring = sm8 + L::ring + size_t(warp) * ST * L::stage;  // stages of K rows, then V groups
+  const uint32_t bar = smem_u32(&bars[warp][0]);                       // [stage]: K, V
   const uint64_t pol = policy_evict_first();
   if (lane == 0) {
-    mbar_init(bar_k, 1);
-    mbar_init(bar_v, 1);
+    for (int i = 0; i < 2 * ST; ++i) mbar_init(bar + 8 * i, 1);
     fence_barrier_init();
   }
   __syncwarp();
@@ -580,24 +602,24 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     const int b = __ldg(list + st / (kB / kStep));
     return b < 0 || b >= blocks_seen ? tokens : min(tokens, b * kB + st % (kB / kStep) * kStep);
   };
-  // the copies of one step's K and V, rows below `tokens` only
-  const auto copy_k = [&](int t0) {
-    if (t0 < tokens && lane == 0) {
-      const uint32_t bytes = min(kStep, tokens - t0) * HD;
-      mbar_arrive_expect_tx(bar_k, bytes);
-      if (!a.stall) bulk_g2s(smem_u32(sk), kg + int64_t(t0) * HD, bytes, bar_k, pol);
+  // the copies of one step's K and V, rows below `tokens` only; step number i of this
+  // warp's (steps without tokens not counted) goes through stage i % ST
+  int sent_k = 0, sent_v = 0, done = 0;
+  const auto copy = [&](const uint8_t* from, int which, int t0, int& sent) {
+    if (t0 >= tokens) return;
+    if (lane == 0) {
+      const int i = sent % ST;
+      const uint32_t bytes = min(kStep, tokens - t0) * HD, on = bar + 16 * i + 8 * which;
+      mbar_arrive_expect_tx(on, bytes);
+      if (!a.stall)
+        bulk_g2s(smem_u32(ring + i * L::stage + which * kStep * HD), from + int64_t(t0) * HD, bytes, on, pol);
     }
+    ++sent;
   };
-  const auto copy_v = [&](int t0) {
-    if (t0 < tokens && lane < 4) {
-      const int left = tokens - t0, mine = max(0, min(4 * U, left - 4 * U * lane));
-      if (lane == 0) mbar_arrive_expect_tx(bar_v, min(kStep, left) * HD);
-      if (mine && !a.stall)
-        bulk_g2s(smem_u32(sv + lane * L::group), vg + int64_t(t0 + 4 * U * lane) * HD, mine * HD, bar_v, pol);
-    }
-  };
-  const auto wait = [&](uint32_t bar, uint32_t phase) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, a.stall ? kStallSpin : kMaxSpin));
+  const auto wait = [&](int which) {
+    const uint32_t on = bar + 16 * (done % ST) + 8 * which, phase = (done / ST) & 1;
+    if (mbar_test(on, phase)) return true;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(on, phase, a.stall ? kStallSpin : kMaxSpin));
     if (!ok && lane == 0) flag_error(a.err, kErrWaitTimeout);
     return ok;
   };
@@ -605,21 +627,23 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     return t0 < tokens ? make_float2(__ldg(ksg + t0 / kB), __ldg(vsg + t0 / kB)) : make_float2(0.f, 0.f);
   };
   int st = st0 + warp;
-  int t0 = step_token(st), t1 = step_token(st + kAttnWarps);  // this step's first token, the next one's
-  copy_k(t0);
-  copy_v(t0);
-  float2 kvs = scales(t0);
+  int tq[ST + 1];   // first tokens of this step and the next ones
+  float2 kvq[ST];
+#pragma unroll
+  for (int i = 0; i <= ST; ++i) tq[i] = step_token(st + i * kAttnWarps);
+#pragma unroll
+  for (int i = 0; i < ST; ++i) {
+    copy(kg, 0, tq[i], sent_k);
+    copy(vg, 1, tq[i], sent_v);
+    kvq[i] = scales(tq[i]);
+  }
 
   // q: each row scaled by a power of two to amax in [2^13, 2^14), split, laid out as
   // fragments: warp w holds k-step w % KS of every row
-  constexpr int QI = (R * KS + kAttnWarps - 1) / kAttnWarps;  // fragments per thread
-  float4 qv[QI];
 #pragma unroll
   for (int i = 0; i < QI; ++i) {
-    const int f = warp + i * kAttnWarps, j = f % KS, r = f / KS * 8 + n;
-    qv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int f = warp + i * kAttnWarps;
     if (f >= R * KS) continue;
-    if (r < rows) qv[i] = load4(a.q + vec_of(r) * HD + 64 * (j >> 2) + 16 * c + 4 * (j & 3));
     float x = fmaxf(fmaxf(fabsf(qv[i].x), fabsf(qv[i].y)), fmaxf(fabsf(qv[i].z), fabsf(qv[i].w)));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -662,14 +686,21 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     for (int i = 0; i < NT; ++i) o[t][i] = make_float2(0.f, 0.f);
   }
   const int fewest = SPARSE ? tokens : n_pos + query_of(0);  // positions every row sees
-  uint32_t phase = 0;
   for (; st < st1; st += kAttnWarps) {
-    const int t2 = step_token(st + 2 * kAttnWarps);
-    const float2 kvs1 = scales(t1);
+    const int t0 = tq[0];
+    const float2 kvs = kvq[0];
+    const uint8_t* sk = ring + done % ST * L::stage;
+    const uint8_t* sv = sk + kStep * HD;
+#pragma unroll
+    for (int i = 0; i < ST; ++i) tq[i] = tq[i + 1];
+#pragma unroll
+    for (int i = 0; i + 1 < ST; ++i) kvq[i] = kvq[i + 1];
+    kvq[ST - 1] = scales(tq[ST - 1]);
+    tq[ST] = step_token(st + (ST + 1) * kAttnWarps);
     // ---- scores
     float sc[R][2 * U][CH][4];
     if (t0 < tokens) {
-      if (!wait(bar_k, phase)) break;
+      if (!wait(0)) break;
 #pragma unroll
       for (int t = 0; t < R; ++t)
 #pragma unroll
@@ -698,7 +729,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       }
     }
     __syncwarp();  // this step's K is in registers and used
-    copy_k(t1);
+    copy(kg, 0, tq[ST - 1], sent_k);
     uint4 pf[R][U];
     if (t0 < tokens) {
       // ---- online softmax: p = 2^(s - m + kPTop).  The f16 operand of P V is p
@@ -766,8 +797,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       }
     }
     if (t0 < tokens) {
-      if (!wait(bar_v, phase)) break;
-      phase ^= 1;
+      if (!wait(1)) break;
+      ++done;
       // ---- P V: words of two tokens interleaved into (token, token + 1) pairs per
       // channel.  Each step's products start from zero and are added to the output
       // in fp32: the tensor cores round their sums towards zero, and a bias of one
@@ -778,7 +809,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
         uint32_t vw[4 * U][2];
 #pragma unroll
         for (int x = 0; x < 4 * U; ++x) {
-          const uint2 r = *reinterpret_cast<const uint2*>(sv + c * L::group + x * HD + n * (HD / 8) + 4 * w);
+          const uint2 r = *reinterpret_cast<const uint2*>(sv + (4 * U * c + x) * HD + n * (HD / 8) + 4 * w);
           vw[x][0] = r.x;
           vw[x][1] = r.y;
         }
@@ -817,10 +848,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       }
     }
     __syncwarp();  // and its V
-    copy_v(t1);
-    t0 = t1;
-    t1 = t2;
-    kvs = kvs1;
+    copy(vg, 1, tq[ST - 1], sent_v);
   }
 
   // ---- merge the warps
@@ -861,7 +889,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       sum = fmaf(mll[w * ROWS + r], f[w], sum);
     }
     const int64_t vec = vec_of(r);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
     for (int i = warp; i < NT; i += kAttnWarps) {
       float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
@@ -895,15 +924,22 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   for (int k = warp; k < own; k += kAttnWarps) {
     const int tile = s * own + k, r = tile / NT * 8 + n, i = tile % NT;
     if (r >= rows) continue;
+    float2 y[kMaxCluster], z[kMaxCluster];  // all in flight together
     float M = -INFINITY, sum = 0.f;
-    for (int x = 0; x < a.S; ++x) M = fmaxf(M, pushed_ml[x * ROWS + r].x);
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+      y[x] = x < a.S ? pushed_ml[x * ROWS + r] : make_float2(-INFINITY, 0.f);
+      z[x] = x < a.S ? pushed[(x * own + k) * 32 + lane] : make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) M = fmaxf(M, y[x].x);
     float2 acc = make_float2(0.f, 0.f);
-    for (int x = 0; x < a.S; ++x) {
-      const float2 y = pushed_ml[x * ROWS + r], z = pushed[(x * own + k) * 32 + lane];
-      const float f = y.x == -INFINITY ? 0.f : ex2(y.x - M);
-      sum = fmaf(y.y, f, sum);
-      acc.x = fmaf(z.x, f, acc.x);
-      acc.y = fmaf(z.y, f, acc.y);
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+      const float f = y[x].x == -INFINITY ? 0.f : ex2(y[x].x - M);
+      sum = fmaf(y[x].y, f, sum);
+      acc.x = fmaf(z[x].x, f, acc.x);
+      acc.y = fmaf(z[x].y, f, acc.y);
     }
     const int64_t vec = vec_of(r);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -1462,21 +1498,20 @@ nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, 
   int64_t S = int64_t(c->num_sms) * (R == 1 ? 2 : 1) / (int64_t(kv.n_kvh) * z);
   if (S > kMaxSplits) S = kMaxSplits;
   if (S < 1) S = 1;
-  int U = R == 2 || most >= S * kAttnWarps * kv8_u2_tokens() ? 2 : 1;
-  const int64_t useful = (most + 16 * kAttnWarps * U - 1) / (16 * kAttnWarps * U);
+  int U = R == 2 || most <= 32 * kAttnWarps || most >= S * kAttnWarps * kv8_u2_tokens() ? 2 : 1;
+  const auto useful = [&](int u) { return std::max<int64_t>(1, (most + 16 * kAttnWarps * u - 1) / (16 * kAttnWarps * u)); };
   const size_t vecs = size_t(n_qh) * nq, row = vecs * (kv.head_dim * 4 + 8);
   // short sequences: the splits of a head as one cluster, which saves the second launch
+  const int64_t groups = int64_t(kv.n_kvh) * z;
+  const int64_t widest = std::min<int64_t>({kMaxCluster, R * kv.head_dim / 8, S, R == 1 ? S : c->num_sms / 2 / groups});
   int64_t C = 1;
-  const int64_t widest = std::min<int64_t>(std::min(kMaxCluster, R * kv.head_dim / 8), S);
-  while (C < (most + 16 * kAttnWarps * R - 1) / (16 * kAttnWarps * R) && 2 * C <= widest) C *= 2;
-  a.cluster = C > 1 && most <= kv8_cluster_tokens() * C;
+  while (C < useful(R) && 2 * C <= widest) C *= 2;
+  a.cluster = useful(2) > 1 && C > 1 && most <= kv8_cluster_tokens() * C;
   if (a.cluster) {
     S = C;
     U = R == 2 || most >= S * kAttnWarps * kv8_u2_tokens() ? 2 : 1;
   } else {
-    if (S > useful) S = useful;
-    if (S * int64_t(row) > int64_t(scratch_bytes)) S = int64_t(scratch_bytes / row);
-    if (S < 1) S = 1;
+    S = std::min<int64_t>({S, useful(U), std::max<int64_t>(1, int64_t(scratch_bytes / row))});
   }
   a.S = int(S);
   a.part = reinterpret_cast<float*>(scratch);
