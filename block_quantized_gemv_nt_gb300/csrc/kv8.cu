@@ -11,6 +11,7 @@
 #include <cuda_fp16.h>
 #include <algorithm>
 #include <cstdlib>
+#include <type_traits>
 
 #include "nt_internal.cuh"
 #include "ops.cuh"
@@ -1044,6 +1045,9 @@ AttnKv8Variant attn_kv8_for(int fmt, int hd, int R, int U) {
 // 12-bit integers every sum is a whole number below 2^31: the scores, and with
 // them the choice, do not depend on the order of additions.
 constexpr int kSelBins = 1024;
+constexpr int kSelWide = 1024, kSelNarrow = 256;  // threads of a selection
+constexpr int kSelNarrowBlocks = kSelNarrow;      // most blocks of the narrow one: one a thread
+constexpr int kSelCluster = 8;  // clusters of 16 CTAs of this size do not all fit at once (15,626 blocks: 22 us, 18 with 8)
 constexpr uint32_t kForced = 0xFFFFFFFFu;  // key of a block that is taken whatever its score
 
 struct SelectArgs {
@@ -1083,9 +1087,9 @@ constexpr int kScorePass = 4 * 32 / (HD / 8);
 // put(block, key).  A lane holds 8 channels of a block; four blocks are loaded and
 // summed together: their lanes' sums are exchanged so that lane j (mod 4) of a group
 // ends with block j, in 5 or 4 shuffles for the four.
-template <int NT, int HD, typename Put>
+template <int NT, int HD, typename Ready, typename Put>
 __device__ __forceinline__ void score_blocks(const SelectArgs& a, int g, int qi, int blocks, int rank, int ranks,
-                                             Put put) {
+                                             Ready ready, Put put) {
   constexpr int LB = HD / 8, BW = 32 / LB;
   constexpr int W = NT / 32;
   __shared__ float red[W];
@@ -1141,6 +1145,7 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, int g, int qi,
     p2[i] = (sums[0][d] & 0xFFFF) | (sums[0][d + 1] << 16);
     n2[i] = (sums[1][d] & 0xFFFF) | (sums[1][d + 1] << 16);
   }
+  ready();
   for (; b0 < blocks; b0 += stride) {
     int v[4];
 #pragma unroll
@@ -1171,7 +1176,8 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, int g, int qi,
 
 // The n_sel largest of `blocks` keys, as ascending indices: radix rounds of up to
 // ten bits below the keys' common prefix, ending as soon as the chosen bin is taken
-// whole; then one scan in index order.  Thread t holds blocks t K .. t K + K - 1 in
+// whole; once a bin holds no more keys than there are threads, later rounds look at
+// those alone, one a thread; then one scan in index order.  Thread t holds blocks t K .. t K + K - 1 in
 // registers (K odd, so that the threads of a warp read different banks), or re-reads
 // them every time (K = 0).  key(b): the key of block b.
 template <int NT>
@@ -1180,7 +1186,8 @@ struct SelShared {
   int hist[kSelBins];
   int wsum[NT / 32];
   uint32_t wmin[NT / 32], wmax[NT / 32];
-  int bin, above, count;
+  int bin, above, count, listed;
+  uint32_t list[NT];
 };
 template <int NT, int K, typename Key>
 __device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, int32_t* idx, SelShared<NT>& sh, Key key) {
@@ -1222,12 +1229,19 @@ __device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, i
     mx = __reduce_max_sync(0xffffffffu, sh.wmax[lane % W]);
     int bits = mx == mn ? 0 : 32 - __clz(mx ^ mn);
     cut = bits == 32 ? 0u : (mx >> bits) << bits;
+    bool short_list = false;  // the keys in question are sh.list
+    uint32_t mine = kForced;  // this thread's of them
     while (bits > 0) {
       const int dig = min(10, bits), shift = bits - dig;
-      each([&](int, uint32_t k) {
+      const auto count = [&](uint32_t k) {
         if (k != kForced && (bits == 32 || (k >> bits) == (cut >> bits)))
           atomicAdd(&sh.hist[(k >> shift) & ((1u << dig) - 1u)], 1);
-      });
+      };
+      if (short_list)
+        count(mine);
+      else
+        each([&](int, uint32_t k) { count(k); });
+      if (tid == 0) sh.listed = 0;
       __syncthreads();
       // thread 0 holds the highest bins
       constexpr int HB = kSelBins / NT;
@@ -1265,23 +1279,34 @@ __device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, i
         need = 0;
         break;
       }
+      if (bits > 0 && !short_list && sh.count <= NT) {
+        each([&](int, uint32_t k) {
+          if (k != kForced && (k >> bits) == (cut >> bits)) sh.list[atomicAdd(&sh.listed, 1)] = k;
+        });
+        __syncthreads();
+        mine = tid < sh.listed ? sh.list[tid] : kForced;
+        short_list = true;
+      }
     }
   }
-  unsigned long long cnt = 0;  // blocks taken above the cut, and (high half) blocks at it
-  each([&](int, uint32_t k) { cnt += k == kForced || k > cut ? 1ull : (k == cut ? 1ull << 32 : 0ull); });
-  unsigned long long incl = cnt;
+  // blocks taken above the cut and (upper half) blocks at it; K > 0 has fewer than 2^16
+  using Count = std::conditional_t<(K > 0), uint32_t, unsigned long long>;
+  constexpr int H = K > 0 ? 16 : 32;
+  Count cnt = 0;
+  each([&](int, uint32_t k) { cnt += k == kForced || k > cut ? Count(1) : (k == cut ? Count(1) << H : Count(0)); });
+  Count incl = cnt;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    const Count t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
   if (lane == 31) sh.wscan[warp] = incl;
   __syncthreads();
-  unsigned long long base = lane < warp ? sh.wscan[lane % W] : 0ull;
+  Count base = lane < warp ? Count(sh.wscan[lane % W]) : Count(0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
   base += incl - cnt;
-  int above = int(base & 0xFFFFFFFFull), ties = int(base >> 32);
+  int above = int(base & ((Count(1) << H) - 1)), ties = int(base >> H);
   each([&](int b, uint32_t k) {
     if (k == kForced || k > cut) {
       idx[above + min(ties, need)] = b;
@@ -1293,12 +1318,38 @@ __device__ __forceinline__ void select_blocks(const SelectArgs& a, int blocks, i
   });
 }
 
+// The same for at most NT blocks: thread b counts the keys before its own.  keys
+// holds up to three more entries than blocks.
+template <int NT>
+__device__ __forceinline__ void rank_blocks(const SelectArgs& a, int blocks, int32_t* idx, SelShared<NT>& sh,
+                                            uint32_t* keys) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 3) keys[blocks + tid] = 0u;  // never before a real key
+  __syncthreads();
+  const uint32_t own = tid < blocks ? keys[tid] : 0u;
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < blocks; j += 4) {
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + j);
+    rank += (k.x > own || (k.x == own && j < tid)) + (k.y > own || (k.y == own && j + 1 < tid)) +
+            (k.z > own || (k.z == own && j + 2 < tid)) + (k.w > own || (k.w == own && j + 3 < tid));
+  }
+  const bool take = tid < blocks && rank < a.n_sel;  // a forced block's key is the largest
+  const unsigned m = __ballot_sync(0xffffffffu, take);
+  if (lane == 0) sh.wsum[warp] = __popc(m);
+  __syncthreads();
+  int at = __popc(m & ((1u << lane) - 1u));
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) at += w < warp ? sh.wsum[w] : 0;
+  if (take) idx[at] = tid;
+}
+
 // One cluster per (KV head, query): its CTAs score the head's blocks and put the
 // keys into the first CTA's shared memory, which selects.  Bound by the latency of
 // its phases for short sequences and by reading the bounds for long ones.
 template <int NT, int HD>
 __global__ void __launch_bounds__(NT) kv8_select_kernel(const SelectArgs a) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ SelShared<NT> sh;
   pdl_wait();
   pdl_trigger();
@@ -1311,18 +1362,24 @@ __global__ void __launch_bounds__(NT) kv8_select_kernel(const SelectArgs a) {
     return;
   }
   if (ranks == 1) {
-    score_blocks<NT, HD>(a, g, qi, blocks, 0, 1, [&](int b, uint32_t k) { keys[b] = k; });
+    score_blocks<NT, HD>(a, g, qi, blocks, 0, 1, [] {}, [&](int b, uint32_t k) { keys[b] = k; });
     __syncthreads();
   } else {
     uint32_t first;
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(first) : "r"(smem_u32(keys)));
     // no CTA writes into the first one before it runs
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    score_blocks<NT, HD>(a, g, qi, blocks, rank, ranks, [&](int b, uint32_t k) {
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first + 4u * uint32_t(b)), "r"(k) : "memory");
-    });
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    score_blocks<NT, HD>(
+        a, g, qi, blocks, rank, ranks, [] { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); },
+        [&](int b, uint32_t k) {
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first + 4u * uint32_t(b)), "r"(k) : "memory");
+        });
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank) return;
+  }
+  if (NT == kSelNarrow) {  // launched for at most kSelNarrowBlocks
+    rank_blocks<NT>(a, blocks, idx, sh, keys);
+    return;
   }
   const auto key = [&](int b) { return keys[b]; };
   if (blocks <= NT) select_blocks<NT, 1>(a, blocks, idx, sh, key);
@@ -1341,7 +1398,7 @@ __global__ void __launch_bounds__(NT) kv8_score_kernel(const SelectArgs a) {
   const int blocks = int(kv8_blocks(seen_positions(a) + qi));
   if (blocks == 0) return;
   uint32_t* out = a.keys + (int64_t(qi) * a.n_kvh + g) * a.nb;
-  score_blocks<NT, HD>(a, g, qi, blocks, blockIdx.x, gridDim.x, [&](int b, uint32_t k) { out[b] = k; });
+  score_blocks<NT, HD>(a, g, qi, blocks, blockIdx.x, gridDim.x, [] {}, [&](int b, uint32_t k) { out[b] = k; });
 }
 template <int NT>
 __global__ void __launch_bounds__(NT) kv8_select_scratch_kernel(const SelectArgs a) {
@@ -1358,10 +1415,6 @@ __global__ void __launch_bounds__(NT) kv8_select_scratch_kernel(const SelectArgs
   const uint32_t* keys = a.keys + (int64_t(qi) * a.n_kvh + g) * a.nb;
   select_blocks<NT, 0>(a, blocks, idx, sh, [&](int b) { return __ldcg(keys + b); });
 }
-
-constexpr int kSelWide = 1024, kSelNarrow = 256;  // threads of a selection
-constexpr int kSelNarrowBlocks = 256;             // most blocks of the narrow one
-constexpr int kSelCluster = 8;  // clusters of 16 CTAs of this size do not all fit at once (15,626 blocks: 22 us, 18 with 8)
 
 }  // namespace
 
@@ -1531,7 +1584,7 @@ nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, 
 }
 
 // dynamic shared memory of a selection, its static part held back
-constexpr size_t kSelStatic = 8192;
+constexpr size_t kSelStatic = 13312;
 
 static bool kv8_select_fits(const Ctx* c, int64_t blocks) {
   return size_t(blocks) * sizeof(uint32_t) + kSelStatic <= c->smem_optin;
@@ -1571,7 +1624,7 @@ nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, 
   const int64_t groups = int64_t(kv.n_kvh) * nq;
   if (blocks <= kSelNarrowBlocks)
     return cuda_check(c, launch_k(c, h128 ? kv8_select_kernel<kSelNarrow, 128> : kv8_select_kernel<kSelNarrow, 64>,
-                                  dim3(1, kv.n_kvh, nq), dim3(kSelNarrow), size_t(blocks) * sizeof(uint32_t), st, a),
+                                  dim3(1, kv.n_kvh, nq), dim3(kSelNarrow), size_t(blocks + 3) * sizeof(uint32_t), st, a),
                       "block select launch");
   if (kv8_select_fits(c, blocks)) {
     // CTAs per cluster: a pass of work for each, and the grid within the SMs
