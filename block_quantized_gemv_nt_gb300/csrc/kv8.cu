@@ -548,9 +548,19 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   __shared__ float s_amax[R * KS][8];  // by k-step and row
   constexpr int ST = L::stages;
   __shared__ __align__(8) uint64_t bars[kAttnWarps][2 * ST];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = lane >> 2, c = lane & 3;
+  // what needs no input runs before the wait for the kernel in front
+  if (a.cluster) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // our shared memory may be written
+  const uint8_t* ring = sm8 + L::ring + size_t(warp) * ST * L::stage;  // stages of K rows, then V rows
+  const uint32_t bar = smem_u32(&bars[warp][0]);                       // [stage]: K, V
+  const uint64_t pol = policy_evict_first();
+  if (lane == 0) {
+    for (int i = 0; i < 2 * ST; ++i) mbar_init(bar + 8 * i, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = lane >> 2, c = lane & 3;
   const int g = blockIdx.x, s = blockIdx.y;
   const int qi0 = SPARSE ? blockIdx.z / a.chunks : 0;
   const int row0 = (SPARSE ? blockIdx.z % a.chunks : blockIdx.z) * ROWS;
@@ -566,10 +576,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const int steps = SPARSE ? a.n_sel * (kB / kStep) : (tokens + kStep - 1) / kStep;
   const int per = split_steps(steps, a.S);
   const int st0 = s * per, st1 = min(steps, st0 + per);
-  if (a.cluster)
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA's shared memory may be written
-  else if (st0 >= st1 && s > 0)
-    return;
+  if (!a.cluster && st0 >= st1 && s > 0) return;
 
   // this thread's q values, requested before the copies of K and V fill the memory system
   constexpr int QI = (R * KS + kAttnWarps - 1) / kAttnWarps;  // fragments per thread
@@ -586,14 +593,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const float* vsg = a.vs + int64_t(g) * a.nb;
   const int32_t* list = SPARSE ? a.idx + (int64_t(qi0) * a.n_kvh + g) * a.n_sel : nullptr;
   const int blocks_seen = (tokens + kB - 1) / kB;
-  const uint8_t* ring = sm8 + L::ring + size_t(warp) * ST * L::stage;  // stages of K rows, then V groups
-  const uint32_t bar = smem_u32(&bars[warp][0]);                       // [stage]: K, V
-  const uint64_t pol = policy_evict_first();
-  if (lane == 0) {
-    for (int i = 0; i < 2 * ST; ++i) mbar_init(bar + 8 * i, 1);
-    fence_barrier_init();
-  }
-  __syncwarp();
 
   // first token of step st (tokens: nothing to do)
   const auto step_token = [&](int st) {
