@@ -520,9 +520,6 @@ __device__ __forceinline__ void st_cluster(uint32_t at, int rank, float2 v) {
 // outputs [warps][R][HD / 8][32] x 8
 template <int HD, int R, int U>
 struct AttnKv8Smem {
-  // steps in flight per warp: one of 32 tokens with 16 warps on an SM keeps HBM busy;
-  // short steps, and the 8 warps of R = 2, take two
-  static constexpr int stages = R == 2 || U == 1 ? 2 : 1;
   static constexpr size_t q = 0;
   static constexpr size_t ml = q + size_t(R) * (HD / 16) * 512;
   static constexpr size_t push = ml + size_t(2) * kAttnWarps * 8 * R * 4;           // from the cluster: outputs
@@ -530,7 +527,7 @@ struct AttnKv8Smem {
   static constexpr size_t ring = push_ml + size_t(kMaxCluster) * 8 * R * 8;
   static constexpr size_t stage = size_t(16 * U) * HD * 2;           // K, then V
   static constexpr size_t outs = size_t(R) * (HD / 8) * 256;         // one warp's outputs
-  static constexpr size_t bytes = ring + kAttnWarps * (stages * stage > outs ? stages * stage : outs);
+  static constexpr size_t bytes = ring + kAttnWarps * (stage > outs ? stage : outs);
 };
 
 template <int FMT, int HD, int R, int U, bool SPARSE>
@@ -546,16 +543,17 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   extern __shared__ __align__(16) uint8_t sm8[];
   uint4* qa = reinterpret_cast<uint4*>(sm8 + L::q);
   __shared__ float s_amax[R * KS][8];  // by k-step and row
-  constexpr int ST = L::stages;
-  __shared__ __align__(8) uint64_t bars[kAttnWarps][2 * ST];
+  __shared__ __align__(8) uint64_t bars[kAttnWarps][2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = lane >> 2, c = lane & 3;
   // what needs no input runs before the wait for the kernel in front
   if (a.cluster) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // our shared memory may be written
-  const uint8_t* ring = sm8 + L::ring + size_t(warp) * ST * L::stage;  // stages of K rows, then V rows
-  const uint32_t bar = smem_u32(&bars[warp][0]);                       // [stage]: K, V
+  const uint8_t* sk = sm8 + L::ring + size_t(warp) * L::stage;  // this warp's K rows of a step
+  const uint8_t* sv = sk + kStep * HD;                           // and its V rows
+  const uint32_t bar = smem_u32(&bars[warp][0]);                 // K, V
   const uint64_t pol = policy_evict_first();
   if (lane == 0) {
-    for (int i = 0; i < 2 * ST; ++i) mbar_init(bar + 8 * i, 1);
+    mbar_init(bar, 1);
+    mbar_init(bar + 8, 1);
     fence_barrier_init();
   }
   __syncwarp();
@@ -601,22 +599,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     const int b = __ldg(list + st / (kB / kStep));
     return b < 0 || b >= blocks_seen ? tokens : min(tokens, b * kB + st % (kB / kStep) * kStep);
   };
-  // the copies of one step's K and V, rows below `tokens` only; step number i of this
-  // warp's (steps without tokens not counted) goes through stage i % ST
-  int sent_k = 0, sent_v = 0, done = 0;
-  const auto copy = [&](const uint8_t* from, int which, int t0, int& sent) {
-    if (t0 >= tokens) return;
-    if (lane == 0) {
-      const int i = sent % ST;
-      const uint32_t bytes = min(kStep, tokens - t0) * HD, on = bar + 16 * i + 8 * which;
-      mbar_arrive_expect_tx(on, bytes);
-      if (!a.stall)
-        bulk_g2s(smem_u32(ring + i * L::stage + which * kStep * HD), from + int64_t(t0) * HD, bytes, on, pol);
-    }
-    ++sent;
+  // the copy of one step's K (which 0) or V (1), rows below `tokens` only
+  const auto copy = [&](const uint8_t* from, int which, int t0) {
+    if (t0 >= tokens || lane != 0) return;
+    const uint32_t bytes = min(kStep, tokens - t0) * HD, on = bar + 8 * which;
+    mbar_arrive_expect_tx(on, bytes);
+    if (!a.stall) bulk_g2s(smem_u32(which ? sv : sk), from + int64_t(t0) * HD, bytes, on, pol);
   };
+  uint32_t phase = 0;
   const auto wait = [&](int which) {
-    const uint32_t on = bar + 16 * (done % ST) + 8 * which, phase = (done / ST) & 1;
+    const uint32_t on = bar + 8 * which;
     if (mbar_test(on, phase)) return true;
     const bool ok = __all_sync(0xffffffffu, mbar_wait(on, phase, a.stall ? kStallSpin : kMaxSpin));
     if (!ok && lane == 0) flag_error(a.err, kErrWaitTimeout);
@@ -626,16 +618,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     return t0 < tokens ? make_float2(__ldg(ksg + t0 / kB), __ldg(vsg + t0 / kB)) : make_float2(0.f, 0.f);
   };
   int st = st0 + warp;
-  int tq[ST + 1];   // first tokens of this step and the next ones
-  float2 kvq[ST];
-#pragma unroll
-  for (int i = 0; i <= ST; ++i) tq[i] = step_token(st + i * kAttnWarps);
-#pragma unroll
-  for (int i = 0; i < ST; ++i) {
-    copy(kg, 0, tq[i], sent_k);
-    copy(vg, 1, tq[i], sent_v);
-    kvq[i] = scales(tq[i]);
-  }
+  int t0 = step_token(st), t1 = step_token(st + kAttnWarps);  // this step's first token, the next one's
+  copy(kg, 0, t0);
+  copy(vg, 1, t0);
+  float2 kvs = scales(t0);
 
   // q: each row scaled by a power of two to amax in [2^13, 2^14), split, laid out as
   // fragments: warp w holds k-step w % KS of every row
@@ -686,16 +672,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   }
   const int fewest = SPARSE ? tokens : n_pos + query_of(0);  // positions every row sees
   for (; st < st1; st += kAttnWarps) {
-    const int t0 = tq[0];
-    const float2 kvs = kvq[0];
-    const uint8_t* sk = ring + done % ST * L::stage;
-    const uint8_t* sv = sk + kStep * HD;
-#pragma unroll
-    for (int i = 0; i < ST; ++i) tq[i] = tq[i + 1];
-#pragma unroll
-    for (int i = 0; i + 1 < ST; ++i) kvq[i] = kvq[i + 1];
-    kvq[ST - 1] = scales(tq[ST - 1]);
-    tq[ST] = step_token(st + (ST + 1) * kAttnWarps);
+    const int t2 = step_token(st + 2 * kAttnWarps);
+    const float2 kvs1 = scales(t1);
     // ---- scores
     float sc[R][2 * U][CH][4];
     if (t0 < tokens) {
@@ -728,7 +706,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       }
     }
     __syncwarp();  // this step's K is in registers and used
-    copy(kg, 0, tq[ST - 1], sent_k);
+    copy(kg, 0, t1);
     uint4 pf[R][U];
     if (t0 < tokens) {
       // ---- online softmax: p = 2^(s - m + kPTop).  The f16 operand of P V is p
@@ -797,7 +775,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     }
     if (t0 < tokens) {
       if (!wait(1)) break;
-      ++done;
+      phase ^= 1;
       // ---- P V: words of two tokens interleaved into (token, token + 1) pairs per
       // channel.  Each step's products start from zero and are added to the output
       // in fp32: the tensor cores round their sums towards zero, and a bias of one
@@ -847,7 +825,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       }
     }
     __syncwarp();  // and its V
-    copy(vg, 1, tq[ST - 1], sent_v);
+    copy(vg, 1, t1);
+    t0 = t1;
+    t1 = t2;
+    kvs = kvs1;
   }
 
   // ---- merge the warps
