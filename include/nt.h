@@ -89,8 +89,10 @@ nt_status nt_ctx_destroy(nt_ctx* ctx);
 /* [road] Wait for all work of this context's device, then report any asynchronous
  * CUDA error or device-side flag and clear the flag: NT_ERR_TIMEOUT when a
  * bounded wait inside a kernel ran out; NT_ERR_INVALID_ARG when a position
- * held on the device (a decode step continued with token < 0) ran past the
- * KV cache — the kernels then wrote nothing outside the caches. */
+ * held on the device (a decode step continued with token < 0, or the pos_dev
+ * of an 8-bit cache call) ran past the KV cache — the kernels then wrote
+ * nothing outside the caches — or a NaN or an infinity was written to an 8-bit
+ * KV cache. */
 nt_status nt_ctx_sync(nt_ctx* ctx);
 /* [road] Wait at most timeout_us for the work enqueued on `stream` to finish (a
  * host-side poll with a deadline), then report like nt_ctx_sync:
@@ -109,10 +111,11 @@ nt_status nt_debug_fail_copy(nt_ctx* ctx, int nth);
 /* [road] Test hook for the device-side bounded waits (failure detection; no
  * GPU is made to fault or hang): the next n eager launches in this process
  * of the kernels that wait on bulk copies — the quant GEMV (nt_gemv_q,
- * nt_gemv_q_multi, nt_gemv_swiglu), nt_attn_decode and
- * nt_attn_decode_static — issue no copies, so their waits run out after a
- * few tries and take the timeout path: the context flag that nt_ctx_sync
- * reports as NT_ERR_TIMEOUT, or NaN output from nt_attn_decode_static.
+ * nt_gemv_q_multi, nt_gemv_swiglu), nt_attn_decode, nt_attn_decode_static,
+ * nt_attn_kv8 and nt_attn_kv8_blocks — issue no copies, so their waits run out
+ * after a few tries and take the timeout path: the context flag that
+ * nt_ctx_sync reports as NT_ERR_TIMEOUT, or NaN output from
+ * nt_attn_decode_static.
  * Launches on a stream being captured are never armed.  n = 0 disarms;
  * n outside 0..1000 is NT_ERR_INVALID_ARG. */
 nt_status nt_debug_stall_waits(int n);
@@ -330,8 +333,8 @@ nt_status nt_kv8_read(nt_ctx* ctx, const nt_kv8* cache, int64_t pos0, int64_t n,
  *   out_h = softmax_j(q_h . K_g[j] / sqrt(head_dim)) . V_g[j].
  * q_dev, out_dev fp32 [n_query][n_qh][head_dim], 16-byte aligned; n_qh is 1..16
  * times n_kvh.  A query with no positions (n_pos = 0) gives zeros.  Positions
- * the query does not see may hold anything.  Scales may be any normal positive
- * floats.  Scores, probabilities and sums are fp32-accurate: q and the
+ * from n_pos + n_query - 1 on may hold anything.  Scales may be any normal
+ * positive floats.  Scores, probabilities and sums are fp32-accurate: q and the
  * probabilities enter the tensor cores as two f16 parts each.
  * pos_dev (nullable): n_pos = *pos_dev + 1 is read from the device and the
  * argument ignored (a captured call can be replayed); a value outside the cache
@@ -354,8 +357,10 @@ nt_status nt_attn_kv8(nt_ctx* ctx, const float* q_dev, const nt_kv8* cache, floa
  * order; all B and then -1 when B <= n_sel.  The whole-number sums make the
  * choice independent of the order of additions.  Needs kmin / kmax;
  * n_first + n_last <= n_sel <= 2^24; q, n_pos, n_query and pos_dev as
- * nt_attn_kv8.  Uses the context scratch beyond its first 32 MiB: NT_ERR_OOM
- * when 4 * n_query * n_kvh * ceil(kv_stride / 64) bytes do not fit. */
+ * nt_attn_kv8.  One launch without scratch up to about 54,000 blocks (of the
+ * query, or of kv_stride with pos_dev); beyond that two, with the context scratch
+ * beyond its first 32 MiB: NT_ERR_OOM when 4 * n_query * n_kvh *
+ * ceil(kv_stride / 64) bytes do not fit. */
 nt_status nt_kv8_select(nt_ctx* ctx, const float* q_dev, const nt_kv8* cache, int n_qh, int64_t n_pos, int n_query,
                         const int64_t* pos_dev, int n_sel, int n_first, int n_last, int32_t* idx_dev, void* stream);
 

@@ -32,7 +32,7 @@ def _e4m3_table():
     return t
 
 
-E4M3_VALUES = _e4m3_table()  # 0x7F and 0xFF (NaN in E4M3) read as the 480 their bits would be
+E4M3_VALUES = _e4m3_table()  # (0x7F and 0xFF are NaN in E4M3 and never written)
 
 
 def to_values(b, fmt):

@@ -504,6 +504,56 @@ def test_captured_step_replays_with_a_device_position(ctx):
     ctx.sync()
 
 
+@pytest.mark.parametrize("n", [200, 1000, 20000])
+def test_stalled_copies_are_reported(ctx, n):
+    """Bounded waits: with the copies held back (the test hook) the attention gives up, the sync reports a timeout, and
+    the next call on the context is right (one CTA a head, a cluster, two launches)."""
+    _, nt = _mods()
+    H, G, hd = 2, 4, 128
+    g, c, rng = _filled(ctx, I8, H, hd, n, n, 25)
+    q = rng.normal(size=(1, H * G, hd)).astype(np.float32)
+    out = torch.empty((1, H * G, hd), device="cuda")
+    idx = torch.arange(ref.blocks(n), dtype=torch.int32, device="cuda").repeat(1, H, 1).contiguous()
+    for call in (lambda: g.attend(dev(q), out, n), lambda: g.attend_blocks(dev(q), out, n, idx)):
+        nt.nt_debug_stall_waits(1)
+        try:
+            call()
+        finally:
+            nt.nt_debug_stall_waits(0)
+        with pytest.raises(nt.NtError) as e:
+            ctx.sync()
+        assert e.value.status == nt.NT_ERR_TIMEOUT
+        call()
+        ctx.sync()
+        _check(host(out), *ref.attend_cache(c, q, n))
+
+
+def test_rewriting_rows_changes_nothing(ctx):
+    """The same rows written again at the same positions: the scales and bytes stay."""
+    rng = np.random.default_rng(26)
+    g, c = _cache(ctx, E4M3, 2, 64, 300)
+    k, v = _rows(rng, 200, 2, 64, 2.0), _rows(rng, 200, 2, 64)
+    g.append(dev(k), dev(v), 0)
+    g.append(dev(k[70:]), dev(v[70:]), 70)
+    c.append(k, v, 0)
+    c.append(k[70:], v[70:], 70)
+    before = {n: host(b).copy() for n, b in g.buffers.items()}
+    _same(g, c, 200)
+    g.append(dev(k[70:]), dev(v[70:]), 70)
+    for n, b in g.buffers.items():
+        assert np.array_equal(host(b), before[n], equal_nan=b.dtype == torch.float32), n
+
+
+def test_output_in_place_of_q(ctx):
+    """out may be q itself, whatever the number of splits."""
+    for n, nq in ((100, 1), (1000, 3), (9000, 1), (9000, 8)):
+        g, c, rng = _filled(ctx, I8, 2, 128, n + nq - 1, n + nq, 27)
+        q = rng.normal(size=(nq, 8, 128)).astype(np.float32)
+        x = dev(q)
+        g.attend(x, x, n)
+        _check(host(x), *ref.attend_cache(c, q, n))
+
+
 def test_streams_and_contexts(ctx):
     """Two contexts on two streams at once, each ordered on its own stream behind the work that makes its inputs."""
     _, nt = _mods()
