@@ -135,8 +135,8 @@ struct AppendShared {
 // is read once.  Rows the block already holds are loaded in the same round and
 // restated only when the scale grows.  FULL: the rows are the whole block, and no
 // row is tested.  Prompts are bound by HBM (32,767 F32 rows of 8 x 128: 51 us, 335 MB
-// at 6.6 TB/s); F16 rows to E4M3 by instruction issue (131,072 rows: 138 us, 5.8
-// TB/s); a single token by the latency of its two memory round trips (2.4 us).
+// at 6.6 TB/s; 131,072 F16 rows to E4M3: 129 us, 805 MB at 6.3 TB/s); a single token
+// by the latency of its two memory round trips (2.4 us).
 template <int FMT, int HD, typename T, bool FULL>
 __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& sh, int64_t pos, int64_t blk, int r0,
                                              int r1) {
@@ -229,46 +229,91 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
   if (threadIdx.x == 0) *scale = t;
 
   const bool sums = w == 0 && a.kmin;
-  __half2 lo[VEC / 2], hi[VEC / 2];  // the stored values' bounds, in the order of to_h2; exact in f16
+  // bounds of the stored values (plus `offset`), exact in f16; pair j: channels ch and ch + PS
+  constexpr bool HALF = FULL && VEC == 8;
+  constexpr int PS = HALF ? 1 : kPairStep<FMT>;
+  float offset = 0.f;
+  __half2 lo[VEC / 2], hi[VEC / 2];
 #pragma unroll
   for (int j = 0; j < VEC / 2; ++j) {
     lo[j] = __half2half2(__ushort_as_half(0x7C00));  // +inf
     hi[j] = __half2half2(__ushort_as_half(0xFC00));
   }
+  const auto bound = [&](int j, uint32_t z) {
+    const __half2 y = *reinterpret_cast<const __half2*>(&z);
+    lo[j] = __hmin2(lo[j], y);
+    hi[j] = __hmax2(hi[j], y);
+  };
+  if (HALF && clean && inv <= 32768.f) {
+    // F16 rows stay F16: the product with a power of two is exact down to the f16
+    // subnormals, which are far below half of the least 8-bit value; I8 adds 1.5 *
+    // 2^10 in the same step, which rounds to the whole number in the low byte
+    const __half2 inv2 = __half2half2(__float2half_rn(inv)), magic = __half2half2(__ushort_as_half(0x6600));
+    if (FMT == NT_KV8_I8) offset = 1536.f;
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = row + i * RP;
-    if (!FULL && r >= r1) continue;
-    const float f = !FULL && r < r0 ? restate : inv;
-    uint32_t packed[VEC / 4];
+    for (int i = 0; i < NP; ++i) {
+      const __half2* x = reinterpret_cast<const __half2*>(&raw[i]);
+      uint32_t packed[2];
 #pragma unroll
-    for (int k = 0; k < VEC / 4; ++k) {
-      float v[4];
-      values(i, k, v);
-      if (!clean && (FULL || r >= r0)) {  // NaN is stored as 0, an infinity as the largest value
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float top = (FMT == NT_KV8_I8 ? 127.f : 448.f) * t;
-          v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j], -top), top);
-        }
-      }
-      packed[k] = pack8<FMT>(v, f);
-      if (sums) {
+      for (int k = 0; k < 2; ++k) {
         uint32_t z[2];
-        to_h2<FMT>(packed[k], z[0], z[1]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const __half2 y = *reinterpret_cast<const __half2*>(&z[j]);
-          lo[2 * k + j] = __hmin2(lo[2 * k + j], y);
-          hi[2 * k + j] = __hmax2(hi[2 * k + j], y);
+        if (FMT == NT_KV8_I8) {
+          const __half2 q0 = __hfma2(x[2 * k], inv2, magic), q1 = __hfma2(x[2 * k + 1], inv2, magic);
+          z[0] = *reinterpret_cast<const uint32_t*>(&q0);
+          z[1] = *reinterpret_cast<const uint32_t*>(&q1);
+          packed[k] = __byte_perm(z[0], z[1], 0x6420);
+        } else {
+          const __half2 q0 = __hmul2(x[2 * k], inv2), q1 = __hmul2(x[2 * k + 1], inv2);
+          uint16_t b0, b1;
+          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b0) : "r"(*reinterpret_cast<const uint32_t*>(&q0)));
+          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(*reinterpret_cast<const uint32_t*>(&q1)));
+          packed[k] = uint32_t(b0) | (uint32_t(b1) << 16);
+          if (sums) to_h2<FMT>(packed[k], z[0], z[1]);
+        }
+        if (sums) {
+          bound(2 * k, z[0]);
+          bound((2 * k + 1) % (VEC / 2), z[1]);
         }
       }
+      *reinterpret_cast<uint2*>(dst + (row + i * RP) * HD) = make_uint2(packed[0], packed[1]);
     }
-    if (FULL || r >= r0 || restate != 1.f) {
-      if (VEC == 4)
-        *reinterpret_cast<uint32_t*>(dst + r * HD) = packed[0];
-      else
-        *reinterpret_cast<uint2*>(dst + r * HD) = make_uint2(packed[0], packed[VEC / 4 - 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int r = row + i * RP;
+      if (!FULL && r >= r1) continue;
+      const float f = !FULL && r < r0 ? restate : inv;
+      uint32_t packed[VEC / 4];
+#pragma unroll
+      for (int k = 0; k < VEC / 4; ++k) {
+        float v[4];
+        values(i, k, v);
+        if (!clean && (FULL || r >= r0)) {  // NaN is stored as 0, an infinity as the largest value
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float top = (FMT == NT_KV8_I8 ? 127.f : 448.f) * t;
+            v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j], -top), top);
+          }
+        }
+        packed[k] = pack8<FMT>(v, f);
+        if (sums) {
+          uint32_t z[2];
+          to_h2<FMT>(packed[k], z[0], z[1]);
+          if (PS != kPairStep<FMT>) {
+            const uint32_t y = __byte_perm(z[0], z[1], 0x5410);
+            z[1] = __byte_perm(z[0], z[1], 0x7632);
+            z[0] = y;
+          }
+          bound(2 * k, z[0]);
+          bound(2 * k + 1, z[1]);
+        }
+      }
+      if (FULL || r >= r0 || restate != 1.f) {
+        if (VEC == 4)
+          *reinterpret_cast<uint32_t*>(dst + r * HD) = packed[0];
+        else
+          *reinterpret_cast<uint2*>(dst + r * HD) = make_uint2(packed[0], packed[VEC / 4 - 1]);
+      }
     }
   }
   if (!sums) return;
@@ -282,13 +327,12 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
   if (lane < TR) {
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) {
-      // pair j of to_h2 holds bytes b and b + kPairStep
-      const int ch = VEC * tr + 4 * (j / 2) + (j & 1) * (3 - kPairStep<FMT>);
+      const int ch = VEC * tr + 4 * (j / 2) + (j & 1) * (3 - PS);
       const float2 l = __half22float2(lo[j]), u = __half22float2(hi[j]);
-      sh.smin[warp][ch] = l.x;
-      sh.smin[warp][ch + kPairStep<FMT>] = l.y;
-      sh.smax[warp][ch] = u.x;
-      sh.smax[warp][ch + kPairStep<FMT>] = u.y;
+      sh.smin[warp][ch] = l.x - offset;
+      sh.smin[warp][ch + PS] = l.y - offset;
+      sh.smax[warp][ch] = u.x - offset;
+      sh.smax[warp][ch + PS] = u.y - offset;
     }
   }
   __syncthreads();

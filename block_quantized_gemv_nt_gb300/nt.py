@@ -161,9 +161,7 @@ def lib():
 
 # ---------------------------------------------------------------------------
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 

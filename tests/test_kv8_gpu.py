@@ -208,6 +208,41 @@ def test_write_strides_and_f16_cache(ctx):
 
 
 @pytest.mark.parametrize("fmt", [I8, E4M3])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_write_f16_rows(ctx, fmt, hd):
+    """F16 rows, whole blocks and ragged ones: every f16 magnitude from subnormals to 65504, ties, a block with an
+    infinity, one with a NaN, and blocks so small that 1 / scale is no f16 number."""
+    _, nt = _mods()
+    rng = np.random.default_rng(40 + fmt)
+    H, n = 2, 64 * 12 + 30
+    x = rng.normal(size=(n, H, hd)) * np.exp2(rng.integers(-3, 4, size=(n, H, 1)))
+    x *= np.repeat(np.exp2(np.array([0, -24, -20, -14, -9, -8, -6, 3, 10, 13, 0, 0, 0.0])), 64)[:n, None, None]
+    x[64 * 10:64 * 11] = (np.arange(64) - 31.5)[:, None, None] / 2
+    x = np.clip(x, -65504, 65504).astype(np.float16)
+    x[0, 0, 0], x[64 * 9, 0, 3], x[64 * 9 + 1, 1, 4] = 65504, 65504, -65504
+    g, c = _cache(ctx, fmt, H, hd, n + 10)
+    d = dev(x)
+    g.append(d[:100], d[:100], 0)
+    g.append(d[100:], d[100:], 100)
+    c.append(x[:100], x[:100], 0)
+    c.append(x[100:], x[100:], 100)
+    ctx.sync()
+    _same(g, c, n)
+    y = x[:128].copy()
+    y[70, 0, 5], y[71, 1, 6], y[72, 1, 7] = np.nan, np.inf, -np.inf
+    g.append(dev(y), dev(y), 0)
+    c.append(y, y, 0)
+    with pytest.raises(nt.NtError):
+        ctx.sync()
+    nb = ref.blocks(128)
+    for w in "kv":
+        assert np.array_equal(host(g.buffers[w])[:, :128], c.data[w][:, :128])
+        assert np.array_equal(host(g.buffers[w + "scale"])[:, :nb].astype(np.float64), c.scale[w][:, :nb])
+    assert np.array_equal(host(g.buffers["kmin"])[:, :nb], c.kmin[:, :nb])
+    assert np.array_equal(host(g.buffers["kmax"])[:, :nb], c.kmax[:, :nb])
+
+
+@pytest.mark.parametrize("fmt", [I8, E4M3])
 def test_write_extremes_and_non_finite(ctx, fmt):
     """Zeros, the smallest and largest floats, values at a scale's border; NaN and infinities are stored as 0
     and as the largest value, move no scale, and are reported by the sync."""
