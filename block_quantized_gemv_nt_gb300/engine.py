@@ -57,6 +57,9 @@ class HostBlobs:
         return self.blob[layer].numpy()[o:o + r * rb].reshape(r, rb)
 
 
+_ROW_FMT = {torch.float32: nt.F32, torch.float16: nt.F16}
+
+
 class KV8Cache:
     """One layer's 8-bit KV cache in HBM (torch allocations, or `buffers`: a dict
     of tensors k, v, kscale, vscale and, for block selection, kmin, kmax) and the
@@ -82,10 +85,10 @@ class KV8Cache:
 
     def _rows(self, k, v, tok, head):
         shape, stride, dtype = k.shape, k.stride(), k.dtype
-        if (len(shape) != 3 or shape != v.shape or dtype != v.dtype or stride != v.stride() or stride[2] != 1
-                or shape[head] != self.n_kvh or shape[2] != self.head_dim):
+        if (len(shape) != 3 or shape[head] != self.n_kvh or shape[2] != self.head_dim or stride[2] != 1
+                or v.stride() != stride or v.shape != shape or v.dtype is not dtype):
             raise ValueError("k and v: rows of n_kvh heads of head_dim channels, alike in layout")
-        fmt = nt.F32 if dtype is torch.float32 else nt.F16 if dtype is torch.float16 else None
+        fmt = _ROW_FMT.get(dtype)
         if fmt is None:
             raise ValueError("rows must be float32 or float16")
         return fmt, shape[tok], stride[tok], stride[head]

@@ -308,29 +308,36 @@ def nt_attn_verify(ctx, q, kcache, vcache, out, n_qh, n_kvh, head_dim, n_pos0, n
                                          head_dim, n_pos0, n_query, kv_stride, _stream(stream, out)))
 
 
+# the calls of a decode step: the C functions are looked up once (ctypes takes the structure by reference)
+_kv8_append, _kv8_read, _attn_kv8 = _lib.nt_kv8_append, _lib.nt_kv8_read, _lib.nt_attn_kv8
+_kv8_select, _attn_kv8_blocks = _lib.nt_kv8_select, _lib.nt_attn_kv8_blocks
+
+
 def nt_kv8_append(ctx, cache: nt_kv8, src_fmt, k, v, n_tok, tok_stride, head_stride, pos, pos_dev=None, stream=None):
-    return ctx.check(_lib.nt_kv8_append(ctx.handle, ctypes.byref(cache), src_fmt, _ptr(k), _ptr(v), n_tok, tok_stride,
-                                        head_stride, pos, _ptr(pos_dev), _stream(stream, k)))
+    return ctx.check(_kv8_append(ctx.handle, cache, src_fmt, _ptr(k), _ptr(v), n_tok, tok_stride, head_stride, pos,
+                                 pos_dev if pos_dev is None else _ptr(pos_dev), _stream(stream, k)))
 
 
 def nt_kv8_read(ctx, cache: nt_kv8, pos0, n, dst_fmt, k, v, head_stride, stream=None):
-    return ctx.check(_lib.nt_kv8_read(ctx.handle, ctypes.byref(cache), pos0, n, dst_fmt, _ptr(k), _ptr(v), head_stride,
-                                      _stream(stream, v if k is None else k)))
+    return ctx.check(_kv8_read(ctx.handle, cache, pos0, n, dst_fmt, _ptr(k), _ptr(v), head_stride,
+                               _stream(stream, v if k is None else k)))
 
 
 def nt_attn_kv8(ctx, q, cache: nt_kv8, out, n_qh, n_pos, n_query=1, pos_dev=None, stream=None):
-    return ctx.check(_lib.nt_attn_kv8(ctx.handle, _ptr(q), ctypes.byref(cache), _ptr(out), n_qh, n_pos, n_query,
-                                      _ptr(pos_dev), _stream(stream, out)))
+    return ctx.check(_attn_kv8(ctx.handle, _ptr(q), cache, _ptr(out), n_qh, n_pos, n_query,
+                               pos_dev if pos_dev is None else _ptr(pos_dev), _stream(stream, out)))
 
 
 def nt_kv8_select(ctx, q, cache: nt_kv8, n_qh, n_pos, n_query, n_sel, n_first, n_last, idx, pos_dev=None, stream=None):
-    return ctx.check(_lib.nt_kv8_select(ctx.handle, _ptr(q), ctypes.byref(cache), n_qh, n_pos, n_query, _ptr(pos_dev),
-                                        n_sel, n_first, n_last, _ptr(idx), _stream(stream, idx)))
+    return ctx.check(_kv8_select(ctx.handle, _ptr(q), cache, n_qh, n_pos, n_query,
+                                 pos_dev if pos_dev is None else _ptr(pos_dev), n_sel, n_first, n_last, _ptr(idx),
+                                 _stream(stream, idx)))
 
 
 def nt_attn_kv8_blocks(ctx, q, cache: nt_kv8, out, n_qh, n_pos, n_query, idx, n_sel, pos_dev=None, stream=None):
-    return ctx.check(_lib.nt_attn_kv8_blocks(ctx.handle, _ptr(q), ctypes.byref(cache), _ptr(out), n_qh, n_pos, n_query,
-                                             _ptr(pos_dev), _ptr(idx), n_sel, _stream(stream, out)))
+    return ctx.check(_attn_kv8_blocks(ctx.handle, _ptr(q), cache, _ptr(out), n_qh, n_pos, n_query,
+                                      pos_dev if pos_dev is None else _ptr(pos_dev), _ptr(idx), n_sel,
+                                      _stream(stream, out)))
 
 
 def nt_host_register(ctx, host_ptr: int, nbytes: int, read_only: bool = True):
