@@ -1,4 +1,4 @@
-"""The 8-bit KV cache and its attentions in plain numpy, 64 bits: the checker of
+"""The 8-bit KV cache and its attentions in plain numpy, 64 bits: the oracle of
 the GPU kernels (its own pins are in test_kv8_ref.py)."""
 import math
 

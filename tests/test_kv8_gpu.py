@@ -1,4 +1,4 @@
-"""The 8-bit KV cache on the GPU against the 64-bit numpy checker (kv8_ref):
+"""The 8-bit KV cache on the GPU against the 64-bit numpy oracle (kv8_ref):
 rows quantised as they are written and read back (bit-exact), attention over
 the cache, block selection (exact indices) and attention over chosen blocks."""
 import numpy as np
@@ -27,7 +27,7 @@ def _mods():
 
 
 def _cache(ctx, fmt, H, hd, stride):
-    """A device cache and its checker; the device buffers start as noise (nothing needs initialising)."""
+    """A device cache and its oracle; the device buffers start as noise (nothing needs initialising)."""
     engine, _ = _mods()
     g = engine.KV8Cache(ctx, fmt, H, hd, stride)
     gen = torch.Generator(device="cuda").manual_seed(7)
@@ -46,7 +46,7 @@ def _rows(rng, n, H, hd, grow=0.0):
 
 
 def _same(g, c, n):
-    """The device state equals the checker's for positions below n."""
+    """The device state equals the oracle's for positions below n."""
     nb = ref.blocks(n)
     for w in "kv":
         assert np.array_equal(host(g.buffers[w])[:, :n], c.data[w][:, :n]), w
@@ -462,7 +462,7 @@ def test_block_lists(ctx, fmt):
 @pytest.mark.parametrize("fmt", [I8, E4M3])
 def test_decode_run(ctx, fmt):
     """A prompt, then decode steps: append, attend, select, attend to the chosen blocks, all enqueued on one stream
-    without a sync in between; each step against the checker."""
+    without a sync in between; each step against the oracle."""
     H, G, hd, prompt, steps, n_sel = 2, 4, 128, 250, 140, 4
     rng = np.random.default_rng(19)
     stride = prompt + steps
@@ -494,13 +494,17 @@ def test_decode_run(ctx, fmt):
     _same(g, c, stride)
 
 
-def test_captured_step_replays_with_a_device_position(ctx):
+@pytest.mark.parametrize("capacity", [200, 3000, 20000])
+def test_captured_step_replays_with_a_device_position(ctx, capacity):
     """One CUDA graph of a whole step (append, attend, select, attend to blocks) replayed while the position moves on
-    the device; past the cache's end it writes nothing and the sync reports it."""
+    the device (the launches are sized by the capacity: one CTA a head, a cluster, two launches); past the cache's
+    end it writes nothing and the sync reports it."""
     _, nt = _mods()
-    H, G, hd, start, stride, n_sel = 2, 4, 128, 120, 200, 3
+    H, G, hd, n_sel, steps = 2, 4, 128, 3, 80
+    stride, start = capacity, capacity - steps
+    if capacity > 200:  # short at first, then at the end
+        start = 120
     g, c, rng = _filled(ctx, I8, H, hd, start, stride, 20)
-    steps = stride - start
     k, v = _rows(rng, steps, H, hd), _rows(rng, steps, H, hd)
     q = rng.normal(size=(steps, 1, H * G, hd)).astype(np.float32)
     pos = torch.tensor([start], dtype=torch.int64, device="cuda")
@@ -514,6 +518,12 @@ def test_captured_step_replays_with_a_device_position(ctx):
         g.select(qb, ib, 0, n_first=0, n_last=1, pos_dev=pos)
         g.attend_blocks(qb, sb, 0, ib, pos_dev=pos)
 
+    def compare(t, n):
+        _check(host(ob), *ref.attend_cache(c, q[t], n))
+        want = ref.select(c, q[t], n, n_sel, 0, 1)
+        assert np.array_equal(host(ib), want)
+        _check(host(sb), *ref.attend_cache(c, q[t], n, want))
+
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         step()
@@ -522,11 +532,17 @@ def test_captured_step_replays_with_a_device_position(ctx):
         graph.replay()
         c.append(k[t:t + 1], v[t:t + 1], start + t)
         if t % 9 == 0 or t == steps - 1:
-            _check(host(ob), *ref.attend_cache(c, q[t], start + t + 1))
-            want = ref.select(c, q[t], start + t + 1, n_sel, 0, 1)
-            assert np.array_equal(host(ib), want)
-            _check(host(sb), *ref.attend_cache(c, q[t], start + t + 1, want))
+            compare(t, start + t + 1)
         pos += 1
+    if capacity > 200:  # the rest of the cache at once, with rows at a device position; the last position by replay
+        m = stride - start - steps - 1
+        km, vm = _rows(rng, m, H, hd), _rows(rng, m, H, hd)
+        g.append(dev(km), dev(vm), 0, pos_dev=pos)
+        c.append(km, vm, start + steps)
+        pos += m
+        graph.replay()
+        c.append(k[steps - 1:], v[steps - 1:], stride - 1)
+        compare(steps - 1, stride)
     ctx.sync()
     before = {n: b.clone() for n, b in g.buffers.items()}
     for bad in (stride, -1, 2 ** 62):

@@ -1,4 +1,4 @@
-"""Pins of the 64-bit checker of the 8-bit KV cache (kv8_ref), and what the
+"""Pins of the 64-bit oracle of the 8-bit KV cache (kv8_ref), and what the
 binding and its cache class refuse without a GPU."""
 import ctypes
 import math
