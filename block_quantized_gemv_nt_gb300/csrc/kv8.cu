@@ -1566,25 +1566,26 @@ nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, 
   int64_t S = int64_t(c->num_sms) * (R == 1 ? 2 : 1) / (int64_t(kv.n_kvh) * z);
   if (S > kMaxSplits) S = kMaxSplits;
   if (S < 1) S = 1;
-  // Steps of 32 tokens unless 16 give more warps work: 8 KV heads, 32,768 positions
-  // 19.9 us against 21.0; 1024 positions 6.5 against 5.7.  One CTA a head does up to
-  // 256 positions in one step (4.4 us; two CTAs of shorter steps 4.9).
-  const auto long_steps = [&](int64_t splits) {
-    return R == 2 || most <= 32 * kAttnWarps || most >= splits * 32 * kAttnWarps;
-  };
   const auto useful = [&](int u) { return std::max<int64_t>(1, (most + 16 * kAttnWarps * u - 1) / (16 * kAttnWarps * u)); };
   const size_t vecs = size_t(n_qh) * nq, row = vecs * (kv.head_dim * 4 + 8);
-  // Up to 512 positions a split, the splits of a head run as one cluster of at most 16
+  // Up to 768 positions a split, the splits of a head run as one cluster of at most 16
   // and join in shared memory: one launch instead of two (2 us of host time; on the
-  // GPU 1024 positions 5.0 against 5.7 us, 8192 equal, 16,384 16.0 against 15.2).  The
-  // CTAs of R = 2 fill an SM each, so their clusters take at most half of the SMs.
+  // GPU, 8 KV heads, 1024 positions 5.0 against 5.7 us, 12,000 13.2 against 15.7,
+  // 16,384 15.8 against 14.3).  The CTAs of R = 2 fill an SM each, so their clusters
+  // take at most half of the SMs.
   const int64_t groups = int64_t(kv.n_kvh) * z;
   const int64_t widest = std::min<int64_t>({kMaxCluster, R * kv.head_dim / 8, S, R == 1 ? S : c->num_sms / 2 / groups});
   int64_t C = 1;
   while (C < useful(R) && 2 * C <= widest) C *= 2;
-  a.cluster = useful(2) > 1 && C > 1 && most <= 512 * C;
-  S = a.cluster ? C : S;
-  const int U = long_steps(S) ? 2 : 1;
+  a.cluster = useful(2) > 1 && C > 1 && most <= 768 * C;
+  if (a.cluster) S = C;
+  // Steps of 32 tokens where every warp has one, else of 16, which give more warps
+  // work (two launches, 8 KV heads: 32,768 positions 19.9 against 21.0 us, 1024 6.5
+  // against 5.7); a cluster's few warps take 16 up to 640 positions a split (4160
+  // positions 8.1 against 8.6 us, 12,000 13.2 against 13.6).  One CTA a head does up
+  // to 256 positions in one step (4.4 us; two CTAs of shorter steps 4.9).
+  const int64_t long_from = a.cluster ? 640 * S : 32 * kAttnWarps * S;
+  const int U = R == 2 || most <= 32 * kAttnWarps || most >= long_from ? 2 : 1;
   if (!a.cluster) S = std::min<int64_t>({S, useful(U), std::max<int64_t>(1, int64_t(scratch_bytes / row))});
   a.S = int(S);
   a.part = reinterpret_cast<float*>(scratch);
