@@ -1072,7 +1072,9 @@ AttnKv8Variant attn_kv8_for(int fmt, int hd, int R, int U) {
 constexpr int kSelBins = 1024;
 constexpr int kSelWide = 1024, kSelNarrow = 256;  // threads of a selection
 constexpr int kSelNarrowBlocks = kSelNarrow;      // most blocks of the narrow one: one a thread
-constexpr int kSelCluster = 8;  // clusters of 16 CTAs of this size do not all fit at once (15,626 blocks: 22 us, 18 with 8)
+// most CTAs of a selection's cluster, an SM each: larger clusters of 8 heads do not all
+// fit on the GPU at once (15,626 blocks: 8 CTAs 18.0 us, 12 17.0, 14 22.9, 16 22.0)
+constexpr int kSelCluster = 12;
 constexpr uint32_t kForced = 0xFFFFFFFFu;  // key of a block that is taken whatever its score
 
 struct SelectArgs {
@@ -1649,8 +1651,7 @@ nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, 
                       "block select launch");
   if (kv8_select_fits(c, blocks)) {
     // CTAs per cluster: a pass of work for each, and the grid within the SMs
-    int ranks = 1;
-    while (ranks < kSelCluster && ranks * pass < blocks && 2 * ranks * groups <= c->num_sms) ranks *= 2;
+    const int ranks = int(std::max<int64_t>(1, std::min<int64_t>({kSelCluster, (blocks + pass - 1) / pass, c->num_sms / groups})));
     return cuda_check(c, launch_cluster(c, h128 ? kv8_select_kernel<kSelWide, 128> : kv8_select_kernel<kSelWide, 64>,
                                         dim3(ranks, kv.n_kvh, nq), dim3(kSelWide), size_t(blocks) * sizeof(uint32_t),
                                         st, dim3(ranks, 1, 1), a),
