@@ -76,12 +76,12 @@ class KV8Cache:
         if buffers is None:
             names = list(shapes) if bounds else list(shapes)[:4]
             buffers = {n: torch.zeros(shapes[n][0], dtype=shapes[n][1], device=device) for n in names}
-        self.device = buffers["k"].device
+        self.device, self.index = buffers["k"].device, buffers["k"].get_device()  # index -1: host memory
         for n, t in buffers.items():
             if (tuple(t.shape) != shapes[n][0] or t.dtype != shapes[n][1] or not t.is_contiguous()
                     or t.device != self.device):
                 raise ValueError(f"{n}: need a contiguous {shapes[n][1]} tensor of shape {shapes[n][0]}, all on one device")
-        if ctx is not None and (self.device.type != "cuda" or self.device.index != ctx.device):
+        if ctx is not None and self.index != ctx.device:
             raise ValueError("the cache must be on the context's device")
         self.buffers = buffers
         self.desc = nt.nt_kv8(fmt, n_kvh, head_dim, kv_stride,
@@ -91,7 +91,7 @@ class KV8Cache:
         shape, stride, dtype = k.shape, k.stride(), k.dtype
         if (len(shape) != 3 or shape[head] != self.n_kvh or shape[2] != self.head_dim or stride[2] != 1
                 or v.stride() != stride or v.shape != shape or v.dtype is not dtype
-                or k.device != self.device or v.device != self.device):
+                or k.get_device() != self.index or v.get_device() != self.index):
             raise ValueError("k and v: rows of n_kvh heads of head_dim channels on the cache's device, alike in layout")
         fmt = _ROW_FMT.get(dtype)
         if fmt is None:
@@ -118,10 +118,10 @@ class KV8Cache:
     def _queries(self, q, out=None):
         shape = q.shape
         if (len(shape) != 3 or shape[2] != self.head_dim or q.dtype is not torch.float32 or not q.is_contiguous()
-                or q.device != self.device):
+                or q.get_device() != self.index):
             raise ValueError("q: contiguous float32 [n_query][n_qh][head_dim] on the cache's device")
         if out is not None and (out.shape != shape or out.dtype is not torch.float32 or not out.is_contiguous()
-                                or out.device != self.device):
+                                or out.get_device() != self.index):
             raise ValueError("out: like q")
         return shape[0], shape[1]
 
@@ -133,7 +133,7 @@ class KV8Cache:
     def _list(self, idx, nq):
         shape = idx.shape
         if (len(shape) != 3 or shape[0] != nq or shape[1] != self.n_kvh or idx.dtype is not torch.int32
-                or not idx.is_contiguous() or idx.device != self.device):
+                or not idx.is_contiguous() or idx.get_device() != self.index):
             raise ValueError("idx: contiguous int32 [n_query][n_kvh][n_sel] on the cache's device")
         return shape[2]
 
