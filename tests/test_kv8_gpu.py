@@ -319,7 +319,7 @@ def test_attention_lengths(ctx, fmt, n_pos, nq):
 @pytest.mark.parametrize("fmt", [I8, E4M3])
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("H,G,nq", [(1, 1, 1), (8, 1, 2), (3, 3, 1), (4, 7, 1), (8, 8, 1), (2, 16, 1), (2, 16, 16),
-                                    (1, 5, 7), (64, 2, 1)])
+                                    (1, 5, 7), (64, 2, 1), (2, 3, 6), (1, 11, 3), (3, 16, 2), (1, 1, 16)])
 def test_attention_heads(ctx, fmt, hd, H, G, nq):
     n_pos = 777
     g, c, rng = _filled(ctx, fmt, H, hd, n_pos + nq - 1, n_pos + nq - 1, 200 + H)
@@ -555,16 +555,16 @@ def test_captured_step_replays_with_a_device_position(ctx, capacity):
     ctx.sync()
 
 
-@pytest.mark.parametrize("n", [200, 1000, 20000])
-def test_stalled_copies_are_reported(ctx, n):
+@pytest.mark.parametrize("n,nq", [(200, 1), (1000, 1), (20000, 1), (3000, 3), (3000, 7)])
+def test_stalled_copies_are_reported(ctx, n, nq):
     """Bounded waits: with the copies held back (the test hook) the attention gives up, the sync reports a timeout, and
-    the next call on the context is right (one CTA a head, a cluster, two launches)."""
+    the next call on the context is right (one CTA a head, a cluster, two launches, more rows than a warp's 8)."""
     _, nt = _mods()
     H, G, hd = 2, 4, 128
-    g, c, rng = _filled(ctx, I8, H, hd, n, n, 25)
-    q = rng.normal(size=(1, H * G, hd)).astype(np.float32)
-    out = torch.empty((1, H * G, hd), device="cuda")
-    idx = torch.arange(ref.blocks(n), dtype=torch.int32, device="cuda").repeat(1, H, 1).contiguous()
+    g, c, rng = _filled(ctx, I8, H, hd, n + nq - 1, n + nq - 1, 25)
+    q = rng.normal(size=(nq, H * G, hd)).astype(np.float32)
+    out = torch.empty((nq, H * G, hd), device="cuda")
+    idx = torch.arange(ref.blocks(n + nq), dtype=torch.int32, device="cuda").repeat(nq, H, 1).contiguous()
     for call in (lambda: g.attend(dev(q), out, n), lambda: g.attend_blocks(dev(q), out, n, idx)):
         nt.nt_debug_stall_waits(1)
         try:
