@@ -107,8 +107,8 @@ class Cache:
         return to_values(self.data[w][:, at], self.fmt) * self.scale[w][:, at // B][..., None]
 
 
-def attend(q, k, v):
-    """q [R][hd], k, v [n][hd] -> (out [R][hd], tolerance [R][hd]).
+def attend(q, k, v, vs=None):
+    """q [R][hd], k, v [n][hd], vs [n] the scales of v (None: ones) -> (out [R][hd], tolerance [R][hd]).
 
     The tolerance follows the kernel's arithmetic.  A score: q's two f16 parts
     carry 2^-22 of each product's size; the tensor cores add hd / 16 groups
@@ -116,6 +116,11 @@ def attend(q, k, v):
     maximum round three times.  A probability: the exponential 2^-21, its two f16
     parts 2^-22.  Sums over positions: at most one rounding of 2^-23 per step of
     16 positions a warp takes (n / 16 bounds them) and per merged partial (200).
+    Underflow: the f16 operand of position i is p_i vs_i 2^8 / 2^m with 2^m at most the
+    largest p_j 2^floor(log2 vs_j) (vs_j floored at 2^-64), and its low part is a
+    multiple of f16's smallest step 2^-24: half of it, 2^-25, times 2^m / 2^8 and the
+    cached value |v_i| / vs_i, for every position.  It is all that is left of a channel
+    whose dominant positions hold an exact zero.
     """
     R, hd = q.shape
     if k.shape[0] == 0:
@@ -129,7 +134,10 @@ def attend(q, k, v):
     es = size.max(axis=1, keepdims=True) * (2.0 ** -22 * (hd / 16 + 2)) + 3 * 2.0 ** -24 * np.abs(s).max(
         axis=1, keepdims=True)
     rel = 2 * (es + 2.0 ** -21) + 2.0 ** -21 + (min(k.shape[0] / 16, 200) + 200) * 2.0 ** -23
-    return out, rel * (p @ np.abs(v)) + 1e-30
+    vs = np.ones(k.shape[0]) if vs is None else vs
+    top = (p * np.maximum(vs, 2.0 ** -64)).max(axis=1, keepdims=True)
+    cached = (np.abs(v) / np.where(vs == 0, 1.0, vs)[:, None]).sum(axis=0)
+    return out, rel * (p @ np.abs(v)) + 2.0 ** -33 * top * cached + 1e-30
 
 
 def attend_cache(c, q, n_pos, lists=None):
@@ -140,18 +148,18 @@ def attend_cache(c, q, n_pos, lists=None):
     full = None
     if lists is None:
         at = np.arange(n_pos + nq - 1)
-        full = c.read("k", at), c.read("v", at)
+        full = c.read("k", at), c.read("v", at), c.scale["v"][:, at // B]
     for i in range(nq):
         n = n_pos + i
         for g in range(c.H):
             if lists is None:
-                k, v = full[0][g, :n], full[1][g, :n]
+                k, v, vs = (x[g, :n] for x in full)
             else:
                 at = [np.arange(b * B, min(n, b * B + B)) for b in lists[i][g] if 0 <= b < blocks(n)]
                 at = np.concatenate(at) if at else np.zeros(0, np.int64)
-                k, v = c.read("k", at)[g], c.read("v", at)[g]
+                k, v, vs = c.read("k", at)[g], c.read("v", at)[g], c.scale["v"][g, at // B]
             sl = slice(g * G, (g + 1) * G)
-            out[i, sl], tol[i, sl] = attend(q[i, sl].astype(np.float64), k, v)
+            out[i, sl], tol[i, sl] = attend(q[i, sl].astype(np.float64), k, v, vs)
     return out, tol
 
 

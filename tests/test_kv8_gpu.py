@@ -365,6 +365,25 @@ def test_attention_scale_ranges(ctx):
             _check(host(out), *ref.attend_cache(c, q, n_pos))
 
 
+@pytest.mark.parametrize("fmt", [I8, E4M3])
+def test_attention_any_scales(ctx, fmt):
+    """Scales that are no powers of two (a cache quantised elsewhere), every byte of I8 (-128 included)."""
+    H, G, hd, n = 2, 4, 128, 64 * 9 + 5
+    g, c, rng = _filled(ctx, fmt, H, hd, n, n, 28)
+    for w in "kv":
+        c.scale[w] = (c.scale[w] * rng.uniform(0.3, 3.0, size=c.scale[w].shape)).astype(np.float32).astype(np.float64)
+        g.buffers[w + "scale"].copy_(torch.from_numpy(c.scale[w].astype(np.float32)))
+        if fmt == I8:
+            c.data[w][:, :32] = rng.integers(0, 256, size=c.data[w][:, :32].shape, dtype=np.uint8)
+            c.data[w][:, 3] = 0x80
+            g.buffers[w].copy_(torch.from_numpy(c.data[w]))
+    for nq in (1, 5):
+        q = rng.normal(size=(nq, H * G, hd)).astype(np.float32)
+        out = torch.empty((nq, H * G, hd), device="cuda")
+        g.attend(dev(q), out, n - nq + 1)
+        _check(host(out), *ref.attend_cache(c, q, n - nq + 1))
+
+
 def test_attention_nan_query_stays_in_its_row(ctx):
     H, G, hd, n = 2, 4, 128, 300
     g, c, rng = _filled(ctx, I8, H, hd, n, n, 15)
