@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 // q (and of the probabilities) is split into hi = f16(x), lo = f16(x - hi), which
 // carries 22 bits; the M = 16 rows of an MMA are the hi parts of 8 rows and, 8
 // below, their lo parts, so the two halves of a product meet in one thread:
-// accumulators c0 + c2 and c1 + c3.
+// accumulators c0 + c2 and c1 + c3.  A probability's parts stop at f16's smallest step:
+// 2^-33 of the largest weight is what is lost of each position.
 //
 // Fragments come without a transpose: MMA k and n indices are ours to name.  Lane
 // (n = lane / 4, c = lane % 4), a step of 16 U tokens:
@@ -661,19 +662,27 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     mbar_arrive_expect_tx(on, bytes);
     if (!a.stall) bulk_g2s(smem_u32(which ? sv : sk), from + int64_t(t0) * HD, bytes, on, pol);
   };
+  int st = st0 + warp;
+  int t0 = step_token(st), t1 = step_token(st + kAttnWarps);  // this step's first token, the next one's
   uint32_t phase = 0;
   const auto wait = [&](int which) {
     const uint32_t on = bar + 8 * which;
     if (mbar_test(on, phase)) return true;
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(on, phase, a.stall ? kStallSpin : kMaxSpin));
-    if (!ok && lane == 0) flag_error(a.err, kErrWaitTimeout);
+    const int cap = a.stall ? kStallSpin : kMaxSpin;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(on, phase, cap));
+    if (!ok) {  // flag it, wait (bounded) for the copies still in flight, go on to the merge
+      if (lane == 0) flag_error(a.err, kErrWaitTimeout);
+      mbar_wait(on, phase, cap);
+      if (which == 0)
+        mbar_wait(bar + 8, phase, cap);  // this step's V
+      else if (t1 < tokens)
+        mbar_wait(bar, phase ^ 1, cap);  // the next step's K
+    }
     return ok;
   };
   const auto scales = [&](int t0) {
     return t0 < tokens ? make_float2(__ldcg(ksg + t0 / kB), __ldcg(vsg + t0 / kB)) : make_float2(0.f, 0.f);
   };
-  int st = st0 + warp;
-  int t0 = step_token(st), t1 = step_token(st + kAttnWarps);  // this step's first token, the next one's
   copy(kg, 0, t0);
   copy(vg, 1, t0);
   float2 kvs = scales(t0);
