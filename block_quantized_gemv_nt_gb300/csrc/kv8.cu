@@ -37,6 +37,10 @@ __device__ __forceinline__ float kv8_scale(float a) {
   if (FMT == NT_KV8_I8) return pow2_scale<6, 0x7E0000u>(a);  // QMAX 127 = 1.984375 * 2^6
   return pow2_scale<8, 0x600000u>(a);                        // QMAX 448 = 1.75 * 2^8
 }
+// the least power of two >= t (positive and normal)
+__device__ __forceinline__ float pow2_ceil(float t) {
+  return __uint_as_float((__float_as_uint(t) + 0x7FFFFFu) & 0xFF800000u);
+}
 __device__ __forceinline__ float pow2_inv(float t) { return __uint_as_float((254u << 23) - __float_as_uint(t)); }
 
 // four finite values times inv (1 / scale) -> four bytes, nearest, ties to even.  I8:
@@ -224,7 +228,9 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
 #pragma unroll
     for (int i = 0; i < W; ++i) amax = fmaxf(amax, sh.red[i]);
   }
-  const float t = fmaxf(kv8_scale<FMT>(amax), t_old);
+  // A block begun elsewhere may have any scale: it goes on at the next power of two,
+  // and its rows are restated to it like those of a block that grows.
+  const float t = fmaxf(kv8_scale<FMT>(amax), pow2_ceil(t_old));
   const float inv = pow2_inv(t), restate = t_old * inv;
   if (threadIdx.x == 0) *scale = t;
 

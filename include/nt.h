@@ -275,12 +275,13 @@ enum { NT_KV8_I8 = 0, NT_KV8_E4M3 = 1 };
 #define NT_KV8_BLOCK 64
 
 /* One layer's 8-bit KV cache, in buffers of the caller.  The value at position p
- * of head h is byte value * scale[h][p / 64].  Scales are powers of two, at
- * least 2^-100.  kmin / kmax (both or neither) bound each block's k per channel
- * in units of its scale (I8) or of 4 times its scale (E4M3, rounded outwards);
- * nt_kv8_append keeps them and nt_kv8_select reads them.  k, v, kmin and kmax
- * 16-byte aligned, scales 4-byte.  Nothing needs to be initialised: a block is
- * begun by the append that writes its first position. */
+ * of head h is byte value * scale[h][p / 64].  The scales that nt_kv8_append
+ * writes are powers of two from 2^-100 to 2^122; a cache quantised elsewhere may
+ * have others (each call says which).  kmin / kmax (both or neither) bound each
+ * block's k per channel in units of its scale (I8) or of 4 times its scale (E4M3,
+ * rounded outwards); nt_kv8_append keeps them and nt_kv8_select reads them.  k, v,
+ * kmin and kmax 16-byte aligned, scales 4-byte.  Nothing needs to be initialised:
+ * a block is begun by the append that writes its first position. */
 typedef struct {
   int fmt;              /* NT_KV8_I8 or NT_KV8_E4M3 */
   int n_kvh, head_dim;  /* 1..64 heads of 64 or 128 channels */
@@ -299,9 +300,11 @@ typedef struct {
  * head_stride = kv_stride * head_dim.  For each block touched, head, and K and V:
  *   need = the least power of two >= 2^-100 with max |x| <= 127 (I8) or 448
  *   (E4M3) times it, over the block's new rows;  scale = need when the rows
- *   begin the block, else max(old scale, need);
+ *   begin the block, else max(old scale, need), where an old scale that is no
+ *   power of two (a block begun elsewhere; normal, at most 2^126) counts as the
+ *   next one above it;
  *   new rows are x / scale rounded to nearest, ties to even; when the scale
- *   grows, the block's earlier rows are rounded the same way to the new scale.
+ *   changes, the block's earlier rows are rounded the same way to the new scale.
  * Rows of the block behind the last one written no longer count: a shorter
  * sequence is continued by appending at its end (a speculative step that was
  * cut back), and kmin / kmax then bound the block's rows up to the last written.

@@ -1,0 +1,102 @@
+"""The 8-bit cache at the edges of its formats: blocks begun elsewhere with scales
+that are no powers of two."""
+import math
+
+import numpy as np
+import pytest
+
+import kv8_ref as ref
+from gpu_util import dev, host, need_gpu, torch
+
+pytestmark = pytest.mark.gpu
+I8, E4M3 = ref.I8, ref.E4M3
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    need_gpu()
+    from block_quantized_gemv_nt_gb300 import nt
+    c = nt.Context(0)
+    yield c
+    c.sync()
+    c.close()
+
+
+def _new(ctx, fmt, H, hd, n):
+    from block_quantized_gemv_nt_gb300 import engine
+    return engine.KV8Cache(ctx, fmt, H, hd, n), ref.Cache(fmt, H, hd, n)
+
+
+def _upload(g, c):
+    for w in "kv":
+        g.buffers[w].copy_(torch.from_numpy(c.data[w]))
+        g.buffers[w + "scale"].copy_(torch.from_numpy(c.scale[w].astype(np.float32)))
+
+
+class Continued(ref.Cache):
+    """A cache whose blocks may have been begun elsewhere: an old scale that is no power of two counts as the next one
+    above it, and the block's earlier rows are rounded to the new scale (E4M3: from the fp32 product with the ratio)."""
+
+    def _block(self, w, h, b, lo, hi, x):
+        fmt, data, finite = self.fmt, self.data[w][h], np.abs(x)[np.isfinite(x)]
+        t = ref.scale_for(finite.max() if finite.size else 0.0, ref.QMAX[fmt])
+        if lo > b * ref.B:
+            old = self.scale[w][h, b]
+            t = max(t, old if math.frexp(old)[0] == 0.5 else 2.0 ** math.ceil(math.log2(old)))
+            v = ref.to_values(data[b * ref.B:lo], fmt) * (old / t)
+            # I8 -128 is a value of such a cache: it stays where the ratio rounds it
+            q = np.rint(v) if fmt == I8 else ref.round8(v.astype(np.float32).astype(np.float64), fmt)
+            data[b * ref.B:lo] = ref.to_bytes(q, fmt)
+        data[lo:hi] = ref.to_bytes(ref.round8(np.where(np.isnan(x), 0.0, x) / t, fmt), fmt)
+        self.scale[w][h, b] = t
+        if w == "k":
+            q, u = ref.to_values(data[b * ref.B:hi], fmt), 1.0 if fmt == I8 else 4.0
+            self.kmin[h, b], self.kmax[h, b] = np.floor(q.min(axis=0) / u), np.ceil(q.max(axis=0) / u)
+
+
+@pytest.mark.parametrize("src", ["f32", "f16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("fmt", [I8, E4M3])
+def test_append_continues_blocks_of_any_scale(ctx, fmt, hd, src):
+    """Rows behind those of a cache quantised elsewhere: the old rows keep their values to half a step of the new
+    scale, the new rows are right, in growing blocks and in blocks that need no larger scale."""
+    H, n0, n1 = 3, 64 + 21, 64 * 2 + 9
+    rng = np.random.default_rng(50 + fmt)
+    g, _ = _new(ctx, fmt, H, hd, n1)
+    for size in (0.01, 1.0, 300.0):
+        c = Continued(fmt, H, hd, n1)
+        for w in "kv":
+            b = rng.integers(0, 256, size=(H, n1, hd), dtype=np.uint8)
+            if fmt == E4M3:
+                b[(b & 0x7F) == 0x7F] = 0x7E
+            c.data[w] = b
+            s = rng.uniform(0.01, 0.1, size=c.scale[w].shape).astype(np.float32)
+            s[:, 0], s[0, 1], s[1, 1] = 0.03, 1.5 / 64, np.nextafter(np.float32(1 / 64), np.float32(0))
+            c.scale[w] = s.astype(np.float64)
+        c.data["k"][:, n0 - 1, 0] = 0x80 if fmt == I8 else 0xFE
+        _upload(g, c)
+        before = {w: c.read(w, np.arange(n0)) for w in "kv"}
+        x = (rng.normal(size=(2, n1 - n0, H, hd)) * size).astype(np.float32 if src == "f32" else np.float16)
+        at = n0
+        for m in (1, 1, 45, n1 - n0 - 47):  # within the block, over its end
+            rows = x[:, at - n0:at - n0 + m]
+            g.append(dev(rows[0]), dev(rows[1]), at)
+            c.append(rows[0], rows[1], at)
+            at += m
+            nb = ref.blocks(at)
+            for w in "kv":
+                assert np.array_equal(host(g.buffers[w + "scale"])[:, 1:nb].astype(np.float64), c.scale[w][:, 1:nb]), w
+                assert np.array_equal(host(g.buffers[w])[:, :at], c.data[w][:, :at]), w
+            assert np.array_equal(host(g.buffers["kmin"])[:, 1:nb], c.kmin[:, 1:nb])
+            assert np.array_equal(host(g.buffers["kmax"])[:, 1:nb], c.kmax[:, 1:nb])
+        ctx.sync()
+        back = torch.empty(H, n1, hd, device="cuda"), torch.empty(H, n1, hd, device="cuda")
+        g.read(0, *back)
+        for w, got in zip("kv", back):
+            got = host(got).astype(np.float64)
+            t = host(g.buffers[w + "scale"]).astype(np.float64)[:, np.arange(n1) // 64][..., None]
+            new = x["kv".index(w)].astype(np.float64).transpose(1, 0, 2)
+            for have, want, step in ((got[:, 64:n0], before[w][:, 64:], t[:, 64:n0]), (got[:, n0:], new, t[:, n0:])):
+                # half a step a rounding; the scale grows at most log2 times, each time by a factor of two or more
+                half = step / 2 if fmt == I8 else np.maximum(np.abs(want) * 2.0 ** -4, step * 2.0 ** -10)
+                assert np.all(np.abs(have - want) <= 2.0 * half * (1 + 2.0 ** -4)), w
