@@ -288,17 +288,18 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
     for (int i = 0; i < NP; ++i) {
       const int r = row + i * RP;
       if (!FULL && r >= r1) continue;
-      const float f = !FULL && r < r0 ? restate : inv;
+      const bool mend = !clean && (FULL || r >= r0);
+      const float f = !FULL && r < r0 ? restate : mend ? 1.f : inv;
       uint32_t packed[VEC / 4];
 #pragma unroll
       for (int k = 0; k < VEC / 4; ++k) {
         float v[4];
         values(i, k, v);
-        if (!clean && (FULL || r >= r0)) {  // NaN is stored as 0, an infinity as the largest value
+        if (mend) {  // NaN is stored as 0, an infinity as the largest value: over the scale, where that cannot overflow
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float top = (FMT == NT_KV8_I8 ? 127.f : 448.f) * t;
-            v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j], -top), top);
+            constexpr float top = FMT == NT_KV8_I8 ? 127.f : 448.f;
+            v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j] * inv, -top), top);
           }
         }
         packed[k] = pack8<FMT>(v, f);

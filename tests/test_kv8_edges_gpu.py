@@ -1,5 +1,5 @@
 """The 8-bit cache at the edges of its formats: blocks begun elsewhere with scales
-that are no powers of two."""
+that are no powers of two, the largest floats beside an infinity."""
 import math
 
 import numpy as np
@@ -100,3 +100,28 @@ def test_append_continues_blocks_of_any_scale(ctx, fmt, hd, src):
                 # half a step a rounding; the scale grows at most log2 times, each time by a factor of two or more
                 half = step / 2 if fmt == I8 else np.maximum(np.abs(want) * 2.0 ** -4, step * 2.0 ** -10)
                 assert np.all(np.abs(have - want) <= 2.0 * half * (1 + 2.0 ** -4)), w
+
+
+@pytest.mark.parametrize("fmt", [I8, E4M3])
+def test_infinity_beside_the_largest_floats(ctx, fmt):
+    """An infinity is stored as the largest 8-bit value also in a block whose finite values reach the largest float,
+    a NaN as 0; whole blocks and ragged ones."""
+    from block_quantized_gemv_nt_gb300 import nt
+    H, hd, n = 1, 64, 64 * 3 + 20
+    g, c = _new(ctx, fmt, H, hd, n)
+    top = np.finfo(np.float32).max
+    rng = np.random.default_rng(51)
+    x = (rng.uniform(-1, 1, size=(n, H, hd)) * top).astype(np.float32)
+    x[70, 0, 3] = top
+    x[64 * 3 + 2, 0, 3] = -top
+    for r in (5, 71, 64 * 3 + 5):
+        x[r, 0, 7], x[r, 0, 8], x[r, 0, 9] = np.inf, -np.inf, np.nan
+    g.append(dev(x), dev(-x), 0)
+    c.append(x, -x, 0)
+    with pytest.raises(nt.NtError) as e:
+        ctx.sync()
+    assert e.value.status == nt.NT_ERR_INVALID_ARG
+    for w in "kv":
+        assert np.array_equal(host(g.buffers[w + "scale"]).astype(np.float64), c.scale[w]), w
+        assert np.array_equal(host(g.buffers[w]), c.data[w]), w
+    assert np.array_equal(host(g.buffers["kmin"]), c.kmin) and np.array_equal(host(g.buffers["kmax"]), c.kmax)
