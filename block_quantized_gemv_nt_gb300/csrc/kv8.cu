@@ -10,6 +10,7 @@
 // loses nothing but the low bits that the larger scale cannot hold.
 #include <cuda_fp16.h>
 #include <algorithm>
+#include <type_traits>
 
 #include "kv8_choose.cuh"
 #include "nt_internal.cuh"
@@ -138,9 +139,9 @@ struct AppendShared {
 // the store: the largest |x| is reduced over the CTA between them, so the source
 // is read once.  Rows the block already holds are loaded in the same round and
 // restated only when the scale grows.  FULL: the rows are the whole block, and no
-// row is tested.  Prompts are bound by HBM (32,767 F32 rows of 8 x 128: 51 us, 335 MB
-// at 6.6 TB/s; 131,072 F16 rows to E4M3: 129 us, 805 MB at 6.3 TB/s); a single token
-// by the latency of its two memory round trips (2.4 us).
+// row is tested.  Prompts are bound by HBM (32,767 F32 rows of 8 x 128: 50 us, 335 MB
+// at 6.7 TB/s; 131,072 F16 rows to E4M3: 120 us, 805 MB at 6.7 TB/s); a single token
+// by the latency of its two memory round trips (2.35 us).
 template <int FMT, int HD, typename T, bool FULL>
 __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& sh, int64_t pos, int64_t blk, int r0,
                                              int r1) {
@@ -157,30 +158,32 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
   uint8_t* dst = (w ? a.dst[1] : a.dst[0]) + (int64_t(h) * a.kv_stride + p0) * HD + VEC * tr;
   float* scale = (w ? a.scale[1] : a.scale[0]) + int64_t(h) * a.nb + blk;
 
+  // row r of the block, this thread's channels: the source's, or (below r0) the cache's
+  const auto load_row = [&](int r) {
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (FULL || (r >= r0 && r < r1)) {
+      x = *reinterpret_cast<const uint4*>(src + r * a.tok_stride);
+    } else if (r < r0) {
+      x.x = *reinterpret_cast<const uint32_t*>(dst + r * HD);
+      if (VEC == 8) x.y = *reinterpret_cast<const uint32_t*>(dst + r * HD + 4);
+    }
+    return x;
+  };
   uint4 raw[NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = row + i * RP;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (FULL || (r >= r0 && r < r1)) {
-      raw[i] = *reinterpret_cast<const uint4*>(src + r * a.tok_stride);
-    } else if (r < r0) {
-      raw[i].x = *reinterpret_cast<const uint32_t*>(dst + r * HD);
-      if (VEC == 8) raw[i].y = *reinterpret_cast<const uint32_t*>(dst + r * HD + 4);
-    }
-  }
+  for (int i = 0; i < NP; ++i) raw[i] = load_row(row + i * RP);
   const float t_old = !FULL && r0 > 0 ? *scale : 0.f;
-  // channels 4 k .. 4 k + 3 of pass i: the source's values, or over the old scale the cache's
-  const auto values = [&](int i, int k, float v[4]) {
-    if (!FULL && row + i * RP < r0) {
-      const float4 f = unpack8<FMT>(k ? raw[i].y : raw[i].x);
+  // channels 4 k .. 4 k + 3 of a loaded row: the source's values, or over the old scale the cache's
+  const auto values = [&](const uint4& x, int r, int k, float v[4]) {
+    if (!FULL && r < r0) {
+      const float4 f = unpack8<FMT>(k ? x.y : x.x);
       v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
     } else if (VEC == 4) {
-      v[0] = __uint_as_float(raw[i].x), v[1] = __uint_as_float(raw[i].y);
-      v[2] = __uint_as_float(raw[i].z), v[3] = __uint_as_float(raw[i].w);
+      v[0] = __uint_as_float(x.x), v[1] = __uint_as_float(x.y);
+      v[2] = __uint_as_float(x.z), v[3] = __uint_as_float(x.w);
     } else {
-      const float2 x = h2f(k ? raw[i].z : raw[i].x), y = h2f(k ? raw[i].w : raw[i].y);
-      v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
+      const float2 y = h2f(k ? x.z : x.x), z = h2f(k ? x.w : x.y);
+      v[0] = y.x, v[1] = y.y, v[2] = z.x, v[3] = z.y;
     }
   };
   float amax = 0.f;
@@ -189,7 +192,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
     if (!FULL && row + i * RP < r0) continue;
     if (VEC == 4) {
       float v[4];
-      values(i, 0, v);
+      values(raw[i], row + i * RP, 0, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) amax = max_nan(amax, fabsf(v[j]));
     } else {
@@ -207,19 +210,25 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
   for (int i = 0; i < W; ++i) amax = max_nan(amax, sh.red[i]);
   const bool clean = amax <= 3.402823466e38f;
   if (!clean) {
-    // a NaN or an infinity: the scale follows the finite values
+    // a NaN or an infinity: the scale follows the finite values.  Here and below the
+    // rows are loaded again, in loops that are not unrolled: this rare case's code in
+    // the loops of the others cost every call (one token 2.48 against 2.35 us, the
+    // 131,072-row conversion 129.8 against 119.7).
     if (threadIdx.x == 0) flag_error(a.err, kErrNonFinite);
     amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
+#pragma unroll 1
+    for (int r = row; r < r1; r += RP) {
+      if (r < r0) continue;
+      const uint4 x = load_row(r);
 #pragma unroll
       for (int k = 0; k < VEC / 4; ++k) {
         float v[4];
-        values(i, k, v);
-        if (FULL || row + i * RP >= r0)
-          for (int j = 0; j < 4; ++j)
-            if (fabsf(v[j]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(v[j]));
+        values(x, r, k, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (fabsf(v[j]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(v[j]));
       }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     __syncthreads();
@@ -249,6 +258,41 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
     const __half2 y = *reinterpret_cast<const __half2*>(&z);
     lo[j] = __hmin2(lo[j], y);
     hi[j] = __hmax2(hi[j], y);
+  };
+  // one row: packed, stored, bounded.  CLEAN: finite values; else NaN is stored as 0 and an
+  // infinity as the largest value, clamped over the scale, where that cannot overflow
+  const auto put_row = [&](auto clean_row, int r, const uint4& x) {
+    constexpr bool CLEAN = decltype(clean_row)::value;
+    const bool old = !FULL && r < r0;
+    uint32_t packed[VEC / 4];
+#pragma unroll
+    for (int k = 0; k < VEC / 4; ++k) {
+      float v[4];
+      values(x, r, k, v);
+      if (!CLEAN && !old) {
+        constexpr float top = FMT == NT_KV8_I8 ? 127.f : 448.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j] * inv, -top), top);
+      }
+      packed[k] = pack8<FMT>(v, old ? restate : CLEAN ? inv : 1.f);
+      if (sums) {
+        uint32_t z[2];
+        to_h2<FMT>(packed[k], z[0], z[1]);
+        if (PS != kPairStep<FMT>) {
+          const uint32_t y = __byte_perm(z[0], z[1], 0x5410);
+          z[1] = __byte_perm(z[0], z[1], 0x7632);
+          z[0] = y;
+        }
+        bound(2 * k, z[0]);
+        bound(2 * k + 1, z[1]);
+      }
+    }
+    if (!old || restate != 1.f) {
+      if (VEC == 4)
+        *reinterpret_cast<uint32_t*>(dst + r * HD) = packed[0];
+      else
+        *reinterpret_cast<uint2*>(dst + r * HD) = make_uint2(packed[0], packed[VEC / 4 - 1]);
+    }
   };
   if (HALF && clean && inv <= 32768.f) {
     // F16 rows stay F16: the product with a power of two is exact down to the f16
@@ -283,45 +327,13 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, AppendShared& 
       }
       *reinterpret_cast<uint2*>(dst + (row + i * RP) * HD) = make_uint2(packed[0], packed[1]);
     }
+  } else if (clean) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      if (FULL || row + i * RP < r1) put_row(std::true_type{}, row + i * RP, raw[i]);
   } else {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int r = row + i * RP;
-      if (!FULL && r >= r1) continue;
-      const bool mend = !clean && (FULL || r >= r0);
-      const float f = !FULL && r < r0 ? restate : mend ? 1.f : inv;
-      uint32_t packed[VEC / 4];
-#pragma unroll
-      for (int k = 0; k < VEC / 4; ++k) {
-        float v[4];
-        values(i, k, v);
-        if (mend) {  // NaN is stored as 0, an infinity as the largest value: over the scale, where that cannot overflow
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            constexpr float top = FMT == NT_KV8_I8 ? 127.f : 448.f;
-            v[j] = v[j] != v[j] ? 0.f : fminf(fmaxf(v[j] * inv, -top), top);
-          }
-        }
-        packed[k] = pack8<FMT>(v, f);
-        if (sums) {
-          uint32_t z[2];
-          to_h2<FMT>(packed[k], z[0], z[1]);
-          if (PS != kPairStep<FMT>) {
-            const uint32_t y = __byte_perm(z[0], z[1], 0x5410);
-            z[1] = __byte_perm(z[0], z[1], 0x7632);
-            z[0] = y;
-          }
-          bound(2 * k, z[0]);
-          bound(2 * k + 1, z[1]);
-        }
-      }
-      if (FULL || r >= r0 || restate != 1.f) {
-        if (VEC == 4)
-          *reinterpret_cast<uint32_t*>(dst + r * HD) = packed[0];
-        else
-          *reinterpret_cast<uint2*>(dst + r * HD) = make_uint2(packed[0], packed[VEC / 4 - 1]);
-      }
-    }
+#pragma unroll 1
+    for (int r = row; r < r1; r += RP) put_row(std::false_type{}, r, load_row(r));
   }
   if (!sums) return;
 #pragma unroll
