@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 // q (and of the probabilities) is split into hi = f16(x), lo = f16(x - hi), which
 // carries 22 bits; the M = 16 rows of an MMA are the hi parts of 8 rows and, 8
 // below, their lo parts, so the two halves of a product meet in one thread:
-// accumulators c0 + c2 and c1 + c3.  A probability's parts stop at f16's smallest step:
-// 2^-33 of the largest weight is what is lost of each position.
+// accumulators c0 + c2 and c1 + c3.  The parts of a probability times its V scale stop
+// at f16's smallest step: 2^-33 of the largest such product is what is lost of each position.
 //
 // Fragments come without a transpose: MMA k and n indices are ours to name.  Lane
 // (n = lane / 4, c = lane % 4), a step of 16 U tokens:
@@ -483,7 +483,9 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 // registers and two CTAs an SM: fewer registers spill, a second buffer per warp
 // changes nothing.
 constexpr int kAttnWarps = 8;
-constexpr float kPTop = 8.f, kSlack = 6.f;  // see the softmax
+constexpr float kPTop = 8.f, kLUnit = 0x1p-13f;                   // see the softmax
+constexpr float kSlack = 6.f, kFar = 90.f, kMid = (kFar - kSlack) / 2;
+constexpr float kLowest = -3.402823466e38f;  // the merges' maximum of nothing: 2^(-inf - kLowest) is 0
 constexpr int kMaxCluster = 16;
 
 struct AttnKv8Args {
@@ -792,14 +794,21 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     copy(kg, 0, t1);
     uint4 pf[R][U];
     if (t0 < tokens) {
-      // ---- online softmax: p = 2^(s - m + kPTop).  The f16 operand of P V is p
-      // times the block's V scale, so m follows s plus the exponent of that scale
-      // (floored where a block's V is all but zero).  m is left behind by up to
-      // kSlack before the accumulators are rescaled to a new one: the operand
-      // then stays below 2^(kPTop + kSlack + 1), the largest f16 exponent, and a
-      // warp rescales once or twice in a sequence instead of at every new maximum.
+      // ---- online softmax.  The f16 operand of P V is a probability times the block's
+      // V scale vs = vn 2^lv, 1 <= vn < 2, so the running m follows s + lv and the operand
+      // is p vn with p = 2^(s + lv - m + kPTop).  m is a whole number (base is exact) and is
+      // left behind by up to kSlack before the accumulators are rescaled to a new one:
+      // the operand then stays below 2^(kPTop + kSlack + 1), the largest f16 exponent, and a
+      // warp rescales once or twice in a sequence instead of at every new maximum.  The sum
+      // l takes p 2^-lv in units of 2^13, which keep it within fp32 for every scale that
+      // the cache can hold (2^26 weights of the largest exponent at 2^-100, one at 2^122).
+      // Where s + lv is kFar below m (an all-zero block beside large ones) the outputs
+      // gain nothing, and l takes the exponentials lifted by kFar, out of reach of the
+      // underflow.  Registers hold m - kMid: one comparison finds both cases.
       const float vs = kvs.y;
-      const float lv = fmaxf(float(int(__float_as_uint(vs) >> 23) - 127), -64.f);
+      const uint32_t ve = min(max(__float_as_uint(vs) >> 23, 27u), 249u);  // 2^-100 .. 2^122
+      const float lv = __uint_as_float(0x4B000000u + ve) - (8388608.f + 127.f);
+      const float il = __uint_as_float((254u - ve) << 23), vn = vs * il, lu = il * kLUnit;
 #pragma unroll
       for (int t = 0; t < R; ++t) {
         const float f = rscale[t] * kvs.x;
@@ -824,21 +833,34 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
         float mx = p[0];
 #pragma unroll
         for (int x = 1; x < 4 * U; ++x) mx = fmaxf(mx, p[x]);
-        mx += lv;
-        if (__any_sync(0xffffffffu, mx > m[t] + kSlack)) {
+        float ml = m[t] - lv;
+        if (__any_sync(0xffffffffu, fabsf(mx - ml) > kMid + kSlack)) {
           float mn = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
-          mn = fmaxf(m[t], mn);
-          const float corr = m[t] == -INFINITY ? 0.f : ex2(m[t] - mn);
-          l[t] *= corr;
+          mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2)) + lv;
+          mn = fmaxf(m[t], floorf(mn) - kMid);
+          const float down = m[t] == -INFINITY ? -INFINITY : m[t] - mn;
+          const float corr = ex2(fmaxf(down, -kFar));
+          l[t] = l[t] * corr * ex2(fminf(down + kFar, 0.f));  // in two steps: it may be large
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             o[t][i].x *= corr;
             o[t][i].y *= corr;
           }
           m[t] = mn;
+          ml = mn - lv;
+          if (ml - mx > kMid + kSlack) {
+            const float lifted = (kPTop - kMid + kFar) - ml;
+            float2 far = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < 4 * U; x += 2) {
+              const float2 e = add2(make_float2(p[x], p[x + 1]), make_float2(lifted, lifted));
+              far = add2(far, make_float2(ex2(e.x), ex2(e.y)));
+              p[x] = p[x + 1] = -INFINITY;
+            }
+            l[t] = fmaf(far.x + far.y, lu * ex2(-kFar), l[t]);
+          }
         }
-        const float base = m[t] == -INFINITY ? 0.f : kPTop - m[t];
+        const float base = m[t] == -INFINITY ? 0.f : (kPTop - kMid) - ml;
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -848,12 +870,12 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
             y[x] = add2(make_float2(p[4 * u + 2 * x], p[4 * u + 2 * x + 1]), make_float2(base, base));
             y[x] = make_float2(ex2(y[x].x), ex2(y[x].y));
             sum = add2(sum, y[x]);
-            y[x] = mul2(y[x], make_float2(vs, vs));
+            y[x] = mul2(y[x], make_float2(vn, vn));
           }
           split_h2(y[0].x, y[0].y, pf[t][u].x, pf[t][u].y);
           split_h2(y[1].x, y[1].y, pf[t][u].z, pf[t][u].w);
         }
-        l[t] += sum.x + sum.y;
+        l[t] = fmaf(sum.x + sum.y, lu, l[t]);
       }
     }
     if (t0 < tokens) {
@@ -923,6 +945,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   for (int t = 0; t < R; ++t) {
     l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
     l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
+    if (l[t] > 0x1p40f) {
+      // (V all but zero) m rises by the exponent of l, and l and o fall: in the merges the
+      // weights 2^(m - M) then underflow only where l does not matter either
+      const uint32_t k = __float_as_uint(l[t]) & 0x7F800000u;
+      const float down = __uint_as_float((254u << 23) - k);
+      l[t] *= down;
+      m[t] += float(int(k >> 23) - 127);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[t][i] = mul2(o[t][i], make_float2(down, down));
+    }
     if (c == 0) {
       mm[warp * ROWS + t * 8 + n] = m[t];
       mll[warp * ROWS + t * 8 + n] = l[t];
@@ -940,7 +972,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   for (int t = 0; t < R; ++t) {
     const int r = t * 8 + n;
     if (r >= rows && !a.cluster) continue;
-    float f[kAttnWarps], M = -INFINITY, sum = 0.f;
+    float f[kAttnWarps], M = kLowest, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
       f[w] = mm[w * ROWS + r];
@@ -948,7 +980,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     }
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
-      f[w] = f[w] == -INFINITY ? 0.f : ex2(f[w] - M);
+      f[w] = ex2(f[w] - M);
       sum = fmaf(mll[w * ROWS + r], f[w], sum);
     }
     const int64_t vec = vec_of(r);
@@ -966,8 +998,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
         const int tile = t * NT + i;
         st_cluster(push + ((s * own + tile % own) * 32 + lane) * 8, tile / own, acc);
       } else if (whole) {
-        a.out[vec * HD + (HD / 8) * (2 * c) + i] = acc.x * inv;
-        a.out[vec * HD + (HD / 8) * (2 * c + 1) + i] = acc.y * inv;
+        a.out[vec * HD + (HD / 8) * (2 * c) + i] = acc.x * kLUnit * inv;
+        a.out[vec * HD + (HD / 8) * (2 * c + 1) + i] = acc.y * kLUnit * inv;
       } else {
         *reinterpret_cast<float2*>(a.part + (vec * a.S + s) * HD + (i * 4 + c) * 2) = acc;
       }
@@ -988,7 +1020,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     const int tile = s * own + k, r = tile / NT * 8 + n, i = tile % NT;
     if (r >= rows) continue;
     float2 y[kMaxCluster], z[kMaxCluster];  // all in flight together
-    float M = -INFINITY, sum = 0.f;
+    float M = kLowest, sum = 0.f;
 #pragma unroll
     for (int x = 0; x < kMaxCluster; ++x) {
       y[x] = x < a.S ? pushed_ml[x * ROWS + r] : make_float2(-INFINITY, 0.f);
@@ -999,15 +1031,15 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int x = 0; x < kMaxCluster; ++x) {
-      const float f = y[x].x == -INFINITY ? 0.f : ex2(y[x].x - M);
+      const float f = ex2(y[x].x - M);
       sum = fmaf(y[x].y, f, sum);
       acc.x = fmaf(z[x].x, f, acc.x);
       acc.y = fmaf(z[x].y, f, acc.y);
     }
     const int64_t vec = vec_of(r);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    a.out[vec * HD + (HD / 8) * (2 * c) + i] = acc.x * inv;
-    a.out[vec * HD + (HD / 8) * (2 * c + 1) + i] = acc.y * inv;
+    a.out[vec * HD + (HD / 8) * (2 * c) + i] = acc.x * kLUnit * inv;
+    a.out[vec * HD + (HD / 8) * (2 * c + 1) + i] = acc.y * kLUnit * inv;
   }
 }
 
@@ -1038,7 +1070,7 @@ __global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args 
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = i < used ? __ldcg(part + int64_t(i) * HD) : 0.f;
   float2 x[kMaxSplits / HD];
-  float M = -INFINITY;
+  float M = kLowest;
 #pragma unroll
   for (int i = 0; i < kMaxSplits / HD; ++i) {
     x[i] = d + i * HD < used ? __ldcg(ml + d + i * HD) : make_float2(-INFINITY, 0.f);
@@ -1055,7 +1087,7 @@ __global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args 
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kMaxSplits / HD; ++i) {
-    const float f = x[i].x == -INFINITY ? 0.f : ex2(x[i].x - M);
+    const float f = ex2(x[i].x - M);
     if (d + i * HD < used) wts[d + i * HD] = f;
     sum = fmaf(x[i].y, f, sum);
   }
@@ -1078,7 +1110,7 @@ __global__ void __launch_bounds__(HD) attn_kv8_combine_kernel(const AttnKv8Args 
   }
   // fragment order (n-tile, lane pair, column) -> channel
   const int ch = (HD / 8) * (d & 7) + (d >> 3);
-  a.out[vec * HD + ch] = acc * (sum == 0.f ? 0.f : 1.f / sum);
+  a.out[vec * HD + ch] = acc * kLUnit * (sum == 0.f ? 0.f : 1.f / sum);
 }
 
 using AttnKv8Kernel = void (*)(AttnKv8Args);

@@ -336,9 +336,13 @@ nt_status nt_kv8_read(nt_ctx* ctx, const nt_kv8* cache, int64_t pos0, int64_t n,
  *   out_h = softmax_j(q_h . K_g[j] / sqrt(head_dim)) . V_g[j].
  * q_dev, out_dev fp32 [n_query][n_qh][head_dim], 16-byte aligned; n_qh is 1..16
  * times n_kvh.  A query with no positions (n_pos = 0) gives zeros.  Positions
- * from n_pos + n_query - 1 on may hold anything.  Scales may be any normal
- * positive floats.  Scores, probabilities and sums are fp32-accurate: q and the
- * probabilities enter the tensor cores as two f16 parts each.
+ * from n_pos + n_query - 1 on may hold anything.  K scales may be any normal
+ * positive floats, V scales any from 2^-100 to 2^122 (what nt_kv8_append writes,
+ * and others between), in any mix.  Scores, probabilities and sums are
+ * fp32-accurate: q and the probabilities enter the tensor cores as two f16 parts
+ * each.  Those of a probability times its V scale end at 2^-33 of the query's
+ * largest such product: a position below that adds nothing to the output, but
+ * still counts in the sum.
  * pos_dev (nullable): n_pos = *pos_dev + 1 is read from the device and the
  * argument ignored (a captured call can be replayed); a value outside the cache
  * sets the device flag and is held to the cache.

@@ -1,11 +1,13 @@
 """The 8-bit cache at the edges of its formats: blocks begun elsewhere with scales
-that are no powers of two, the largest floats beside an infinity."""
+that are no powers of two, the largest floats beside an infinity, V scales
+from the least to nearly the largest."""
 import math
 
 import numpy as np
 import pytest
 
 import kv8_ref as ref
+import kv8_tight as tight
 from gpu_util import dev, host, need_gpu, torch
 
 pytestmark = pytest.mark.gpu
@@ -125,3 +127,114 @@ def test_infinity_beside_the_largest_floats(ctx, fmt):
         assert np.array_equal(host(g.buffers[w + "scale"]).astype(np.float64), c.scale[w]), w
         assert np.array_equal(host(g.buffers[w]), c.data[w]), w
     assert np.array_equal(host(g.buffers["kmin"]), c.kmin) and np.array_equal(host(g.buffers["kmax"]), c.kmax)
+
+
+@pytest.mark.parametrize("fmt", [I8, E4M3])
+@pytest.mark.parametrize("e", [-100, -90, -80, -66, -30, 0, 60, 90, 104, 112, 122])
+def test_every_v_scale_is_accurate(ctx, fmt, e):
+    """V scales of about 2^e throughout, e down to the least the append writes: the output is as accurate as at 1.
+    One CTA a head, a cluster and two launches, one query and several."""
+    from block_quantized_gemv_nt_gb300 import nt  # noqa: F401
+    H, G, hd = 2, 4, 128
+    rng = np.random.default_rng(e + 200)
+    for n, nq in ((150, 1), (1500, 1), (20001, 1), (1500, 7)):
+        g, c = _new(ctx, fmt, H, hd, n + nq - 1)
+        for w in "kv":
+            size = 1 if w == "v" and e > 112 else 30  # (the values stay below the largest float)
+            b = np.clip(np.rint(rng.normal(size=c.data[w].shape) * size), -127, 127)
+            c.data[w] = b.astype(np.int8).view(np.uint8) if fmt == I8 else ref.to_bytes(ref.round8(b, fmt), fmt)
+        c.scale["k"][:] = 2.0 ** -5
+        up = rng.integers(0, 3, size=c.scale["v"].shape)
+        c.scale["v"] = 2.0 ** (e + up if e < 100 else e - up)
+        _upload(g, c)
+        q = rng.normal(size=(nq, H * G, hd)).astype(np.float32)
+        out = torch.empty((nq, H * G, hd), device="cuda")
+        g.attend(dev(q), out, n)
+        ctx.sync()
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        tight.check(host(out), c, q, n, tight.plan(sms, H, G, hd, nq, n))
+
+
+@pytest.mark.parametrize("fmt", [I8, E4M3])
+def test_written_tiny_values_are_attended_to(ctx, fmt):
+    """Rows of v around 1e-28 through the append: their scales lie near the least, and the attention over them, over
+    blocks of 1 among them and over all-zero blocks keeps its accuracy."""
+    H, G, hd, n = 1, 4, 64, 64 * 6
+    rng = np.random.default_rng(52)
+    g, c = _new(ctx, fmt, H, hd, n)
+    k, v = (rng.normal(size=(n, H, hd)).astype(np.float32) for _ in range(2))
+    v[:] *= np.float32(1e-28)
+    v[64:128] = 0
+    g.append(dev(k), dev(v), 0)
+    c.append(k, v, 0)
+    q = rng.normal(size=(1, G, hd)).astype(np.float32)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    out = torch.empty((1, G, hd), device="cuda")
+    for n_pos in (64, 200, n):
+        g.attend(dev(q), out, n_pos)
+        tight.check(host(out), c, q, n_pos, tight.plan(sms, H, G, hd, 1, n_pos))
+    for size in (1.0, 1e9, 1e30):
+        v[256:320] = rng.normal(size=(64, H, hd)) * size
+        g.append(dev(k), dev(v), 0)
+        c.append(k, v, 0)
+        g.attend(dev(q), out, n)
+        tight.check(host(out), c, q, n, tight.plan(sms, H, G, hd, 1, n), rms=False)
+    ctx.sync()
+
+
+@pytest.mark.parametrize("order", ["large first", "large last"])
+@pytest.mark.parametrize("fmt", [I8, E4M3])
+def test_zero_blocks_keep_their_weight(ctx, fmt, order):
+    """One warp walks a block of large values and then all-zero ones, or the other way round: the zeros' probabilities
+    stay in the sum, however large the other block is."""
+    H, G, hd, blocks = 1, 4, 64, 76 * 8
+    rng = np.random.default_rng(53)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    g, c = _new(ctx, fmt, H, hd, 64 * blocks)
+    for w in "kv":
+        b = np.clip(np.rint(rng.normal(size=c.data[w].shape) * 30), -127, 127)
+        c.data[w] = b.astype(np.int8).view(np.uint8) if fmt == I8 else ref.to_bytes(ref.round8(b, fmt), fmt)
+    c.scale["k"][:] = 2.0 ** -5
+    q = rng.normal(size=(1, G, hd)).astype(np.float32)
+    out = torch.empty((1, G, hd), device="cuda")
+    p = tight.plan(sms, H, G, hd, 1, 64 * blocks)
+    for e in (0, 30, 60, 100):
+        zero = np.ones(blocks, bool)
+        zero[slice(0, blocks // 4) if order == "large first" else slice(blocks - blocks // 4, blocks)] = False
+        c.scale["v"][:] = np.where(zero, 2.0 ** -100, 2.0 ** e)
+        c.data["v"][:, np.repeat(zero, 64)] = 0
+        _upload(g, c)
+        g.attend(dev(q), out, 64 * blocks)
+        tight.check(host(out), c, q, 64 * blocks, p)
+    # one CTA, lists of one large block among zeros: every warp meets both
+    at = np.flatnonzero(~zero)[:4]
+    n_sel = 40
+    lists = np.concatenate([np.flatnonzero(zero)[:n_sel // 2], at, np.flatnonzero(zero)[n_sel // 2:n_sel - 4]])
+    lists = lists[None, None] if order == "large last" else lists[None, None, ::-1]
+    g.attend_blocks(dev(q), out, 64 * blocks, dev(np.ascontiguousarray(lists).astype(np.int32)))
+    tight.check(host(out), c, q, 64 * blocks, tight.plan(sms, H, G, hd, 1, 64 * blocks, n_sel), lists)
+    ctx.sync()
+
+
+@pytest.mark.parametrize("fmt", [I8, E4M3])
+@pytest.mark.parametrize("s", [-700.0, -90.0, 90.0, 700.0])
+def test_scores_far_from_zero(ctx, fmt, s):
+    """Every score about s, far below or above zero, with ordinary and with all-zero V blocks, from one position on."""
+    H, G, hd = 1, 4, 64
+    rng = np.random.default_rng(54)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for n in (1, 70, 1500, 40000):
+        g, c = _new(ctx, fmt, H, hd, n)
+        for w in "kv":
+            b = np.rint(rng.normal(size=c.data[w].shape) * 10).clip(-40, 40) + (64 if w == "k" else 0)
+            c.data[w] = b.astype(np.int8).view(np.uint8) if fmt == I8 else ref.to_bytes(ref.round8(b, fmt), fmt)
+        c.scale["k"][:] = 2.0 ** -6
+        c.scale["v"][:] = 2.0 ** -5
+        if n > 64:
+            c.data["v"][:, :64], c.scale["v"][:, 0] = 0, 2.0 ** -100
+        _upload(g, c)
+        q = (s / 8 + 0.2 * rng.normal(size=(1, G, hd))).astype(np.float32)  # s = 64 (s / 8) 1 / 8
+        out = torch.empty((1, G, hd), device="cuda")
+        g.attend(dev(q), out, n)
+        tight.check(host(out), c, q, n, tight.plan(sms, H, G, hd, 1, n), rms=False)
+    ctx.sync()
