@@ -64,7 +64,8 @@ class KV8Cache:
     """One layer's 8-bit KV cache in HBM (torch allocations, or `buffers`: a dict
     of tensors k, v, kscale, vscale and, for block selection, kmin, kmax) and the
     calls on it.  fmt: nt.KV8_I8 or nt.KV8_E4M3.  Tensors must be contiguous
-    where no stride is named."""
+    where no stride is named.  pos_dev: an int64 tensor on the cache's device (or
+    its address) that the call reads its position from."""
 
     def __init__(self, ctx: nt.Context, fmt: int, n_kvh: int, head_dim: int, kv_stride: int, device: str = "cuda",
                  bounds: bool = True, buffers: dict | None = None):
@@ -98,14 +99,23 @@ class KV8Cache:
             raise ValueError("rows must be float32 or float16")
         return fmt, shape[tok], stride[tok], stride[head]
 
+    def _pos(self, pos_dev):
+        if (not isinstance(pos_dev, int) and (pos_dev.dtype is not torch.int64 or pos_dev.numel() < 1
+                                              or pos_dev.get_device() != self.index)):
+            raise ValueError("pos_dev: an int64 tensor on the cache's device, or a device address")
+
     def append(self, k, v, pos: int, pos_dev=None, stream=None):
         """Rows [n][n_kvh][head_dim] (fp32 or f16, any strides between rows and heads) to positions pos .."""
         fmt, n, ts, hs = self._rows(k, v, 0, 1)
+        if pos_dev is not None:
+            self._pos(pos_dev)
         nt.nt_kv8_append(self.ctx, self.desc, fmt, k, v, n, ts, hs, pos, pos_dev, stream)
 
     def append_from_heads(self, k, v, pos: int, pos_dev=None, stream=None):
         """Rows [n_kvh][n][head_dim], the layout of an F16 cache (a slice of its positions), to positions pos .."""
         fmt, n, ts, hs = self._rows(k, v, 1, 0)
+        if pos_dev is not None:
+            self._pos(pos_dev)
         nt.nt_kv8_append(self.ctx, self.desc, fmt, k, v, n, ts, hs, pos, pos_dev, stream)
 
     def read(self, pos0: int, k, v, stream=None):
@@ -128,6 +138,8 @@ class KV8Cache:
     def attend(self, q, out, n_pos: int, pos_dev=None, stream=None):
         """Attention of q [n_query][n_qh][head_dim] into out; query i sees n_pos + i positions."""
         nq, n_qh = self._queries(q, out)
+        if pos_dev is not None:
+            self._pos(pos_dev)
         nt.nt_attn_kv8(self.ctx, q, self.desc, out, n_qh, n_pos, nq, pos_dev, stream)
 
     def _list(self, idx, nq):
@@ -140,12 +152,16 @@ class KV8Cache:
     def select(self, q, idx, n_pos: int, n_first: int = 0, n_last: int = 1, pos_dev=None, stream=None):
         """The blocks each query reads into idx [n_query][n_kvh][n_sel]."""
         nq, n_qh = self._queries(q)
+        if pos_dev is not None:
+            self._pos(pos_dev)
         nt.nt_kv8_select(self.ctx, q, self.desc, n_qh, n_pos, nq, self._list(idx, nq), n_first, n_last, idx, pos_dev,
                          stream)
 
     def attend_blocks(self, q, out, n_pos: int, idx, pos_dev=None, stream=None):
         """Attention over the listed blocks only."""
         nq, n_qh = self._queries(q, out)
+        if pos_dev is not None:
+            self._pos(pos_dev)
         nt.nt_attn_kv8_blocks(self.ctx, q, self.desc, out, n_qh, n_pos, nq, idx, self._list(idx, nq), pos_dev, stream)
 
 
