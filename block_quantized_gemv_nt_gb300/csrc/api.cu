@@ -190,11 +190,13 @@ static nt_status take_device_flag(nt_ctx* ctx) {
   if (e != cudaSuccess) return cuda_check(ctx, e, "read device error flag");
   if (flag) {
     cudaMemset(ctx->err_flag, 0, sizeof(unsigned));
-    if (flag & kErrWaitTimeout)
-      return set_err(ctx, NT_ERR_TIMEOUT, "a device-side bounded wait ran out (flag 0x%x)", flag);
-    if (flag & kErrPosRange)
-      return set_err(ctx, NT_ERR_INVALID_ARG, "a device-side position ran past the KV cache (flag 0x%x)", flag);
-    return set_err(ctx, NT_ERR_INVALID_ARG, "a NaN or an infinity was written to an 8-bit KV cache (flag 0x%x)", flag);
+    // one status, every cause by name: the flag collects what happened since it was last read
+    const char *timeout = "", *range = "", *finite = "";
+    if (flag & kErrWaitTimeout) timeout = "a device-side bounded wait ran out; ";
+    if (flag & kErrPosRange) range = "a device-side position ran past the KV cache; ";
+    if (flag & kErrNonFinite) finite = "a NaN or an infinity was written to an 8-bit KV cache; ";
+    return set_err(ctx, flag & kErrWaitTimeout ? NT_ERR_TIMEOUT : NT_ERR_INVALID_ARG, "%s%s%s(flag 0x%x)", timeout, range,
+                   finite, flag);
   }
   return NT_OK;
 }

@@ -27,8 +27,9 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream).  Calls only enqueue work.  The device error flag (a bounded
  *    wait inside a kernel that ran out, a device-held position past the KV
- *    cache) is read and cleared by nt_ctx_sync() and nt_stream_sync(); a
- *    CUDA fault also fails the next launch on the context.
+ *    cache, a NaN or an infinity written to an 8-bit KV cache) is read and
+ *    cleared by nt_ctx_sync() and nt_stream_sync(); a CUDA fault also fails
+ *    the next launch on the context.
  *  - Pointers named *_dev are device (HBM) pointers; pointers named *_host
  *    are host pointers.  The caller owns every weight, activation, KV-cache
  *    and output buffer; the context owns only its scratch, events, side
@@ -92,13 +93,14 @@ nt_status nt_ctx_destroy(nt_ctx* ctx);
  * held on the device (a decode step continued with token < 0, or the pos_dev
  * of an 8-bit cache call) ran past the KV cache — the kernels then wrote
  * nothing outside the caches — or a NaN or an infinity was written to an 8-bit
- * KV cache. */
+ * KV cache.  nt_last_error names every cause since the flag was last read. */
 nt_status nt_ctx_sync(nt_ctx* ctx);
 /* [road] Wait at most timeout_us for the work enqueued on `stream` to finish (a
  * host-side poll with a deadline), then report like nt_ctx_sync:
  * NT_ERR_TIMEOUT when the deadline passes first (the work is not
  * cancelled; call again to keep waiting), else the device-side error flag
- * (bounded-wait timeout or position out of range), cleared when read. */
+ * (bounded-wait timeout, position out of range, NaN or infinity written to an
+ * 8-bit KV cache), cleared when read. */
 nt_status nt_stream_sync(nt_ctx* ctx, void* stream, int64_t timeout_us);
 /* Fault injection for the streaming engine's tests ([feat] SLEP streaming;
  * host side only; nothing is ever made to fail on the GPU): the nth following

@@ -1,6 +1,6 @@
 """The 8-bit cache at the edges of its formats: blocks begun elsewhere with scales
 that are no powers of two, the largest floats beside an infinity, V scales
-from the least to nearly the largest."""
+from the least to nearly the largest, and what the sync reports of several causes."""
 import math
 
 import numpy as np
@@ -237,4 +237,36 @@ def test_scores_far_from_zero(ctx, fmt, s):
         out = torch.empty((1, G, hd), device="cuda")
         g.attend(dev(q), out, n)
         tight.check(host(out), c, q, n, tight.plan(sms, H, G, hd, 1, n), rms=False)
+    ctx.sync()
+
+
+def test_sync_names_every_cause(ctx):
+    """A row that is not finite and a device position past the end between two syncs: the report names both."""
+    from block_quantized_gemv_nt_gb300 import nt
+    g, _ = _new(ctx, I8, 1, 64, 100)
+    x = torch.zeros(1, 1, 64, device="cuda")
+    x[0, 0, 3] = float("nan")
+    pos = torch.tensor([100], dtype=torch.int64, device="cuda")
+
+    def report():
+        with pytest.raises(nt.NtError) as e:
+            ctx.sync()
+        return e.value.status, str(e.value)
+
+    g.append(x, x, 5)
+    g.append(x, x, 0, pos_dev=pos)
+    status, text = report()
+    assert status == nt.NT_ERR_INVALID_ARG and "infinity" in text and "position" in text
+    q = torch.ones(1, 1, 64, device="cuda")
+    g.append(x, x, 5)
+    nt.nt_debug_stall_waits(1)
+    try:
+        g.attend(q, torch.empty_like(q), 6)
+    finally:
+        nt.nt_debug_stall_waits(0)
+    status, text = report()
+    assert status == nt.NT_ERR_TIMEOUT and "infinity" in text and "position" not in text
+    g.append(x, x, 5)
+    status, text = report()
+    assert status == nt.NT_ERR_INVALID_ARG and "infinity" in text and "position" not in text
     ctx.sync()
