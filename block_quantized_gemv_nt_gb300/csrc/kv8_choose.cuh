@@ -147,13 +147,12 @@ __device__ __forceinline__ void select_blocks(const Args& a, int blocks, int32_t
   base += incl - cnt;
   int above = int(base & ((Count(1) << H) - 1)), ties = int(base >> H);
   each([&](int b, uint32_t k) {
-    if (k == kForced || k > cut) {
-      idx[above + min(ties, need)] = b;
-      ++above;
-    } else if (k == cut) {
-      if (ties < need) idx[above + ties] = b;
-      ++ties;
-    }
+    const bool over = k == kForced || k > cut;
+    if (!over && (k != cut || ties >= need)) return;
+    const int at = above + min(ties, need);
+    if (unsigned(at) < unsigned(a.n_sel)) idx[at] = b;  // outside only if the keys changed between two reads of them (K = 0)
+    if (over) ++above;
+    else ++ties;
   });
 }
 

@@ -5,6 +5,8 @@
 //   low    the lowest runnable thread first: thread 0's warp runs ahead of all others
 //   high   the highest first: thread 0's warp is the last everywhere
 //   mixed  a random one, and random changes at every atomic and key read
+//   torn   mixed, and the keys change between reads, as if another call wrote the
+//          scratch that holds them: any list may come out, but nothing beside it is written
 // Reads cases from stdin:  threads K n_sel n_first n_last blocks schedule seed, then the keys;
 // writes the n_sel entries, then 1 if anything beside them was written.
 #include <ucontext.h>
@@ -23,6 +25,7 @@
 namespace emu {
 struct Dim { unsigned x; } tid;
 enum Schedule { kLow, kHigh, kMixed } schedule;
+bool torn;
 int n;
 std::mt19937 rng;
 ucontext_t home;
@@ -187,7 +190,7 @@ void choose(const Args& a, int K, int blocks, int32_t* idx, uint32_t* keys) {
   std::generate_n(reinterpret_cast<unsigned char*>(&sh), sizeof sh, [] { return (unsigned char)emu::rng(); });
   const auto key = [&](int b) {
     emu::maybe_yield();
-    return keys[b];
+    return keys[emu::torn && emu::rng() % 2 ? (b * 7LL + 3) % blocks : b];
   };
   emu::run(NT, [&] {
     if (K < 0) nt::rank_blocks<NT>(a, blocks, idx, sh, keys);
@@ -203,7 +206,8 @@ int main() {
   unsigned seed;
   Args a;
   while (std::scanf("%d %d %d %d %d %d %d %u", &threads, &K, &a.n_sel, &a.n_first, &a.n_last, &blocks, &sched, &seed) == 8) {
-    emu::schedule = emu::Schedule(sched);
+    emu::torn = sched == 3;
+    emu::schedule = emu::Schedule(emu::torn ? 2 : sched);
     emu::rng.seed(seed);
     std::vector<uint4> store((blocks + 3) / 4 + 1);
     uint32_t* keys = reinterpret_cast<uint32_t*>(store.data());
