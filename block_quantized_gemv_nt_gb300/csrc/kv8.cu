@@ -62,8 +62,7 @@ __device__ __forceinline__ uint32_t pack8(const float v[4], float inv) {
   return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
-// (x & m) ^ b as one operation (written as two, the compiler keeps both constants as
-// immediates and spends two)
+// (x & m) ^ b as one three-input operation
 __device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t m, uint32_t b) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "r"(m), "r"(b));
@@ -1308,9 +1307,12 @@ __global__ void __launch_bounds__(NT) kv8_select_kernel(const SelectArgs a) {
     return;
   }
   const auto key = [&](int b) { return keys[b]; };
+  // Keys in registers where a thread has up to five (8 heads, against shared memory: 1024
+  // blocks 6.2 and 7.5 us, 1100 7.55 and 7.25, 5120 8.7 and 9.45); more of them cost more
+  // than they save (17 a thread: 10,000 blocks 14.6 against 12.95, 17,408 17.0 and 16.7;
+  // 33: 30,000 26.1 and 24.1).  54,784 blocks take 47 us.
   if (blocks <= NT) select_blocks<NT, 1>(a, blocks, idx, sh, key);
   else if (blocks <= 5 * NT) select_blocks<NT, 5>(a, blocks, idx, sh, key);
-  else if (blocks <= 17 * NT) select_blocks<NT, 17>(a, blocks, idx, sh, key);
   else select_blocks<NT, 0>(a, blocks, idx, sh, key);
 }
 

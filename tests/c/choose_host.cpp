@@ -196,7 +196,6 @@ void choose(const Args& a, int K, int blocks, int32_t* idx, uint32_t* keys) {
     if (K < 0) nt::rank_blocks<NT>(a, blocks, idx, sh, keys);
     else if (K == 1) nt::select_blocks<NT, 1>(a, blocks, idx, sh, key);
     else if (K == 5) nt::select_blocks<NT, 5>(a, blocks, idx, sh, key);
-    else if (K == 17) nt::select_blocks<NT, 17>(a, blocks, idx, sh, key);
     else nt::select_blocks<NT, 0>(a, blocks, idx, sh, key);
   });
 }

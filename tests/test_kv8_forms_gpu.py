@@ -132,7 +132,7 @@ def test_block_attention_forms(ctx, form, H, G, hd, n_pos, nq, n_sel, fmt):
 @pytest.mark.parametrize("hd,H,nq,n_blocks", [(64, 2, 1, 257), (128, 2, 2, 1024), (64, 1, 1, 5120), (64, 1, 1, 17408),
                                               (64, 2, 1, 17409), (64, 1, 2, 30000), (128, 1, 1, 54784), (64, 1, 1, 54785)])
 def test_selection_forms(ctx, hd, H, nq, n_blocks):
-    """Every form of the choice and its borders (keys in registers by 1, 5 and 17, re-read from shared memory, in
+    """Every form of the choice and its borders (keys in registers by 1 and 5, re-read from shared memory, in
     scratch), each call many times: the list is exact every time and nothing beside it is written."""
     G, n = 3, 64 * n_blocks - 63
     rng = np.random.default_rng(n_blocks)
