@@ -1140,7 +1140,9 @@ AttnKv8Variant attn_kv8_for(int fmt, int hd, int R, int U) {
 constexpr int kSelWide = 1024, kSelNarrow = 256;  // threads of a selection
 constexpr int kSelNarrowBlocks = kSelNarrow;      // most blocks of the narrow one: one a thread
 // most CTAs of a selection's cluster, an SM each: larger clusters of 8 heads do not all
-// fit on the GPU at once (15,626 blocks: 8 CTAs 18.0 us, 12 17.0, 14 22.9, 16 22.0)
+// fit on the GPU at once (15,626 blocks: 8 CTAs 17.8 us, 12 16.5, 14 22.3, 16 21.1).  Of
+// fewer heads they do, and 12 is not the best (15,626 blocks of 4 heads: 8 CTAs 17.0 us,
+// 12 15.5, 16 14.3; of one head 15.0, 13.7, 12.8).
 constexpr int kSelCluster = 12;
 
 struct SelectArgs {
@@ -1271,7 +1273,7 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, int g, int qi,
 // keys into the first CTA's shared memory, which selects.  Bound by the latency of
 // its phases (65 blocks 3.3 us) and, for long sequences, about equally by reading the
 // bounds from the cluster's SMs and by the choice in one SM (15,626 blocks of 8
-// heads 16.9 us: 3.6 launch and q, 6 scoring 32 MB, 7 choice).
+// heads 16.6 us: 3.6 launch and q, 6 scoring 32 MB, 7 choice).
 template <int NT, int HD>
 __global__ void __launch_bounds__(NT) kv8_select_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint32_t keys[];
