@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 // changes nothing.
 constexpr int kAttnWarps = 8;
 constexpr float kPTop = 8.f, kLUnit = 0x1p-13f;                   // see the softmax
-constexpr float kSlack = 6.f, kFar = 90.f, kMid = (kFar - kSlack) / 2;
+constexpr float kSlack = 6.f, kFar = 90.f, kMid = (kFar - kSlack) / 2, kLift = 110.f;
 constexpr float kLowest = -3.402823466e38f;  // the merges' maximum of nothing: 2^(-inf - kLowest) is 0
 constexpr int kMaxCluster = 16;
 
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
       // l takes p 2^-lv in units of 2^13, which keep it within fp32 for every scale that
       // the cache can hold (2^26 weights of the largest exponent at 2^-100, one at 2^122).
       // Where s + lv is kFar below m (an all-zero block beside large ones) the outputs
-      // gain nothing, and l takes the exponentials lifted by kFar, out of reach of the
+      // gain nothing, and l takes the exponentials lifted by kLift, out of reach of the
       // underflow.  Registers hold m - kMid: one comparison finds both cases.
       const float vs = kvs.y;
       const uint32_t ve = min(max(__float_as_uint(vs) >> 23, 27u), 249u);  // 2^-100 .. 2^122
@@ -838,8 +838,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
           mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2)) + lv;
           mn = fmaxf(m[t], floorf(mn) - kMid);
           const float down = m[t] == -INFINITY ? -INFINITY : m[t] - mn;
-          const float corr = ex2(fmaxf(down, -kFar));
-          l[t] = l[t] * corr * ex2(fminf(down + kFar, 0.f));  // in two steps: it may be large
+          const float corr = ex2(fmaxf(down, -kLift));
+          l[t] = l[t] * corr * ex2(fminf(down + kLift, 0.f));  // in two steps: it may be large
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             o[t][i].x *= corr;
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
           m[t] = mn;
           ml = mn - lv;
           if (ml - mx > kMid + kSlack) {
-            const float lifted = (kPTop - kMid + kFar) - ml;
+            const float lifted = (kPTop - kMid + kLift) - ml;
             float2 far = make_float2(0.f, 0.f);
 #pragma unroll
             for (int x = 0; x < 4 * U; x += 2) {
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
               far = add2(far, make_float2(ex2(e.x), ex2(e.y)));
               p[x] = p[x + 1] = -INFINITY;
             }
-            l[t] = fmaf(far.x + far.y, lu * ex2(-kFar), l[t]);
+            l[t] = fmaf((far.x + far.y) * lu, ex2(-kLift), l[t]);
           }
         }
         const float base = m[t] == -INFINITY ? 0.f : (kPTop - kMid) - ml;
@@ -944,10 +944,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, R == 1 ? 2 : 1) attn_kv8_kern
   for (int t = 0; t < R; ++t) {
     l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
     l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
-    if (l[t] > 0x1p40f) {
-      // (V all but zero) m rises by the exponent of l, and l and o fall: in the merges the
-      // weights 2^(m - M) then underflow only where l does not matter either
-      const uint32_t k = __float_as_uint(l[t]) & 0x7F800000u;
+    if (!(l[t] >= 0x1p-60f && l[t] <= 0x1p20f)) {
+      // (very small or very large V scales) m takes over the exponent of l, down to -60, and
+      // l and o lose it: in the merges the weights 2^(m - M) then underflow only where l does
+      // not matter either
+      const uint32_t k = max(__float_as_uint(l[t]) & 0x7F800000u, 67u << 23);
       const float down = __uint_as_float((254u << 23) - k);
       l[t] *= down;
       m[t] += float(int(k >> 23) - 127);

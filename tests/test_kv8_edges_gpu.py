@@ -217,6 +217,32 @@ def test_zero_blocks_keep_their_weight(ctx, fmt, order):
 
 
 @pytest.mark.parametrize("fmt", [I8, E4M3])
+@pytest.mark.parametrize("span", [(-100, 122), (-100, 60), (-45, 100), (0, 122)])
+def test_v_scales_in_any_mix(ctx, fmt, span):
+    """Blocks of V scales all over the range, every position about as probable: each block's probabilities count in the
+    sum, and the outputs are those of the largest.  In every order a warp or a merge can meet them."""
+    H, G, hd = 1, 4, 64
+    rng = np.random.default_rng(55)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for n in (150, 700, 5000, 64 * 76 * 8):
+        g, c = _new(ctx, fmt, H, hd, n)
+        for w in "kv":
+            b = np.clip(np.rint(rng.normal(size=c.data[w].shape) * (20 if w == "k" else 1)), -127, 127)
+            c.data[w] = b.astype(np.int8).view(np.uint8) if fmt == I8 else ref.to_bytes(ref.round8(b, fmt), fmt)
+        c.scale["k"][:] = 2.0 ** -5
+        q = rng.normal(size=(1, G, hd)).astype(np.float32)
+        out = torch.empty((1, G, hd), device="cuda")
+        nb = c.scale["v"].shape[1]
+        few = np.where(rng.random(nb) < 0.1, span[1], span[0])  # mostly the least, some the largest
+        for e in (rng.integers(span[0], span[1] + 1, size=nb), few, np.sort(few), np.sort(few)[::-1]):
+            c.scale["v"][0] = 2.0 ** e.astype(np.float64)
+            _upload(g, c)
+            g.attend(dev(q), out, n)
+            tight.check(host(out), c, q, n, tight.plan(sms, H, G, hd, 1, n), rms=False)
+    ctx.sync()
+
+
+@pytest.mark.parametrize("fmt", [I8, E4M3])
 @pytest.mark.parametrize("s", [-700.0, -90.0, 90.0, 700.0])
 def test_scores_far_from_zero(ctx, fmt, s):
     """Every score about s, far below or above zero, with ordinary and with all-zero V blocks, from one position on."""
