@@ -475,10 +475,10 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a
 // while it works on K; no barrier joins the warps.
 //
 // Long sequences are bound by HBM (32 q heads over 8 of 128 channels, I8: 1,000,003
-// positions 290 us, 7.06 TB/s; 131,071 47.4 us, of which about 9 are the ramp, the
+// positions 290 us, 7.06 TB/s; 131,071 47.3 us, of which about 9 are the ramp, the
 // tail and the combine); short ones by the latency of launch, copy, step and merge
 // (1088 positions 5.4 us); several queries by the chain of a 16-row step (8 queries of
-// 32 heads, 16,381 positions 24.5 us, tensor pipe at 41%).  Eight warps of 128
+// 32 heads, 16,381 positions 24.3 us, tensor pipe at 40%).  Eight warps of 128
 // registers and two CTAs an SM: fewer registers spill, a second buffer per warp
 // changes nothing.
 constexpr int kAttnWarps = 8;
