@@ -28,7 +28,7 @@ own = False
 PAGE = 64
 GROUP = 32
 PART = 1024
-TOP_SCALE = 8160.0  # the largest scale, 255 * 2^5
+TOP_SCALE = 2720.0  # the largest scale, 170 * 2^4
 
 
 # ---- cases -----------------------------------------------------------------------
