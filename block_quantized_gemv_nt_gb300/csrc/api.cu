@@ -161,7 +161,7 @@ nt_status nt_ctx_create(nt_ctx** out, int device, size_t scratch_bytes) {
   }
   c->err_flag = reinterpret_cast<unsigned*>(c->scratch + kScratchErr);
   if (configure_gemv(c) != NT_OK || configure_ops(c) != NT_OK || configure_gemm(c) != NT_OK ||
-      configure_kv8(c) != NT_OK) {
+      configure_kv8(c) != NT_OK || configure_kv4(c) != NT_OK) {
     g_create_error = c->last_error;
     cudaFree(c->scratch);
     delete c;
@@ -191,12 +191,14 @@ static nt_status take_device_flag(nt_ctx* ctx) {
   if (flag) {
     cudaMemset(ctx->err_flag, 0, sizeof(unsigned));
     // one status, every cause by name: the flag collects what happened since it was last read
-    const char *timeout = "", *range = "", *finite = "";
+    const char *timeout = "", *range = "", *finite = "", *finite4 = "", *paged = "";
     if (flag & kErrWaitTimeout) timeout = "a device-side bounded wait ran out; ";
     if (flag & kErrPosRange) range = "a device-side position ran past the KV cache; ";
     if (flag & kErrNonFinite) finite = "a NaN or an infinity was written to an 8-bit KV cache; ";
-    return set_err(ctx, flag & kErrWaitTimeout ? NT_ERR_TIMEOUT : NT_ERR_INVALID_ARG, "%s%s%s(flag 0x%x)", timeout, range,
-                   finite, flag);
+    if (flag & kErrNonFinite4) finite4 = "a NaN or an infinity was written to a 4-bit KV cache; ";
+    if (flag & kErrPaged) paged = "a length, page or slot that the paged KV cache or its tables do not have; ";
+    return set_err(ctx, flag & kErrWaitTimeout ? NT_ERR_TIMEOUT : NT_ERR_INVALID_ARG, "%s%s%s%s%s(flag 0x%x)", timeout, range,
+                   finite, finite4, paged, flag);
   }
   return NT_OK;
 }
@@ -593,6 +595,159 @@ nt_status nt_attn_kv8_blocks(nt_ctx* ctx, const float* q, const nt_kv8* kv, floa
   NT_REQUIRE(aligned(idx, 4), NT_ERR_ALIGNMENT, "idx must be 4-byte aligned");
   NT_REQUIRE(n_sel >= 1 && n_sel <= (1 << 24), NT_ERR_INVALID_ARG, "n_sel must be 1..2^24");
   return attn_kv8_entry(ctx, q, kv, out, n_qh, n_pos, n_query, pos_dev, idx, n_sel, stream);
+}
+
+namespace {
+nt_status check_kv4(nt_ctx* ctx, const nt_kv4* kv) {
+  NT_REQUIRE(kv, NT_ERR_INVALID_ARG, "null cache");
+  NT_REQUIRE(kv->fmt == NT_KV4_I4 || kv->fmt == NT_KV4_E2M1, NT_ERR_UNSUPPORTED_FMT, "unknown 4-bit cache format %d",
+             kv->fmt);
+  NT_REQUIRE(kv->head_dim == 64 || kv->head_dim == 128, NT_ERR_INVALID_ARG, "head_dim must be 64 or 128");
+  NT_REQUIRE(kv->n_kvh >= 1 && kv->n_kvh <= 64, NT_ERR_INVALID_ARG, "n_kvh must be 1..64");
+  NT_REQUIRE(kv->n_pages >= 1 && kv->n_pages < (int64_t(1) << 31), NT_ERR_INVALID_ARG, "n_pages must be 1..2^31 - 1");
+  NT_REQUIRE(kv->data, NT_ERR_INVALID_ARG, "null cache buffer");
+  NT_REQUIRE(aligned(kv->data, 16), NT_ERR_ALIGNMENT, "the cache must be 16-byte aligned");
+  return NT_OK;
+}
+
+// the rows of a write to or a read from a 4-bit cache
+nt_status check_kv4_rows(nt_ctx* ctx, const nt_kv4* kv, int fmt, const void* k, const void* v, int64_t n_tok,
+                         int64_t tok_stride, int64_t head_stride, const int64_t* slots) {
+  NT_TRY(check_kv4(ctx, kv));
+  NT_REQUIRE(fmt == NT_F32 || fmt == NT_F16, NT_ERR_UNSUPPORTED_FMT, "rows must be NT_F32 or NT_F16");
+  NT_REQUIRE(n_tok >= 0 && n_tok <= (int64_t(1) << 28), NT_ERR_INVALID_ARG, "n_tok must be 0..2^28");
+  if (n_tok == 0) return NT_OK;
+  NT_REQUIRE(slots, NT_ERR_INVALID_ARG, "slots is NULL");
+  NT_REQUIRE(aligned(slots, 8), NT_ERR_ALIGNMENT, "slots must be 8-byte aligned");
+  const int vec = fmt == NT_F32 ? 4 : 8;
+  NT_REQUIRE(aligned(k, 16) && aligned(v, 16) && tok_stride % vec == 0 && head_stride % vec == 0, NT_ERR_ALIGNMENT,
+             "rows must be 16-byte aligned, strides multiples of %d", vec);
+  const int64_t far = int64_t(1) << 40;
+  NT_REQUIRE(tok_stride > -far && tok_stride < far && head_stride > -far && head_stride < far, NT_ERR_INVALID_ARG,
+             "strides must be within 2^40");
+  return NT_OK;
+}
+
+// whether n0 x n1 rows of `row` elements at strides s0 and s1 are apart from one another
+bool rows_apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t row) {
+  if ((n0 > 1 && s0 < row) || (n1 > 1 && s1 < row)) return false;
+  return n0 == 1 || n1 == 1 || s0 >= (n1 - 1) * s1 + row || s1 >= (n0 - 1) * s0 + row;
+}
+}  // namespace
+
+nt_status nt_kv4_layout(int head_dim, size_t* page_bytes) {
+  if ((head_dim != 64 && head_dim != 128) || !page_bytes) return NT_ERR_INVALID_ARG;
+  *page_bytes = kv4_page_bytes(head_dim);
+  return NT_OK;
+}
+
+nt_status nt_kv4_pages(nt_ctx* ctx, int n_req, int32_t* table, int64_t max_pages, const int32_t* held, const int32_t* keep,
+                       const int32_t* n_new, int32_t* free_pages, int64_t n_pages, const int32_t* n_free,
+                       int32_t* held_out, int32_t* n_free_out, int32_t* q_start, int64_t* slots, int32_t* positions,
+                       int64_t n_tok, void* stream) {
+  NvtxRange nvtx_range("nt_kv4_pages");
+  NT_TRY(pre_call(ctx));
+  NT_REQUIRE(n_req >= 1 && n_req <= 1024, NT_ERR_INVALID_ARG, "n_req must be 1..1024");
+  NT_REQUIRE(max_pages >= 1 && max_pages <= (int64_t(1) << 24), NT_ERR_INVALID_ARG, "max_pages must be 1..2^24");
+  NT_REQUIRE(n_pages >= 1 && n_pages < (int64_t(1) << 31), NT_ERR_INVALID_ARG, "n_pages must be 1..2^31 - 1");
+  NT_REQUIRE(n_tok >= 0 && n_tok <= (int64_t(1) << 28), NT_ERR_INVALID_ARG, "n_tok must be 0..2^28");
+  NT_REQUIRE(table && held && n_new && free_pages && n_free && held_out && n_free_out && q_start, NT_ERR_INVALID_ARG,
+             "null pointer");
+  NT_REQUIRE(n_tok == 0 || (slots && positions), NT_ERR_INVALID_ARG, "slots or positions is NULL");
+  for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(held), static_cast<const void*>(keep),
+                        static_cast<const void*>(n_new), static_cast<const void*>(free_pages),
+                        static_cast<const void*>(n_free), static_cast<const void*>(held_out),
+                        static_cast<const void*>(n_free_out), static_cast<const void*>(q_start),
+                        static_cast<const void*>(positions)})
+    NT_REQUIRE(aligned(p, 4), NT_ERR_ALIGNMENT, "tables and lengths must be 4-byte aligned");
+  NT_REQUIRE(aligned(slots, 8), NT_ERR_ALIGNMENT, "slots must be 8-byte aligned");
+  DeviceGuard g(ctx->device);
+  return launch_kv4_pages(ctx, n_req, table, max_pages, held, keep, n_new, free_pages, n_pages, n_free, held_out, n_free_out,
+                          q_start, slots, positions, n_tok, as_stream(stream));
+}
+
+nt_status nt_kv4_append(nt_ctx* ctx, const nt_kv4* kv, int src_fmt, const void* k, const void* v, int64_t n_tok,
+                        int64_t tok_stride, int64_t head_stride, const int64_t* slots, void* stream) {
+  NvtxRange nvtx_range("nt_kv4_append");
+  NT_TRY(pre_call(ctx));
+  NT_TRY(check_kv4_rows(ctx, kv, src_fmt, k, v, n_tok, tok_stride, head_stride, slots));
+  if (n_tok == 0) return NT_OK;
+  NT_REQUIRE(k && v, NT_ERR_INVALID_ARG, "null rows");
+  DeviceGuard g(ctx->device);
+  return launch_kv4_append(ctx, *kv, src_fmt, k, v, n_tok, tok_stride, head_stride, slots, as_stream(stream));
+}
+
+nt_status nt_kv4_read(nt_ctx* ctx, const nt_kv4* kv, int dst_fmt, void* k, void* v, int64_t n_tok, int64_t tok_stride,
+                      int64_t head_stride, const int64_t* slots, void* stream) {
+  NvtxRange nvtx_range("nt_kv4_read");
+  NT_TRY(pre_call(ctx));
+  NT_TRY(check_kv4_rows(ctx, kv, dst_fmt, k, v, n_tok, tok_stride, head_stride, slots));
+  if (n_tok == 0) return NT_OK;
+  NT_REQUIRE(k || v, NT_ERR_INVALID_ARG, "no output");
+  NT_REQUIRE(rows_apart(n_tok, tok_stride, kv->n_kvh, head_stride, kv->head_dim), NT_ERR_INVALID_ARG,
+             "the output's rows overlap");
+  DeviceGuard g(ctx->device);
+  return launch_kv4_read(ctx, *kv, dst_fmt, k, v, n_tok, tok_stride, head_stride, slots, as_stream(stream));
+}
+
+nt_status nt_attn_kv4(nt_ctx* ctx, const float* q, const nt_kv4* kv, float* out, int n_qh, int64_t n_tok, int n_req,
+                      const int32_t* q_start, const int32_t* held, const int32_t* table, int64_t max_pages, void* stream) {
+  NvtxRange nvtx_range("nt_attn_kv4");
+  NT_TRY(pre_call(ctx));
+  NT_TRY(check_kv4(ctx, kv));
+  NT_REQUIRE(n_qh >= 1 && n_qh % kv->n_kvh == 0 && n_qh / kv->n_kvh <= 16, NT_ERR_INVALID_ARG,
+             "n_qh must be 1..16 times n_kvh");
+  NT_REQUIRE(n_tok >= 0 && n_tok <= (int64_t(1) << 24), NT_ERR_INVALID_ARG, "n_tok must be 0..2^24");
+  NT_REQUIRE(n_req >= 1 && n_req <= 1024, NT_ERR_INVALID_ARG, "n_req must be 1..1024");
+  NT_REQUIRE(max_pages >= 1 && max_pages <= (int64_t(1) << 24), NT_ERR_INVALID_ARG, "max_pages must be 1..2^24");
+  NT_REQUIRE(q_start && held && table, NT_ERR_INVALID_ARG, "null lengths or table");
+  NT_REQUIRE(aligned(q_start, 4) && aligned(held, 4) && aligned(table, 4), NT_ERR_ALIGNMENT,
+             "lengths and tables must be 4-byte aligned");
+  if (n_tok == 0) return NT_OK;
+  NT_TRY(check_vec(ctx, q, "q"));
+  NT_TRY(check_vec(ctx, out, "out"));
+  NT_REQUIRE(ctx->scratch_bytes >= kScratchGemm &&
+                 ctx->scratch_bytes - kScratchGemm >= kv4_attn_scratch(ctx, kv->head_dim),
+             NT_ERR_OOM, "the context scratch has no room for the attention's partials");
+  DeviceGuard g(ctx->device);
+  return launch_attn_kv4(ctx, *kv, q, out, n_qh, n_tok, n_req, q_start, held, table, max_pages, ctx->scratch + kScratchGemm,
+                         reinterpret_cast<unsigned*>(ctx->scratch + kScratchAttn), as_stream(stream));
+}
+
+nt_status nt_rope_rows(nt_ctx* ctx, const nt_rope_plan* plan, int fmt, const nt_rope_job* jobs, int n_jobs, int64_t n_tok,
+                       const int32_t* positions, int64_t pos0, void* stream) {
+  NvtxRange nvtx_range("nt_rope_rows");
+  NT_TRY(pre_call(ctx));
+  NT_REQUIRE(plan, NT_ERR_INVALID_ARG, "null plan");
+  NT_REQUIRE((plan->layout == NT_ROPE_PAIRS || plan->layout == NT_ROPE_HALVES) && plan->head_dim >= 8 &&
+                 plan->head_dim <= 256 && plan->head_dim % 8 == 0 && plan->rot_dim >= 8 &&
+                 plan->rot_dim <= plan->head_dim && plan->rot_dim % 8 == 0,
+             NT_ERR_INVALID_ARG, "the plan was not made by nt_rope_plan_init");
+  NT_REQUIRE(fmt == NT_F32 || fmt == NT_F16, NT_ERR_UNSUPPORTED_FMT, "rows must be NT_F32 or NT_F16");
+  NT_REQUIRE(jobs && n_jobs >= 1 && n_jobs <= 3, NT_ERR_INVALID_ARG, "need 1..3 tensors");
+  NT_REQUIRE(n_tok >= 0 && n_tok <= (int64_t(1) << 24), NT_ERR_INVALID_ARG, "n_tok must be 0..2^24");
+  NT_REQUIRE(aligned(positions, 4), NT_ERR_ALIGNMENT, "positions must be 4-byte aligned");
+  NT_REQUIRE(positions || (pos0 >= -(int64_t(1) << 31) && pos0 + n_tok <= (int64_t(1) << 31)), NT_ERR_INVALID_ARG,
+             "positions must fit 32 bits");
+  const int vec = fmt == NT_F32 ? 4 : 8;
+  const int64_t far = int64_t(1) << 40;
+  for (int i = 0; i < n_jobs; ++i) {
+    const nt_rope_job& j = jobs[i];
+    NT_REQUIRE(j.n_heads >= 1 && j.n_heads <= 1024, NT_ERR_INVALID_ARG, "n_heads must be 1..1024");
+    for (int64_t s : {j.x_tok_stride, j.x_head_stride, j.y_tok_stride, j.y_head_stride}) {
+      NT_REQUIRE(s > -far && s < far, NT_ERR_INVALID_ARG, "strides must be within 2^40");
+      NT_REQUIRE(s % vec == 0, NT_ERR_ALIGNMENT, "strides must be multiples of %d", vec);
+    }
+    NT_REQUIRE(n_tok == 0 || (j.x_dev && j.y_dev), NT_ERR_INVALID_ARG, "null rows");
+    NT_REQUIRE(aligned(j.x_dev, 16) && aligned(j.y_dev, 16), NT_ERR_ALIGNMENT, "rows must be 16-byte aligned");
+    NT_REQUIRE(n_tok == 0 || rows_apart(n_tok, j.y_tok_stride, j.n_heads, j.y_head_stride, plan->head_dim),
+               NT_ERR_INVALID_ARG, "the output's rows overlap");
+    NT_REQUIRE(j.x_dev != j.y_dev || (j.x_tok_stride == j.y_tok_stride && j.x_head_stride == j.y_head_stride),
+               NT_ERR_INVALID_ARG, "in place, the strides of input and output are the same");
+  }
+  if (n_tok == 0) return NT_OK;
+  DeviceGuard g(ctx->device);
+  return launch_rope_rows(ctx, *plan, fmt, jobs, n_jobs, n_tok, positions, pos0, as_stream(stream));
 }
 
 nt_status nt_host_register(nt_ctx* ctx, const void* p, size_t bytes, int read_only) {

@@ -1,0 +1,1016 @@
+// kv4.cu — the paged 4-bit KV cache of several requests: rows quantised into their
+// slots and read back, and the attention of each request's rows over its own pages.
+// It stands beside the F16 cache ("Ntransformer", en.unwiki.net, roadmap) and the
+// 8-bit one (kv8.cu).
+//
+// A page holds 64 positions.  Per page and KV head there is one block: the K half,
+// then the V half, each 64 rows of HD / 2 bytes and 64 HD / 32 scales.  Channels 8 j
+// .. 8 j + 7 of a row are one word, channel 8 j + n its nibble n.  The order inside a
+// half is the one in which the attention's MMA fragments read it (see there):
+//  - K row t at t HD / 2; scale (t, group) at ((t % 8) NG + group) 8 + t / 8
+//  - V word j of row t: plane j % WPL, line swap(t), word j / WPL of the line, where
+//    WPL = HD / 64 and swap(t) puts t, t + 2, t + 4, t + 6 of every 8 side by side;
+//    scale (t, group) at (group 4 + t / 2 % 4) 16 + t / 16 4 + t / 8 % 2 2 + t % 2
+//
+// A scale has at most 8 significant bits and a code at most 3, so every value is exact
+// in f16: the attention multiplies the scale in as it unpacks, and its products lose
+// nothing.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <algorithm>
+
+#include "nt_internal.cuh"
+#include "ops.cuh"
+
+namespace nt {
+namespace {
+
+constexpr int kPg = NT_KV4_PAGE;
+constexpr float kTopScale = 2720.f;
+
+template <int HD>
+struct Kv4Block {
+  static constexpr int NG = HD / 32;                  // scales of a row
+  static constexpr int row = HD / 2;                  // bytes of a row's codes
+  static constexpr int scales = kPg * row;            // the scales' place in a half
+  static constexpr int half = scales + kPg * NG * 2;  // bytes of the K or V half
+  static constexpr int bytes = 2 * half;
+  static constexpr int WPL = HD / 64;                 // V words of a line's lane: planes
+};
+__host__ __device__ constexpr int kv4_swap(int t) { return (t & ~7) | ((t & 1) << 2) | ((t >> 1) & 3); }
+
+// byte of word j of row t, and of the scale of (t, group), in the K (0) or V (1) half
+template <int HD>
+__device__ __forceinline__ int kv4_word_at(int which, int t, int j) {
+  using B = Kv4Block<HD>;
+  if (which == 0) return t * B::row + 4 * j;
+  return (j % B::WPL) * (kPg * 32) + kv4_swap(t) * 32 + (j / B::WPL) * 4;
+}
+template <int HD>
+__device__ __forceinline__ int kv4_scale_at(int which, int t, int group) {
+  using B = Kv4Block<HD>;
+  const int at = which == 0 ? ((t & 7) * B::NG + group) * 8 + (t >> 3)
+                            : (group * 4 + ((t >> 1) & 3)) * 16 + (t >> 4) * 4 + ((t >> 3) & 1) * 2 + (t & 1);
+  return B::scales + 2 * at;
+}
+
+// ---- codes -----------------------------------------------------------------------
+// (x & m) | b as one three-input operation
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(m), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+
+// I4: nibble i of either 16-bit half of x, in bits 6..9 of 0x4C00: the f16 number 16 + code
+template <int I>
+__device__ __forceinline__ __half2 i4_biased(uint32_t x) {
+  const uint32_t y = I == 0 ? x << 6 : I == 1 ? x << 2 : I == 2 ? x >> 2 : x >> 6;
+  return as_h2(and_or(y, 0x03C003C0u, 0x4C004C00u));
+}
+// E2M1: the four bytes of x, two codes each, through the hardware's conversion
+__device__ __forceinline__ void e2m1_to_h2(uint32_t x, uint32_t h[4]) {
+  asm("{\n\t.reg .b8 p, q, r, s;\n\tmov.b32 {p, q, r, s}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, p;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, q;\n\tcvt.rn.f16x2.e2m1x2 %2, r;\n\tcvt.rn.f16x2.e2m1x2 %3, s;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(x));
+}
+// a word's 8 values over the scale, in the order of its channels
+template <int FMT>
+__device__ __forceinline__ void unpack4(uint32_t x, float v[8]) {
+  if (FMT == NT_KV4_I4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = float(int((x >> (4 * i)) & 15u) - 8);
+  } else {
+    uint32_t h[4];
+    e2m1_to_h2(x, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(as_h2(h[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ float max_nan4(float a, float b) {  // the larger; NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// the scale: d0 held to the largest, rounded to 8 bits, then to f16
+__device__ __forceinline__ float scale8(float d0) {
+  d0 = fminf(fmaxf(d0, -kTopScale), kTopScale);
+  return __half2float(__float2half_rn(__bfloat162float(__float2bfloat16_rn(d0))));
+}
+// a / 6 so that its rounding to 8 bits is that of the exact quotient: an fp32 quotient
+// halfway between two of them is moved to the side on which the exact one lies
+__device__ __forceinline__ float sixth(float a) {
+  const float q = __fdiv_rn(a, 6.f);
+  uint32_t u = __float_as_uint(q);
+  if ((u & 0xFFFFu) == 0x8000u) {
+    const float rest = fmaf(-6.f, q, a);
+    u += rest > 0.f ? 1u : rest < 0.f ? ~0u : 0u;
+  }
+  return __uint_as_float(u);
+}
+
+// The 8 codes of x over the scale d (inv about 1 / d, 0 for d = 0), as a word.  The
+// products x inv are within 2^-22 of the quotients; where one of them is that near the
+// border between two codes, the group's word is decided again by products of the border
+// and d, which are exact in fp32.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(const float x[8], float d, float inv) {
+  uint32_t w = 0;
+  bool close = false;
+  if (FMT == NT_KV4_I4) {
+    float worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = fminf(fmaxf(x[i] * inv, -8.f), 7.f);
+      const float z = y + 12582920.f;              // 1.5 * 2^23 + 8: the code in the low bits
+      worst = fmaxf(worst, fabsf(y - (z - 12582920.f)));
+      w |= (__float_as_uint(z) & 15u) << (4 * i);
+    }
+    close = worst > 0.49999f;
+  } else {
+    uint32_t up[4], dn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
+      constexpr float hi = 1.f + 0x1p-20f, lo = 1.f - 0x1p-20f;
+      asm("{\n\t.reg .b8 p, q;\n\tcvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+          "mov.b32 %0, {p, q, p, q};\n\t}"
+          : "=r"(up[i])
+          : "f"(a * hi), "f"(b * hi), "f"(a * lo), "f"(b * lo));
+      dn[i] = (up[i] >> 8) & 255u;
+      up[i] &= 255u;
+      close |= up[i] != dn[i];
+      w |= up[i] << (8 * i);
+    }
+  }
+  if (close) {
+    w = 0;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      float v = x[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) v = k == i ? x[k] : v;
+      uint32_t code;
+      if (FMT == NT_KV4_I4) {
+        float q = rintf(fminf(fmaxf(v * inv, -9.f), 9.f));
+        // x / d - q, as x - q d with the sign of d; exact wherever it is near half of d
+        const float rest = copysignf(1.f, d) * fmaf(-q, d, v), half = 0.5f * fabsf(d);
+        if (fabsf(rest) > half || (fabsf(rest) == half && (int(q) & 1))) q += rest > 0.f ? 1.f : -1.f;
+        code = uint32_t(int(fminf(fmaxf(q, -8.f), 7.f)) + 8);
+        if (inv == 0.f) code = 8u;
+      } else {
+        const float m = fabsf(v);
+        code = (m > 0.25f * d) + (m >= 0.75f * d) + (m > 1.25f * d) + (m >= 1.75f * d) + (m > 2.5f * d) +
+               (m >= 3.5f * d) + (m > 5.f * d);
+        if (inv == 0.f) code = 0u;
+        code |= v < 0.f ? 8u : 0u;
+      }
+      w |= code << (4 * i);
+    }
+  }
+  return w;
+}
+
+// ---- write and read back ------------------------------------------------------------
+constexpr int kRowThreads = 256;
+
+struct Kv4RowsArgs {
+  char* row[2];  // K, V rows (either may be null when read)
+  int64_t tok_stride, head_stride;  // bytes
+  uint8_t* data;
+  const int64_t* slots;
+  int64_t n_tok, n_slots;
+  int n_kvh;
+  unsigned* err;
+};
+
+__device__ __forceinline__ void load8(const float* p, float v[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __half* p, float v[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(as_h2(w[i]));
+    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+  }
+}
+
+// A thread has 8 channels of a row, one word of codes; the four threads of a group
+// reduce its extremes.
+template <int FMT, int HD, typename T>
+__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowsArgs a) {
+  using B = Kv4Block<HD>;
+  constexpr int TR = HD / 8;  // threads of a row
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) / TR;
+  const int j = threadIdx.x % TR, which = blockIdx.y;
+  const int64_t tok = row / a.n_kvh;
+  const int h = int(row - tok * a.n_kvh);
+  int64_t slot = tok < a.n_tok ? a.slots[tok] : -1;
+  if (slot >= a.n_slots) {
+    if (j == 0) flag_error(a.err, kErrPaged);
+    slot = -1;
+  }
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (slot >= 0)
+    load8(reinterpret_cast<const T*>((which ? a.row[1] : a.row[0]) + tok * a.tok_stride + h * a.head_stride) + 8 * j, x);
+  float bad = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bad = max_nan4(bad, fabsf(x[i]));
+  const bool clean = bad <= 3.402823466e38f;
+  float hi = 0.f, lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (!clean) {  // NaN becomes 0, an infinity leaves the scale alone
+      if (x[i] != x[i]) x[i] = 0.f;
+      if (fabsf(x[i]) > 3.402823466e38f) continue;
+    }
+    hi = fmaxf(hi, x[i]);
+    lo = fminf(lo, x[i]);
+  }
+  if (!clean) flag_error(a.err, kErrNonFinite4);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+  const float d = scale8(FMT == NT_KV4_I4 ? (hi >= -lo ? hi : lo) * -0.125f : sixth(fmaxf(hi, -lo)));
+  const float inv = d != 0.f ? __frcp_rn(d) : 0.f;
+  if (!clean) {  // an infinity: a finite value that the codes end below, and 0 over a scale of 0
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -1e38f), 1e38f);
+  }
+  const uint32_t w = codes4<FMT>(x, d, inv);
+  if (slot < 0) return;
+  uint8_t* half = a.data + ((slot / kPg) * a.n_kvh + h) * B::bytes + which * B::half;
+  const int t = int(slot % kPg);
+  *reinterpret_cast<uint32_t*>(half + kv4_word_at<HD>(which, t, j)) = w;
+  if (j % 4 == 0) *reinterpret_cast<__half*>(half + kv4_scale_at<HD>(which, t, j / 4)) = __float2half_rn(d);
+}
+
+template <int FMT, int HD, typename T>
+__global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs a) {
+  using B = Kv4Block<HD>;
+  constexpr int TR = HD / 8;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) / TR;
+  const int j = threadIdx.x % TR, which = blockIdx.y;
+  char* out = which ? a.row[1] : a.row[0];
+  const int64_t tok = row / a.n_kvh;
+  const int h = int(row - tok * a.n_kvh);
+  if (!out || tok >= a.n_tok) return;
+  const int64_t slot = a.slots[tok];
+  if (slot < 0) return;
+  if (slot >= a.n_slots) {
+    if (j == 0) flag_error(a.err, kErrPaged);
+    return;
+  }
+  const uint8_t* half = a.data + ((slot / kPg) * a.n_kvh + h) * B::bytes + which * B::half;
+  const int t = int(slot % kPg);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(half + kv4_word_at<HD>(which, t, j));
+  const float d = __half2float(*reinterpret_cast<const __half*>(half + kv4_scale_at<HD>(which, t, j / 4)));
+  float v[8];
+  unpack4<FMT>(w, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= d;
+  T* to = reinterpret_cast<T*>(out + tok * a.tok_stride + h * a.head_stride) + 8 * j;
+  if (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = as_u32(__floats2half2_rn(v[2 * i], v[2 * i + 1]));
+    *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+}
+
+// ---- attention -----------------------------------------------------------------------
+// Scores and outputs on the tensor cores (mma.sync m16n8k16, f16 products, fp32 sums)
+// with fp32-level operands.  K and V are the A operands: 16 positions by 16 channels of
+// K, 16 channels by 16 positions of V, exact in f16 with their scales.  A column pair
+// (2 r, 2 r + 1) of the B operand holds hi = f16(x) and lo = f16(x - hi) of query row r
+// (or of its probabilities), which together carry 22 bits: a tile of 8 columns is 4 rows
+// (NT tiles: 4 NT rows), and the two parts of a product meet in one thread.
+//
+// Fragments come without a transpose in shared memory: the names of MMA rows and k slots
+// are ours.  Lane (g = lane / 4, c = lane % 4), 16 positions 16 m .. of a page:
+//  - K: the lane reads rows 16 m + g and 16 m + 8 + g, channels c HD / 4 .. of them; word
+//    w, pairs 2 u and 2 u + 1 of either row are its part of k-step (w, u).
+//  - S^T: the lane then has the scores of those positions with row c of each tile.
+//  - P: (hi, lo) of a position and row is one register, an 8 x 8 transpose in the
+//    registers (movmatrix) turns them into the B fragment whose k slots are positions.
+//  - V: the lane reads word w of channels g HD / 8 .. of rows 16 m + 2 c, + 1, + 8, + 9;
+//    channel n of the word is MMA row g or g + 8 of m-tile n % 4 (I4) or n / 2 (E2M1).
+//
+// Work: the steps (a page of one KV head for one chunk of 4 NT query rows) of all
+// requests in one line, the same number to each warp, whatever the requests' lengths.
+// A warp walks its steps with an online softmax; where it begins or ends inside an item
+// (request, head, chunk) it leaves a partial (m, l, o).  The CTA joins its warps'
+// partials of one item, and the last CTA to arrive at an item that several share joins
+// theirs, in the order of the line: nothing depends on who arrives when.
+constexpr int kWarps = 8;
+constexpr int kMaxCtas = 512;                 // one counter each
+constexpr float kPTop = 8.f, kSlack = 6.f;    // probabilities are up to 2^(kPTop + kSlack), in f16's range
+constexpr float kLowest = -3.402823466e38f;
+
+struct AttnKv4Args {
+  const float* q;
+  const uint8_t* data;
+  float* out;
+  const int32_t *q_start, *held, *table;
+  float* part;         // [CTA][2][rows][HD]
+  float2* ml;          // [CTA][2][rows]
+  unsigned* counters;  // [CTA], zero at rest
+  unsigned* err;
+  int64_t max_pages, n_pages, n_tok;
+  uint64_t inv_g;      // ceil(2^32 / G): row / G = row inv_g >> 32 below 2^28 rows
+  int n_req, n_qh, n_kvh, G;
+  int stall;
+};
+
+__device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (hi, lo) f16 parts of x in one register; hi is x with 11 bits, so x - hi is exact
+__device__ __forceinline__ uint32_t hi_lo(float x) {
+  const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
+  return as_u32(__floats2half2_rn(hi, x - hi));
+}
+
+// shared memory: each warp's K and V halves; its partial of the item that it found
+// begun; the sums of steps over the requests.  At the end the warps' last partials lie in
+// their own K and V halves.
+template <int HD, int NT>
+struct AttnKv4Smem {
+  static constexpr int ROWS = 4 * NT;
+  static constexpr int line = HD + 4;                                  // floats of a row of a partial
+  static constexpr size_t slot = size_t(ROWS) * line * 4 + ROWS * 8;   // then (m, l) of each row
+  static constexpr size_t ring = 0;
+  static constexpr size_t first = size_t(kWarps) * Kv4Block<HD>::bytes;
+  static constexpr size_t sums = first + kWarps * slot;
+  static size_t bytes(int n_req) { return sums + size_t(n_req + 1) * 8; }
+  static_assert(slot <= size_t(Kv4Block<HD>::bytes), "a partial fits a warp's halves");
+  static_assert(kMaxCtas * ROWS * 4 <= first, "the weights of a join fit the ring");
+};
+
+// a request: its first row, rows and positions, held to what the arguments allow
+struct Req {
+  int row0, rows, len;
+};
+__device__ __forceinline__ Req request(const AttnKv4Args& a, int r, bool tell) {
+  const int b = a.q_start[r], e = a.q_start[r + 1], n = a.held[r];
+  Req x{b, e - b, n};
+  const int64_t cap = a.max_pages * kPg;
+  const bool rows_ok = b >= 0 && e >= b && e <= a.n_tok, len_ok = n >= 0 && n <= cap;
+  if (!rows_ok) x.rows = 0;
+  if (!len_ok) x.len = n < 0 ? 0 : int(cap);
+  if (tell && !(rows_ok && len_ok)) flag_error(a.err, kErrPaged);
+  return x;
+}
+
+// the item and page of a step
+struct Step {
+  int r;           // request
+  Req q;
+  int pages, chunks;
+  int64_t item0;   // the item's first step
+  int h, z, page;  // KV head, chunk of rows, page
+};
+
+template <int FMT, int HD, int NT, int CTAS>
+__global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnKv4Args a) {
+  using B = Kv4Block<HD>;
+  using L = AttnKv4Smem<HD, NT>;
+  constexpr int ROWS = 4 * NT;
+  constexpr int WK = HD / 32;  // K words of a lane and row
+  constexpr int KS = HD / 16;  // k-steps of the scores
+  constexpr int CW = HD / 8;   // output channels of a lane and row
+  extern __shared__ __align__(16) uint8_t sm4[];
+  __shared__ __align__(8) uint64_t bars[kWarps][2];
+  __shared__ int64_t seg_item[kWarps][2];   // item (its first step) of a warp's partials, -1: none
+  __shared__ int64_t wsum[kWarps];
+  __shared__ unsigned arrived;
+  int64_t* sums = reinterpret_cast<int64_t*>(sm4 + L::sums);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const uint32_t bar = smem_u32(&bars[warp][0]);
+  const uint64_t pol = policy_evict_first();
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    mbar_init(bar + 8, 1);
+    fence_barrier_init();
+    seg_item[warp][0] = seg_item[warp][1] = -1;
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- steps of the requests, summed
+  const auto steps_of = [&](const Req& q, int& pages, int& chunks) {
+    pages = max(1, (q.len + kPg - 1) / kPg);
+    chunks = int((int64_t(q.rows) * a.G + ROWS - 1) / ROWS);
+    return int64_t(chunks) * a.n_kvh * pages;
+  };
+  {
+    int64_t run = 0;
+    for (int r0 = 0; r0 < a.n_req; r0 += kWarps * 32) {
+      const int r = r0 + tid;
+      int64_t v = 0;
+      if (r < a.n_req) {
+        int pages, chunks;
+        v = steps_of(request(a, r, blockIdx.x == 0), pages, chunks);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      if (lane == 31) wsum[warp] = v;
+      __syncthreads();
+      int64_t before = run;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += wsum[w];
+        run += wsum[w];
+      }
+      if (r < a.n_req) sums[r + 1] = before + v;
+      if (r == 0) sums[0] = 0;
+      __syncthreads();
+    }
+  }
+  const int64_t total = sums[a.n_req];
+  const int64_t per = max(int64_t(1), (total + int64_t(gridDim.x) * kWarps - 1) / (int64_t(gridDim.x) * kWarps));
+  const int64_t cta0 = min(total, int64_t(blockIdx.x) * kWarps * per), cta1 = min(total, cta0 + kWarps * per);
+  if (cta0 >= cta1) return;
+  const int64_t s0 = min(total, cta0 + warp * per), s1 = min(total, s0 + per);
+
+  const auto locate = [&](int64_t s) {
+    int lo = 0, hi = a.n_req;  // sums[lo] <= s < sums[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid] <= s) lo = mid; else hi = mid;
+    }
+    Step x;
+    x.r = lo;
+    x.q = request(a, lo, false);
+    steps_of(x.q, x.pages, x.chunks);
+    const int64_t off = s - sums[lo], it = off / x.pages;
+    x.page = int(off - it * x.pages);
+    x.item0 = s - x.page;
+    x.h = int(it / x.chunks);
+    x.z = int(it - int64_t(x.h) * x.chunks);
+    return x;
+  };
+  const auto query_of = [&](int row) { return int((uint64_t(unsigned(row)) * a.inv_g) >> 32); };
+  // rows of a chunk, the query of its last row, and the positions that one sees
+  const auto chunk_rows = [&](const Step& x) { return int(min(int64_t(ROWS), int64_t(x.q.rows) * a.G - int64_t(x.z) * ROWS)); };
+  const auto seen = [&](const Step& x, int row) {  // by row `row` of the chunk
+    return x.q.len - (x.q.rows - 1 - query_of(x.z * ROWS + row));
+  };
+  // the offset of (row of the chunk)'s vector in q and out
+  const auto vec_of = [&](const Step& x, int row) {
+    const int at = x.z * ROWS + row, qi = query_of(at);
+    return (int64_t(x.q.row0 + qi) * a.n_qh + x.h * a.G + (at - qi * a.G)) * HD;
+  };
+  // where a step's block lies; null: none of its positions is seen
+  const auto block_of = [&](const Step& x) -> const uint8_t* {
+    if (x.page * kPg >= seen(x, chunk_rows(x) - 1)) return nullptr;
+    const int p = a.table[x.r * a.max_pages + x.page];
+    if (p < 0 || p >= a.n_pages) {
+      if (lane == 0) flag_error(a.err, kErrPaged);
+      return nullptr;
+    }
+    return a.data + (int64_t(p) * a.n_kvh + x.h) * B::bytes;
+  };
+  uint8_t* const sk = sm4 + L::ring + size_t(warp) * B::bytes;
+  const uint8_t* const sv = sk + B::half;
+  const auto copy = [&](const uint8_t* from, int which) {
+    if (!from || lane != 0) return;
+    mbar_arrive_expect_tx(bar + 8 * which, B::half);
+    if (!a.stall) bulk_g2s(smem_u32(which ? sv : sk), from + which * B::half, B::half, bar + 8 * which, pol);
+  };
+  uint32_t phase = 0;
+  bool dead = false;  // a wait ran out: the rest is taken as not seen
+  const auto wait = [&](int which, bool next_k) {
+    const int cap = a.stall ? kStallSpin : kMaxSpin;
+    if (__all_sync(0xffffffffu, mbar_wait(bar + 8 * which, phase, cap))) return true;
+    if (lane == 0) flag_error(a.err, kErrWaitTimeout);
+    mbar_wait(bar + 8 * which, phase, cap);
+    if (which == 0) mbar_wait(bar + 8, phase, cap);
+    else if (next_k) mbar_wait(bar, phase ^ 1, cap);
+    dead = true;
+    return false;
+  };
+
+  Step x{};
+  const uint8_t* blk = nullptr;
+  if (s0 < s1) {
+    x = locate(s0);
+    blk = block_of(x);
+    copy(blk, 0);
+    copy(blk, 1);
+  }
+  uint32_t qf[NT][KS][2];
+  float rscale[NT], m[NT], l[NT], o[NT][CW];
+  int limit[NT];
+  int rows = 0, tokens = 0, fewest = 0;
+  bool fresh = true;
+  for (int64_t s = s0; s < s1; ++s) {
+    if (fresh) {  // a new item: its rows of q, scaled by a power of two to amax in [2^13, 2^14) and split
+      fresh = false;
+      rows = chunk_rows(x);
+      tokens = seen(x, rows - 1);
+      fewest = seen(x, 0);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int row = 4 * j + (g >> 1);
+        float v[HD / 4];
+#pragma unroll
+        for (int i = 0; i < HD / 4; ++i) v[i] = 0.f;
+        if (row < rows) {
+          const float* q = a.q + vec_of(x, row) + c * (HD / 4);
+#pragma unroll
+          for (int i = 0; i < HD / 4; i += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(q + i);
+            v[i] = y.x, v[i + 1] = y.y, v[i + 2] = y.z, v[i + 3] = y.w;
+          }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < HD / 4; ++i) top = fmaxf(top, fabsf(v[i]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = min(100, 140 - int(__float_as_uint(top) >> 23));
+        const float sc = __uint_as_float(uint32_t(e + 127) << 23);
+#pragma unroll
+        for (int w = 0; w < WK; ++w)
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {  // pair p of word w
+            const int i0 = 8 * w + (FMT == NT_KV4_I4 ? p : 2 * p), i1 = 8 * w + (FMT == NT_KV4_I4 ? p + 4 : 2 * p + 1);
+            const __half2 hi = __floats2half2_rn(v[i0] * sc, v[i1] * sc);
+            const float2 f = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn(v[i0] * sc - f.x, v[i1] * sc - f.y);
+            qf[j][2 * w + p / 2][p & 1] = as_u32(g & 1 ? lo : hi);
+          }
+        // of row c of the tile: lanes 8 c .. hold its q
+        rscale[j] = __uint_as_float(uint32_t(127 - __shfl_sync(0xffffffffu, e, 8 * c)) << 23) *
+                    (1.44269504088896f * rsqrtf(float(HD)));
+        limit[j] = 4 * j + c < rows ? seen(x, 4 * j + c) : 0;
+        m[j] = -INFINITY;
+        l[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < CW; ++i) o[j][i] = 0.f;
+      }
+    }
+    // the next step, its table entry requested before this step's work
+    Step nx = x;
+    const uint8_t* nblk = nullptr;
+    const bool ends = x.page + 1 == x.pages;
+    if (s + 1 < s1) {
+      if (!ends) {
+        ++nx.page;
+      } else if (x.z + 1 < x.chunks) {
+        nx.page = 0, ++nx.z, nx.item0 = s + 1;
+      } else if (x.h + 1 < a.n_kvh) {
+        nx.page = 0, nx.z = 0, ++nx.h, nx.item0 = s + 1;
+      } else {
+        nx = locate(s + 1);
+      }
+      if (!dead) nblk = block_of(nx);
+    }
+    bool live = blk != nullptr && !dead;
+    const int t0 = x.page * kPg;
+    float sc[NT][4][4];
+    if (live) live = wait(0, false);
+    if (live) {
+      // ---- scores
+      const uint4 ksw = *reinterpret_cast<const uint4*>(sk + B::scales + (g * B::NG + (HD == 128 ? c : c >> 1)) * 16);
+      const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};  // rows g + 8 i of the page: two a word
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        uint32_t kw[2][WK];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint8_t* p = sk + (16 * mt + 8 * e + g) * B::row + c * (HD / 8);
+          if (HD == 128) {
+            const uint4 y = *reinterpret_cast<const uint4*>(p);
+            kw[e][0] = y.x, kw[e][1] = y.y, kw[e][WK - 2] = y.z, kw[e][WK - 1] = y.w;
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(p);
+            kw[e][0] = y.x, kw[e][1] = y.y;
+          }
+        }
+        const __half2 d2[2] = {as_h2(__byte_perm(ks[mt], 0u, 0x1010)), as_h2(__byte_perm(ks[mt], 0u, 0x3232))};
+        const __half2 off[2] = {__hmul2(d2[0], __float2half2_rn(-24.f)), __hmul2(d2[1], __float2half2_rn(-24.f))};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sc[j][mt][0] = sc[j][mt][1] = sc[j][mt][2] = sc[j][mt][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+          uint32_t kv[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (FMT == NT_KV4_I4) {
+              kv[e][0] = as_u32(__hfma2(i4_biased<0>(kw[e][w]), d2[e], off[e]));
+              kv[e][1] = as_u32(__hfma2(i4_biased<1>(kw[e][w]), d2[e], off[e]));
+              kv[e][2] = as_u32(__hfma2(i4_biased<2>(kw[e][w]), d2[e], off[e]));
+              kv[e][3] = as_u32(__hfma2(i4_biased<3>(kw[e][w]), d2[e], off[e]));
+            } else {
+              e2m1_to_h2(kw[e][w], kv[e]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) kv[e][i] = as_u32(__hmul2(as_h2(kv[e][i]), d2[e]));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t af[4] = {kv[0][2 * u], kv[1][2 * u], kv[0][2 * u + 1], kv[1][2 * u + 1]};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16816(sc[j][mt], af, qf[j][2 * w + u][0], qf[j][2 * w + u][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();  // this step's K is in registers and used
+    if (!dead) copy(nblk, 0);
+    uint32_t pf[NT][4][2];
+    if (live) {
+      // ---- online softmax, base 2: m is left behind by up to kSlack before the sums are rescaled
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float p[8];  // positions 16 i / 2 + 8 (i % 2) + g of the page
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = (sc[j][i / 2][2 * (i & 1)] + sc[j][i / 2][2 * (i & 1) + 1]) * rscale[j];
+        if (t0 + kPg > fewest) {
+          const int left = limit[j] - t0 - g;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = 8 * i < left ? p[i] : -INFINITY;
+        }
+        float mx = p[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, p[i]);
+        if (__any_sync(0xffffffffu, mx > m[j] + kSlack)) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          const float mn = fmaxf(m[j], mx);
+          const float corr = mn == -INFINITY ? 1.f : ex2(m[j] - mn);
+          m[j] = mn;
+          l[j] *= corr;
+#pragma unroll
+          for (int i = 0; i < CW; ++i) o[j][i] *= corr;
+        }
+        const float base = m[j] == -INFINITY ? 0.f : kPTop - m[j];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i] = ex2(p[i] + base);
+          sum += p[i];
+        }
+        l[j] += sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pf[j][i / 2][i & 1] = transpose8(hi_lo(p[i]));
+      }
+      live = wait(1, nblk != nullptr);
+    }
+    if (live) {
+      // ---- P V.  Each page's products start from zero and are added to the output in
+      // fp32: the tensor cores round their sums towards zero, and that bias would grow
+      // with the length.
+      const uint4* vsp = reinterpret_cast<const uint4*>(sv + B::scales + ((HD == 128 ? g >> 1 : g >> 2) * 4 + c) * 32);
+      const uint4 va = vsp[0], vb = vsp[1];
+      uint32_t vs[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};  // positions 8 i + 2 c, + 1
+      if (t0 + kPg > tokens) {  // positions that no row sees: whatever their bytes are, they count as 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int left = tokens - t0 - 8 * i - 2 * c;
+          vs[i] = left > 1 ? vs[i] : left == 1 ? vs[i] & 0xFFFFu : 0u;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < B::WPL; ++w) {
+        float acc[NT][4][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) acc[j][n][0] = acc[j][n][1] = acc[j][n][2] = acc[j][n][3] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          uint32_t vv[2][2][4];  // [positions 2 c, + 1 or + 8, + 9][MMA row g or g + 8][m-tile]
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint8_t* p = sv + w * (kPg * 32) + (16 * mt + 8 * e + c) * 32 + g * 4;
+            const uint32_t r0 = *reinterpret_cast<const uint32_t*>(p), r1 = *reinterpret_cast<const uint32_t*>(p + 128);
+            const __half2 d2 = as_h2(vs[2 * mt + e]);
+            if (FMT == NT_KV4_I4) {
+              const __half2 off = __hmul2(d2, __float2half2_rn(-24.f));
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                const uint32_t y = __byte_perm(r0, r1, f ? 0x7632 : 0x5410);
+                vv[e][f][0] = as_u32(__hfma2(i4_biased<0>(y), d2, off));
+                vv[e][f][1] = as_u32(__hfma2(i4_biased<1>(y), d2, off));
+                vv[e][f][2] = as_u32(__hfma2(i4_biased<2>(y), d2, off));
+                vv[e][f][3] = as_u32(__hfma2(i4_biased<3>(y), d2, off));
+              }
+            } else {
+              // bytes of two nibbles: the even (odd) channels of both positions
+              const uint32_t even = and_or(r0, 0x0F0F0F0Fu, (r1 << 4) & 0xF0F0F0F0u);
+              const uint32_t odd = and_or(r0 >> 4, 0x0F0F0F0Fu, r1 & 0xF0F0F0F0u);
+              e2m1_to_h2(even, vv[e][0]);
+              e2m1_to_h2(odd, vv[e][1]);
+#pragma unroll
+              for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) vv[e][f][n] = as_u32(__hmul2(as_h2(vv[e][f][n]), d2));
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t af[4] = {vv[0][0][n], vv[0][1][n], vv[1][0][n], vv[1][1][n]};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16816(acc[j][n], af, pf[j][mt][0], pf[j][mt][1]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            o[j][8 * w + (FMT == NT_KV4_I4 ? n : 2 * n)] += acc[j][n][0] + acc[j][n][1];
+            o[j][8 * w + (FMT == NT_KV4_I4 ? n + 4 : 2 * n + 1)] += acc[j][n][2] + acc[j][n][3];
+          }
+      }
+    }
+    __syncwarp();  // and its V
+    if (!dead) copy(nblk, 1);
+    if (blk) phase ^= 1;
+    if (ends || s + 1 == s1) {
+      // ---- the item's end, or the warp's: the output, or a partial
+      const bool begun = x.item0 >= s0;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
+      if (begun && ends) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (4 * j + c >= rows) continue;
+          const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
+          float* to = a.out + vec_of(x, 4 * j + c) + g * CW;
+#pragma unroll
+          for (int i = 0; i < CW; i += 4)
+            *reinterpret_cast<float4*>(to + i) =
+                make_float4(o[j][i] * inv, o[j][i + 1] * inv, o[j][i + 2] * inv, o[j][i + 3] * inv);
+        }
+      } else {
+        const int which = ends ? 0 : 1;
+        uint8_t* base = which ? sk : sm4 + L::first + warp * L::slot;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float* to = reinterpret_cast<float*>(base) + (4 * j + c) * L::line + g * CW;
+#pragma unroll
+          for (int i = 0; i < CW; i += 4)
+            *reinterpret_cast<float4*>(to + i) = make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]);
+          if (g == 0) reinterpret_cast<float2*>(base + ROWS * L::line * 4)[4 * j + c] = make_float2(m[j], l[j]);
+        }
+        if (lane == 0) seg_item[warp][which] = x.item0;
+      }
+      fresh = true;
+    }
+    x = nx;
+    blk = nblk;
+  }
+  __syncthreads();
+
+  // ---- join the warps' partials of one item: runs of (warp, first or last) in the line's order
+  const auto slot_of = [&](int i) {
+    return i & 1 ? sm4 + L::ring + size_t(i >> 1) * B::bytes : sm4 + L::first + size_t(i >> 1) * L::slot;
+  };
+  const auto item_of = [&](int i) { return seg_item[i >> 1][i & 1]; };
+  int64_t shared_item[2] = {-1, -1};  // items that other CTAs have parts of: begun elsewhere, ending elsewhere
+  for (int i0 = 0; i0 < 2 * kWarps; ++i0) {
+    const int64_t item = item_of(i0);
+    if (item < 0) continue;
+    int i1 = i0 + 1;
+    while (i1 < 2 * kWarps && (item_of(i1) < 0 || item_of(i1) == item)) ++i1;
+    const Step y = locate(item);
+    const bool begun = item >= cta0, ended = item + y.pages <= cta1, whole = begun && ended;
+    const int side = begun ? 1 : 0;
+    const int n_rows = chunk_rows(y);
+    for (int e = tid; e < ROWS * HD; e += kWarps * 32) {
+      const int row = e / HD, ch = e % HD;
+      float M = kLowest;
+      for (int i = i0; i < i1; ++i)
+        if (item_of(i) == item) M = fmaxf(M, reinterpret_cast<const float2*>(slot_of(i) + ROWS * L::line * 4)[row].x);
+      float acc = 0.f, sum = 0.f;
+      for (int i = i0; i < i1; ++i) {
+        if (item_of(i) != item) continue;
+        const float2 ml = reinterpret_cast<const float2*>(slot_of(i) + ROWS * L::line * 4)[row];
+        const float f = ex2(ml.x - M);
+        sum = fmaf(ml.y, f, sum);
+        acc = fmaf(reinterpret_cast<const float*>(slot_of(i))[row * L::line + ch], f, acc);
+      }
+      if (whole) {
+        if (row < n_rows) a.out[vec_of(y, row) + ch] = sum == 0.f ? 0.f : acc / sum;
+      } else {
+        const int64_t at = (int64_t(blockIdx.x) * 2 + side) * ROWS + row;
+        a.part[at * HD + ch] = acc;
+        if (ch == 0) a.ml[at] = make_float2(M, sum);
+      }
+    }
+    if (!whole) shared_item[side] = item;
+    i0 = i1 - 1;
+  }
+
+  // ---- join the CTAs' partials of an item: the last to arrive does, in the line's order
+  for (int side = 0; side < 2; ++side) {
+    const int64_t item = shared_item[side];
+    if (item < 0) continue;
+    const Step y = locate(item);
+    const int first = int(item / (kWarps * per)), last = int((item + y.pages - 1) / (kWarps * per)), n = last - first + 1;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) arrived = atomicAdd(a.counters + first, 1u);
+    __syncthreads();
+    if (arrived + 1 != unsigned(n)) continue;
+    __threadfence();
+    if (tid == 0) a.counters[first] = 0u;
+    float* wts = reinterpret_cast<float*>(sm4 + L::ring);
+    __shared__ float inv[ROWS];
+    // the partial of CTA first + i: its item began there (i = 0), or elsewhere
+    const auto part_row = [&](int i, int row) { return (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
+    if (warp < ROWS) {
+      for (int row = warp; row < ROWS; row += kWarps) {
+        float M = kLowest, sum = 0.f;
+        for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.ml + part_row(i, row)).x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        for (int i = lane; i < n; i += 32) {
+          const float2 ml = __ldcg(a.ml + part_row(i, row));
+          const float f = ex2(ml.x - M);
+          wts[i * ROWS + row] = f;
+          sum = fmaf(ml.y, f, sum);
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) inv[row] = sum == 0.f ? 0.f : 1.f / sum;
+      }
+    }
+    __syncthreads();
+    const int n_rows = chunk_rows(y);
+    for (int e = tid; e < n_rows * HD; e += kWarps * 32) {
+      const int row = e / HD, ch = e % HD;
+      float acc = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) acc = fmaf(__ldcg(a.part + part_row(i, row) * HD + ch), wts[i * ROWS + row], acc);
+      a.out[vec_of(y, row) + ch] = acc * inv[row];
+    }
+    __syncthreads();  // the weights are read before the other side's
+  }
+}
+
+using RowsKernel = void (*)(Kv4RowsArgs);
+template <template <int, int, typename> class Pick>
+RowsKernel kv4_rows_for(int fmt, int hd, int row_fmt) {
+  if (fmt == NT_KV4_I4)
+    return row_fmt == NT_F32 ? (hd == 128 ? Pick<NT_KV4_I4, 128, float>::kernel : Pick<NT_KV4_I4, 64, float>::kernel)
+                             : (hd == 128 ? Pick<NT_KV4_I4, 128, __half>::kernel : Pick<NT_KV4_I4, 64, __half>::kernel);
+  return row_fmt == NT_F32 ? (hd == 128 ? Pick<NT_KV4_E2M1, 128, float>::kernel : Pick<NT_KV4_E2M1, 64, float>::kernel)
+                           : (hd == 128 ? Pick<NT_KV4_E2M1, 128, __half>::kernel : Pick<NT_KV4_E2M1, 64, __half>::kernel);
+}
+template <int FMT, int HD, typename T>
+struct AppendPick {
+  static constexpr RowsKernel kernel = kv4_append_kernel<FMT, HD, T>;
+};
+template <int FMT, int HD, typename T>
+struct ReadPick {
+  static constexpr RowsKernel kernel = kv4_read_kernel<FMT, HD, T>;
+};
+
+Kv4RowsArgs rows_args(const Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v, int64_t n, int64_t tok_stride,
+                      int64_t head_stride, const int64_t* slots) {
+  const int size = fmt == NT_F32 ? 4 : 2;
+  Kv4RowsArgs a{};
+  a.row[0] = static_cast<char*>(k);
+  a.row[1] = static_cast<char*>(v);
+  a.tok_stride = tok_stride * size;
+  a.head_stride = head_stride * size;
+  a.data = static_cast<uint8_t*>(kv.data);
+  a.slots = slots;
+  a.n_tok = n;
+  a.n_slots = kv.n_pages * kPg;
+  a.n_kvh = kv.n_kvh;
+  a.err = c->err_flag;
+  return a;
+}
+dim3 rows_grid(const nt_kv4& kv, int64_t n) {
+  const int64_t per = kRowThreads / (kv.head_dim / 8), rows = n * kv.n_kvh;
+  return dim3(unsigned((rows + per - 1) / per), 2);
+}
+
+using AttnKernel = void (*)(AttnKv4Args);
+struct AttnVariant {
+  AttnKernel kernel;
+  size_t smem;  // without the sums
+  int rows, ctas;
+};
+template <int FMT, int HD>
+AttnVariant attn_pick(int NT) {
+  if (NT == 1) return {attn_kv4_kernel<FMT, HD, 1, 2>, AttnKv4Smem<HD, 1>::sums, 4, 2};
+  return {attn_kv4_kernel<FMT, HD, 2, 1>, AttnKv4Smem<HD, 2>::sums, 8, 1};
+}
+AttnVariant attn_for(int fmt, int hd, int NT) {
+  if (fmt == NT_KV4_I4) return hd == 128 ? attn_pick<NT_KV4_I4, 128>(NT) : attn_pick<NT_KV4_I4, 64>(NT);
+  return hd == 128 ? attn_pick<NT_KV4_E2M1, 128>(NT) : attn_pick<NT_KV4_E2M1, 64>(NT);
+}
+
+}  // namespace
+
+size_t kv4_page_bytes(int head_dim) { return head_dim == 128 ? Kv4Block<128>::bytes : Kv4Block<64>::bytes; }
+
+nt_status launch_kv4_append(Ctx* c, const nt_kv4& kv, int fmt, const void* k, const void* v, int64_t n, int64_t tok_stride,
+                            int64_t head_stride, const int64_t* slots, cudaStream_t st) {
+  const Kv4RowsArgs a = rows_args(c, kv, fmt, const_cast<void*>(k), const_cast<void*>(v), n, tok_stride, head_stride, slots);
+  return cuda_check(c, launch_k(c, kv4_rows_for<AppendPick>(kv.fmt, kv.head_dim, fmt), rows_grid(kv, n), dim3(kRowThreads), 0,
+                                st, a),
+                    "4-bit cache write launch");
+}
+
+nt_status launch_kv4_read(Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v, int64_t n, int64_t tok_stride,
+                          int64_t head_stride, const int64_t* slots, cudaStream_t st) {
+  const Kv4RowsArgs a = rows_args(c, kv, fmt, k, v, n, tok_stride, head_stride, slots);
+  return cuda_check(c, launch_k(c, kv4_rows_for<ReadPick>(kv.fmt, kv.head_dim, fmt), rows_grid(kv, n), dim3(kRowThreads), 0,
+                                st, a),
+                    "4-bit cache read launch");
+}
+
+size_t kv4_attn_scratch(const Ctx* c, int head_dim) {
+  const size_t ctas = std::min(2 * c->num_sms, kMaxCtas);
+  return ctas * 2 * 8 * (head_dim * sizeof(float) + sizeof(float2));
+}
+
+nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, int n_qh, int64_t n_tok, int n_req,
+                          const int32_t* q_start, const int32_t* held, const int32_t* table, int64_t max_pages, char* scratch,
+                          unsigned* counters, cudaStream_t st) {
+  AttnKv4Args a{};
+  a.q = q;
+  a.data = static_cast<const uint8_t*>(kv.data);
+  a.out = out;
+  a.q_start = q_start;
+  a.held = held;
+  a.table = table;
+  a.counters = counters;
+  a.err = c->err_flag;
+  a.max_pages = max_pages;
+  a.n_pages = kv.n_pages;
+  a.n_tok = n_tok;
+  a.n_req = n_req;
+  a.n_qh = n_qh;
+  a.n_kvh = kv.n_kvh;
+  a.G = n_qh / kv.n_kvh;
+  a.inv_g = ((uint64_t(1) << 32) + a.G - 1) / a.G;
+  a.stall = take_stall(st);
+  const int64_t rows = (n_tok + n_req - 1) / n_req * a.G;
+  const AttnVariant k = attn_for(kv.fmt, kv.head_dim, rows <= 4 ? 1 : 2);
+  const int ctas = std::min(k.ctas * c->num_sms, kMaxCtas);
+  a.ml = reinterpret_cast<float2*>(scratch);
+  a.part = reinterpret_cast<float*>(scratch + size_t(ctas) * 2 * k.rows * sizeof(float2));
+  return cuda_check(c, launch_k(c, k.kernel, dim3(ctas), dim3(kWarps * 32), k.smem + size_t(n_req + 1) * 8, st, a),
+                    "4-bit attention launch");
+}
+
+nt_status configure_kv4(Ctx* c) {
+  for (int fmt : {NT_KV4_I4, NT_KV4_E2M1})
+    for (int hd : {64, 128})
+      for (int NT : {1, 2}) {
+        const AttnVariant k = attn_for(fmt, hd, NT);
+        nt_status s = cuda_check(
+            c, cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.smem + 1025 * 8)),
+            "4-bit attention shared-memory attribute");
+        if (s) return s;
+      }
+  return NT_OK;
+}
+
+}  // namespace nt

@@ -1416,29 +1416,6 @@ nt_status launch_kv8_read(Ctx* c, const nt_kv8& kv, int64_t pos, int64_t n, int 
   return cuda_check(c, launch_k(c, kern, grid, block, 0, st, a), "8-bit cache read launch");
 }
 
-// launch_k with a cluster shape (1, 1, 1: none)
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(const Ctx* c, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                           dim3 cluster, Args&&... args) {
-  if (cluster.x * cluster.y * cluster.z == 1) return launch_k(c, kernel, grid, block, smem, st, std::forward<Args>(args)...);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster.x;
-  attr[0].val.clusterDim.y = cluster.y;
-  attr[0].val.clusterDim.z = cluster.z;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = (c->pdl && !c->pdl_hold) ? 2 : 1;
-  c->pdl_hold = false;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
 nt_status launch_attn_kv8(Ctx* c, const nt_kv8& kv, const float* q, float* out, int n_qh, int64_t n_pos, int nq,
                           const int64_t* pos_dev, const int32_t* idx, int n_sel, char* scratch, size_t scratch_bytes,
                           cudaStream_t st) {

@@ -24,6 +24,8 @@ constexpr unsigned kWaitHintNs = 50000;  // each try_wait may sleep this long (c
 constexpr unsigned kErrWaitTimeout = 1u;
 constexpr unsigned kErrPosRange = 2u;  // a device-side position fell outside the KV cache: nothing written there
 constexpr unsigned kErrNonFinite = 4u;  // a NaN or an infinity was written to an 8-bit cache
+constexpr unsigned kErrNonFinite4 = 8u;  // the same of a 4-bit cache
+constexpr unsigned kErrPaged = 16u;  // a length, page or slot that a paged cache or its tables do not have
 
 // a GEMV launch configuration: warps per CTA and stage-size cap (what the
 // tuner chooses), and, for the record, the shape's arithmetic: column parts
@@ -84,13 +86,13 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 // scratch layout (bytes from ctx->scratch) ------------------------------------
 constexpr size_t kScratchErr = 0;            // unsigned err flag (also ctx->err_flag)
 constexpr size_t kScratchArgmax = 256;       // unsigned long long key + unsigned counter
-constexpr size_t kScratchAttn = 4096;        // attention: a reserved head (kAttnCounterBytes), then partials
+constexpr size_t kScratchAttn = 4096;        // attention: the 4-bit cache's counters (kAttnCounterBytes), then partials
 constexpr size_t kAttnCounterBytes = 2048;
 constexpr size_t kScratchSample = size_t(20) << 20;  // sampler state (one row of kSampRowBytes)
 constexpr size_t kSampRowBytes = 32768;             // sampler state per logits row
 constexpr int64_t kSampMaxN = 256 * 4000;           // longest row the sampler takes
 constexpr size_t kScratchTune = size_t(24) << 20;  // GEMV plan tuning outputs (8 MiB)
-constexpr size_t kScratchGemm = size_t(32) << 20;  // verify-GEMM partial sums and the 8-bit cache's partials and block scores, to the end of the scratch
+constexpr size_t kScratchGemm = size_t(32) << 20;  // verify-GEMM partial sums, the 8-bit cache's partials and block scores, the 4-bit cache's partials, to the end of the scratch
 
 // 8-bit KV cache: positions per scale
 constexpr int kKv8Block = NT_KV8_BLOCK;
@@ -213,6 +215,29 @@ cudaError_t launch_k(const Ctx* c, void (*kernel)(KArgs...), dim3 grid, dim3 blo
   // early part (weight prefetch) must not run before the awaited work
   cfg.numAttrs = (c && c->pdl && !c->pdl_hold) ? 1 : 0;
   if (c) c->pdl_hold = false;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// launch_k with a cluster shape (1, 1, 1: none)
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(const Ctx* c, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                           dim3 cluster, Args&&... args) {
+  if (cluster.x * cluster.y * cluster.z == 1) return launch_k(c, kernel, grid, block, smem, st, std::forward<Args>(args)...);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster.x;
+  attr[0].val.clusterDim.y = cluster.y;
+  attr[0].val.clusterDim.z = cluster.z;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = (c->pdl && !c->pdl_hold) ? 2 : 1;
+  c->pdl_hold = false;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 

@@ -18,8 +18,8 @@ nt_status launch_rope_append(Ctx* c, float* q, const float* k, const float* v, v
                              cudaStream_t st);
 int attn_splits(const Ctx* c, int n_kvh, int64_t kv_stride);
 int64_t attn_max_stride();
-// a reserved head of kAttnCounterBytes (unused since the combine became its own
-// launch) followed by the partials of nq queries
+// a reserved head of kAttnCounterBytes (in the context's scratch, the counters of the
+// 4-bit cache's attention) followed by the partials of nq queries
 size_t attn_scratch_bytes(int n_qh, int n_kvh, int S, int nq = 1);
 size_t attn_part_floats(int n_qh, int n_kvh, int S);
 // nq queries: query i sees n_pos + i positions (pos_dev set: *pos_dev + 1 + i);
@@ -73,5 +73,24 @@ nt_status launch_kv8_select(Ctx* c, const nt_kv8& kv, const float* q, int n_qh, 
                             const int64_t* pos_dev, int n_sel, int n_first, int n_last, int32_t* idx, char* scratch,
                             cudaStream_t st);
 nt_status configure_kv8(Ctx* c);
+
+// paged 4-bit KV cache (kv4.cu, pages.cu), rotary rows (rope.cu)
+size_t kv4_page_bytes(int head_dim);
+nt_status launch_kv4_pages(Ctx* c, int n_req, int32_t* table, int64_t max_pages, const int32_t* held, const int32_t* keep,
+                           const int32_t* n_new, int32_t* free_pages, int64_t n_pages, const int32_t* n_free,
+                           int32_t* held_out, int32_t* n_free_out, int32_t* q_start, int64_t* slots, int32_t* positions,
+                           int64_t n_tok, cudaStream_t st);
+nt_status launch_kv4_append(Ctx* c, const nt_kv4& kv, int fmt, const void* k, const void* v, int64_t n, int64_t tok_stride,
+                            int64_t head_stride, const int64_t* slots, cudaStream_t st);
+nt_status launch_kv4_read(Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v, int64_t n, int64_t tok_stride,
+                          int64_t head_stride, const int64_t* slots, cudaStream_t st);
+size_t kv4_attn_scratch(const Ctx* c, int head_dim);
+// counters: kAttnCounterBytes, zero at rest (the launch leaves them so)
+nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, int n_qh, int64_t n_tok, int n_req,
+                          const int32_t* q_start, const int32_t* held, const int32_t* table, int64_t max_pages, char* scratch,
+                          unsigned* counters, cudaStream_t st);
+nt_status configure_kv4(Ctx* c);
+nt_status launch_rope_rows(Ctx* c, const nt_rope_plan& plan, int fmt, const nt_rope_job* jobs, int n_jobs, int64_t n_tok,
+                           const int32_t* pos, int64_t pos0, cudaStream_t st);
 
 }  // namespace nt

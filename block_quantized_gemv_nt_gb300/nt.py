@@ -19,6 +19,12 @@ FMT_NAMES = {Q8_0: "Q8_0", Q4_0: "Q4_0", Q4_K: "Q4_K", Q5_K: "Q5_K", Q6_K: "Q6_K
 KV8_I8, KV8_E4M3 = 0, 1
 KV8_BLOCK = 64
 
+KV4_I4, KV4_E2M1 = 0, 1
+KV4_PAGE = 64
+
+ROPE_PAIRS, ROPE_HALVES = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDS, ROPE_RAMP = range(5)
+
 NT_OK, NT_ERR_INVALID_ARG, NT_ERR_UNSUPPORTED_FMT, NT_ERR_ALIGNMENT, NT_ERR_CUDA, NT_ERR_OOM, NT_ERR_TIMEOUT = range(7)
 STATUS_NAMES = ["NT_OK", "NT_ERR_INVALID_ARG", "NT_ERR_UNSUPPORTED_FMT", "NT_ERR_ALIGNMENT", "NT_ERR_CUDA",
                 "NT_ERR_OOM", "NT_ERR_TIMEOUT"]
@@ -89,6 +95,34 @@ _sig("nt_kv8_select", [_vp, _vp, ctypes.POINTER(nt_kv8), _ci, _i64, _ci, _vp, _c
 _sig("nt_attn_kv8_blocks", [_vp, _vp, ctypes.POINTER(nt_kv8), _vp, _ci, _i64, _ci, _vp, _vp, _ci, _vp])
 
 
+class nt_kv4(ctypes.Structure):
+    _fields_ = [("fmt", _ci), ("n_kvh", _ci), ("head_dim", _ci), ("n_pages", _i64), ("data", _vp)]
+
+
+class nt_rope_desc(ctypes.Structure):
+    _fields_ = [("layout", _ci), ("head_dim", _ci), ("rot_dim", _ci), ("scaling", _ci)] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "old_len", "low", "high", "mag")] + [
+        ("divisors", ctypes.POINTER(ctypes.c_double))]
+
+
+class nt_rope_plan(ctypes.Structure):
+    _fields_ = [("layout", _ci), ("head_dim", _ci), ("rot_dim", _ci), ("mag", _cf), ("turns", ctypes.c_uint64 * 128)]
+
+
+class nt_rope_job(ctypes.Structure):
+    _fields_ = [("x_dev", _vp), ("y_dev", _vp), ("n_heads", _ci), ("x_tok_stride", _i64), ("x_head_stride", _i64),
+                ("y_tok_stride", _i64), ("y_head_stride", _i64)]
+
+
+_sig("nt_kv4_layout", [_ci, ctypes.POINTER(_sz)])
+_sig("nt_kv4_pages", [_vp, _ci, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp])
+_sig("nt_kv4_append", [_vp, ctypes.POINTER(nt_kv4), _ci, _vp, _vp, _i64, _i64, _i64, _vp, _vp])
+_sig("nt_kv4_read", [_vp, ctypes.POINTER(nt_kv4), _ci, _vp, _vp, _i64, _i64, _i64, _vp, _vp])
+_sig("nt_attn_kv4", [_vp, _vp, ctypes.POINTER(nt_kv4), _vp, _ci, _i64, _ci, _vp, _vp, _vp, _i64, _vp])
+_sig("nt_rope_plan_init", [ctypes.POINTER(nt_rope_desc), ctypes.POINTER(nt_rope_plan)])
+_sig("nt_rope_rows", [_vp, ctypes.POINTER(nt_rope_plan), _ci, ctypes.POINTER(nt_rope_job), _ci, _i64, _vp, _i64, _vp])
+
+
 class nt_model_desc(ctypes.Structure):
     _fields_ = [(n, _ci) for n in ("n_layers", "d_model", "n_qh", "n_kvh", "head_dim", "ffn", "vocab")] + [
         ("eps", _cf), ("theta", _cf), ("kv_cap", _i64)] + [
@@ -151,7 +185,8 @@ EXPORTED = ["nt_ctx_create", "nt_ctx_destroy", "nt_ctx_sync", "nt_last_error", "
             "nt_host_register", "nt_host_unregister", "nt_stream_sync", "nt_debug_fail_copy", "nt_debug_host_delay",
             "nt_debug_stall_waits", "nt_ctx_gemv_plans", "nt_model_graph_count", "nt_model_prefill_chunk",
             "nt_kv8_append", "nt_kv8_read", "nt_attn_kv8", "nt_kv8_select", "nt_attn_kv8_blocks",
-            "nt_file_open", "nt_file_close", "nt_file_desc", "nt_file_header", "nt_file_entry", "nt_file_lock",
+            "nt_kv4_layout", "nt_kv4_pages", "nt_kv4_append", "nt_kv4_read", "nt_attn_kv4", "nt_rope_plan_init",
+            "nt_rope_rows", "nt_file_open", "nt_file_close", "nt_file_desc", "nt_file_header", "nt_file_entry", "nt_file_lock",
             "nt_file_unlock", "nt_debug_file_refuse_in_place"]
 
 
@@ -338,6 +373,62 @@ def nt_attn_kv8_blocks(ctx, q, cache: nt_kv8, out, n_qh, n_pos, n_query, idx, n_
     return ctx.check(_attn_kv8_blocks(ctx.handle, _ptr(q), cache, _ptr(out), n_qh, n_pos, n_query,
                                       pos_dev if pos_dev is None else _ptr(pos_dev), _ptr(idx), n_sel,
                                       _stream(stream, out)))
+
+
+_kv4_pages, _kv4_append, _kv4_read = _lib.nt_kv4_pages, _lib.nt_kv4_append, _lib.nt_kv4_read
+_attn_kv4, _rope_rows = _lib.nt_attn_kv4, _lib.nt_rope_rows
+
+
+def nt_kv4_layout(head_dim: int) -> int:
+    """Bytes of one page of one head of a 4-bit cache."""
+    n = _sz()
+    st = _lib.nt_kv4_layout(head_dim, ctypes.byref(n))
+    if st != NT_OK:
+        raise NtError(st, "nt_kv4_layout: head_dim must be 64 or 128")
+    return n.value
+
+
+def nt_kv4_pages(ctx, n_req, table, max_pages, held, keep, n_new, free, n_pages, n_free, held_out, n_free_out, q_start,
+                 slots, positions, n_tok, stream=None):
+    return ctx.check(_kv4_pages(ctx.handle, n_req, _ptr(table), max_pages, _ptr(held), _ptr(keep), _ptr(n_new), _ptr(free),
+                                n_pages, _ptr(n_free), _ptr(held_out), _ptr(n_free_out), _ptr(q_start), _ptr(slots),
+                                _ptr(positions), n_tok, _stream(stream, table)))
+
+
+def nt_kv4_append(ctx, cache: nt_kv4, src_fmt, k, v, n_tok, tok_stride, head_stride, slots, stream=None):
+    return ctx.check(_kv4_append(ctx.handle, cache, src_fmt, _ptr(k), _ptr(v), n_tok, tok_stride, head_stride,
+                                 _ptr(slots), _stream(stream, slots)))
+
+
+def nt_kv4_read(ctx, cache: nt_kv4, dst_fmt, k, v, n_tok, tok_stride, head_stride, slots, stream=None):
+    return ctx.check(_kv4_read(ctx.handle, cache, dst_fmt, _ptr(k), _ptr(v), n_tok, tok_stride, head_stride,
+                               _ptr(slots), _stream(stream, slots)))
+
+
+def nt_attn_kv4(ctx, q, cache: nt_kv4, out, n_qh, n_tok, n_req, q_start, held, table, max_pages, stream=None):
+    return ctx.check(_attn_kv4(ctx.handle, _ptr(q), cache, _ptr(out), n_qh, n_tok, n_req, _ptr(q_start), _ptr(held),
+                               _ptr(table), max_pages, _stream(stream, out)))
+
+
+def nt_rope_plan_init(head_dim, rot_dim=None, layout=ROPE_PAIRS, theta=10000.0, scaling=ROPE_PLAIN, factor=1.0,
+                      old_len=0.0, low=0.0, high=0.0, mag=0.0, divisors=None) -> nt_rope_plan:
+    """How rows turn: the plan that nt_rope_rows takes (host arithmetic only)."""
+    rot_dim = head_dim if rot_dim is None else rot_dim
+    d = nt_rope_desc(layout, head_dim, rot_dim, scaling, theta, factor, old_len, low, high, mag, None)
+    if divisors is not None:
+        if len(divisors) != rot_dim // 2:
+            raise NtError(NT_ERR_INVALID_ARG, "nt_rope_plan_init: one divisor for each pair")
+        d.divisors = (ctypes.c_double * max(1, len(divisors)))(*[float(x) for x in divisors])
+    plan = nt_rope_plan()
+    st = _lib.nt_rope_plan_init(ctypes.byref(d), ctypes.byref(plan))
+    if st != NT_OK:
+        raise NtError(st, "nt_rope_plan_init: a layout, scaling, size or number that the header does not allow")
+    return plan
+
+
+def nt_rope_rows(ctx, plan: nt_rope_plan, fmt, jobs, n_jobs, n_tok, positions, pos0, stream=None):
+    """jobs: a ctypes array of nt_rope_job."""
+    return ctx.check(_rope_rows(ctx.handle, plan, fmt, jobs, n_jobs, n_tok, _ptr(positions), pos0, _stream(stream)))
 
 
 def nt_host_register(ctx, host_ptr: int, nbytes: int, read_only: bool = True):

@@ -27,7 +27,8 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream).  Calls only enqueue work.  The device error flag (a bounded
  *    wait inside a kernel that ran out, a device-held position past the KV
- *    cache, a NaN or an infinity written to an 8-bit KV cache) is read and
+ *    cache, a NaN or an infinity written to an 8-bit or a 4-bit KV cache, a
+ *    length, page or slot that a paged cache does not have) is read and
  *    cleared by nt_ctx_sync() and nt_stream_sync(); a CUDA fault also fails
  *    the next launch on the context.
  *  - Pointers named *_dev are device (HBM) pointers; pointers named *_host
@@ -38,9 +39,9 @@
  *    a time (its tuning state, scratch and per-call settings are shared);
  *    separate contexts are independent.  Work from calls on one context that
  *    share scratch (the standalone kernels, the sampler, the attention and the
- *    selection over an 8-bit cache) must not overlap on the GPU, nor may
- *    replays of graphs that captured it: keep it on one stream or order the
- *    streams.
+ *    selection over an 8-bit cache, the attention over a 4-bit one) must not
+ *    overlap on the GPU, nor may replays of graphs that captured it: keep it on
+ *    one stream or order the streams.
  *  - Block-quantized matrices are row-major: row r is cols/block_elems
  *    consecutive blocks.  cols must be a multiple of the format's block size
  *    (32 for Q8_0/Q4_0/F16/F32, 256 for Q4_K/Q5_K/Q6_K).  Block bytes: Q8_0
@@ -95,7 +96,9 @@ nt_status nt_ctx_destroy(nt_ctx* ctx);
  * held on the device (a decode step continued with token < 0, or the pos_dev
  * of an 8-bit cache call) ran past the KV cache — the kernels then wrote
  * nothing outside the caches — or a NaN or an infinity was written to an 8-bit
- * KV cache.  nt_last_error names every cause since the flag was last read. */
+ * or a 4-bit KV cache, or a paged call met a length, page or slot that its cache
+ * or tables do not have.  nt_last_error names every cause since the flag was
+ * last read. */
 nt_status nt_ctx_sync(nt_ctx* ctx);
 /* [road] Wait at most timeout_us for the work enqueued on `stream` to finish (a
  * host-side poll with a deadline), then report like nt_ctx_sync:
@@ -116,7 +119,7 @@ nt_status nt_debug_fail_copy(nt_ctx* ctx, int nth);
  * GPU is made to fault or hang): the next n eager launches in this process
  * of the kernels that wait on bulk copies — the quant GEMV (nt_gemv_q,
  * nt_gemv_q_multi, nt_gemv_swiglu), nt_attn_decode, nt_attn_decode_static,
- * nt_attn_kv8 and nt_attn_kv8_blocks — issue no copies, so their waits run out
+ * nt_attn_kv8, nt_attn_kv8_blocks and nt_attn_kv4 — issue no copies, so their waits run out
  * after a few tries and take the timeout path: the context flag that
  * nt_ctx_sync reports as NT_ERR_TIMEOUT, or NaN output from
  * nt_attn_decode_static.
@@ -384,6 +387,160 @@ nt_status nt_kv8_select(nt_ctx* ctx, const float* q_dev, const nt_kv8* cache, in
 nt_status nt_attn_kv8_blocks(nt_ctx* ctx, const float* q_dev, const nt_kv8* cache, float* out_dev, int n_qh,
                              int64_t n_pos, int n_query, const int64_t* pos_dev, const int32_t* idx_dev, int n_sel,
                              void* stream);
+
+/* ---- several requests over a paged 4-bit KV cache ------------------------------ */
+
+/* One layer's K and V in 4 bits, in pages of 64 positions: a second step below
+ * the F16 KV cache [road] after the 8-bit one, and the place where several
+ * requests keep theirs.  data is n_pages * n_kvh blocks of nt_kv4_layout's bytes,
+ * 16-byte aligned: position p of KV head h of page g lies in block g * n_kvh + h.
+ * Slot s of the cache is position s % 64 of page s / 64.
+ *
+ * A row's channels share a scale by 32: d, an f16 number of at most 8
+ * significant bits and at most 2720, so that every value, code times d, is exact
+ * in f16.
+ *   NT_KV4_I4    codes -8 .. 7; d the nearest to x / -8, x the value of the largest
+ *                magnitude (the positive one of two that tie): x itself is -8 d
+ *   NT_KV4_E2M1  codes 0 0.5 1 1.5 2 3 4 6 and their negatives; d the nearest to
+ *                max |x| / 6
+ * A value goes to the nearest code, a tie to the even one (of I4 the even number,
+ * of E2M1 the code without a last bit), one beyond the codes to the last.  NaN is
+ * stored as 0, an infinity as the largest code; the scale follows the finite
+ * values.  Values above 2720 times the largest code are stored as that.
+ * A block: the K half, then the V half, each of 64 rows of head_dim / 2 bytes and
+ * 64 * head_dim / 32 scales, in the order in which the attention reads them; the
+ * order is the library's own, nt_kv4_append writes it and nt_kv4_read reads it. */
+#define NT_KV4_I4 0
+#define NT_KV4_E2M1 1
+#define NT_KV4_PAGE 64
+typedef struct {
+  int fmt;         /* NT_KV4_I4 or NT_KV4_E2M1 */
+  int n_kvh;       /* 1 .. 64 */
+  int head_dim;    /* 64 or 128 */
+  int64_t n_pages; /* 1 .. 2^31 - 1 */
+  void* data;
+} nt_kv4;
+
+/* [road] Bytes of one page of one head (K and V): 4608 for 64 channels, 9216 for 128. */
+nt_status nt_kv4_layout(int head_dim, size_t* page_bytes);
+
+/* Block tables and slots of the next step of n_req requests, from their lengths
+ * [road].  Request r holds held[r] positions, in the pages table[r * max_pages +
+ * j], j < ceil(held[r] / 64).  It goes on with its first keep[r] of them (keep
+ * NULL: all; fewer after rejected drafts, 0 when it ends) and n_new[r] >= 0 new
+ * tokens.  Pages behind the new length go back to the stack of free pages
+ * (free_dev[0 .. *n_free), room for n_pages), in the order of the requests and of
+ * their pages; then each request that grows takes its pages from the stack's top, in
+ * the order of the requests.  Entries of the table behind a request's pages keep
+ * what they held.
+ *   held_out[r], *n_free_out   the new lengths and stack size (may be held, n_free)
+ *   q_start[0 .. n_req]        the first row of each request: sums of n_new
+ *   slots[i], positions[i]     row i's slot in the cache and position in its request,
+ *                              i < n_tok; rows behind the last request get -1 and 0
+ * slots and positions have room for n_tok rows, the most the step takes; with a
+ * larger sum of n_new the rows behind n_tok are not written and the device flag is
+ * set.  A request is refused, with slots of -1 and its length as it was, and the
+ * device flag set, when its new length does not fit max_pages, keep[r] is not in
+ * 0 .. held[r], or n_new[r] is negative (it then has no rows), and when it and the
+ * growing requests before it need more pages than the stack has.  n_req 1..1024;
+ * integers 4-byte, slots 8-byte aligned.  One launch without scratch. */
+nt_status nt_kv4_pages(nt_ctx* ctx, int n_req, int32_t* table_dev, int64_t max_pages, const int32_t* held_dev,
+                       const int32_t* keep_dev, const int32_t* n_new_dev, int32_t* free_dev, int64_t n_pages,
+                       const int32_t* n_free_dev, int32_t* held_out_dev, int32_t* n_free_out_dev, int32_t* q_start_dev,
+                       int64_t* slots_dev, int32_t* positions_dev, int64_t n_tok, void* stream);
+
+/* Rows of K and V [road], NT_F32 or NT_F16, into the cache's slots: row i of head h
+ * at k + i * tok_stride + h * head_stride (elements; multiples of 16 bytes),
+ * head_dim values.  A negative slot's row is left out; one behind the cache sets the
+ * device flag and is left out.  Two rows of one call with the same slot leave one
+ * of their values, group by group.  slots 8-byte aligned. */
+nt_status nt_kv4_append(nt_ctx* ctx, const nt_kv4* cache, int src_fmt, const void* k_dev, const void* v_dev,
+                        int64_t n_tok, int64_t tok_stride, int64_t head_stride, const int64_t* slots_dev, void* stream);
+
+/* The values [road] of the slots' rows, exact in NT_F32 and in NT_F16, to rows laid
+ * out as nt_kv4_append reads them (k or v may be NULL; rows must not overlap).  Rows
+ * of negative slots, and of slots behind the cache (device flag), keep what they held. */
+nt_status nt_kv4_read(nt_ctx* ctx, const nt_kv4* cache, int dst_fmt, void* k_dev, void* v_dev, int64_t n_tok,
+                      int64_t tok_stride, int64_t head_stride, const int64_t* slots_dev, void* stream);
+
+/* Attention with grouped KV heads [feat] GQA of each request's rows over its own
+ * pages.  q, out fp32 [n_tok][n_qh][head_dim], 16-byte aligned (out may be q).
+ * Request r has the rows q_start[r] .. q_start[r + 1] - 1 (none: a slot of the batch
+ * that nobody uses) and held[r] positions, the rows' own included; its i-th last row
+ * sees all but the last i of them:
+ *   out = softmax_j(q . K[j] / sqrt(head_dim)) . V[j],  j < held[r] - i,
+ * zeros where that leaves none.  Any number of rows a request; each 4, 8 or 16 of
+ * (row, query head) pairs of a KV head read its pages once.  Rows of no request are
+ * left as they were.  The device flag is set, and what is wrong taken as absent, where
+ * q_start decreases or leaves 0 .. n_tok (that request has no rows), held[r] is not
+ * in 0 .. 64 * max_pages (held to it), or a page is not in 0 .. n_pages - 1 (its
+ * positions are not seen).  n_qh 1..16 times n_kvh, n_req 1..1024.  One launch;
+ * uses the context scratch. */
+nt_status nt_attn_kv4(nt_ctx* ctx, const float* q_dev, const nt_kv4* cache, float* out_dev, int n_qh, int64_t n_tok,
+                      int n_req, const int32_t* q_start_dev, const int32_t* held_dev, const int32_t* table_dev,
+                      int64_t max_pages, void* stream);
+
+/* ---- rotary positions of rows --------------------------------------------------- */
+
+/* How rows turn.  Pair i < rot_dim / 2 of a row at position p turns by p * w_i:
+ *   (a, b) -> m (a cos - b sin, a sin + b cos),
+ * pairs (2 i, 2 i + 1) in NT_ROPE_PAIRS (what nt_rope does), (i, i + rot_dim / 2)
+ * in NT_ROPE_HALVES; channels from rot_dim on stay.  With u_i = theta^(-2 i /
+ * rot_dim), L = old_len, the length a model was trained for, and s = factor:
+ *   NT_ROPE_PLAIN   w = u
+ *   NT_ROPE_LINEAR  w = u / s
+ *   NT_ROPE_BASE    w of the base theta * s^(rot_dim / (rot_dim - 2))
+ *   NT_ROPE_BANDS   w = u k + u / s (1 - k), k = clamp((L u / 2 pi - low) / (high - low), 0, 1)
+ *   NT_ROPE_RAMP    w = u (1 - k) + u / s k, k = clamp((i - a) / (b - a), 0, 1), from the pair
+ *                   a that turns high times over L (rounded down, at least 0) to the pair b
+ *                   that turns low times (rounded up, at most the last; b = a + 0.001 where
+ *                   they meet); pair(t) = rot_dim ln(L / (2 pi t)) / (2 ln theta)
+ * low and high of 0: 1 and 4 in BANDS, 1 and 32 in RAMP.  mag of 0: 0.1 ln s + 1 in
+ * RAMP (s > 1), else 1.  divisors: NULL, or rot_dim / 2 numbers that each w_i is
+ * divided by (frequency factors that come with a model). */
+#define NT_ROPE_PAIRS 0
+#define NT_ROPE_HALVES 1
+#define NT_ROPE_PLAIN 0
+#define NT_ROPE_LINEAR 1
+#define NT_ROPE_BASE 2
+#define NT_ROPE_BANDS 3
+#define NT_ROPE_RAMP 4
+typedef struct {
+  int layout;   /* NT_ROPE_PAIRS or NT_ROPE_HALVES */
+  int head_dim; /* 8 .. 256, a multiple of 8 */
+  int rot_dim;  /* 8 .. head_dim, a multiple of 8 */
+  int scaling;
+  double theta, factor, old_len, low, high, mag;
+  const double* divisors; /* host, nullable */
+} nt_rope_desc;
+/* A plan holds w_i / 2 pi modulo 1 in 64-bit fixed point, so that p * w_i is exact
+ * modulo a turn for any 32-bit position: made once, passed to every call. */
+typedef struct {
+  int layout, head_dim, rot_dim;
+  float mag;
+  uint64_t turns[128];
+} nt_rope_plan;
+
+/* RoPE [feat]: the plan of a description (host arithmetic only). */
+nt_status nt_rope_plan_init(const nt_rope_desc* desc, nt_rope_plan* plan);
+
+/* Rows of one tensor (q, or k): row i of head h at x + i * x_tok_stride + h *
+ * x_head_stride, to y alike (elements; y may be x with the same strides: in place). */
+typedef struct {
+  const void* x_dev;
+  void* y_dev;
+  int n_heads; /* 1 .. 1024 */
+  int64_t x_tok_stride, x_head_stride, y_tok_stride, y_head_stride;
+} nt_rope_job;
+
+/* RoPE [feat] of the rows of up to 3 tensors, NT_F32 or NT_F16 (computed in fp32):
+ * row i stands at positions[i], or at pos0 + i when positions_dev is NULL.
+ * Positions may be negative: the turn of -p undoes that of p.  Pointers and
+ * strides multiples of 16 bytes; an output overlaps no other rows than its own input
+ * in place.  One launch without scratch. */
+nt_status nt_rope_rows(nt_ctx* ctx, const nt_rope_plan* plan, int fmt, const nt_rope_job* jobs, int n_jobs, int64_t n_tok,
+                       const int32_t* positions_dev, int64_t pos0, void* stream);
+
 
 /* ---- whole decode step ------------------------------------------------------ */
 
