@@ -317,16 +317,18 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs
 //  - V: the lane reads word w of channels g HD / 8 .. of rows 16 m + 2 c, + 1, + 8, + 9;
 //    channel n of the word is MMA row g or g + 8 of m-tile n % 4 (I4) or n / 2 (E2M1).
 //
-// Work: the steps (a page of one KV head for one chunk of 4 NT query rows) of all
-// requests in one line, the same number to each warp, whatever the requests' lengths.
-// A warp walks its steps with an online softmax; where it begins or ends inside an item
-// (request, head, chunk) it leaves a partial (m, l, o).  The CTA joins its warps'
-// partials of one item, and the last CTA to arrive at an item that several share joins
-// theirs, in the order of the line: nothing depends on who arrives when.
+// Work: the steps (a page, or a half or a quarter of one, of one KV head for one chunk of
+// 4 NT query rows) of all requests in one line, the same number to each warp, whatever the
+// requests' lengths.  A warp walks its steps with an online softmax; where it begins or
+// ends inside an item (request, head, chunk) it leaves a partial (m, l, o).  The CTA joins
+// its warps' partials of one item, and the last CTA to arrive at an item that several
+// share joins theirs, in the order of the line: nothing depends on who arrives when.
 constexpr int kWarps = 8;
 constexpr int kMaxCtas = 512;                 // one counter each
 constexpr float kPTop = 8.f, kSlack = 6.f;    // probabilities are up to 2^(kPTop + kSlack), in f16's range
 constexpr float kLowest = -3.402823466e38f;
+constexpr int64_t kMaxSteps = int64_t(1) << 28;
+constexpr int kJoin = 16;                     // partials of an item that a join has in flight together
 
 struct AttnKv4Args {
   const float* q;
@@ -349,6 +351,13 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same from zero
+__device__ __forceinline__ void mma16816_zero(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -364,10 +373,21 @@ __device__ __forceinline__ uint32_t hi_lo(float x) {
   const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
   return as_u32(__floats2half2_rn(hi, x - hi));
 }
+// an arrival that orders what this CTA wrote before it and reads what earlier ones wrote
+__device__ __forceinline__ unsigned arrive_counter(unsigned* at) {
+  unsigned old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(at) : "memory");
+  return old;
+}
+
+// a request: its first row, rows and positions, held to what the arguments allow, and
+// the steps of it and of those before it
+struct Req {
+  int row0, rows, len, steps;
+};
 
 // shared memory: each warp's K and V halves; its partial of the item that it found
-// begun; the sums of steps over the requests.  At the end the warps' last partials lie in
-// their own K and V halves.
+// begun; the requests.  At the end the warps' last partials lie in their own K and V halves.
 template <int HD, int NT>
 struct AttnKv4Smem {
   static constexpr int ROWS = 4 * NT;
@@ -375,34 +395,18 @@ struct AttnKv4Smem {
   static constexpr size_t slot = size_t(ROWS) * line * 4 + ROWS * 8;   // then (m, l) of each row
   static constexpr size_t ring = 0;
   static constexpr size_t first = size_t(kWarps) * Kv4Block<HD>::bytes;
-  static constexpr size_t sums = first + kWarps * slot;
-  static size_t bytes(int n_req) { return sums + size_t(n_req + 1) * 8; }
+  static constexpr size_t reqs = first + kWarps * slot;
   static_assert(slot <= size_t(Kv4Block<HD>::bytes), "a partial fits a warp's halves");
   static_assert(kMaxCtas * ROWS * 4 <= first, "the weights of a join fit the ring");
+  static_assert(reqs % 16 == 0, "requests are read as 16 bytes");
 };
 
-// a request: its first row, rows and positions, held to what the arguments allow
-struct Req {
-  int row0, rows, len;
-};
-__device__ __forceinline__ Req request(const AttnKv4Args& a, int r, bool tell) {
-  const int b = a.q_start[r], e = a.q_start[r + 1], n = a.held[r];
-  Req x{b, e - b, n};
-  const int64_t cap = a.max_pages * kPg;
-  const bool rows_ok = b >= 0 && e >= b && e <= a.n_tok, len_ok = n >= 0 && n <= cap;
-  if (!rows_ok) x.rows = 0;
-  if (!len_ok) x.len = n < 0 ? 0 : int(cap);
-  if (tell && !(rows_ok && len_ok)) flag_error(a.err, kErrPaged);
-  return x;
-}
-
-// the item and page of a step
-struct Step {
-  int r;           // request
-  Req q;
-  int pages, chunks;
-  int64_t item0;   // the item's first step
-  int h, z, page;  // KV head, chunk of rows, page
+// an item, and the step of it that comes next
+struct Item {
+  int r, h;          // request, KV head
+  int row0, at;      // the chunk's first row: of q the request's, of the request's (query, head) rows
+  int rows, q_rows;  // rows of the chunk, queries of the request
+  int len, steps, j;
 };
 
 template <int FMT, int HD, int NT, int CTAS>
@@ -415,10 +419,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   constexpr int CW = HD / 8;   // output channels of a lane and row
   extern __shared__ __align__(16) uint8_t sm4[];
   __shared__ __align__(8) uint64_t bars[kWarps][2];
-  __shared__ int64_t seg_item[kWarps][2];   // item (its first step) of a warp's partials, -1: none
+  __shared__ int seg_item[2 * kWarps];   // item (its first step) of a warp's partials, -1: none
   __shared__ int64_t wsum[kWarps];
   __shared__ unsigned arrived;
-  int64_t* sums = reinterpret_cast<int64_t*>(sm4 + L::sums);
+  Req* const reqs = reinterpret_cast<Req*>(sm4 + L::reqs);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const uint32_t bar = smem_u32(&bars[warp][0]);
   const uint64_t pol = policy_evict_first();
@@ -426,94 +430,130 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     mbar_init(bar, 1);
     mbar_init(bar + 8, 1);
     fence_barrier_init();
-    seg_item[warp][0] = seg_item[warp][1] = -1;
+    seg_item[2 * warp] = seg_item[2 * warp + 1] = -1;
   }
   pdl_wait();
   pdl_trigger();
 
-  // ---- steps of the requests, summed
-  const auto steps_of = [&](const Req& q, int& pages, int& chunks) {
-    pages = max(1, (q.len + kPg - 1) / kPg);
-    chunks = int((int64_t(q.rows) * a.G + ROWS - 1) / ROWS);
-    return int64_t(chunks) * a.n_kvh * pages;
+  // ---- the requests and the sums of their pages' steps
+  int64_t total64 = 0;
+  const auto read_req = [&](int r, int64_t& v) {
+    Req x{0, 0, 0, 0};
+    v = 0;
+    if (r < a.n_req) {
+      const int b = a.q_start[r], e = a.q_start[r + 1], n = a.held[r];
+      const int64_t cap = a.max_pages * kPg;
+      const bool rows_ok = b >= 0 && e >= b && e <= a.n_tok, len_ok = n >= 0 && n <= cap;
+      x.row0 = b;
+      x.rows = rows_ok ? e - b : 0;
+      x.len = len_ok ? n : n < 0 ? 0 : int(cap);
+      if (!(rows_ok && len_ok) && blockIdx.x == 0) flag_error(a.err, kErrPaged);
+      v = ((int64_t(x.rows) * a.G + ROWS - 1) / ROWS) * a.n_kvh * max(1, (x.len + kPg - 1) / kPg);
+    }
+    return x;
   };
-  {
-    int64_t run = 0;
-    for (int r0 = 0; r0 < a.n_req; r0 += kWarps * 32) {
-      const int r = r0 + tid;
-      int64_t v = 0;
-      if (r < a.n_req) {
-        int pages, chunks;
-        v = steps_of(request(a, r, blockIdx.x == 0), pages, chunks);
-      }
+  const auto scan = [&](int64_t v) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    return v;
+  };
+  if (a.n_req <= 32) {  // every warp by itself: all write the same
+    int64_t v;
+    Req x = read_req(lane, v);
+    v = scan(v);
+    total64 = __shfl_sync(0xffffffffu, v, 31);
+    x.steps = int(min(v, kMaxSteps));
+    if (lane < a.n_req) reqs[lane] = x;
+    __syncwarp();
+  } else {
+    for (int r0 = 0; r0 < a.n_req; r0 += kWarps * 32) {
+      int64_t v;
+      Req x = read_req(r0 + tid, v);
+      v = scan(v);
       if (lane == 31) wsum[warp] = v;
       __syncthreads();
-      int64_t before = run;
+      v += total64;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += wsum[w];
-        run += wsum[w];
+        if (w < warp) v += wsum[w];
+        total64 += wsum[w];
       }
-      if (r < a.n_req) sums[r + 1] = before + v;
-      if (r == 0) sums[0] = 0;
+      x.steps = int(min(v, kMaxSteps));
+      if (r0 + tid < a.n_req) reqs[r0 + tid] = x;
       __syncthreads();
     }
   }
-  const int64_t total = sums[a.n_req];
-  const int64_t per = max(int64_t(1), (total + int64_t(gridDim.x) * kWarps - 1) / (int64_t(gridDim.x) * kWarps));
-  const int64_t cta0 = min(total, int64_t(blockIdx.x) * kWarps * per), cta1 = min(total, cta0 + kWarps * per);
+  if (total64 > kMaxSteps) {
+    if (blockIdx.x == 0 && tid == 0) flag_error(a.err, kErrPaged);
+    return;
+  }
+  // steps of a quarter or half of a page where whole ones would leave warps without any
+  const int warps = gridDim.x * kWarps;
+  const int sh = 4 * total64 <= warps ? 2 : 2 * total64 <= warps ? 1 : 0;
+  const int total = int(total64) << sh;
+  const int per = max(1, (total + warps - 1) / warps);
+  const int cta0 = min(int64_t(total), int64_t(blockIdx.x) * (kWarps * per)), cta1 = min(total, cta0 + kWarps * per);
   if (cta0 >= cta1) return;
-  const int64_t s0 = min(total, cta0 + warp * per), s1 = min(total, s0 + per);
+  const int s0 = min(total, cta0 + warp * per), s1 = min(total, s0 + per);
 
-  const auto locate = [&](int64_t s) {
-    int lo = 0, hi = a.n_req;  // sums[lo] <= s < sums[hi]
+  const auto query_of = [&](int row) { return int((uint64_t(unsigned(row)) * a.inv_g) >> 32); };
+  const auto locate = [&](int s) {
+    int lo = -1, hi = a.n_req - 1;  // the first request whose sum is above s
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (sums[mid] <= s) lo = mid; else hi = mid;
+      if ((reqs[mid].steps << sh) > s) hi = mid; else lo = mid;
     }
-    Step x;
-    x.r = lo;
-    x.q = request(a, lo, false);
-    steps_of(x.q, x.pages, x.chunks);
-    const int64_t off = s - sums[lo], it = off / x.pages;
-    x.page = int(off - it * x.pages);
-    x.item0 = s - x.page;
-    x.h = int(it / x.chunks);
-    x.z = int(it - int64_t(x.h) * x.chunks);
+    const Req q = reqs[hi];
+    const int before = hi ? reqs[hi - 1].steps << sh : 0;
+    Item x;
+    x.r = hi;
+    x.len = q.len;
+    x.row0 = q.row0;
+    x.q_rows = q.rows;
+    x.steps = max(1, (q.len + kPg - 1) / kPg) << sh;
+    const unsigned chunks = unsigned(q.rows * a.G + ROWS - 1) / ROWS, off = unsigned(s - before);
+    const unsigned it = off / unsigned(x.steps), h = it / chunks;
+    x.j = int(off - it * x.steps);
+    x.h = int(h);
+    x.at = int(it - h * chunks) * ROWS;
+    x.rows = min(ROWS, q.rows * a.G - x.at);
     return x;
   };
-  const auto query_of = [&](int row) { return int((uint64_t(unsigned(row)) * a.inv_g) >> 32); };
-  // rows of a chunk, the query of its last row, and the positions that one sees
-  const auto chunk_rows = [&](const Step& x) { return int(min(int64_t(ROWS), int64_t(x.q.rows) * a.G - int64_t(x.z) * ROWS)); };
-  const auto seen = [&](const Step& x, int row) {  // by row `row` of the chunk
-    return x.q.len - (x.q.rows - 1 - query_of(x.z * ROWS + row));
-  };
-  // the offset of (row of the chunk)'s vector in q and out
-  const auto vec_of = [&](const Step& x, int row) {
-    const int at = x.z * ROWS + row, qi = query_of(at);
-    return (int64_t(x.q.row0 + qi) * a.n_qh + x.h * a.G + (at - qi * a.G)) * HD;
-  };
-  // where a step's block lies; null: none of its positions is seen
-  const auto block_of = [&](const Step& x) -> const uint8_t* {
-    if (x.page * kPg >= seen(x, chunk_rows(x) - 1)) return nullptr;
-    const int p = a.table[x.r * a.max_pages + x.page];
-    if (p < 0 || p >= a.n_pages) {
-      if (lane == 0) flag_error(a.err, kErrPaged);
-      return nullptr;
-    }
-    return a.data + (int64_t(p) * a.n_kvh + x.h) * B::bytes;
+  // positions that row `row` of the chunk sees
+  const auto seen = [&](const Item& x, int row) { return x.len - (x.q_rows - 1 - query_of(x.at + row)); };
+  // the offset of its vector in q and out
+  const auto vec_of = [&](const Item& x, int row) {
+    const int qi = query_of(x.at + row);
+    return (int64_t(x.row0 + qi) * a.n_qh + x.h * a.G + (x.at + row - qi * a.G)) * HD;
   };
   uint8_t* const sk = sm4 + L::ring + size_t(warp) * B::bytes;
   const uint8_t* const sv = sk + B::half;
-  const auto copy = [&](const uint8_t* from, int which) {
-    if (!from || lane != 0) return;
-    mbar_arrive_expect_tx(bar + 8 * which, B::half);
-    if (!a.stall) bulk_g2s(smem_u32(which ? sv : sk), from + which * B::half, B::half, bar + 8 * which, pol);
+  // a step's K (0) or V (1) from block `b`
+  const auto copy = [&](const uint8_t* b, int which, int j) {
+    if (!b || lane != 0) return;
+    const uint32_t to = smem_u32(which ? sv : sk), on = bar + 8 * which;
+    const uint8_t* from = b + which * B::half;
+    if (sh == 0) {
+      mbar_arrive_expect_tx(on, B::half);
+      if (!a.stall) bulk_g2s(to, from, B::half, on, pol);
+      return;
+    }
+    const uint32_t rows = kPg >> sh, row0 = (j & ((1 << sh) - 1)) * rows, sc = B::half - B::scales;
+    mbar_arrive_expect_tx(on, rows * B::row + sc);
+    if (a.stall) return;
+    if (which == 0) {
+      bulk_g2s(to + row0 * B::row, from + row0 * B::row, rows * B::row, on, pol);
+    } else {
+#pragma unroll
+      for (int w = 0; w < B::WPL; ++w) {
+        const uint32_t o = w * (kPg * 32) + row0 * 32;
+        bulk_g2s(to + o, from + o, rows * 32, on, pol);
+      }
+    }
+    bulk_g2s(to + B::scales, from + B::scales, sc, on, pol);
   };
   uint32_t phase = 0;
   bool dead = false;  // a wait ran out: the rest is taken as not seen
@@ -527,364 +567,427 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     dead = true;
     return false;
   };
+  // 32 entries of an item's table, one a lane, from page `p0` on: blocks, or -1 where a
+  // page is not seen or not one of the cache
+  const auto entries = [&](const Item& x, int p0, int pages_seen) {
+    const int p = p0 + lane;
+    if (p >= pages_seen) return -1;
+    const int e = a.table[x.r * a.max_pages + p];
+    if (e >= 0 && e < a.n_pages) return e;
+    flag_error(a.err, kErrPaged);
+    return -1;
+  };
+  const auto block_of = [&](const Item& x, int ent, int j) -> const uint8_t* {
+    const int e = __shfl_sync(0xffffffffu, ent, (j >> sh) & 31);
+    return e < 0 ? nullptr : a.data + (int64_t(e) * a.n_kvh + x.h) * B::bytes;
+  };
 
-  Step x{};
+  Item x{}, nx{};
   const uint8_t* blk = nullptr;
+  int ent = -1;
   if (s0 < s1) {
     x = locate(s0);
-    blk = block_of(x);
-    copy(blk, 0);
-    copy(blk, 1);
+    ent = entries(x, (x.j >> sh) & ~31, (seen(x, x.rows - 1) + kPg - 1) / kPg);
+    blk = block_of(x, ent, x.j);
+    copy(blk, 0, x.j);
+    copy(blk, 1, x.j);
   }
-  uint32_t qf[NT][KS][2];
-  float rscale[NT], m[NT], l[NT], o[NT][CW];
-  int limit[NT];
-  int rows = 0, tokens = 0, fewest = 0;
-  bool fresh = true;
-  for (int64_t s = s0; s < s1; ++s) {
-    if (fresh) {  // a new item: its rows of q, scaled by a power of two to amax in [2^13, 2^14) and split
-      fresh = false;
-      rows = chunk_rows(x);
-      tokens = seen(x, rows - 1);
-      fewest = seen(x, 0);
+  for (int s = s0; s < s1;) {
+    // ---- an item: its rows of q, scaled by a power of two to amax in [2^13, 2^14) and split
+    const int tokens = seen(x, x.rows - 1), fewest = seen(x, 0), pages_seen = (tokens + kPg - 1) / kPg;
+    const int first_j = x.j, last_j = min(x.steps, x.j + (s1 - s));
+    uint32_t qf[NT][KS][2];
+    float rscale[NT], m[NT], l[NT], o[NT][CW];
+    int limit[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int row = 4 * j + (g >> 1);
-        float v[HD / 4];
+    for (int t = 0; t < NT; ++t) {
+      const int row = 4 * t + (g >> 1);
+      float v[HD / 4];
 #pragma unroll
-        for (int i = 0; i < HD / 4; ++i) v[i] = 0.f;
-        if (row < rows) {
-          const float* q = a.q + vec_of(x, row) + c * (HD / 4);
+      for (int i = 0; i < HD / 4; ++i) v[i] = 0.f;
+      if (row < x.rows) {
+        const float* q = a.q + vec_of(x, row) + c * (HD / 4);
 #pragma unroll
-          for (int i = 0; i < HD / 4; i += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(q + i);
-            v[i] = y.x, v[i + 1] = y.y, v[i + 2] = y.z, v[i + 3] = y.w;
-          }
+        for (int i = 0; i < HD / 4; i += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(q + i);
+          v[i] = y.x, v[i + 1] = y.y, v[i + 2] = y.z, v[i + 3] = y.w;
         }
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < HD / 4; ++i) top = fmaxf(top, fabsf(v[i]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = min(100, 140 - int(__float_as_uint(top) >> 23));
-        const float sc = __uint_as_float(uint32_t(e + 127) << 23);
-#pragma unroll
-        for (int w = 0; w < WK; ++w)
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {  // pair p of word w
-            const int i0 = 8 * w + (FMT == NT_KV4_I4 ? p : 2 * p), i1 = 8 * w + (FMT == NT_KV4_I4 ? p + 4 : 2 * p + 1);
-            const __half2 hi = __floats2half2_rn(v[i0] * sc, v[i1] * sc);
-            const float2 f = __half22float2(hi);
-            const __half2 lo = __floats2half2_rn(v[i0] * sc - f.x, v[i1] * sc - f.y);
-            qf[j][2 * w + p / 2][p & 1] = as_u32(g & 1 ? lo : hi);
-          }
-        // of row c of the tile: lanes 8 c .. hold its q
-        rscale[j] = __uint_as_float(uint32_t(127 - __shfl_sync(0xffffffffu, e, 8 * c)) << 23) *
-                    (1.44269504088896f * rsqrtf(float(HD)));
-        limit[j] = 4 * j + c < rows ? seen(x, 4 * j + c) : 0;
-        m[j] = -INFINITY;
-        l[j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < CW; ++i) o[j][i] = 0.f;
       }
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < HD / 4; ++i) top = fmaxf(top, fabsf(v[i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(100, 140 - int(__float_as_uint(top) >> 23));
+      const float sc = __uint_as_float(uint32_t(e + 127) << 23);
+#pragma unroll
+      for (int w = 0; w < WK; ++w)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {  // pair p of word w
+          const int i0 = 8 * w + (FMT == NT_KV4_I4 ? p : 2 * p), i1 = 8 * w + (FMT == NT_KV4_I4 ? p + 4 : 2 * p + 1);
+          const __half2 hi = __floats2half2_rn(v[i0] * sc, v[i1] * sc);
+          const float2 f = __half22float2(hi);
+          const __half2 lo = __floats2half2_rn(v[i0] * sc - f.x, v[i1] * sc - f.y);
+          qf[t][2 * w + p / 2][p & 1] = as_u32(g & 1 ? lo : hi);
+        }
+      // of row c of the tile: lanes 8 c .. hold its q
+      rscale[t] = __uint_as_float(uint32_t(127 - __shfl_sync(0xffffffffu, e, 8 * c)) << 23) *
+                  (1.44269504088896f * rsqrtf(float(HD)));
+      limit[t] = 4 * t + c < x.rows ? seen(x, 4 * t + c) : 0;
+      m[t] = -INFINITY;
+      l[t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < CW; ++i) o[t][i] = 0.f;
     }
-    // the next step, its table entry requested before this step's work
-    Step nx = x;
-    const uint8_t* nblk = nullptr;
-    const bool ends = x.page + 1 == x.pages;
-    if (s + 1 < s1) {
-      if (!ends) {
-        ++nx.page;
-      } else if (x.z + 1 < x.chunks) {
-        nx.page = 0, ++nx.z, nx.item0 = s + 1;
-      } else if (x.h + 1 < a.n_kvh) {
-        nx.page = 0, nx.z = 0, ++nx.h, nx.item0 = s + 1;
-      } else {
+    for (int j = first_j; j < last_j; ++j, ++s) {
+      // the next step's block, requested before this step's work
+      const uint8_t* nblk = nullptr;
+      int nj = j + 1;
+      if (nj < last_j) {
+        if (((nj >> sh) & 31) == 0) ent = entries(x, nj >> sh, pages_seen);
+        if (!dead) nblk = block_of(x, ent, nj);
+      } else if (s + 1 < s1) {
         nx = locate(s + 1);
+        nj = 0;
+        ent = entries(nx, 0, (seen(nx, nx.rows - 1) + kPg - 1) / kPg);
+        if (!dead) nblk = block_of(nx, ent, 0);
       }
-      if (!dead) nblk = block_of(nx);
-    }
-    bool live = blk != nullptr && !dead;
-    const int t0 = x.page * kPg;
-    float sc[NT][4][4];
-    if (live) live = wait(0, false);
-    if (live) {
-      // ---- scores
-      const uint4 ksw = *reinterpret_cast<const uint4*>(sk + B::scales + (g * B::NG + (HD == 128 ? c : c >> 1)) * 16);
-      const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};  // rows g + 8 i of the page: two a word
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        uint32_t kw[2][WK];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint8_t* p = sk + (16 * mt + 8 * e + g) * B::row + c * (HD / 8);
-          if (HD == 128) {
-            const uint4 y = *reinterpret_cast<const uint4*>(p);
-            kw[e][0] = y.x, kw[e][1] = y.y, kw[e][WK - 2] = y.z, kw[e][WK - 1] = y.w;
-          } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(p);
-            kw[e][0] = y.x, kw[e][1] = y.y;
-          }
-        }
-        const __half2 d2[2] = {as_h2(__byte_perm(ks[mt], 0u, 0x1010)), as_h2(__byte_perm(ks[mt], 0u, 0x3232))};
-        const __half2 off[2] = {__hmul2(d2[0], __float2half2_rn(-24.f)), __hmul2(d2[1], __float2half2_rn(-24.f))};
-#pragma unroll
-        for (int j = 0; j < NT; ++j) sc[j][mt][0] = sc[j][mt][1] = sc[j][mt][2] = sc[j][mt][3] = 0.f;
-#pragma unroll
-        for (int w = 0; w < WK; ++w) {
-          uint32_t kv[2][4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (FMT == NT_KV4_I4) {
-              kv[e][0] = as_u32(__hfma2(i4_biased<0>(kw[e][w]), d2[e], off[e]));
-              kv[e][1] = as_u32(__hfma2(i4_biased<1>(kw[e][w]), d2[e], off[e]));
-              kv[e][2] = as_u32(__hfma2(i4_biased<2>(kw[e][w]), d2[e], off[e]));
-              kv[e][3] = as_u32(__hfma2(i4_biased<3>(kw[e][w]), d2[e], off[e]));
-            } else {
-              e2m1_to_h2(kw[e][w], kv[e]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) kv[e][i] = as_u32(__hmul2(as_h2(kv[e][i]), d2[e]));
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t af[4] = {kv[0][2 * u], kv[1][2 * u], kv[0][2 * u + 1], kv[1][2 * u + 1]};
-#pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816(sc[j][mt], af, qf[j][2 * w + u][0], qf[j][2 * w + u][1]);
-          }
-        }
-      }
-    }
-    __syncwarp();  // this step's K is in registers and used
-    if (!dead) copy(nblk, 0);
-    uint32_t pf[NT][4][2];
-    if (live) {
-      // ---- online softmax, base 2: m is left behind by up to kSlack before the sums are rescaled
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float p[8];  // positions 16 i / 2 + 8 (i % 2) + g of the page
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = (sc[j][i / 2][2 * (i & 1)] + sc[j][i / 2][2 * (i & 1) + 1]) * rscale[j];
-        if (t0 + kPg > fewest) {
-          const int left = limit[j] - t0 - g;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) p[i] = 8 * i < left ? p[i] : -INFINITY;
-        }
-        float mx = p[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, p[i]);
-        if (__any_sync(0xffffffffu, mx > m[j] + kSlack)) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-          const float mn = fmaxf(m[j], mx);
-          const float corr = mn == -INFINITY ? 1.f : ex2(m[j] - mn);
-          m[j] = mn;
-          l[j] *= corr;
-#pragma unroll
-          for (int i = 0; i < CW; ++i) o[j][i] *= corr;
-        }
-        const float base = m[j] == -INFINITY ? 0.f : kPTop - m[j];
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          p[i] = ex2(p[i] + base);
-          sum += p[i];
-        }
-        l[j] += sum;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pf[j][i / 2][i & 1] = transpose8(hi_lo(p[i]));
-      }
-      live = wait(1, nblk != nullptr);
-    }
-    if (live) {
-      // ---- P V.  Each page's products start from zero and are added to the output in
-      // fp32: the tensor cores round their sums towards zero, and that bias would grow
-      // with the length.
-      const uint4* vsp = reinterpret_cast<const uint4*>(sv + B::scales + ((HD == 128 ? g >> 1 : g >> 2) * 4 + c) * 32);
-      const uint4 va = vsp[0], vb = vsp[1];
-      uint32_t vs[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};  // positions 8 i + 2 c, + 1
-      if (t0 + kPg > tokens) {  // positions that no row sees: whatever their bytes are, they count as 0
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int left = tokens - t0 - 8 * i - 2 * c;
-          vs[i] = left > 1 ? vs[i] : left == 1 ? vs[i] & 0xFFFFu : 0u;
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < B::WPL; ++w) {
-        float acc[NT][4][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int n = 0; n < 4; ++n) acc[j][n][0] = acc[j][n][1] = acc[j][n][2] = acc[j][n][3] = 0.f;
+      bool live = blk != nullptr && !dead;
+      const int t0 = (j >> sh) * kPg;
+      const int m0 = (j & ((1 << sh) - 1)) * (4 >> sh), m1 = m0 + (4 >> sh);  // 16-position tiles of the step
+      float sc[NT][4][4];
+      if (live) live = wait(0, false);
+      if (live) {
+        // ---- scores
+        const uint4 ksw = *reinterpret_cast<const uint4*>(sk + B::scales + (g * B::NG + (HD == 128 ? c : c >> 1)) * 16);
+        const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};  // rows g + 8 i of the page: two a word
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-          uint32_t vv[2][2][4];  // [positions 2 c, + 1 or + 8, + 9][MMA row g or g + 8][m-tile]
+          if (mt < m0 || mt >= m1) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sc[t][mt][0] = sc[t][mt][1] = sc[t][mt][2] = sc[t][mt][3] = -INFINITY;
+            continue;
+          }
+          uint32_t kw[2][WK];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint8_t* p = sv + w * (kPg * 32) + (16 * mt + 8 * e + c) * 32 + g * 4;
-            const uint32_t r0 = *reinterpret_cast<const uint32_t*>(p), r1 = *reinterpret_cast<const uint32_t*>(p + 128);
-            const __half2 d2 = as_h2(vs[2 * mt + e]);
-            if (FMT == NT_KV4_I4) {
-              const __half2 off = __hmul2(d2, __float2half2_rn(-24.f));
-#pragma unroll
-              for (int f = 0; f < 2; ++f) {
-                const uint32_t y = __byte_perm(r0, r1, f ? 0x7632 : 0x5410);
-                vv[e][f][0] = as_u32(__hfma2(i4_biased<0>(y), d2, off));
-                vv[e][f][1] = as_u32(__hfma2(i4_biased<1>(y), d2, off));
-                vv[e][f][2] = as_u32(__hfma2(i4_biased<2>(y), d2, off));
-                vv[e][f][3] = as_u32(__hfma2(i4_biased<3>(y), d2, off));
-              }
+            const uint8_t* p = sk + (16 * mt + 8 * e + g) * B::row + c * (HD / 8);
+            if (HD == 128) {
+              const uint4 y = *reinterpret_cast<const uint4*>(p);
+              kw[e][0] = y.x, kw[e][1] = y.y, kw[e][WK - 2] = y.z, kw[e][WK - 1] = y.w;
             } else {
-              // bytes of two nibbles: the even (odd) channels of both positions
-              const uint32_t even = and_or(r0, 0x0F0F0F0Fu, (r1 << 4) & 0xF0F0F0F0u);
-              const uint32_t odd = and_or(r0 >> 4, 0x0F0F0F0Fu, r1 & 0xF0F0F0F0u);
-              e2m1_to_h2(even, vv[e][0]);
-              e2m1_to_h2(odd, vv[e][1]);
+              const uint2 y = *reinterpret_cast<const uint2*>(p);
+              kw[e][0] = y.x, kw[e][1] = y.y;
+            }
+          }
+          const __half2 d2[2] = {as_h2(__byte_perm(ks[mt], 0u, 0x1010)), as_h2(__byte_perm(ks[mt], 0u, 0x3232))};
+          const __half2 off[2] = {__hmul2(d2[0], __float2half2_rn(-24.f)), __hmul2(d2[1], __float2half2_rn(-24.f))};
 #pragma unroll
-              for (int f = 0; f < 2; ++f)
+          for (int w = 0; w < WK; ++w) {
+            uint32_t kv[2][4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) vv[e][f][n] = as_u32(__hmul2(as_h2(vv[e][f][n]), d2));
+            for (int e = 0; e < 2; ++e) {
+              if (FMT == NT_KV4_I4) {
+                kv[e][0] = as_u32(__hfma2(i4_biased<0>(kw[e][w]), d2[e], off[e]));
+                kv[e][1] = as_u32(__hfma2(i4_biased<1>(kw[e][w]), d2[e], off[e]));
+                kv[e][2] = as_u32(__hfma2(i4_biased<2>(kw[e][w]), d2[e], off[e]));
+                kv[e][3] = as_u32(__hfma2(i4_biased<3>(kw[e][w]), d2[e], off[e]));
+              } else {
+                e2m1_to_h2(kw[e][w], kv[e]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kv[e][i] = as_u32(__hmul2(as_h2(kv[e][i]), d2[e]));
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t af[4] = {kv[0][2 * u], kv[1][2 * u], kv[0][2 * u + 1], kv[1][2 * u + 1]};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                if (w == 0 && u == 0)
+                  mma16816_zero(sc[t][mt], af, qf[t][0][0], qf[t][0][1]);
+                else
+                  mma16816(sc[t][mt], af, qf[t][2 * w + u][0], qf[t][2 * w + u][1]);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();  // this step's K is in registers and used
+      if (!dead) copy(nblk, 0, nj);
+      uint32_t pf[NT][4][2];
+      if (live) {
+        // ---- online softmax, base 2: m is left behind by up to kSlack before the sums are rescaled
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float p[8];  // positions 8 i + g of the page
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = (sc[t][i / 2][2 * (i & 1)] + sc[t][i / 2][2 * (i & 1) + 1]) * rscale[t];
+          if (t0 + kPg > fewest || sh) {
+            const int left = limit[t] - t0 - g;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = 8 * i < left && i / 2 >= m0 && i / 2 < m1 ? p[i] : -INFINITY;
+          }
+          float mx = p[0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) mx = fmaxf(mx, p[i]);
+          if (__any_sync(0xffffffffu, mx > m[t] + kSlack)) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m[t], mx);
+            const float corr = mn == -INFINITY ? 1.f : ex2(m[t] - mn);
+            m[t] = mn;
+            l[t] *= corr;
+#pragma unroll
+            for (int i = 0; i < CW; ++i) o[t][i] *= corr;
+          }
+          const float base = m[t] == -INFINITY ? 0.f : kPTop - m[t];
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            p[i] = ex2(p[i] + base);
+            sum += p[i];
+          }
+          l[t] += sum;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pf[t][i / 2][i & 1] = transpose8(hi_lo(p[i]));
+        }
+        live = wait(1, nblk != nullptr);
+      }
+      if (live) {
+        // ---- P V.  Each step's products start from zero and are added to the output in
+        // fp32: the tensor cores round their sums towards zero, and that bias would grow
+        // with the length.
+        const uint4* vsp = reinterpret_cast<const uint4*>(sv + B::scales + ((HD == 128 ? g >> 1 : g >> 2) * 4 + c) * 32);
+        const uint4 va = vsp[0], vb = vsp[1];
+        uint32_t vs[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};  // positions 8 i + 2 c, + 1
+        if (t0 + kPg > tokens) {  // positions that no row sees: whatever their bytes are, they count as 0
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int left = tokens - t0 - 8 * i - 2 * c;
+            vs[i] = left > 1 ? vs[i] : left == 1 ? vs[i] & 0xFFFFu : 0u;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < B::WPL; ++w) {
+          float acc[NT][4][4];
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            if (mt < m0 || mt >= m1) {
+              if (mt == 0) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                  for (int n = 0; n < 4; ++n) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.f;
+              }
+              continue;
+            }
+            uint32_t vv[2][2][4];  // [positions 2 c, + 1 or + 8, + 9][MMA row g or g + 8][m-tile]
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint8_t* p = sv + w * (kPg * 32) + (16 * mt + 8 * e + c) * 32 + g * 4;
+              const uint32_t r0 = *reinterpret_cast<const uint32_t*>(p), r1 = *reinterpret_cast<const uint32_t*>(p + 128);
+              const __half2 d2 = as_h2(vs[2 * mt + e]);
+              if (FMT == NT_KV4_I4) {
+                const __half2 off = __hmul2(d2, __float2half2_rn(-24.f));
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                  const uint32_t y = __byte_perm(r0, r1, f ? 0x7632 : 0x5410);
+                  vv[e][f][0] = as_u32(__hfma2(i4_biased<0>(y), d2, off));
+                  vv[e][f][1] = as_u32(__hfma2(i4_biased<1>(y), d2, off));
+                  vv[e][f][2] = as_u32(__hfma2(i4_biased<2>(y), d2, off));
+                  vv[e][f][3] = as_u32(__hfma2(i4_biased<3>(y), d2, off));
+                }
+              } else {
+                // bytes of two nibbles: the even (odd) channels of both positions
+                const uint32_t even = and_or(r0, 0x0F0F0F0Fu, (r1 << 4) & 0xF0F0F0F0u);
+                const uint32_t odd = and_or(r0 >> 4, 0x0F0F0F0Fu, r1 & 0xF0F0F0F0u);
+                e2m1_to_h2(even, vv[e][0]);
+                e2m1_to_h2(odd, vv[e][1]);
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                  for (int n = 0; n < 4; ++n) vv[e][f][n] = as_u32(__hmul2(as_h2(vv[e][f][n]), d2));
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const uint32_t af[4] = {vv[0][0][n], vv[0][1][n], vv[1][0][n], vv[1][1][n]};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                if (mt == 0)
+                  mma16816_zero(acc[t][n], af, pf[t][mt][0], pf[t][mt][1]);
+                else
+                  mma16816(acc[t][n], af, pf[t][mt][0], pf[t][mt][1]);
+              }
             }
           }
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t af[4] = {vv[0][0][n], vv[0][1][n], vv[1][0][n], vv[1][1][n]};
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816(acc[j][n], af, pf[j][mt][0], pf[j][mt][1]);
-          }
+            for (int n = 0; n < 4; ++n) {
+              o[t][8 * w + (FMT == NT_KV4_I4 ? n : 2 * n)] += acc[t][n][0] + acc[t][n][1];
+              o[t][8 * w + (FMT == NT_KV4_I4 ? n + 4 : 2 * n + 1)] += acc[t][n][2] + acc[t][n][3];
+            }
         }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            o[j][8 * w + (FMT == NT_KV4_I4 ? n : 2 * n)] += acc[j][n][0] + acc[j][n][1];
-            o[j][8 * w + (FMT == NT_KV4_I4 ? n + 4 : 2 * n + 1)] += acc[j][n][2] + acc[j][n][3];
-          }
       }
+      __syncwarp();  // and its V
+      if (!dead) copy(nblk, 1, nj);
+      if (blk) phase ^= 1;
+      blk = nblk;
     }
-    __syncwarp();  // and its V
-    if (!dead) copy(nblk, 1);
-    if (blk) phase ^= 1;
-    if (ends || s + 1 == s1) {
-      // ---- the item's end, or the warp's: the output, or a partial
-      const bool begun = x.item0 >= s0;
+    // ---- the item's end, or the warp's: the output, or a partial
+    const bool begun = first_j == 0, ended = last_j == x.steps;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
-      if (begun && ends) {
+      for (int d = 4; d < 32; d <<= 1) l[t] += __shfl_xor_sync(0xffffffffu, l[t], d);
+    if (begun && ended) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (4 * j + c >= rows) continue;
-          const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
-          float* to = a.out + vec_of(x, 4 * j + c) + g * CW;
+      for (int t = 0; t < NT; ++t) {
+        if (4 * t + c >= x.rows) continue;
+        const float inv = l[t] == 0.f ? 0.f : 1.f / l[t];
+        float* to = a.out + vec_of(x, 4 * t + c) + g * CW;
 #pragma unroll
-          for (int i = 0; i < CW; i += 4)
-            *reinterpret_cast<float4*>(to + i) =
-                make_float4(o[j][i] * inv, o[j][i + 1] * inv, o[j][i + 2] * inv, o[j][i + 3] * inv);
-        }
-      } else {
-        const int which = ends ? 0 : 1;
-        uint8_t* base = which ? sk : sm4 + L::first + warp * L::slot;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          float* to = reinterpret_cast<float*>(base) + (4 * j + c) * L::line + g * CW;
-#pragma unroll
-          for (int i = 0; i < CW; i += 4)
-            *reinterpret_cast<float4*>(to + i) = make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]);
-          if (g == 0) reinterpret_cast<float2*>(base + ROWS * L::line * 4)[4 * j + c] = make_float2(m[j], l[j]);
-        }
-        if (lane == 0) seg_item[warp][which] = x.item0;
+        for (int i = 0; i < CW; i += 4)
+          *reinterpret_cast<float4*>(to + i) =
+              make_float4(o[t][i] * inv, o[t][i + 1] * inv, o[t][i + 2] * inv, o[t][i + 3] * inv);
       }
-      fresh = true;
+    } else {
+      const int which = ended ? 0 : 1;
+      uint8_t* base = which ? sk : sm4 + L::first + warp * L::slot;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float* to = reinterpret_cast<float*>(base) + (4 * t + c) * L::line + g * CW;
+#pragma unroll
+        for (int i = 0; i < CW; i += 4)
+          *reinterpret_cast<float4*>(to + i) = make_float4(o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]);
+        if (g == 0) reinterpret_cast<float2*>(base + ROWS * L::line * 4)[4 * t + c] = make_float2(m[t], l[t]);
+      }
+      if (lane == 0) seg_item[2 * warp + which] = s - last_j;
     }
     x = nx;
-    blk = nblk;
   }
   __syncthreads();
 
-  // ---- join the warps' partials of one item: runs of (warp, first or last) in the line's order
+  // ---- join the warps' partials of one item, (warp, first or last) in the line's order
   const auto slot_of = [&](int i) {
     return i & 1 ? sm4 + L::ring + size_t(i >> 1) * B::bytes : sm4 + L::first + size_t(i >> 1) * L::slot;
   };
-  const auto item_of = [&](int i) { return seg_item[i >> 1][i & 1]; };
-  int64_t shared_item[2] = {-1, -1};  // items that other CTAs have parts of: begun elsewhere, ending elsewhere
-  for (int i0 = 0; i0 < 2 * kWarps; ++i0) {
-    const int64_t item = item_of(i0);
-    if (item < 0) continue;
-    int i1 = i0 + 1;
-    while (i1 < 2 * kWarps && (item_of(i1) < 0 || item_of(i1) == item)) ++i1;
-    const Step y = locate(item);
-    const bool begun = item >= cta0, ended = item + y.pages <= cta1, whole = begun && ended;
+  const int mine = lane < 2 * kWarps ? seg_item[lane] : -1;
+  const unsigned same = __match_any_sync(0xffffffffu, mine);
+  unsigned left = __ballot_sync(0xffffffffu, mine >= 0);
+  int shared_item[2] = {-1, -1};  // items that other CTAs have parts of: begun elsewhere, ending elsewhere
+  while (left) {
+    const int i0 = __ffs(left) - 1;
+    const unsigned run = __shfl_sync(0xffffffffu, same, i0);
+    const int item = __shfl_sync(0xffffffffu, mine, i0);
+    left &= ~run;
+    const Item y = locate(item);
+    const bool begun = item >= cta0, whole = begun && item + y.steps <= cta1;
     const int side = begun ? 1 : 0;
-    const int n_rows = chunk_rows(y);
-    for (int e = tid; e < ROWS * HD; e += kWarps * 32) {
+    for (int e = 2 * tid; e < ROWS * HD; e += kWarps * 64) {
       const int row = e / HD, ch = e % HD;
       float M = kLowest;
-      for (int i = i0; i < i1; ++i)
-        if (item_of(i) == item) M = fmaxf(M, reinterpret_cast<const float2*>(slot_of(i) + ROWS * L::line * 4)[row].x);
-      float acc = 0.f, sum = 0.f;
-      for (int i = i0; i < i1; ++i) {
-        if (item_of(i) != item) continue;
-        const float2 ml = reinterpret_cast<const float2*>(slot_of(i) + ROWS * L::line * 4)[row];
+      for (unsigned b = run; b; b &= b - 1)
+        M = fmaxf(M, reinterpret_cast<const float2*>(slot_of(__ffs(b) - 1) + ROWS * L::line * 4)[row].x);
+      float2 acc = make_float2(0.f, 0.f);
+      float sum = 0.f;
+      for (unsigned b = run; b; b &= b - 1) {
+        const uint8_t* slot = slot_of(__ffs(b) - 1);
+        const float2 ml = reinterpret_cast<const float2*>(slot + ROWS * L::line * 4)[row];
+        const float2 v = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(slot) + row * L::line + ch);
         const float f = ex2(ml.x - M);
         sum = fmaf(ml.y, f, sum);
-        acc = fmaf(reinterpret_cast<const float*>(slot_of(i))[row * L::line + ch], f, acc);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
       }
       if (whole) {
-        if (row < n_rows) a.out[vec_of(y, row) + ch] = sum == 0.f ? 0.f : acc / sum;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (row < y.rows) *reinterpret_cast<float2*>(a.out + vec_of(y, row) + ch) = make_float2(acc.x * inv, acc.y * inv);
       } else {
         const int64_t at = (int64_t(blockIdx.x) * 2 + side) * ROWS + row;
-        a.part[at * HD + ch] = acc;
+        *reinterpret_cast<float2*>(a.part + at * HD + ch) = acc;
         if (ch == 0) a.ml[at] = make_float2(M, sum);
       }
     }
     if (!whole) shared_item[side] = item;
-    i0 = i1 - 1;
   }
 
   // ---- join the CTAs' partials of an item: the last to arrive does, in the line's order
   for (int side = 0; side < 2; ++side) {
-    const int64_t item = shared_item[side];
+    const int item = shared_item[side];
     if (item < 0) continue;
-    const Step y = locate(item);
-    const int first = int(item / (kWarps * per)), last = int((item + y.pages - 1) / (kWarps * per)), n = last - first + 1;
-    __threadfence();
+    const Item y = locate(item);
+    const int first = item / (kWarps * per), last = (item + y.steps - 1) / (kWarps * per), n = last - first + 1;
     __syncthreads();
-    if (tid == 0) arrived = atomicAdd(a.counters + first, 1u);
-    __syncthreads();
-    if (arrived + 1 != unsigned(n)) continue;
-    __threadfence();
-    if (tid == 0) a.counters[first] = 0u;
-    float* wts = reinterpret_cast<float*>(sm4 + L::ring);
-    __shared__ float inv[ROWS];
-    // the partial of CTA first + i: its item began there (i = 0), or elsewhere
-    const auto part_row = [&](int i, int row) { return (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
-    if (warp < ROWS) {
-      for (int row = warp; row < ROWS; row += kWarps) {
-        float M = kLowest, sum = 0.f;
-        for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.ml + part_row(i, row)).x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        for (int i = lane; i < n; i += 32) {
-          const float2 ml = __ldcg(a.ml + part_row(i, row));
-          const float f = ex2(ml.x - M);
-          wts[i * ROWS + row] = f;
-          sum = fmaf(ml.y, f, sum);
-        }
-        sum = warp_sum(sum);
-        if (lane == 0) inv[row] = sum == 0.f ? 0.f : 1.f / sum;
-      }
+    if (tid == 0) {
+      arrived = arrive_counter(a.counters + first);
+      if (arrived + 1 == unsigned(n)) a.counters[first] = 0u;
     }
     __syncthreads();
-    const int n_rows = chunk_rows(y);
-    for (int e = tid; e < n_rows * HD; e += kWarps * 32) {
+    if (arrived + 1 != unsigned(n)) continue;
+    // the partial of CTA first + i: its item began there (i = 0), or elsewhere
+    const auto part_row = [&](int i, int row) { return (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
+    if (n <= kJoin) {  // few: all in flight together
+      for (int e = 2 * tid; e < y.rows * HD; e += kWarps * 64) {
+        const int row = e / HD, ch = e % HD;
+        float2 ml[kJoin], v[kJoin];
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+          ml[i] = i < n ? __ldcg(a.ml + part_row(i, row)) : make_float2(-INFINITY, 0.f);
+          v[i] = i < n ? __ldcg(reinterpret_cast<const float2*>(a.part + part_row(i, row) * HD + ch)) : make_float2(0.f, 0.f);
+        }
+        float M = kLowest, sum = 0.f;
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) M = fmaxf(M, ml[i].x);
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+          const float f = ex2(ml[i].x - M);
+          sum = fmaf(ml[i].y, f, sum);
+          acc.x = fmaf(v[i].x, f, acc.x);
+          acc.y = fmaf(v[i].y, f, acc.y);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<float2*>(a.out + vec_of(y, row) + ch) = make_float2(acc.x * inv, acc.y * inv);
+      }
+      continue;
+    }
+    float* wts = reinterpret_cast<float*>(sm4 + L::ring);
+    __shared__ float inv[ROWS];
+    for (int row = warp; row < ROWS; row += kWarps) {
+      float M = kLowest, sum = 0.f;
+      for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.ml + part_row(i, row)).x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      for (int i = lane; i < n; i += 32) {
+        const float2 ml = __ldcg(a.ml + part_row(i, row));
+        const float f = ex2(ml.x - M);
+        wts[i * ROWS + row] = f;
+        sum = fmaf(ml.y, f, sum);
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) inv[row] = sum == 0.f ? 0.f : 1.f / sum;
+    }
+    __syncthreads();
+    for (int e = 2 * tid; e < y.rows * HD; e += kWarps * 64) {
       const int row = e / HD, ch = e % HD;
-      float acc = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) acc = fmaf(__ldcg(a.part + part_row(i, row) * HD + ch), wts[i * ROWS + row], acc);
-      a.out[vec_of(y, row) + ch] = acc * inv[row];
+      float2 acc = make_float2(0.f, 0.f);
+      for (int i0 = 0; i0 < n; i0 += kJoin) {
+        float2 v[kJoin];
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i)
+          v[i] = i0 + i < n ? __ldcg(reinterpret_cast<const float2*>(a.part + part_row(i0 + i, row) * HD + ch))
+                            : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+          if (i0 + i >= n) continue;
+          const float f = wts[(i0 + i) * ROWS + row];
+          acc.x = fmaf(v[i].x, f, acc.x);
+          acc.y = fmaf(v[i].y, f, acc.y);
+        }
+      }
+      *reinterpret_cast<float2*>(a.out + vec_of(y, row) + ch) = make_float2(acc.x * inv[row], acc.y * inv[row]);
     }
     __syncthreads();  // the weights are read before the other side's
   }
@@ -932,13 +1035,13 @@ dim3 rows_grid(const nt_kv4& kv, int64_t n) {
 using AttnKernel = void (*)(AttnKv4Args);
 struct AttnVariant {
   AttnKernel kernel;
-  size_t smem;  // without the sums
+  size_t smem;  // without the requests
   int rows, ctas;
 };
 template <int FMT, int HD>
 AttnVariant attn_pick(int NT) {
-  if (NT == 1) return {attn_kv4_kernel<FMT, HD, 1, 2>, AttnKv4Smem<HD, 1>::sums, 4, 2};
-  return {attn_kv4_kernel<FMT, HD, 2, 1>, AttnKv4Smem<HD, 2>::sums, 8, 1};
+  if (NT == 1) return {attn_kv4_kernel<FMT, HD, 1, 2>, AttnKv4Smem<HD, 1>::reqs, 4, 2};
+  return {attn_kv4_kernel<FMT, HD, 2, 1>, AttnKv4Smem<HD, 2>::reqs, 8, 1};
 }
 AttnVariant attn_for(int fmt, int hd, int NT) {
   if (fmt == NT_KV4_I4) return hd == 128 ? attn_pick<NT_KV4_I4, 128>(NT) : attn_pick<NT_KV4_I4, 64>(NT);
@@ -996,7 +1099,7 @@ nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, 
   const int ctas = std::min(k.ctas * c->num_sms, kMaxCtas);
   a.ml = reinterpret_cast<float2*>(scratch);
   a.part = reinterpret_cast<float*>(scratch + size_t(ctas) * 2 * k.rows * sizeof(float2));
-  return cuda_check(c, launch_k(c, k.kernel, dim3(ctas), dim3(kWarps * 32), k.smem + size_t(n_req + 1) * 8, st, a),
+  return cuda_check(c, launch_k(c, k.kernel, dim3(ctas), dim3(kWarps * 32), k.smem + size_t(n_req) * sizeof(Req), st, a),
                     "4-bit attention launch");
 }
 
@@ -1006,7 +1109,7 @@ nt_status configure_kv4(Ctx* c) {
       for (int NT : {1, 2}) {
         const AttnVariant k = attn_for(fmt, hd, NT);
         nt_status s = cuda_check(
-            c, cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.smem + 1025 * 8)),
+            c, cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.smem + 1024 * sizeof(Req))),
             "4-bit attention shared-memory attribute");
         if (s) return s;
       }
