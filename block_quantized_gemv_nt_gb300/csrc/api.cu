@@ -161,7 +161,8 @@ nt_status nt_ctx_create(nt_ctx** out, int device, size_t scratch_bytes) {
   }
   c->err_flag = reinterpret_cast<unsigned*>(c->scratch + kScratchErr);
   if (configure_gemv(c) != NT_OK || configure_ops(c) != NT_OK || configure_gemm(c) != NT_OK ||
-      configure_kv8(c) != NT_OK || configure_kv4(c) != NT_OK) {
+      configure_kv8(c) != NT_OK || configure_kv4(c) != NT_OK ||
+      configure_pages(c) != NT_OK) {
     g_create_error = c->last_error;
     cudaFree(c->scratch);
     delete c;

@@ -90,6 +90,7 @@ nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, 
                           const int32_t* q_start, const int32_t* held, const int32_t* table, int64_t max_pages, char* scratch,
                           unsigned* counters, cudaStream_t st);
 nt_status configure_kv4(Ctx* c);
+nt_status configure_pages(Ctx* c);
 nt_status launch_rope_rows(Ctx* c, const nt_rope_plan& plan, int fmt, const nt_rope_job* jobs, int n_jobs, int64_t n_tok,
                            const int32_t* pos, int64_t pos0, cudaStream_t st);
 
