@@ -14,7 +14,8 @@
 //
 // A scale has at most 8 significant bits and a code at most 3, so every value is exact
 // in f16: the attention multiplies the scale in as it unpacks, and its products lose
-// nothing.
+// nothing.  (Half of the least E2M1 scale would not be; the cache holds those scales
+// doubled, kStored d, and what is read or attended to is halved in fp32.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <algorithm>
@@ -27,6 +28,8 @@ namespace {
 
 constexpr int kPg = NT_KV4_PAGE;
 constexpr float kTopScale = 2720.f;
+template <int FMT>
+constexpr float kStored = FMT == NT_KV4_E2M1 ? 2.f : 1.f;
 
 template <int HD>
 struct Kv4Block {
@@ -77,27 +80,33 @@ __device__ __forceinline__ void e2m1_to_h2(uint32_t x, uint32_t h[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(x));
 }
-// a word's 8 values over the scale, in the order of its channels
+// a word's 8 values times kStored, exact in f16, as pairs (0, 1), (2, 3), (4, 5), (6, 7) of its channels
 template <int FMT>
-__device__ __forceinline__ void unpack4(uint32_t x, float v[8]) {
+__device__ __forceinline__ void unpack4(uint32_t x, __half2 d2, uint32_t v[4]) {
   if (FMT == NT_KV4_I4) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = float(int((x >> (4 * i)) & 15u) - 8);
+    const __half2 off = __hmul2(d2, __float2half2_rn(-24.f));
+    const uint32_t p[4] = {as_u32(__hfma2(i4_biased<0>(x), d2, off)), as_u32(__hfma2(i4_biased<1>(x), d2, off)),
+                           as_u32(__hfma2(i4_biased<2>(x), d2, off)), as_u32(__hfma2(i4_biased<3>(x), d2, off))};
+    v[0] = __byte_perm(p[0], p[1], 0x5410);  // channels i (low halves) and i + 4
+    v[1] = __byte_perm(p[2], p[3], 0x5410);
+    v[2] = __byte_perm(p[0], p[1], 0x7632);
+    v[3] = __byte_perm(p[2], p[3], 0x7632);
   } else {
-    uint32_t h[4];
-    e2m1_to_h2(x, h);
+    e2m1_to_h2(x, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(as_h2(h[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = as_u32(__hmul2(as_h2(v[i]), d2));
   }
 }
 
-__device__ __forceinline__ float max_nan4(float a, float b) {  // the larger; NaN if either is
+// the largest (smallest) of three; NaN if one is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -118,70 +127,121 @@ __device__ __forceinline__ float sixth(float a) {
   return __uint_as_float(u);
 }
 
-// The 8 codes of x over the scale d (inv about 1 / d, 0 for d = 0), as a word.  The
-// products x inv are within 2^-22 of the quotients; where one of them is that near the
-// border between two codes, the group's word is decided again by products of the border
-// and d, which are exact in fp32.
+// The codes of 8 values over the scale d (inv about 1 / d, 0 for d = 0), as a word, decided
+// by products of the borders and d, which are exact in fp32.
+template <int FMT>
+__device__ __noinline__ uint32_t codes4_exact(float4 a, float4 b, float d, float inv) {
+  uint32_t w = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const float v = i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+    uint32_t code;
+    if (FMT == NT_KV4_I4) {
+      float q = rintf(fminf(fmaxf(v * inv, -9.f), 9.f));
+      // x / d - q, as x - q d with the sign of d; exact wherever it is near half of d
+      const float rest = copysignf(1.f, d) * fmaf(-q, d, v), half = 0.5f * fabsf(d);
+      if (fabsf(rest) > half || (fabsf(rest) == half && (int(q) & 1))) q += rest > 0.f ? 1.f : -1.f;
+      code = inv == 0.f ? 8u : uint32_t(int(fminf(fmaxf(q, -8.f), 7.f)) + 8);
+    } else {
+      const float m = fabsf(v);
+      code = (m > 0.25f * d) + (m >= 0.75f * d) + (m > 1.25f * d) + (m >= 1.75f * d) + (m > 2.5f * d) + (m >= 3.5f * d) +
+             (m > 5.f * d);
+      code = (inv == 0.f ? 0u : code) | (v < 0.f ? 8u : 0u);
+    }
+    w |= code << (4 * i);
+  }
+  return w;
+}
+
+// The same where the scale has its 8 bits and is below the largest one: the products x inv
+// are within 2^-22 of the quotients, which are at most 8 (6) and a 2^-8th.  Where one of
+// them is that near a border the exact products decide again.
 template <int FMT>
 __device__ __forceinline__ uint32_t codes4(const float x[8], float d, float inv) {
-  uint32_t w = 0;
-  bool close = false;
   if (FMT == NT_KV4_I4) {
-    float worst = 0.f;
+    // x / d + 200.5: of 192 + 8 + the quotient, the whole part's low 4 bits are the code,
+    // rounded half up; 16 bits of the rest stand below them, and a border is where they are 0
+    uint32_t z[8], least = ~0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float y = fminf(fmaxf(x[i] * inv, -8.f), 7.f);
-      const float z = y + 12582920.f;              // 1.5 * 2^23 + 8: the code in the low bits
-      worst = fmaxf(worst, fabsf(y - (z - 12582920.f)));
-      w |= (__float_as_uint(z) & 15u) << (4 * i);
+      z[i] = __float_as_uint(fminf(fmaf(x[i], inv, 200.5f), 207.9375f));
+      least = min(least, z[i] * 65536u + (8u << 16));
     }
-    close = worst > 0.49999f;
-  } else {
-    uint32_t up[4], dn[4];
+    if (least < (16u << 16)) {
+      const float half = 0.5f * fabsf(d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
-      constexpr float hi = 1.f + 0x1p-20f, lo = 1.f - 0x1p-20f;
-      asm("{\n\t.reg .b8 p, q;\n\tcvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
-          "mov.b32 %0, {p, q, p, q};\n\t}"
-          : "=r"(up[i])
-          : "f"(a * hi), "f"(b * hi), "f"(a * lo), "f"(b * lo));
-      dn[i] = (up[i] >> 8) & 255u;
-      up[i] &= 255u;
-      close |= up[i] != dn[i];
-      w |= up[i] << (8 * i);
-    }
-  }
-  if (close) {
-    w = 0;
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      float v = x[0];
-#pragma unroll
-      for (int k = 1; k < 8; ++k) v = k == i ? x[k] : v;
-      uint32_t code;
-      if (FMT == NT_KV4_I4) {
-        float q = rintf(fminf(fmaxf(v * inv, -9.f), 9.f));
-        // x / d - q, as x - q d with the sign of d; exact wherever it is near half of d
-        const float rest = copysignf(1.f, d) * fmaf(-q, d, v), half = 0.5f * fabsf(d);
-        if (fabsf(rest) > half || (fabsf(rest) == half && (int(q) & 1))) q += rest > 0.f ? 1.f : -1.f;
-        code = uint32_t(int(fminf(fmaxf(q, -8.f), 7.f)) + 8);
-        if (inv == 0.f) code = 8u;
-      } else {
-        const float m = fabsf(v);
-        code = (m > 0.25f * d) + (m >= 0.75f * d) + (m > 1.25f * d) + (m >= 1.75f * d) + (m > 2.5f * d) +
-               (m >= 3.5f * d) + (m > 5.f * d);
-        if (inv == 0.f) code = 0u;
-        code |= v < 0.f ? 8u : 0u;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u = z[i] & 0xFFFF0000u;                 // 200 + the rounded quotient
+        const float rest = copysignf(1.f, d) * fmaf(200.f - __uint_as_float(u), d, x[i]);
+        const bool move = fabsf(rest) > half || (fabsf(rest) == half && (u & 0x10000u));
+        z[i] = min(move ? (rest > 0.f ? u + 0x10000u : u - 0x10000u) : u, 0x434F0000u);  // 207: code 15
       }
-      w |= code << (4 * i);
     }
+    const uint32_t e0 = __byte_perm(z[0], z[2], 0x0062), e1 = __byte_perm(z[4], z[6], 0x0062);
+    const uint32_t o0 = __byte_perm(z[1], z[3], 0x0062), o1 = __byte_perm(z[5], z[7], 0x0062);
+    const uint32_t even = __byte_perm(e0, e1, 0x5410), odd = __byte_perm(o0, o1, 0x5410);
+    return and_or(even, 0x0F0F0F0Fu, (odd << 4) & 0xF0F0F0F0u);
+  }
+  // the codes of products a little larger and a little smaller: where they differ, the border is near
+  const auto pack = [&](float by) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 p, q, r, s;\n\tcvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\tmov.b32 %0, {p, q, r, s};\n\t}"
+        : "=r"(w)
+        : "f"(x[0] * by), "f"(x[1] * by), "f"(x[2] * by), "f"(x[3] * by), "f"(x[4] * by), "f"(x[5] * by), "f"(x[6] * by),
+          "f"(x[7] * by));
+    return w;
+  };
+  uint32_t w = pack(inv * (1.f + 0x1p-20f));
+  for (uint32_t diff = w ^ pack(inv * (1.f - 0x1p-20f)); diff;) {
+    const int at = (__ffs(diff) - 1) & ~3, i = at >> 2;
+    const uint32_t up = (w >> at) & 7u;
+    uint32_t h[4];
+    e2m1_to_h2(up | ((up - 1u) << 4), h);
+    const float2 g = __half22float2(as_h2(h[0]));
+    float m = x[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) m = k == i ? x[k] : m;
+    m = fabsf(m);
+    const float border = 0.5f * (g.x + g.y) * d;
+    if (m < border || (m == border && (up & 1u))) w -= 1u << at;
+    diff &= ~(15u << at);
+  }
+  return w;
+}
+
+// The same of F16 values.  One of them is on a border (k + 1/2) d, 12 bits, or at least a
+// 2^-12th of it away: the quotient after one correction, which is exact on borders and within
+// 2^-22 of itself elsewhere, rounds as the exact one does.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4_f16(const float x[8], float d, float inv) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[i] = x[i] * inv;
+    y[i] = fmaf(fmaf(-y[i], d, x[i]), inv, y[i]);
+  }
+  uint32_t w;
+  if (FMT == NT_KV4_I4) {
+    uint32_t z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(fminf(y[i], 7.f) + 12582920.f);  // 1.5 * 2^23 + 8: the code in the low bits
+    const uint32_t a = __byte_perm(z[1] * 16u + z[0], z[3] * 16u + z[2], 0x0040);
+    w = __byte_perm(a, __byte_perm(z[5] * 16u + z[4], z[7] * 16u + z[6], 0x0040), 0x5410);
+  } else {
+    asm("{\n\t.reg .b8 p, q, r, s;\n\tcvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\tmov.b32 %0, {p, q, r, s};\n\t}"
+        : "=r"(w)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   }
   return w;
 }
 
 // ---- write and read back ------------------------------------------------------------
+// A thread has 16 channels of a row, two words of codes: half of a group.
 constexpr int kRowThreads = 256;
+template <typename T>
+constexpr int kRowPasses = sizeof(T) == 4 ? 2 : 4;  // rows a thread has in flight: 128 bytes
 
 struct Kv4RowsArgs {
   char* row[2];  // K, V rows (either may be null when read)
@@ -190,112 +250,227 @@ struct Kv4RowsArgs {
   const int64_t* slots;
   int64_t n_tok, n_slots;
   int n_kvh;
+  bool wide;     // rows start at multiples of 32 bytes
   unsigned* err;
 };
 
-__device__ __forceinline__ void load8(const float* p, float v[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// the two words j, j + 1 (j even) of row t of a half
+template <int HD>
+__device__ __forceinline__ void store_words(uint8_t* half, int which, int t, int j, uint32_t a, uint32_t b) {
+  if (which && HD == 128) {  // a plane each
+    *reinterpret_cast<uint32_t*>(half + kv4_word_at<HD>(1, t, j)) = a;
+    *reinterpret_cast<uint32_t*>(half + kv4_word_at<HD>(1, t, j + 1)) = b;
+  } else {
+    *reinterpret_cast<uint2*>(half + kv4_word_at<HD>(which, t, j)) = make_uint2(a, b);
+  }
 }
-__device__ __forceinline__ void load8(const __half* p, float v[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+template <int HD>
+__device__ __forceinline__ uint2 load_words(const uint8_t* half, int which, int t, int j) {
+  if (which && HD == 128)
+    return make_uint2(*reinterpret_cast<const uint32_t*>(half + kv4_word_at<HD>(1, t, j)),
+                      *reinterpret_cast<const uint32_t*>(half + kv4_word_at<HD>(1, t, j + 1)));
+  return *reinterpret_cast<const uint2*>(half + kv4_word_at<HD>(which, t, j));
+}
+
+// 16 values of a row as they are loaded
+template <typename T>
+struct Raw16 {
+  uint32_t w[4 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ void load16(const char* p, bool wide, Raw16<T>& v) {
+  if (wide) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(as_h2(w[i]));
+    for (int i = 0; i < 4 * int(sizeof(T)); i += 8)
+      asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          : "=r"(v.w[i]), "=r"(v.w[i + 1]), "=r"(v.w[i + 2]), "=r"(v.w[i + 3]), "=r"(v.w[i + 4]), "=r"(v.w[i + 5]),
+            "=r"(v.w[i + 6]), "=r"(v.w[i + 7])
+          : "l"(p + 4 * i)
+          : "memory");
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T)); ++i) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[i];
+    v.w[4 * i] = a.x, v.w[4 * i + 1] = a.y, v.w[4 * i + 2] = a.z, v.w[4 * i + 3] = a.w;
+  }
+}
+__device__ __forceinline__ void floats(const Raw16<float>& r, float v[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r.w[i]);
+}
+__device__ __forceinline__ void floats(const Raw16<__half>& r, float v[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(as_h2(r.w[i]));
     v[2 * i] = f.x, v[2 * i + 1] = f.y;
   }
 }
+// the largest and the smallest value over the two threads of a group; NaN if one is
+__device__ __forceinline__ void extremes(const Raw16<float>& r, float& hi, float& lo) {
+  float v[16];
+  floats(r, v);
+  hi = lo = v[0];
+#pragma unroll
+  for (int i = 1; i < 15; i += 2) {
+    hi = max3_nan(hi, v[i], v[i + 1]);
+    lo = min3_nan(lo, v[i], v[i + 1]);
+  }
+  const float up = max3_nan(hi, v[15], v[15]), dn = min3_nan(lo, v[15], v[15]);
+  const float a = __shfl_xor_sync(0xffffffffu, up, 1), b = __shfl_xor_sync(0xffffffffu, dn, 1);
+  hi = max3_nan(up, a, a);
+  lo = min3_nan(dn, b, b);
+}
+__device__ __forceinline__ void extremes(const Raw16<__half>& r, float& hi, float& lo) {
+  __half2 up = as_h2(r.w[0]), dn = up;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    up = __hmax2_nan(up, as_h2(r.w[i]));
+    dn = __hmin2_nan(dn, as_h2(r.w[i]));
+  }
+  const uint32_t a = as_u32(up), b = as_u32(__hneg2(dn));
+  __half2 m = __hmax2_nan(as_h2(__byte_perm(a, b, 0x5410)), as_h2(__byte_perm(a, b, 0x7632)));  // (largest, - smallest)
+  m = __hmax2_nan(m, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(m), 1)));
+  const float2 f = __half22float2(m);
+  hi = f.x;
+  lo = -f.y;
+}
+__device__ __forceinline__ float about_inverse(float d) {  // within 2^-23; 0 for 0
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return d != 0.f ? r : 0.f;
+}
 
-// A thread has 8 channels of a row, one word of codes; the four threads of a group
-// reduce its extremes.
+// One CTA: kRowPasses * 4096 / HD tokens of one head's K or V.  Bound by HBM where rows
+// are many, by two round trips of latency where they are few.
 template <int FMT, int HD, typename T>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowsArgs a) {
   using B = Kv4Block<HD>;
-  constexpr int TR = HD / 8;  // threads of a row
+  constexpr int TR = HD / 16;  // threads of a row
+  constexpr int RP = kRowThreads / TR, NP = kRowPasses<T>;
+  constexpr float kMax = 3.402823466e38f;
   pdl_wait();
   pdl_trigger();
-  const int64_t row = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) / TR;
-  const int j = threadIdx.x % TR, which = blockIdx.y;
-  const int64_t tok = row / a.n_kvh;
-  const int h = int(row - tok * a.n_kvh);
-  int64_t slot = tok < a.n_tok ? a.slots[tok] : -1;
-  if (slot >= a.n_slots) {
-    if (j == 0) flag_error(a.err, kErrPaged);
-    slot = -1;
-  }
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (slot >= 0)
-    load8(reinterpret_cast<const T*>((which ? a.row[1] : a.row[0]) + tok * a.tok_stride + h * a.head_stride) + 8 * j, x);
-  float bad = 0.f;
+  const int j = 2 * (threadIdx.x % TR), h = blockIdx.y, which = blockIdx.z;
+  const int64_t tok0 = int64_t(blockIdx.x) * (RP * NP) + threadIdx.x / TR;
+  const char* src = (which ? a.row[1] : a.row[0]) + h * a.head_stride + int(sizeof(T)) * 8 * j;
+  int64_t slot[NP];
+  Raw16<T> x[NP];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) bad = max_nan4(bad, fabsf(x[i]));
-  const bool clean = bad <= 3.402823466e38f;
-  float hi = 0.f, lo = 0.f;
+  for (int i = 0; i < NP; ++i) slot[i] = tok0 + i * RP < a.n_tok ? a.slots[tok0 + i * RP] : -1;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (!clean) {  // NaN becomes 0, an infinity leaves the scale alone
-      if (x[i] != x[i]) x[i] = 0.f;
-      if (fabsf(x[i]) > 3.402823466e38f) continue;
+  for (int i = 0; i < NP; ++i) {
+    if (slot[i] >= a.n_slots) {
+      if (j == 0) flag_error(a.err, kErrPaged);
+      slot[i] = -1;
     }
-    hi = fmaxf(hi, x[i]);
-    lo = fminf(lo, x[i]);
-  }
-  if (!clean) flag_error(a.err, kErrNonFinite4);
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    for (uint32_t& w : x[i].w) w = 0u;
+    if (slot[i] >= 0) load16(src + (tok0 + i * RP) * a.tok_stride, a.wide, x[i]);
   }
-  const float d = scale8(FMT == NT_KV4_I4 ? (hi >= -lo ? hi : lo) * -0.125f : sixth(fmaxf(hi, -lo)));
-  const float inv = d != 0.f ? __frcp_rn(d) : 0.f;
-  if (!clean) {  // an infinity: a finite value that the codes end below, and 0 over a scale of 0
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -1e38f), 1e38f);
+  for (int i = 0; i < NP; ++i) {
+    if (!__any_sync(0xffffffffu, slot[i] >= 0)) continue;
+    float hi, lo, v[16];
+    extremes(x[i], hi, lo);
+    floats(x[i], v);
+    const bool clean = hi <= kMax && lo >= -kMax;  // the same for the group's two threads
+    if (__any_sync(0xffffffffu, !clean)) {
+      float up = hi, dn = lo;
+      if (!clean) {  // NaN becomes 0, an infinity leaves the scale alone
+        flag_error(a.err, kErrNonFinite4);
+        up = dn = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          if (v[k] != v[k]) v[k] = 0.f;
+          if (fabsf(v[k]) <= kMax) up = fmaxf(up, v[k]), dn = fminf(dn, v[k]);
+          v[k] = fminf(fmaxf(v[k], -1e38f), 1e38f);
+        }
+      }
+      hi = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
+      lo = fminf(dn, __shfl_xor_sync(0xffffffffu, dn, 1));
+    }
+    const float d = scale8(FMT == NT_KV4_I4 ? (hi >= -lo ? hi : lo) * -0.125f : sixth(fmaxf(hi, -lo)));
+    const float inv = about_inverse(d);
+    // a scale that lost bits to f16's least numbers, or is the largest, may leave quotients beyond the codes
+    const bool plain = clean && (d == 0.f || (fabsf(d) >= 0x1p-16f && fabsf(d) < kTopScale));
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float* y = v + 8 * k;
+      if (!plain)
+        w[k] = codes4_exact<FMT>(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), d, inv);
+      else
+        w[k] = sizeof(T) == 4 ? codes4<FMT>(y, d, inv) : codes4_f16<FMT>(y, d, inv);
+    }
+    if (slot[i] < 0) continue;
+    const uint64_t page = uint64_t(slot[i]) / kPg;
+    const int t = int(slot[i]) & (kPg - 1);
+    uint8_t* half = a.data + (page * a.n_kvh + h) * B::bytes + which * B::half;
+    store_words<HD>(half, which, t, j, w[0], w[1]);
+    if (j % 4 == 0) *reinterpret_cast<__half*>(half + kv4_scale_at<HD>(which, t, j / 4)) = __float2half_rn(d * kStored<FMT>);
   }
-  const uint32_t w = codes4<FMT>(x, d, inv);
-  if (slot < 0) return;
-  uint8_t* half = a.data + ((slot / kPg) * a.n_kvh + h) * B::bytes + which * B::half;
-  const int t = int(slot % kPg);
-  *reinterpret_cast<uint32_t*>(half + kv4_word_at<HD>(which, t, j)) = w;
-  if (j % 4 == 0) *reinterpret_cast<__half*>(half + kv4_scale_at<HD>(which, t, j / 4)) = __float2half_rn(d);
 }
 
 template <int FMT, int HD, typename T>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs a) {
   using B = Kv4Block<HD>;
-  constexpr int TR = HD / 8;
+  constexpr int TR = HD / 16;
+  constexpr int RP = kRowThreads / TR, NP = kRowPasses<T>;
   pdl_wait();
   pdl_trigger();
-  const int64_t row = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) / TR;
-  const int j = threadIdx.x % TR, which = blockIdx.y;
+  const int j = 2 * (threadIdx.x % TR), h = blockIdx.y, which = blockIdx.z;
   char* out = which ? a.row[1] : a.row[0];
-  const int64_t tok = row / a.n_kvh;
-  const int h = int(row - tok * a.n_kvh);
-  if (!out || tok >= a.n_tok) return;
-  const int64_t slot = a.slots[tok];
-  if (slot < 0) return;
-  if (slot >= a.n_slots) {
-    if (j == 0) flag_error(a.err, kErrPaged);
-    return;
+  if (!out) return;
+  out += h * a.head_stride + int(sizeof(T)) * 8 * j;
+  const int64_t tok0 = int64_t(blockIdx.x) * (RP * NP) + threadIdx.x / TR;
+  int64_t slot[NP];
+  uint2 w[NP];
+  __half d[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) slot[i] = tok0 + i * RP < a.n_tok ? a.slots[tok0 + i * RP] : -1;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    if (slot[i] >= a.n_slots) {
+      if (j == 0) flag_error(a.err, kErrPaged);
+      slot[i] = -1;
+    }
+    if (slot[i] < 0) continue;
+    const uint64_t page = uint64_t(slot[i]) / kPg;
+    const int t = int(slot[i]) & (kPg - 1);
+    const uint8_t* half = a.data + (page * a.n_kvh + h) * B::bytes + which * B::half;
+    w[i] = load_words<HD>(half, which, t, j);
+    d[i] = *reinterpret_cast<const __half*>(half + kv4_scale_at<HD>(which, t, j / 4));
   }
-  const uint8_t* half = a.data + ((slot / kPg) * a.n_kvh + h) * B::bytes + which * B::half;
-  const int t = int(slot % kPg);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(half + kv4_word_at<HD>(which, t, j));
-  const float d = __half2float(*reinterpret_cast<const __half*>(half + kv4_scale_at<HD>(which, t, j / 4)));
-  float v[8];
-  unpack4<FMT>(w, v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= d;
-  T* to = reinterpret_cast<T*>(out + tok * a.tok_stride + h * a.head_stride) + 8 * j;
-  if (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint32_t y[4];
+  for (int i = 0; i < NP; ++i) {
+    if (slot[i] < 0) continue;
+    uint32_t v[8];
+    unpack4<FMT>(w[i].x, __half2half2(d[i]), v);
+    unpack4<FMT>(w[i].y, __half2half2(d[i]), v + 4);
+    char* to = out + (tok0 + i * RP) * a.tok_stride;
+    uint32_t y[4 * sizeof(T)];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = as_u32(__floats2half2_rn(v[2 * i], v[2 * i + 1]));
-    *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+    for (int k = 0; k < 8; ++k) {
+      if (sizeof(T) == 4) {
+        const float2 f = __half22float2(as_h2(v[k]));
+        y[2 * k % (4 * sizeof(T))] = __float_as_uint(f.x * (1.f / kStored<FMT>));
+        y[(2 * k + 1) % (4 * sizeof(T))] = __float_as_uint(f.y * (1.f / kStored<FMT>));
+      } else {
+        y[k] = FMT == NT_KV4_E2M1 ? as_u32(__hmul2(as_h2(v[k]), __float2half2_rn(1.f / kStored<FMT>))) : v[k];
+      }
+    }
+    if (a.wide) {
+#pragma unroll
+      for (int k = 0; k < 4 * int(sizeof(T)); k += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 4 * k), "r"(y[k]), "r"(y[k + 1]),
+                     "r"(y[k + 2]), "r"(y[k + 3]), "r"(y[k + 4]), "r"(y[k + 5]), "r"(y[k + 6]), "r"(y[k + 7])
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int k = 0; k < int(sizeof(T)); ++k)
+        reinterpret_cast<uint4*>(to)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+    }
   }
 }
 
@@ -632,7 +807,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         }
       // of row c of the tile: lanes 8 c .. hold its q
       rscale[t] = __uint_as_float(uint32_t(127 - __shfl_sync(0xffffffffu, e, 8 * c)) << 23) *
-                  (1.44269504088896f * rsqrtf(float(HD)));
+                  (1.44269504088896f / kStored<FMT> * rsqrtf(float(HD)));
       limit[t] = 4 * t + c < x.rows ? seen(x, 4 * t + c) : 0;
       m[t] = -INFINITY;
       l[t] = 0.f;
@@ -845,7 +1020,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (4 * t + c >= x.rows) continue;
-        const float inv = l[t] == 0.f ? 0.f : 1.f / l[t];
+        const float inv = l[t] == 0.f ? 0.f : 1.f / kStored<FMT> / l[t];
         float* to = a.out + vec_of(x, 4 * t + c) + g * CW;
 #pragma unroll
         for (int i = 0; i < CW; i += 4)
@@ -902,7 +1077,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         acc.y = fmaf(v.y, f, acc.y);
       }
       if (whole) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = sum == 0.f ? 0.f : 1.f / kStored<FMT> / sum;
         if (row < y.rows) *reinterpret_cast<float2*>(a.out + vec_of(y, row) + ch) = make_float2(acc.x * inv, acc.y * inv);
       } else {
         const int64_t at = (int64_t(blockIdx.x) * 2 + side) * ROWS + row;
@@ -948,7 +1123,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
           acc.x = fmaf(v[i].x, f, acc.x);
           acc.y = fmaf(v[i].y, f, acc.y);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = sum == 0.f ? 0.f : 1.f / kStored<FMT> / sum;
         *reinterpret_cast<float2*>(a.out + vec_of(y, row) + ch) = make_float2(acc.x * inv, acc.y * inv);
       }
       continue;
@@ -967,7 +1142,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         sum = fmaf(ml.y, f, sum);
       }
       sum = warp_sum(sum);
-      if (lane == 0) inv[row] = sum == 0.f ? 0.f : 1.f / sum;
+      if (lane == 0) inv[row] = sum == 0.f ? 0.f : 1.f / kStored<FMT> / sum;
     }
     __syncthreads();
     for (int e = 2 * tid; e < y.rows * HD; e += kWarps * 64) {
@@ -1024,12 +1199,13 @@ Kv4RowsArgs rows_args(const Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v,
   a.n_tok = n;
   a.n_slots = kv.n_pages * kPg;
   a.n_kvh = kv.n_kvh;
+  a.wide = aligned(k, 32) && aligned(v, 32) && a.tok_stride % 32 == 0 && a.head_stride % 32 == 0;
   a.err = c->err_flag;
   return a;
 }
-dim3 rows_grid(const nt_kv4& kv, int64_t n) {
-  const int64_t per = kRowThreads / (kv.head_dim / 8), rows = n * kv.n_kvh;
-  return dim3(unsigned((rows + per - 1) / per), 2);
+dim3 rows_grid(const nt_kv4& kv, int fmt, int64_t n) {
+  const int64_t per = (fmt == NT_F32 ? kRowPasses<float> : kRowPasses<__half>) * kRowThreads / (kv.head_dim / 16);
+  return dim3(unsigned((n + per - 1) / per), kv.n_kvh, 2);
 }
 
 using AttnKernel = void (*)(AttnKv4Args);
@@ -1055,7 +1231,7 @@ size_t kv4_page_bytes(int head_dim) { return head_dim == 128 ? Kv4Block<128>::by
 nt_status launch_kv4_append(Ctx* c, const nt_kv4& kv, int fmt, const void* k, const void* v, int64_t n, int64_t tok_stride,
                             int64_t head_stride, const int64_t* slots, cudaStream_t st) {
   const Kv4RowsArgs a = rows_args(c, kv, fmt, const_cast<void*>(k), const_cast<void*>(v), n, tok_stride, head_stride, slots);
-  return cuda_check(c, launch_k(c, kv4_rows_for<AppendPick>(kv.fmt, kv.head_dim, fmt), rows_grid(kv, n), dim3(kRowThreads), 0,
+  return cuda_check(c, launch_k(c, kv4_rows_for<AppendPick>(kv.fmt, kv.head_dim, fmt), rows_grid(kv, fmt, n), dim3(kRowThreads), 0,
                                 st, a),
                     "4-bit cache write launch");
 }
@@ -1063,7 +1239,7 @@ nt_status launch_kv4_append(Ctx* c, const nt_kv4& kv, int fmt, const void* k, co
 nt_status launch_kv4_read(Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v, int64_t n, int64_t tok_stride,
                           int64_t head_stride, const int64_t* slots, cudaStream_t st) {
   const Kv4RowsArgs a = rows_args(c, kv, fmt, k, v, n, tok_stride, head_stride, slots);
-  return cuda_check(c, launch_k(c, kv4_rows_for<ReadPick>(kv.fmt, kv.head_dim, fmt), rows_grid(kv, n), dim3(kRowThreads), 0,
+  return cuda_check(c, launch_k(c, kv4_rows_for<ReadPick>(kv.fmt, kv.head_dim, fmt), rows_grid(kv, fmt, n), dim3(kRowThreads), 0,
                                 st, a),
                     "4-bit cache read launch");
 }

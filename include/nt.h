@@ -397,8 +397,8 @@ nt_status nt_attn_kv8_blocks(nt_ctx* ctx, const float* q_dev, const nt_kv8* cach
  * Slot s of the cache is position s % 64 of page s / 64.
  *
  * A row's channels share a scale by 32: d, an f16 number of at most 8
- * significant bits and at most 2720, so that every value, code times d, is exact
- * in f16.
+ * significant bits and at most 2720.  Every value, code times d, is exact in fp32, and
+ * in f16 too (but for halves of E2M1 scales below 2^-22, which end in 2^-25).
  *   NT_KV4_I4    codes -8 .. 7; d the nearest to x / -8, x the value of the largest
  *                magnitude (the positive one of two that tie): x itself is -8 d
  *   NT_KV4_E2M1  codes 0 0.5 1 1.5 2 3 4 6 and their negatives; d the nearest to
@@ -457,7 +457,7 @@ nt_status nt_kv4_pages(nt_ctx* ctx, int n_req, int32_t* table_dev, int64_t max_p
 nt_status nt_kv4_append(nt_ctx* ctx, const nt_kv4* cache, int src_fmt, const void* k_dev, const void* v_dev,
                         int64_t n_tok, int64_t tok_stride, int64_t head_stride, const int64_t* slots_dev, void* stream);
 
-/* The values [road] of the slots' rows, exact in NT_F32 and in NT_F16, to rows laid
+/* The values [road] of the slots' rows, NT_F32 or, to nearest, NT_F16, to rows laid
  * out as nt_kv4_append reads them (k or v may be NULL; rows must not overlap).  Rows
  * of negative slots, and of slots behind the cache (device flag), keep what they held. */
 nt_status nt_kv4_read(nt_ctx* ctx, const nt_kv4* cache, int dst_fmt, void* k_dev, void* v_dev, int64_t n_tok,
