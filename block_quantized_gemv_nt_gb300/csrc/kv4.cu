@@ -344,7 +344,7 @@ __device__ __forceinline__ float about_inverse(float d) {  // within 2^-23; 0 fo
 // One CTA: kRowPasses * 4096 / HD tokens of one head's K or V.  Bound by HBM where rows
 // are many, by two round trips of latency where they are few.
 template <int FMT, int HD, typename T>
-__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowsArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const Kv4RowsArgs a) {
   using B = Kv4Block<HD>;
   constexpr int TR = HD / 16;  // threads of a row
   constexpr int RP = kRowThreads / TR, NP = kRowPasses<T>;

@@ -9,8 +9,7 @@
 namespace nt {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeHeads = 4;  // heads a thread turns: its 8 cosines and sines serve them all
+constexpr int kRopeThreads = 128;
 
 struct RopeJob {
   const char* x;
@@ -93,32 +92,32 @@ __device__ __forceinline__ void turn_unit(uint4 w[2], const float c[4], const fl
   }
 }
 
-// One thread: one unit of kRopeHeads heads of one row.  The angle in turns is the
+// One thread: one unit of HEADS heads of one row, which its cosines and sines serve.  The angle in turns is the
 // position times the plan's 64-bit fraction of a turn, modulo 2^64: exact, so far
 // positions lose nothing, and its upper 32 bits are within 2^-33 of a turn.
-template <typename T, bool HALVES>
+template <typename T, bool HALVES, int HEADS>
 __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const RopeRowsArgs a, const __grid_constant__ nt_rope_plan plan) {
   __shared__ uint64_t turns[128];
   for (int i = threadIdx.x; i < plan.rot_dim / 2; i += kRopeThreads) turns[i] = plan.turns[i];
   pdl_wait();
   pdl_trigger();
   __syncthreads();
-  const int groups = (a.heads + kRopeHeads - 1) / kRopeHeads;
+  const int groups = (a.heads + HEADS - 1) / HEADS;
   const int64_t at = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
   const int64_t tg = at / a.units;
   const int u = int(at - tg * a.units);
   const int64_t tok = tg / groups;
-  const int h0 = int(tg - tok * groups) * kRopeHeads;
+  const int h0 = int(tg - tok * groups) * HEADS;
   if (tok >= a.n_tok) return;
   const bool turned = u < a.turned;
   if (!turned && a.in_place) return;
   // the unit's first channel, and that of its other half
   const int c0 = HALVES && turned ? 4 * u : 8 * u;
   const int c1 = HALVES && turned ? c0 + plan.rot_dim / 2 : c0 + 4;
-  uint4 w[kRopeHeads][2];
-  char* to[kRopeHeads];
+  uint4 w[HEADS][2];
+  char* to[HEADS];
 #pragma unroll
-  for (int i = 0; i < kRopeHeads; ++i) {
+  for (int i = 0; i < HEADS; ++i) {
     int h = h0 + i;
     to[i] = nullptr;
     if (h >= a.heads) continue;
@@ -139,10 +138,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const RopeRowsA
       s[i] *= plan.mag;
     }
 #pragma unroll
-    for (int i = 0; i < kRopeHeads; ++i) turn_unit<T, HALVES>(w[i], c, s);
+    for (int i = 0; i < HEADS; ++i) turn_unit<T, HALVES>(w[i], c, s);
   }
 #pragma unroll
-  for (int i = 0; i < kRopeHeads; ++i)
+  for (int i = 0; i < HEADS; ++i)
     if (to[i]) store_unit<T, HALVES>(to[i], c0, c1, w[i]);
 }
 
@@ -169,12 +168,23 @@ nt_status launch_rope_rows(Ctx* c, const nt_rope_plan& plan, int fmt, const nt_r
   a.n_tok = n_tok;
   a.units = (a.in_place ? plan.rot_dim : plan.head_dim) / 8;
   a.turned = plan.rot_dim / 8;
-  const int64_t threads = n_tok * ((a.heads + kRopeHeads - 1) / kRopeHeads) * a.units;
+  // One head a thread while all of them run at once (F16: half of that), where latency counts (16 rows of 40
+  // heads 1.8 us, with four heads 2.5; 480 F32 rows 4.75 and 5.2, F16 4.75 and 3.9).  Else as many as keep 128 bytes in flight: the turns' cosines and sines cost as much as
+  // loading three or four heads (16,381 F32 rows of 40 heads 96.6 us, with one head 114; 8191 F16 rows of 72
+  // heads with eight 50, with four 52, with one 100).
+  const bool few = n_tok * a.heads * a.units <= int64_t(c->num_sms) * (fmt == NT_F32 ? 2048 : 1024);
+  const int each = few ? 1 : fmt == NT_F32 ? 4 : 8;
+  const int64_t threads = n_tok * ((a.heads + each - 1) / each) * a.units;
   const dim3 grid(unsigned((threads + kRopeThreads - 1) / kRopeThreads)), block(kRopeThreads);
   using K = void (*)(RopeRowsArgs, nt_rope_plan);
   const bool halves = plan.layout == NT_ROPE_HALVES;
-  const K k = fmt == NT_F32 ? (halves ? K(rope_rows_kernel<float, true>) : K(rope_rows_kernel<float, false>))
-                            : (halves ? K(rope_rows_kernel<__half, true>) : K(rope_rows_kernel<__half, false>));
+  K k;
+  if (fmt == NT_F32)
+    k = few ? (halves ? K(rope_rows_kernel<float, true, 1>) : K(rope_rows_kernel<float, false, 1>))
+            : (halves ? K(rope_rows_kernel<float, true, 4>) : K(rope_rows_kernel<float, false, 4>));
+  else
+    k = few ? (halves ? K(rope_rows_kernel<__half, true, 1>) : K(rope_rows_kernel<__half, false, 1>))
+            : (halves ? K(rope_rows_kernel<__half, true, 8>) : K(rope_rows_kernel<__half, false, 8>));
   return cuda_check(c, launch_k(c, k, grid, block, 0, st, a, plan), "rope rows launch");
 }
 
