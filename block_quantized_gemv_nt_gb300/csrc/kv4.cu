@@ -492,13 +492,11 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs
 //  - V: the lane reads word w of channels g HD / 8 .. of rows 16 m + 2 c, + 1, + 8, + 9;
 //    channel n of the word is MMA row g or g + 8 of m-tile n % 4 (I4) or n / 2 (E2M1).
 //
-// Work: the steps (a page, or a half or a quarter of one, of one KV head for one chunk of
-// 4 NT query rows) of all requests in one line, the same number to each warp, whatever the
+// Work: the steps (a page of one KV head for one chunk of 4 NT query rows) of all requests in one line, the same number to each warp, whatever the
 // requests' lengths.  A warp walks its steps with an online softmax; where it begins or
 // ends inside an item (request, head, chunk) it leaves a partial (m, l, o).  The CTA joins
 // its warps' partials of one item, and the last CTA to arrive at an item that several
 // share joins theirs, in the order of the line: nothing depends on who arrives when.
-constexpr int kWarps = 8;
 constexpr int kMaxCtas = 512;                 // one counter each
 constexpr float kPTop = 8.f, kSlack = 6.f;    // probabilities are up to 2^(kPTop + kSlack), in f16's range
 constexpr float kLowest = -3.402823466e38f;
@@ -563,7 +561,7 @@ struct Req {
 
 // shared memory: each warp's K and V halves; its partial of the item that it found
 // begun; the requests.  At the end the warps' last partials lie in their own K and V halves.
-template <int HD, int NT>
+template <int HD, int NT, int kWarps>
 struct AttnKv4Smem {
   static constexpr int ROWS = 4 * NT;
   static constexpr int line = HD + 4;                                  // floats of a row of a partial
@@ -584,10 +582,10 @@ struct Item {
   int len, steps, j;
 };
 
-template <int FMT, int HD, int NT, int CTAS>
+template <int FMT, int HD, int NT, int kWarps, int CTAS>
 __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnKv4Args a) {
   using B = Kv4Block<HD>;
-  using L = AttnKv4Smem<HD, NT>;
+  using L = AttnKv4Smem<HD, NT, kWarps>;
   constexpr int ROWS = 4 * NT;
   constexpr int WK = HD / 32;  // K words of a lane and row
   constexpr int KS = HD / 16;  // k-steps of the scores
@@ -595,6 +593,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   extern __shared__ __align__(16) uint8_t sm4[];
   __shared__ __align__(8) uint64_t bars[kWarps][2];
   __shared__ int seg_item[2 * kWarps];   // item (its first step) of a warp's partials, -1: none
+  __shared__ Item seg_of[2 * kWarps];
   __shared__ int64_t wsum[kWarps];
   __shared__ unsigned arrived;
   Req* const reqs = reinterpret_cast<Req*>(sm4 + L::reqs);
@@ -665,10 +664,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     if (blockIdx.x == 0 && tid == 0) flag_error(a.err, kErrPaged);
     return;
   }
-  // steps of a quarter or half of a page where whole ones would leave warps without any
   const int warps = gridDim.x * kWarps;
-  const int sh = 4 * total64 <= warps ? 2 : 2 * total64 <= warps ? 1 : 0;
-  const int total = int(total64) << sh;
+  const int total = int(total64);
   const int per = max(1, (total + warps - 1) / warps);
   const int cta0 = min(int64_t(total), int64_t(blockIdx.x) * (kWarps * per)), cta1 = min(total, cta0 + kWarps * per);
   if (cta0 >= cta1) return;
@@ -679,16 +676,16 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     int lo = -1, hi = a.n_req - 1;  // the first request whose sum is above s
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((reqs[mid].steps << sh) > s) hi = mid; else lo = mid;
+      if (reqs[mid].steps > s) hi = mid; else lo = mid;
     }
     const Req q = reqs[hi];
-    const int before = hi ? reqs[hi - 1].steps << sh : 0;
+    const int before = hi ? reqs[hi - 1].steps : 0;
     Item x;
     x.r = hi;
     x.len = q.len;
     x.row0 = q.row0;
     x.q_rows = q.rows;
-    x.steps = max(1, (q.len + kPg - 1) / kPg) << sh;
+    x.steps = max(1, (q.len + kPg - 1) / kPg);
     const unsigned chunks = unsigned(q.rows * a.G + ROWS - 1) / ROWS, off = unsigned(s - before);
     const unsigned it = off / unsigned(x.steps), h = it / chunks;
     x.j = int(off - it * x.steps);
@@ -706,29 +703,11 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   };
   uint8_t* const sk = sm4 + L::ring + size_t(warp) * B::bytes;
   const uint8_t* const sv = sk + B::half;
-  // a step's K (0) or V (1) from block `b`
-  const auto copy = [&](const uint8_t* b, int which, int j) {
+  // the K (0) or V (1) half of block `b`
+  const auto copy = [&](const uint8_t* b, int which) {
     if (!b || lane != 0) return;
-    const uint32_t to = smem_u32(which ? sv : sk), on = bar + 8 * which;
-    const uint8_t* from = b + which * B::half;
-    if (sh == 0) {
-      mbar_arrive_expect_tx(on, B::half);
-      if (!a.stall) bulk_g2s(to, from, B::half, on, pol);
-      return;
-    }
-    const uint32_t rows = kPg >> sh, row0 = (j & ((1 << sh) - 1)) * rows, sc = B::half - B::scales;
-    mbar_arrive_expect_tx(on, rows * B::row + sc);
-    if (a.stall) return;
-    if (which == 0) {
-      bulk_g2s(to + row0 * B::row, from + row0 * B::row, rows * B::row, on, pol);
-    } else {
-#pragma unroll
-      for (int w = 0; w < B::WPL; ++w) {
-        const uint32_t o = w * (kPg * 32) + row0 * 32;
-        bulk_g2s(to + o, from + o, rows * 32, on, pol);
-      }
-    }
-    bulk_g2s(to + B::scales, from + B::scales, sc, on, pol);
+    mbar_arrive_expect_tx(bar + 8 * which, B::half);
+    if (!a.stall) bulk_g2s(smem_u32(which ? sv : sk), b + which * B::half, B::half, bar + 8 * which, pol);
   };
   uint32_t phase = 0;
   bool dead = false;  // a wait ran out: the rest is taken as not seen
@@ -753,41 +732,47 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     return -1;
   };
   const auto block_of = [&](const Item& x, int ent, int j) -> const uint8_t* {
-    const int e = __shfl_sync(0xffffffffu, ent, (j >> sh) & 31);
+    const int e = __shfl_sync(0xffffffffu, ent, j & 31);
     return e < 0 ? nullptr : a.data + (int64_t(e) * a.n_kvh + x.h) * B::bytes;
+  };
+
+  // this lane's channels of the rows that its columns stand for, requested as soon as the item is known
+  float qv[NT][HD / 4];
+  const auto load_q = [&](const Item& x) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = 4 * t + (g >> 1);
+      const float* q = a.q + vec_of(x, row) + c * (HD / 4);
+#pragma unroll
+      for (int i = 0; i < HD / 4; i += 4) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < x.rows) y = *reinterpret_cast<const float4*>(q + i);
+        qv[t][i] = y.x, qv[t][i + 1] = y.y, qv[t][i + 2] = y.z, qv[t][i + 3] = y.w;
+      }
+    }
   };
 
   Item x{}, nx{};
   const uint8_t* blk = nullptr;
   int ent = -1;
-  if (s0 < s1) {
-    x = locate(s0);
-    ent = entries(x, (x.j >> sh) & ~31, (seen(x, x.rows - 1) + kPg - 1) / kPg);
-    blk = block_of(x, ent, x.j);
-    copy(blk, 0, x.j);
-    copy(blk, 1, x.j);
-  }
   for (int s = s0; s < s1;) {
     // ---- an item: its rows of q, scaled by a power of two to amax in [2^13, 2^14) and split
+    if (s == s0) x = locate(s);
+    load_q(x);
     const int tokens = seen(x, x.rows - 1), fewest = seen(x, 0), pages_seen = (tokens + kPg - 1) / kPg;
+    if (s == s0) {
+      ent = entries(x, x.j & ~31, pages_seen);
+      blk = block_of(x, ent, x.j);
+      copy(blk, 0);
+      copy(blk, 1);
+    }
     const int first_j = x.j, last_j = min(x.steps, x.j + (s1 - s));
     uint32_t qf[NT][KS][2];
     float rscale[NT], m[NT], l[NT], o[NT][CW];
     int limit[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int row = 4 * t + (g >> 1);
-      float v[HD / 4];
-#pragma unroll
-      for (int i = 0; i < HD / 4; ++i) v[i] = 0.f;
-      if (row < x.rows) {
-        const float* q = a.q + vec_of(x, row) + c * (HD / 4);
-#pragma unroll
-        for (int i = 0; i < HD / 4; i += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(q + i);
-          v[i] = y.x, v[i + 1] = y.y, v[i + 2] = y.z, v[i + 3] = y.w;
-        }
-      }
+      const float* v = qv[t];
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < HD / 4; ++i) top = fmaxf(top, fabsf(v[i]));
@@ -817,19 +802,16 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     for (int j = first_j; j < last_j; ++j, ++s) {
       // the next step's block, requested before this step's work
       const uint8_t* nblk = nullptr;
-      int nj = j + 1;
-      if (nj < last_j) {
-        if (((nj >> sh) & 31) == 0) ent = entries(x, nj >> sh, pages_seen);
-        if (!dead) nblk = block_of(x, ent, nj);
+      if (j + 1 < last_j) {
+        if (((j + 1) & 31) == 0) ent = entries(x, j + 1, pages_seen);
+        if (!dead) nblk = block_of(x, ent, j + 1);
       } else if (s + 1 < s1) {
         nx = locate(s + 1);
-        nj = 0;
         ent = entries(nx, 0, (seen(nx, nx.rows - 1) + kPg - 1) / kPg);
         if (!dead) nblk = block_of(nx, ent, 0);
       }
       bool live = blk != nullptr && !dead;
-      const int t0 = (j >> sh) * kPg;
-      const int m0 = (j & ((1 << sh) - 1)) * (4 >> sh), m1 = m0 + (4 >> sh);  // 16-position tiles of the step
+      const int t0 = j * kPg;
       float sc[NT][4][4];
       if (live) live = wait(0, false);
       if (live) {
@@ -838,11 +820,6 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};  // rows g + 8 i of the page: two a word
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-          if (mt < m0 || mt >= m1) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) sc[t][mt][0] = sc[t][mt][1] = sc[t][mt][2] = sc[t][mt][3] = -INFINITY;
-            continue;
-          }
           uint32_t kw[2][WK];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -888,7 +865,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         }
       }
       __syncwarp();  // this step's K is in registers and used
-      if (!dead) copy(nblk, 0, nj);
+      if (!dead) copy(nblk, 0);
       uint32_t pf[NT][4][2];
       if (live) {
         // ---- online softmax, base 2: m is left behind by up to kSlack before the sums are rescaled
@@ -897,10 +874,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
           float p[8];  // positions 8 i + g of the page
 #pragma unroll
           for (int i = 0; i < 8; ++i) p[i] = (sc[t][i / 2][2 * (i & 1)] + sc[t][i / 2][2 * (i & 1) + 1]) * rscale[t];
-          if (t0 + kPg > fewest || sh) {
+          if (t0 + kPg > fewest) {
             const int left = limit[t] - t0 - g;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = 8 * i < left && i / 2 >= m0 && i / 2 < m1 ? p[i] : -INFINITY;
+            for (int i = 0; i < 8; ++i) p[i] = 8 * i < left ? p[i] : -INFINITY;
           }
           float mx = p[0];
 #pragma unroll
@@ -929,7 +906,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         live = wait(1, nblk != nullptr);
       }
       if (live) {
-        // ---- P V.  Each step's products start from zero and are added to the output in
+        // ---- P V.  Each page's products start from zero and are added to the output in
         // fp32: the tensor cores round their sums towards zero, and that bias would grow
         // with the length.
         const uint4* vsp = reinterpret_cast<const uint4*>(sv + B::scales + ((HD == 128 ? g >> 1 : g >> 2) * 4 + c) * 32);
@@ -947,15 +924,6 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
           float acc[NT][4][4];
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            if (mt < m0 || mt >= m1) {
-              if (mt == 0) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                  for (int n = 0; n < 4; ++n) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.f;
-              }
-              continue;
-            }
             uint32_t vv[2][2][4];  // [positions 2 c, + 1 or + 8, + 9][MMA row g or g + 8][m-tile]
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -1006,7 +974,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         }
       }
       __syncwarp();  // and its V
-      if (!dead) copy(nblk, 1, nj);
+      if (!dead) copy(nblk, 1);
       if (blk) phase ^= 1;
       blk = nblk;
     }
@@ -1038,7 +1006,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
           *reinterpret_cast<float4*>(to + i) = make_float4(o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]);
         if (g == 0) reinterpret_cast<float2*>(base + ROWS * L::line * 4)[4 * t + c] = make_float2(m[t], l[t]);
       }
-      if (lane == 0) seg_item[2 * warp + which] = s - last_j;
+      if (lane == 0) {
+        seg_item[2 * warp + which] = s - last_j;
+        seg_of[2 * warp + which] = x;
+      }
     }
     x = nx;
   }
@@ -1051,30 +1022,42 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   const int mine = lane < 2 * kWarps ? seg_item[lane] : -1;
   const unsigned same = __match_any_sync(0xffffffffu, mine);
   unsigned left = __ballot_sync(0xffffffffu, mine >= 0);
-  int shared_item[2] = {-1, -1};  // items that other CTAs have parts of: begun elsewhere, ending elsewhere
+  int shared_seg[2] = {-1, -1};  // a partial of the items that other CTAs have parts of: begun elsewhere, ending elsewhere
   while (left) {
     const int i0 = __ffs(left) - 1;
     const unsigned run = __shfl_sync(0xffffffffu, same, i0);
     const int item = __shfl_sync(0xffffffffu, mine, i0);
     left &= ~run;
-    const Item y = locate(item);
+    const Item& y = seg_of[i0];
     const bool begun = item >= cta0, whole = begun && item + y.steps <= cta1;
     const int side = begun ? 1 : 0;
     for (int e = 2 * tid; e < ROWS * HD; e += kWarps * 64) {
       const int row = e / HD, ch = e % HD;
-      float M = kLowest;
-      for (unsigned b = run; b; b &= b - 1)
-        M = fmaxf(M, reinterpret_cast<const float2*>(slot_of(__ffs(b) - 1) + ROWS * L::line * 4)[row].x);
+      // the warps' last partials, then (at most one in a run) the one that a warp found begun, which is the line's last
+      float2 ml[kWarps + 1], v[kWarps + 1];
+      const int tail = __ffs(run & 0x55555555u) - 1;
+#pragma unroll
+      for (int w = 0; w <= kWarps; ++w) {
+        const int i = w < kWarps ? 2 * w + 1 : tail;
+        const bool in = w < kWarps ? run >> (2 * w + 1) & 1u : tail >= 0;
+        ml[w] = make_float2(-INFINITY, 0.f);
+        v[w] = make_float2(0.f, 0.f);
+        if (in) {
+          const uint8_t* slot = slot_of(i);
+          ml[w] = reinterpret_cast<const float2*>(slot + ROWS * L::line * 4)[row];
+          v[w] = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(slot) + row * L::line + ch);
+        }
+      }
+      float M = kLowest, sum = 0.f;
       float2 acc = make_float2(0.f, 0.f);
-      float sum = 0.f;
-      for (unsigned b = run; b; b &= b - 1) {
-        const uint8_t* slot = slot_of(__ffs(b) - 1);
-        const float2 ml = reinterpret_cast<const float2*>(slot + ROWS * L::line * 4)[row];
-        const float2 v = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(slot) + row * L::line + ch);
-        const float f = ex2(ml.x - M);
-        sum = fmaf(ml.y, f, sum);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
+#pragma unroll
+      for (int w = 0; w <= kWarps; ++w) M = fmaxf(M, ml[w].x);
+#pragma unroll
+      for (int w = 0; w <= kWarps; ++w) {
+        const float f = ex2(ml[w].x - M);
+        sum = fmaf(ml[w].y, f, sum);
+        acc.x = fmaf(v[w].x, f, acc.x);
+        acc.y = fmaf(v[w].y, f, acc.y);
       }
       if (whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / kStored<FMT> / sum;
@@ -1085,14 +1068,15 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         if (ch == 0) a.ml[at] = make_float2(M, sum);
       }
     }
-    if (!whole) shared_item[side] = item;
+    if (!whole) shared_seg[side] = i0;
   }
 
   // ---- join the CTAs' partials of an item: the last to arrive does, in the line's order
   for (int side = 0; side < 2; ++side) {
-    const int item = shared_item[side];
-    if (item < 0) continue;
-    const Item y = locate(item);
+    const int seg = shared_seg[side];
+    if (seg < 0) continue;
+    const Item& y = seg_of[seg];
+    const int item = seg_item[seg];
     const int first = item / (kWarps * per), last = (item + y.steps - 1) / (kWarps * per), n = last - first + 1;
     __syncthreads();
     if (tid == 0) {
@@ -1212,12 +1196,15 @@ using AttnKernel = void (*)(AttnKv4Args);
 struct AttnVariant {
   AttnKernel kernel;
   size_t smem;  // without the requests
-  int rows, ctas;
+  int rows, warps, ctas;
 };
+template <int FMT, int HD, int NT, int WARPS, int CTAS>
+AttnVariant attn_variant() {
+  return {attn_kv4_kernel<FMT, HD, NT, WARPS, CTAS>, AttnKv4Smem<HD, NT, WARPS>::reqs, 4 * NT, WARPS, CTAS};
+}
 template <int FMT, int HD>
 AttnVariant attn_pick(int NT) {
-  if (NT == 1) return {attn_kv4_kernel<FMT, HD, 1, 2>, AttnKv4Smem<HD, 1>::reqs, 4, 2};
-  return {attn_kv4_kernel<FMT, HD, 2, 1>, AttnKv4Smem<HD, 2>::reqs, 8, 1};
+  return NT == 1 ? attn_variant<FMT, HD, 1, 8, 2>() : attn_variant<FMT, HD, 2, 8, 1>();
 }
 AttnVariant attn_for(int fmt, int hd, int NT) {
   if (fmt == NT_KV4_I4) return hd == 128 ? attn_pick<NT_KV4_I4, 128>(NT) : attn_pick<NT_KV4_I4, 64>(NT);
@@ -1245,7 +1232,7 @@ nt_status launch_kv4_read(Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v, i
 }
 
 size_t kv4_attn_scratch(const Ctx* c, int head_dim) {
-  const size_t ctas = std::min(2 * c->num_sms, kMaxCtas);
+  const size_t ctas = std::min(3 * c->num_sms, kMaxCtas);
   return ctas * 2 * 8 * (head_dim * sizeof(float) + sizeof(float2));
 }
 
@@ -1275,7 +1262,7 @@ nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, 
   const int ctas = std::min(k.ctas * c->num_sms, kMaxCtas);
   a.ml = reinterpret_cast<float2*>(scratch);
   a.part = reinterpret_cast<float*>(scratch + size_t(ctas) * 2 * k.rows * sizeof(float2));
-  return cuda_check(c, launch_k(c, k.kernel, dim3(ctas), dim3(kWarps * 32), k.smem + size_t(n_req) * sizeof(Req), st, a),
+  return cuda_check(c, launch_k(c, k.kernel, dim3(ctas), dim3(k.warps * 32), k.smem + size_t(n_req) * sizeof(Req), st, a),
                     "4-bit attention launch");
 }
 
