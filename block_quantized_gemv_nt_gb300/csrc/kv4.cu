@@ -570,7 +570,7 @@ struct AttnKv4Smem {
   static constexpr size_t first = size_t(kWarps) * Kv4Block<HD>::bytes;
   static constexpr size_t reqs = first + kWarps * slot;
   static_assert(slot <= size_t(Kv4Block<HD>::bytes), "a partial fits a warp's halves");
-  static_assert(kMaxCtas * ROWS * 4 <= first, "the weights of a join fit the ring");
+  static_assert(kMaxCtas * ROWS * 8 + kWarps * 32 * 16 <= first, "a join's weights and sums fit the ring");
   static_assert(reqs % 16 == 0, "requests are read as 16 bytes");
 };
 
@@ -609,6 +609,13 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   pdl_wait();
   pdl_trigger();
 
+  // x / d; both below 2^21, as a rule, and then exact in fp32 up to one
+  const auto divide = [](unsigned x, unsigned d) {
+    if (x >= 1u << 21) return x / d;
+    unsigned q = __float2uint_rz(__uint2float_rn(x) * about_inverse(__uint2float_rn(d)));
+    q -= q * d > x;
+    return q + ((q + 1) * d <= x);
+  };
   // ---- the requests and the sums of their pages' steps
   int64_t total64 = 0;
   const auto read_req = [&](int r, int64_t& v) {
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   }
   const int warps = gridDim.x * kWarps;
   const int total = int(total64);
-  const int per = max(1, (total + warps - 1) / warps);
+  const int per = max(1, int(divide(total + warps - 1, warps)));
   const int cta0 = min(int64_t(total), int64_t(blockIdx.x) * (kWarps * per)), cta1 = min(total, cta0 + kWarps * per);
   if (cta0 >= cta1) return;
   const int s0 = min(total, cta0 + warp * per), s1 = min(total, s0 + per);
@@ -687,7 +694,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     x.q_rows = q.rows;
     x.steps = max(1, (q.len + kPg - 1) / kPg);
     const unsigned chunks = unsigned(q.rows * a.G + ROWS - 1) / ROWS, off = unsigned(s - before);
-    const unsigned it = off / unsigned(x.steps), h = it / chunks;
+    const unsigned it = divide(off, x.steps), h = divide(it, chunks);
     x.j = int(off - it * x.steps);
     x.h = int(h);
     x.at = int(it - h * chunks) * ROWS;
@@ -1077,7 +1084,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     if (seg < 0) continue;
     const Item& y = seg_of[seg];
     const int item = seg_item[seg];
-    const int first = item / (kWarps * per), last = (item + y.steps - 1) / (kWarps * per), n = last - first + 1;
+    const int first = divide(item, kWarps * per), last = divide(item + y.steps - 1, kWarps * per), n = last - first + 1;
     __syncthreads();
     if (tid == 0) {
       arrived = arrive_counter(a.counters + first);
@@ -1112,41 +1119,69 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
       }
       continue;
     }
-    float* wts = reinterpret_cast<float*>(sm4 + L::ring);
+    // many: the outputs' quads over all threads, S threads a quad where there are more threads
+    constexpr int kThreads = kWarps * 32, QUADS = ROWS * HD / 4, S = kThreads > QUADS ? kThreads / QUADS : 1;
+    constexpr int kFly = 8;  // loads in flight
+    float2* mls = reinterpret_cast<float2*>(sm4 + L::ring);  // (m, l), then in m's place the weight
     __shared__ float inv[ROWS];
+    for (int i = tid; i < n * ROWS; i += kThreads) mls[i] = __ldcg(a.ml + part_row(i / ROWS, i % ROWS));
+    const int first_quad = tid % QUADS, lane_s = S > 1 ? tid / QUADS : 0;
+    const auto quad = [&](int i, int e) {
+      return i < n ? __ldcg(reinterpret_cast<const float4*>(a.part + part_row(i, e / (HD / 4)) * HD) + e % (HD / 4))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 v[kFly];
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) v[k] = quad(lane_s + k * S, first_quad);
+    __syncthreads();
     for (int row = warp; row < ROWS; row += kWarps) {
       float M = kLowest, sum = 0.f;
-      for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.ml + part_row(i, row)).x);
+      for (int i = lane; i < n; i += 32) M = fmaxf(M, mls[i * ROWS + row].x);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
       for (int i = lane; i < n; i += 32) {
-        const float2 ml = __ldcg(a.ml + part_row(i, row));
+        const float2 ml = mls[i * ROWS + row];
         const float f = ex2(ml.x - M);
-        wts[i * ROWS + row] = f;
+        mls[i * ROWS + row].x = f;
         sum = fmaf(ml.y, f, sum);
       }
       sum = warp_sum(sum);
       if (lane == 0) inv[row] = sum == 0.f ? 0.f : 1.f / kStored<FMT> / sum;
     }
     __syncthreads();
-    for (int e = 2 * tid; e < y.rows * HD; e += kWarps * 64) {
-      const int row = e / HD, ch = e % HD;
-      float2 acc = make_float2(0.f, 0.f);
-      for (int i0 = 0; i0 < n; i0 += kJoin) {
-        float2 v[kJoin];
+    for (int e = first_quad; e < QUADS; e += kThreads) {
+      const int row = e / (HD / 4);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = lane_s; i0 < n; i0 += kFly * S) {
+        if (i0 != lane_s || e != first_quad) {
 #pragma unroll
-        for (int i = 0; i < kJoin; ++i)
-          v[i] = i0 + i < n ? __ldcg(reinterpret_cast<const float2*>(a.part + part_row(i0 + i, row) * HD + ch))
-                            : make_float2(0.f, 0.f);
+          for (int k = 0; k < kFly; ++k) v[k] = quad(i0 + k * S, e);
+        }
 #pragma unroll
-        for (int i = 0; i < kJoin; ++i) {
-          if (i0 + i >= n) continue;
-          const float f = wts[(i0 + i) * ROWS + row];
-          acc.x = fmaf(v[i].x, f, acc.x);
-          acc.y = fmaf(v[i].y, f, acc.y);
+        for (int k = 0; k < kFly; ++k) {
+          const float f = i0 + k * S < n ? mls[(i0 + k * S) * ROWS + row].x : 0.f;
+          acc.x = fmaf(v[k].x, f, acc.x);
+          acc.y = fmaf(v[k].y, f, acc.y);
+          acc.z = fmaf(v[k].z, f, acc.z);
+          acc.w = fmaf(v[k].w, f, acc.w);
         }
       }
-      *reinterpret_cast<float2*>(a.out + vec_of(y, row) + ch) = make_float2(acc.x * inv[row], acc.y * inv[row]);
+      if (S > 1) {  // the quad's threads meet behind the weights
+        float4* meet = reinterpret_cast<float4*>(sm4 + L::ring + size_t(kMaxCtas) * ROWS * 8);
+        if (lane_s) meet[(lane_s - 1) * QUADS + e] = acc;
+        __syncthreads();
+        if (lane_s) break;
+#pragma unroll
+        for (int k = 1; k < S; ++k) {
+          const float4 y = meet[(k - 1) * QUADS + e];
+          acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+        }
+      }
+      if (row < y.rows) {
+        const float f = inv[row];
+        *reinterpret_cast<float4*>(a.out + vec_of(y, row) + 4 * (e % (HD / 4))) =
+            make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      }
     }
     __syncthreads();  // the weights are read before the other side's
   }
