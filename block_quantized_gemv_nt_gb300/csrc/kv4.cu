@@ -501,6 +501,7 @@ constexpr int kMaxCtas = 512;                 // one counter each
 constexpr float kPTop = 8.f, kSlack = 6.f;    // probabilities are up to 2^(kPTop + kSlack), in f16's range
 constexpr float kLowest = -3.402823466e38f;
 constexpr int64_t kMaxSteps = int64_t(1) << 28;
+constexpr int kOwnSteps = 2;                  // most steps a warp takes of an item that is a CTA's own
 constexpr int kJoin = 16;                     // partials of an item that a join has in flight together
 
 struct AttnKv4Args {
@@ -641,14 +642,33 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     }
     return v;
   };
+  // Few requests, whose items all find a CTA of their own and are not much longer than its
+  // warps: then no item is shared among CTAs (16 requests of up to 500 positions 6.9 us, in line
+  // 9.4; with three steps a warp, 1088 positions 11.0, in line 10.2).
+  int own_r = -1, own_it = 0;  // this CTA's request and item of it; -1: steps in line
   if (a.n_req <= 32) {  // every warp by itself: all write the same
     int64_t v;
     Req x = read_req(lane, v);
+    const int64_t mine = v;
     v = scan(v);
     total64 = __shfl_sync(0xffffffffu, v, 31);
     x.steps = int(min(v, kMaxSteps));
     if (lane < a.n_req) reqs[lane] = x;
     __syncwarp();
+    const int pages = max(1, (x.len + kPg - 1) / kPg), longest = __reduce_max_sync(0xffffffffu, mine ? pages : 0);
+    if (longest <= kOwnSteps * kWarps && total64 <= int64_t(gridDim.x) * longest) {
+      int items = int(divide(unsigned(mine), pages));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, items, o);
+        if (lane >= o) items += y;
+      }
+      if (__shfl_sync(0xffffffffu, items, 31) <= int(gridDim.x)) {
+        own_r = __popc(__ballot_sync(0xffffffffu, items <= int(blockIdx.x)));
+        if (own_r == 32) return;
+        own_it = blockIdx.x - (own_r ? __shfl_sync(0xffffffffu, items, own_r - 1) : 0);
+      }
+    }
   } else {
     for (int r0 = 0; r0 < a.n_req; r0 += kWarps * 32) {
       int64_t v;
@@ -672,15 +692,26 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     return;
   }
   const int warps = gridDim.x * kWarps;
+  // the CTA's steps, and of each warp the same number
   const int total = int(total64);
-  const int per = max(1, int(divide(total + warps - 1, warps)));
-  const int cta0 = min(int64_t(total), int64_t(blockIdx.x) * (kWarps * per)), cta1 = min(total, cta0 + kWarps * per);
-  if (cta0 >= cta1) return;
-  const int s0 = min(total, cta0 + warp * per), s1 = min(total, s0 + per);
+  int cta0, cta1, per;
+  if (own_r >= 0) {
+    const int pages = max(1, (reqs[own_r].len + kPg - 1) / kPg);
+    cta0 = (own_r ? reqs[own_r - 1].steps : 0) + own_it * pages;
+    cta1 = cta0 + pages;
+    per = (pages + kWarps - 1) / kWarps;
+  } else {
+    per = max(1, int(divide(total + warps - 1, warps)));
+    cta0 = min(int64_t(total), int64_t(blockIdx.x) * (kWarps * per));
+    cta1 = min(total, cta0 + kWarps * per);
+    if (cta0 >= cta1) return;
+  }
+  const int s0 = min(cta1, cta0 + warp * per), s1 = min(cta1, s0 + per);
 
   const auto query_of = [&](int row) { return int((uint64_t(unsigned(row)) * a.inv_g) >> 32); };
   const auto locate = [&](int s) {
     int lo = -1, hi = a.n_req - 1;  // the first request whose sum is above s
+    if (own_r >= 0) hi = own_r, lo = hi - 1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (reqs[mid].steps > s) hi = mid; else lo = mid;
