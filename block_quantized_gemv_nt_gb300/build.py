@@ -1,19 +1,24 @@
-"""Build libnt.so in-tree (block_quantized_gemv_nt_gb300/_build/) for sm_103a.
+"""Build libnt.so in-tree (block_quantized_gemv_nt_gb300/_build/) for sm_103a, and
+nt_calls.so beside it: the torch side of some calls, against torch's headers.
 
 Each CUDA translation unit compiles in parallel with nvcc, then one link.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 SO = os.path.join(BUILD, "libnt.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS_SO = os.path.join(BUILD, "nt_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]
@@ -26,15 +31,22 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found")
+    return os.path.dirname(spec.origin)
+
+
 def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
 def _stale() -> bool:
-    if not os.path.exists(SO):
+    if not os.path.exists(SO) or not os.path.exists(CALLS_SO):
         return True
-    t = os.path.getmtime(SO)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
+    t = min(os.path.getmtime(SO), os.path.getmtime(CALLS_SO))
+    deps = sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + [
         os.path.join(HERE, "..", "include", "nt.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -56,14 +68,34 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stdout + r.stderr)
         return obj
 
+    def compile_calls():
+        inc = os.path.join(_torch_dir(), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+        obj = os.path.join(BUILD, "calls.o")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+               "-I" + sysconfig.get_paths()["include"], "-I" + cuda, "-c", CALLS_SRC, "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj
+
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, sources()))
+        calls = calls.result()
     tmp = SO + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", *objs, "-o", tmp, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, SO)
+    tmp = CALLS_SO + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", calls, "-o", tmp, "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-L" + BUILD, "-lnt", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_SO)
     return SO
 
 

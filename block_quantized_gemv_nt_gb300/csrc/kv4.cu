@@ -571,7 +571,8 @@ struct AttnKv4Smem {
   static constexpr size_t first = size_t(kWarps) * Kv4Block<HD>::bytes;
   static constexpr size_t reqs = first + kWarps * slot;
   static_assert(slot <= size_t(Kv4Block<HD>::bytes), "a partial fits a warp's halves");
-  static_assert(kMaxCtas * ROWS * 8 + kWarps * 32 * 16 <= first, "a join's weights and sums fit the ring");
+  static constexpr int max_ctas = 4096 / ROWS < kMaxCtas ? 4096 / ROWS : kMaxCtas;
+  static_assert(max_ctas * ROWS * 8 + kWarps * 32 * 16 <= first, "a join's weights and sums fit the ring");
   static_assert(reqs % 16 == 0, "requests are read as 16 bytes");
 };
 
@@ -1198,7 +1199,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         }
       }
       if (S > 1) {  // the quad's threads meet behind the weights
-        float4* meet = reinterpret_cast<float4*>(sm4 + L::ring + size_t(kMaxCtas) * ROWS * 8);
+        float4* meet = reinterpret_cast<float4*>(sm4 + L::ring + size_t(L::max_ctas) * ROWS * 8);
         if (lane_s) meet[(lane_s - 1) * QUADS + e] = acc;
         __syncthreads();
         if (lane_s) break;
@@ -1262,11 +1263,11 @@ using AttnKernel = void (*)(AttnKv4Args);
 struct AttnVariant {
   AttnKernel kernel;
   size_t smem;  // without the requests
-  int rows, warps, ctas;
+  int rows, warps, ctas, max_ctas;
 };
 template <int FMT, int HD, int NT, int WARPS, int CTAS>
 AttnVariant attn_variant() {
-  return {attn_kv4_kernel<FMT, HD, NT, WARPS, CTAS>, AttnKv4Smem<HD, NT, WARPS>::reqs, 4 * NT, WARPS, CTAS};
+  return {attn_kv4_kernel<FMT, HD, NT, WARPS, CTAS>, AttnKv4Smem<HD, NT, WARPS>::reqs, 4 * NT, WARPS, CTAS, AttnKv4Smem<HD, NT, WARPS>::max_ctas};
 }
 template <int FMT, int HD>
 AttnVariant attn_pick(int NT) {
@@ -1298,8 +1299,9 @@ nt_status launch_kv4_read(Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v, i
 }
 
 size_t kv4_attn_scratch(const Ctx* c, int head_dim) {
-  const size_t ctas = std::min(3 * c->num_sms, kMaxCtas);
-  return ctas * 2 * 8 * (head_dim * sizeof(float) + sizeof(float2));
+  // at most 4096 rows of CTAs, two partials each
+  (void)c;
+  return size_t(4096) * 2 * (head_dim * sizeof(float) + sizeof(float2));
 }
 
 nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, int n_qh, int64_t n_tok, int n_req,
@@ -1325,7 +1327,7 @@ nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, 
   a.stall = take_stall(st);
   const int64_t rows = (n_tok + n_req - 1) / n_req * a.G;
   const AttnVariant k = attn_for(kv.fmt, kv.head_dim, rows <= 4 ? 1 : 2);
-  const int ctas = std::min(k.ctas * c->num_sms, kMaxCtas);
+  const int ctas = std::min(k.ctas * c->num_sms, k.max_ctas);
   a.ml = reinterpret_cast<float2*>(scratch);
   a.part = reinterpret_cast<float*>(scratch + size_t(ctas) * 2 * k.rows * sizeof(float2));
   return cuda_check(c, launch_k(c, k.kernel, dim3(ctas), dim3(k.warps * 32), k.smem + size_t(n_req) * sizeof(Req), st, a),

@@ -3,6 +3,8 @@ allocations) and drives the C ABI's decode step.  Marshalling only: every
 step of the computation runs in libnt.so's kernels."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import torch
 
@@ -165,11 +167,16 @@ class KV8Cache:
         nt.nt_attn_kv8_blocks(self.ctx, q, self.desc, out, n_qh, n_pos, nq, idx, self._list(idx, nq), pos_dev, stream)
 
 
+_calls = nt.load_calls()
+_kv4_rows, _attn_kv4, _kv4_pages, _rope_rows = _calls.kv4_rows, _calls.attn_kv4, _calls.kv4_pages, _calls.rope_rows
+
+
 class KV4Cache:
     """One layer's paged 4-bit KV cache in HBM and the calls on it.  fmt: nt.KV4_I4 or
     nt.KV4_E2M1; data: a contiguous uint8 tensor [n_pages][n_kvh][nt.nt_kv4_layout(head_dim)]
     (allocated when not given).  Slots are int64 tensors on the cache's device, page *
-    64 + position in the page; negative ones are left out."""
+    64 + position in the page; negative ones are left out.  A tensor that does not fit
+    raises ValueError."""
 
     def __init__(self, ctx: nt.Context, fmt: int, n_kvh: int, head_dim: int, n_pages: int, device: str = "cuda",
                  data=None):
@@ -183,64 +190,34 @@ class KV4Cache:
         if ctx is not None and self.index != ctx.device:
             raise ValueError("the cache must be on the context's device")
         self.desc = nt.nt_kv4(fmt, n_kvh, head_dim, n_pages, data.data_ptr())
+        self._at = ctypes.addressof(self.desc)
 
-    def _rows(self, k, v, slots):
-        shape, stride, dtype = k.shape, k.stride(), k.dtype
-        if (len(shape) != 3 or shape[1] != self.n_kvh or shape[2] != self.head_dim or stride[2] != 1
-                or v.stride() != stride or v.shape != shape or v.dtype is not dtype
-                or k.get_device() != self.index or v.get_device() != self.index):
-            raise ValueError("k and v: rows [n][n_kvh][head_dim] on the cache's device, alike in layout")
-        if (slots.dtype is not torch.int64 or slots.shape != shape[:1] or not slots.is_contiguous()
-                or slots.get_device() != self.index):
-            raise ValueError("slots: a contiguous int64 tensor on the cache's device, one for each row")
-        fmt = _ROW_FMT.get(dtype)
-        if fmt is None:
-            raise ValueError("rows must be float32 or float16")
-        return fmt, shape[0], stride[0], stride[1]
+    def _check(self, status):
+        if status:
+            self.ctx.check(status)
 
     def append(self, k, v, slots, stream=None):
         """Rows [n][n_kvh][head_dim] (fp32 or f16, any strides between rows and heads) into their slots."""
-        fmt, n, ts, hs = self._rows(k, v, slots)
-        nt.nt_kv4_append(self.ctx, self.desc, fmt, k, v, n, ts, hs, slots, stream)
+        ctx = self.ctx
+        self._check(_kv4_rows(False, ctx and ctx.handle, self._at, self.n_kvh, self.head_dim, self.index, k, v, slots, stream))
 
     def read(self, k, v, slots, stream=None):
         """The slots' values into k and v [n][n_kvh][head_dim] (fp32 or f16)."""
-        fmt, n, ts, hs = self._rows(k, v, slots)
-        nt.nt_kv4_read(self.ctx, self.desc, fmt, k, v, n, ts, hs, slots, stream)
+        ctx = self.ctx
+        self._check(_kv4_rows(True, ctx and ctx.handle, self._at, self.n_kvh, self.head_dim, self.index, k, v, slots, stream))
 
     def attend(self, q, out, q_start, held, table, stream=None):
         """Attention of q [n_tok][n_qh][head_dim] into out: request r has the rows q_start[r] .. q_start[r + 1]
         (the last of its held[r] positions) and the pages table[r] (int32 tensors)."""
-        shape, index = q.shape, self.index
-        if (len(shape) != 3 or shape[2] != self.head_dim or q.dtype is not torch.float32 or not q.is_contiguous()
-                or q.get_device() != index):
-            raise ValueError("q: contiguous float32 [n_tok][n_qh][head_dim] on the cache's device")
-        if (out.shape != shape or out.dtype is not torch.float32 or not out.is_contiguous()
-                or out.get_device() != index):
-            raise ValueError("out: like q")
-        n_req, max_pages = _table(table, index)
-        _ints(q_start, n_req + 1, index, "q_start")
-        _ints(held, n_req, index, "held")
-        nt.nt_attn_kv4(self.ctx, q, self.desc, out, shape[1], shape[0], n_req, q_start, held, table, max_pages, stream)
-
-
-def _ints(t, n, index, name):
-    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != index:
-        raise ValueError(f"{name}: a contiguous int32 tensor of {n} on the tables' device")
-
-
-def _table(table, index):
-    shape = table.shape
-    if len(shape) != 2 or table.dtype is not torch.int32 or not table.is_contiguous() or table.get_device() != index:
-        raise ValueError("table: a contiguous int32 tensor [n_req][max_pages], all on one device")
-    return shape
+        ctx = self.ctx
+        self._check(_attn_kv4(ctx and ctx.handle, self._at, self.head_dim, self.index, q, out, q_start, held, table, stream))
 
 
 class KV4Pages:
     """The block tables of n_req requests over a pool of n_pages pages, shared by the
     layers' caches: table [n_req][max_pages], held [n_req] (positions of each request),
     free [n_pages] (the stack of free pages), n_free [1], int32 tensors; `buffers`: a
-    dict of them that stands already."""
+    dict of them that stands already.  A tensor that does not fit raises ValueError."""
 
     def __init__(self, ctx: nt.Context, n_req: int, max_pages: int, n_pages: int, device: str = "cuda",
                  buffers: dict | None = None):
@@ -251,10 +228,11 @@ class KV4Pages:
                        "free": torch.arange(n_pages, **i32).flip(0).contiguous(), "n_free": torch.full((1,), n_pages, **i32)}
         self.table, self.held, self.free, self.n_free = (buffers[n] for n in ("table", "held", "free", "n_free"))
         self.index = self.table.get_device()
-        if _table(self.table, self.index) != (n_req, max_pages):
-            raise ValueError("table: need [n_req][max_pages]")
-        for name, t, n in (("held", self.held, n_req), ("free", self.free, n_pages), ("n_free", self.n_free, 1)):
-            _ints(t, n, self.index, name)
+        for name, t, shape in (("table", self.table, (n_req, max_pages)), ("held", self.held, (n_req,)),
+                               ("free", self.free, (n_pages,)), ("n_free", self.n_free, (1,))):
+            if (tuple(t.shape) != shape or t.dtype is not torch.int32 or not t.is_contiguous()
+                    or t.get_device() != self.index):
+                raise ValueError(f"{name}: need a contiguous int32 tensor of shape {shape}, all on one device")
         if ctx is not None and self.index != ctx.device:
             raise ValueError("the tables must be on the context's device")
 
@@ -262,19 +240,11 @@ class KV4Pages:
         """The requests go on with their first keep[r] positions (None: all) and n_new[r] new ones: tables and the stack
         are brought up to date, the new rows' places go to q_start [n_req + 1] and slots (int64) and positions (int32)
         [the most rows].  held and n_free are updated in place unless held_out and n_free_out are given."""
-        R, index, n_tok = self.n_req, self.index, slots.shape[0]
-        _ints(n_new, R, index, "n_new")
-        _ints(q_start, R + 1, index, "q_start")
-        _ints(positions, n_tok, index, "positions")
-        if len(slots.shape) != 1 or slots.dtype is not torch.int64 or not slots.is_contiguous() or slots.get_device() != index:
-            raise ValueError("slots: a contiguous int64 tensor on the tables' device")
-        for name, t, n in (("keep", keep, R), ("held_out", held_out, R), ("n_free_out", n_free_out, 1)):
-            if t is not None:
-                _ints(t, n, index, name)
-        held, n_free = self.held, self.n_free
-        nt.nt_kv4_pages(self.ctx, R, self.table, self.max_pages, held, keep, n_new, self.free, self.n_pages, n_free,
-                        held if held_out is None else held_out, n_free if n_free_out is None else n_free_out, q_start,
-                        slots, positions, n_tok, stream)
+        ctx = self.ctx
+        status = _kv4_pages(ctx and ctx.handle, self.index, self.table, self.held, self.free, self.n_free, n_new, q_start,
+                            slots, positions, keep, held_out, n_free_out, stream)
+        if status:
+            ctx.check(status)
 
 
 class Rope:
@@ -283,26 +253,16 @@ class Rope:
     def __init__(self, ctx: nt.Context, head_dim: int, rot_dim: int | None = None, layout: int = nt.ROPE_PAIRS, **plan):
         self.ctx, self.head_dim = ctx, head_dim
         self.plan = nt.nt_rope_plan_init(head_dim, rot_dim, layout, **plan)
+        self._at = ctypes.addressof(self.plan)
 
     def rotate(self, *rows, positions=None, pos0: int = 0, stream=None):
         """rows: up to three (x, y) of tensors [n][n_heads][head_dim], x turned into y (the same tensor: in place), fp32
-        or f16, any strides between rows and heads; row i stands at positions[i] (int32), or at pos0 + i."""
-        x0 = rows[0][0]
-        n, dtype, index, hd = x0.shape[0], x0.dtype, self.ctx.device, self.head_dim
-        fmt = _ROW_FMT.get(dtype)
-        if fmt is None or not 1 <= len(rows) <= 3:
-            raise ValueError("rows: one to three pairs of float32 or float16 tensors")
-        jobs = (nt.nt_rope_job * len(rows))()
-        for job, (x, y) in zip(jobs, rows):
-            shape, xs, ys = x.shape, x.stride(), y.stride()
-            if (len(shape) != 3 or shape[0] != n or shape[2] != hd or y.shape != shape or xs[2] != 1 or ys[2] != 1
-                    or x.dtype is not dtype or y.dtype is not dtype or x.get_device() != index or y.get_device() != index):
-                raise ValueError("rows: [n][n_heads][head_dim] on the context's device, alike in type, contiguous channels")
-            job.x_dev, job.y_dev, job.n_heads = x.data_ptr(), y.data_ptr(), shape[1]
-            job.x_tok_stride, job.x_head_stride, job.y_tok_stride, job.y_head_stride = xs[0], xs[1], ys[0], ys[1]
-        if positions is not None:
-            _ints(positions, n, index, "positions")
-        nt.nt_rope_rows(self.ctx, self.plan, fmt, jobs, len(rows), n, positions, pos0, nt._stream(stream, x0))
+        or f16, any strides between rows and heads; row i stands at positions[i] (int32), or at pos0 + i.  A tensor that
+        does not fit raises ValueError."""
+        ctx = self.ctx
+        status = _rope_rows(ctx.handle, self._at, self.head_dim, ctx.device, rows, positions, pos0, stream)
+        if status:
+            ctx.check(status)
 
 
 class DeviceModel:

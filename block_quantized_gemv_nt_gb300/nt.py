@@ -49,6 +49,17 @@ def _load():
 
 _lib = _load()
 
+def load_calls():
+    """nt_calls.so: the torch side of the calls over the paged 4-bit cache (checks of the tensors, then the C call)."""
+    import importlib.util
+
+    import torch  # noqa: F401  (its libraries, which the module links against)
+    spec = importlib.util.spec_from_file_location("nt_calls", _build.CALLS_SO)
+    calls = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(calls)
+    return calls
+
+
 _vp, _i64, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
 
