@@ -501,7 +501,8 @@ constexpr int kMaxCtas = 512;                 // one counter each
 constexpr float kPTop = 8.f, kSlack = 6.f;    // probabilities are up to 2^(kPTop + kSlack), in f16's range
 constexpr float kLowest = -3.402823466e38f;
 constexpr int64_t kMaxSteps = int64_t(1) << 28;
-constexpr int kOwnSteps = 2;                  // most steps a warp takes of an item that is a CTA's own
+constexpr int kMaxCluster = 8;
+constexpr int kOwnSteps = 2, kSharedSteps = 3;  // most steps a warp takes of an item that is a CTA's, or a cluster's own
 constexpr int kJoin = 16;                     // partials of an item that a join has in flight together
 
 struct AttnKv4Args {
@@ -516,6 +517,7 @@ struct AttnKv4Args {
   int64_t max_pages, n_pages, n_tok;
   uint64_t inv_g;      // ceil(2^32 / G): row / G = row inv_g >> 32 below 2^28 rows
   int n_req, n_qh, n_kvh, G;
+  int cluster_log;     // of CTAs
   int stall;
 };
 
@@ -546,6 +548,18 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t hi_lo(float x) {
   const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
   return as_u32(__floats2half2_rn(hi, x - hi));
+}
+// 8 bytes at this CTA's shared address `at` in the CTA `rank` of the cluster
+__device__ __forceinline__ float2 ld_cluster(uint32_t at, int rank) {
+  float2 v;
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(at), "r"(rank)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // an arrival that orders what this CTA wrote before it and reads what earlier ones wrote
 __device__ __forceinline__ unsigned arrive_counter(unsigned* at) {
@@ -601,6 +615,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   Req* const reqs = reinterpret_cast<Req*>(sm4 + L::reqs);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const uint32_t bar = smem_u32(&bars[warp][0]);
+  const int cluster_rank = blockIdx.x & ((1 << a.cluster_log) - 1);
   const uint64_t pol = policy_evict_first();
   if (lane == 0) {
     mbar_init(bar, 1);
@@ -643,10 +658,11 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     }
     return v;
   };
-  // Few requests, whose items all find a CTA of their own and are not much longer than its
-  // warps: then no item is shared among CTAs (16 requests of up to 500 positions 6.9 us, in line
-  // 9.4; with three steps a warp, 1088 positions 11.0, in line 10.2).
-  int own_r = -1, own_it = 0;  // this CTA's request and item of it; -1: steps in line
+  // Few requests, whose items all find a CTA or a cluster of their own and are not much longer
+  // than its warps: then no item is joined through global memory (16 requests of up to 500
+  // positions 6.9 us, in line 9.4; 1088 positions of one 7.4, in line 10.2; 4160 9.4 and 12.4).
+  int own_r = -1, own_it = 0;  // the request and item of it that this CTA, or its cluster, has; -1: steps in line
+  bool for_cluster = false;    // the cluster has it
   if (a.n_req <= 32) {  // every warp by itself: all write the same
     int64_t v;
     Req x = read_req(lane, v);
@@ -657,17 +673,20 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     if (lane < a.n_req) reqs[lane] = x;
     __syncwarp();
     const int pages = max(1, (x.len + kPg - 1) / kPg), longest = __reduce_max_sync(0xffffffffu, mine ? pages : 0);
-    if (longest <= kOwnSteps * kWarps && total64 <= int64_t(gridDim.x) * longest) {
+    if (longest <= (kSharedSteps * kWarps << a.cluster_log) && total64 <= int64_t(gridDim.x) * longest) {
       int items = int(divide(unsigned(mine), pages));
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, items, o);
         if (lane >= o) items += y;
       }
-      if (__shfl_sync(0xffffffffu, items, 31) <= int(gridDim.x)) {
-        own_r = __popc(__ballot_sync(0xffffffffu, items <= int(blockIdx.x)));
+      const int all = __shfl_sync(0xffffffffu, items, 31);
+      for_cluster = longest > kWarps && all <= int(gridDim.x) >> a.cluster_log;
+      if (for_cluster || (longest <= kOwnSteps * kWarps && all <= int(gridDim.x))) {
+        const int me = for_cluster ? blockIdx.x >> a.cluster_log : blockIdx.x;
+        own_r = __popc(__ballot_sync(0xffffffffu, items <= me));
         if (own_r == 32) return;
-        own_it = blockIdx.x - (own_r ? __shfl_sync(0xffffffffu, items, own_r - 1) : 0);
+        own_it = me - (own_r ? __shfl_sync(0xffffffffu, items, own_r - 1) : 0);
       }
     }
   } else {
@@ -695,12 +714,18 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   const int warps = gridDim.x * kWarps;
   // the CTA's steps, and of each warp the same number
   const int total = int(total64);
-  int cta0, cta1, per;
+  int cta0, cta1, per, own_first = 0;
   if (own_r >= 0) {
     const int pages = max(1, (reqs[own_r].len + kPg - 1) / kPg);
     cta0 = (own_r ? reqs[own_r - 1].steps : 0) + own_it * pages;
     cta1 = cta0 + pages;
-    per = (pages + kWarps - 1) / kWarps;
+    own_first = cta0;
+    if (for_cluster) {
+      const int each = (pages + (1 << a.cluster_log) - 1) >> a.cluster_log;
+      cta0 = min(cta1, cta0 + cluster_rank * each);
+      cta1 = min(cta1, cta0 + each);
+    }
+    per = (cta1 - cta0 + kWarps - 1) / kWarps;
   } else {
     per = max(1, int(divide(total + warps - 1, warps)));
     cta0 = min(int64_t(total), int64_t(blockIdx.x) * (kWarps * per));
@@ -1023,7 +1048,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[t] += __shfl_xor_sync(0xffffffffu, l[t], d);
-    if (begun && ended) {
+    if (begun && ended && !for_cluster) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (4 * t + c >= x.rows) continue;
@@ -1061,6 +1086,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   const int mine = lane < 2 * kWarps ? seg_item[lane] : -1;
   const unsigned same = __match_any_sync(0xffffffffu, mine);
   unsigned left = __ballot_sync(0xffffffffu, mine >= 0);
+  float* const mine_part = reinterpret_cast<float*>(sm4 + L::reqs + size_t(a.n_req) * sizeof(Req));
+  float2* const mine_ml = reinterpret_cast<float2*>(mine_part + ROWS * HD);
   int shared_seg[2] = {-1, -1};  // a partial of the items that other CTAs have parts of: begun elsewhere, ending elsewhere
   while (left) {
     const int i0 = __ffs(left) - 1;
@@ -1098,7 +1125,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
         acc.x = fmaf(v[w].x, f, acc.x);
         acc.y = fmaf(v[w].y, f, acc.y);
       }
-      if (whole) {
+      if (for_cluster) {
+        *reinterpret_cast<float2*>(mine_part + row * HD + ch) = acc;
+        if (ch == 0) mine_ml[row] = make_float2(M, sum);
+      } else if (whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / kStored<FMT> / sum;
         if (row < y.rows) *reinterpret_cast<float2*>(a.out + vec_of(y, row) + ch) = make_float2(acc.x * inv, acc.y * inv);
       } else {
@@ -1108,6 +1138,41 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
       }
     }
     if (!whole) shared_seg[side] = i0;
+  }
+  if (for_cluster) {
+    // ---- the cluster joins its CTAs' partials, each CTA an equal part of the outputs
+    if (cta0 >= cta1) {
+      for (int e = tid; e < ROWS * HD; e += kWarps * 32) mine_part[e] = 0.f;
+      if (tid < ROWS) mine_ml[tid] = make_float2(-INFINITY, 0.f);
+    }
+    cluster_sync();
+    const Item y = locate(own_first);
+    const uint32_t at = smem_u32(mine_part), at_ml = smem_u32(mine_ml);
+    const int ranks = 1 << a.cluster_log, share = ROWS * HD >> a.cluster_log;
+    for (int e = cluster_rank * share + 2 * tid; e < (cluster_rank + 1) * share; e += kWarps * 64) {
+      const int row = e / HD;
+      float2 ml[kMaxCluster], v[kMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        ml[k] = k < ranks ? ld_cluster(at_ml + row * 8, k) : make_float2(-INFINITY, 0.f);
+        v[k] = k < ranks ? ld_cluster(at + e * 4, k) : make_float2(0.f, 0.f);
+      }
+      float M = kLowest, sum = 0.f;
+      float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        const float f = ex2(ml[k].x - M);
+        sum = fmaf(ml[k].y, f, sum);
+        acc.x = fmaf(v[k].x, f, acc.x);
+        acc.y = fmaf(v[k].y, f, acc.y);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / kStored<FMT> / sum;
+      if (row < y.rows) *reinterpret_cast<float2*>(a.out + vec_of(y, row) + e % HD) = make_float2(acc.x * inv, acc.y * inv);
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+    return;
   }
 
   // ---- join the CTAs' partials of an item: the last to arrive does, in the line's order
@@ -1267,7 +1332,8 @@ struct AttnVariant {
 };
 template <int FMT, int HD, int NT, int WARPS, int CTAS>
 AttnVariant attn_variant() {
-  return {attn_kv4_kernel<FMT, HD, NT, WARPS, CTAS>, AttnKv4Smem<HD, NT, WARPS>::reqs, 4 * NT, WARPS, CTAS, AttnKv4Smem<HD, NT, WARPS>::max_ctas};
+  return {attn_kv4_kernel<FMT, HD, NT, WARPS, CTAS>, AttnKv4Smem<HD, NT, WARPS>::reqs + 4 * NT * (HD + 2) * 4,
+          4 * NT, WARPS, CTAS, AttnKv4Smem<HD, NT, WARPS>::max_ctas};
 }
 template <int FMT, int HD>
 AttnVariant attn_pick(int NT) {
@@ -1326,11 +1392,19 @@ nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, 
   a.inv_g = ((uint64_t(1) << 32) + a.G - 1) / a.G;
   a.stall = take_stall(st);
   const int64_t rows = (n_tok + n_req - 1) / n_req * a.G;
-  const AttnVariant k = attn_for(kv.fmt, kv.head_dim, rows <= 4 ? 1 : 2);
-  const int ctas = std::min(k.ctas * c->num_sms, k.max_ctas);
+  const int NT = rows <= 4 ? 1 : 2;
+  const AttnVariant k = attn_for(kv.fmt, kv.head_dim, NT);
+  // Clusters of 8 where no request can be longer than a cluster of its own takes and, by the
+  // rows' average, all items find one; else of 2: larger ones do not fill the SMs (1,000,003
+  // positions 209 us in clusters of 2, 330 in such of 4 with as many CTAs).
+  const int64_t items = n_req * int64_t(kv.n_kvh) * ((rows + k.rows - 1) / k.rows);
+  const bool wide = max_pages <= kSharedSteps * k.warps * kMaxCluster && items <= c->kv4_ctas[NT - 1][1] / kMaxCluster;
+  a.cluster_log = wide ? 3 : 1;
+  const int ctas = std::min(c->kv4_ctas[NT - 1][wide], k.max_ctas) >> a.cluster_log << a.cluster_log;
   a.ml = reinterpret_cast<float2*>(scratch);
   a.part = reinterpret_cast<float*>(scratch + size_t(ctas) * 2 * k.rows * sizeof(float2));
-  return cuda_check(c, launch_k(c, k.kernel, dim3(ctas), dim3(k.warps * 32), k.smem + size_t(n_req) * sizeof(Req), st, a),
+  return cuda_check(c, launch_cluster(c, k.kernel, dim3(ctas), dim3(k.warps * 32), k.smem + size_t(n_req) * sizeof(Req), st,
+                                      dim3(1 << a.cluster_log, 1, 1), a),
                     "4-bit attention launch");
 }
 
@@ -1343,6 +1417,25 @@ nt_status configure_kv4(Ctx* c) {
             c, cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.smem + 1024 * sizeof(Req))),
             "4-bit attention shared-memory attribute");
         if (s) return s;
+        // CTAs that run at once in clusters of 2 and of 8, the least of the variants'
+        for (int wide : {0, 1}) {
+          cudaLaunchConfig_t cfg{};
+          const int size = wide ? kMaxCluster : 2;
+          cfg.gridDim = dim3(unsigned(k.ctas * c->num_sms / size * size));
+          cfg.blockDim = dim3(k.warps * 32);
+          cfg.dynamicSmemBytes = k.smem + 1024 * sizeof(Req);
+          cudaLaunchAttribute attr[1];
+          attr[0].id = cudaLaunchAttributeClusterDimension;
+          attr[0].val.clusterDim = {unsigned(size), 1, 1};
+          cfg.attrs = attr;
+          cfg.numAttrs = 1;
+          int n = 0;
+          s = cuda_check(c, cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg), "4-bit attention occupancy");
+          if (s) return s;
+          int& most = c->kv4_ctas[NT - 1][wide];
+          n = std::max(1, n) * size;
+          most = most ? std::min(most, n) : n;
+        }
       }
   return NT_OK;
 }

@@ -59,6 +59,7 @@ struct Ctx {
   bool gemv_tune = true;         // time candidate plans on a shape's first eager launch
   bool dry = false;              // enqueue nothing: launchers only tune (a dry pass before a capture)
   std::map<std::string, PlanChoice> gemv_plans;  // tuned plan per launch shape
+  int kv4_ctas[2][2] = {};       // 4-bit attention: CTAs that run at once, by rows (up to 4, more) and clusters (2, 8)
   char* flush = nullptr;         // read before each timed tuning launch so its weights come from HBM
   size_t flush_bytes = 0;
 };
