@@ -209,7 +209,7 @@ class Batch:
         used = [-(-n // 64) for n in held]
         n_pages = sum(used) + 2
         order = rng.permutation(n_pages).astype(np.int32)
-        W = max(1, max(used), width)
+        W = max(1, width, *used)
         table = np.full((len(held), W), -5, dtype=np.int32)     # entries behind a request's pages are never read
         self.k, self.v, slots, at = [], [], [], 0
         for r, n in enumerate(held):
@@ -290,6 +290,19 @@ def test_many_requests(ctx, n_req, n, rows):
 @pytest.mark.parametrize("n,H,G,rows", [(70000, 1, 4, 1), (40000, 2, 8, 3), (9000, 8, 4, 1)])
 def test_long(ctx, fmt, n, H, G, rows):
     b = Batch(ctx, fmt, 128, H, G, [n], [rows], seed=2)
+    b.check(b.run())
+    ctx.sync()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("width", [0, 192, 193, 5000])
+@pytest.mark.parametrize("hd,H,G,held,rows", [
+    (128, 2, 4, [520], [1]), (128, 1, 8, [12288], [1]), (64, 2, 4, [4160, 5, 0, 700], [1, 1, 1, 1]),
+    (128, 4, 1, [12289, 64], [1, 1]), (64, 1, 2, [1536] * 5, [1] * 5), (128, 2, 8, [1025, 1], [2, 1]),
+    (64, 3, 4, [512] * 32, [1] * 32), (64, 3, 4, [600] * 33, [1] * 33), (64, 8, 3, [9000] + [20] * 8, [1] * 9)])
+def test_who_has_an_item(ctx, fmt, width, hd, H, G, held, rows):
+    """Items of a CTA's own, of a cluster's own and in line, by the tables' width, the lengths and their number."""
+    b = Batch(ctx, fmt, hd, H, G, held, rows, seed=len(held) + hd, width=width)
     b.check(b.run())
     ctx.sync()
 
