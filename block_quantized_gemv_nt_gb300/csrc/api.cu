@@ -605,7 +605,7 @@ nt_status check_kv4(nt_ctx* ctx, const nt_kv4* kv) {
              kv->fmt);
   NT_REQUIRE(kv->head_dim == 64 || kv->head_dim == 128, NT_ERR_INVALID_ARG, "head_dim must be 64 or 128");
   NT_REQUIRE(kv->n_kvh >= 1 && kv->n_kvh <= 64, NT_ERR_INVALID_ARG, "n_kvh must be 1..64");
-  NT_REQUIRE(kv->n_pages >= 1 && kv->n_pages < (int64_t(1) << 31), NT_ERR_INVALID_ARG, "n_pages must be 1..2^31 - 1");
+  NT_REQUIRE(kv->n_pages >= 1 && kv->n_pages <= (int64_t(1) << 26), NT_ERR_INVALID_ARG, "n_pages must be 1..2^26");
   NT_REQUIRE(kv->data, NT_ERR_INVALID_ARG, "null cache buffer");
   NT_REQUIRE(aligned(kv->data, 16), NT_ERR_ALIGNMENT, "the cache must be 16-byte aligned");
   return NT_OK;
@@ -650,8 +650,8 @@ nt_status nt_kv4_pages(nt_ctx* ctx, int n_req, int32_t* table, int64_t max_pages
   NT_TRY(pre_call(ctx));
   NT_REQUIRE(n_req >= 1 && n_req <= 1024, NT_ERR_INVALID_ARG, "n_req must be 1..1024");
   NT_REQUIRE(max_pages >= 1 && max_pages <= (int64_t(1) << 24), NT_ERR_INVALID_ARG, "max_pages must be 1..2^24");
-  NT_REQUIRE(n_pages >= 1 && n_pages < (int64_t(1) << 31), NT_ERR_INVALID_ARG, "n_pages must be 1..2^31 - 1");
-  NT_REQUIRE(n_tok >= 0 && n_tok <= (int64_t(1) << 28), NT_ERR_INVALID_ARG, "n_tok must be 0..2^28");
+  NT_REQUIRE(n_pages >= 1 && n_pages <= (int64_t(1) << 26), NT_ERR_INVALID_ARG, "n_pages must be 1..2^26");
+  NT_REQUIRE(n_tok >= 0 && n_tok < (int64_t(1) << 26), NT_ERR_INVALID_ARG, "n_tok must be 0..2^26 - 1");
   NT_REQUIRE(table && held && n_new && free_pages && n_free && held_out && n_free_out && q_start, NT_ERR_INVALID_ARG,
              "null pointer");
   NT_REQUIRE(n_tok == 0 || (slots && positions), NT_ERR_INVALID_ARG, "slots or positions is NULL");

@@ -417,7 +417,7 @@ typedef struct {
   int fmt;         /* NT_KV4_I4 or NT_KV4_E2M1 */
   int n_kvh;       /* 1 .. 64 */
   int head_dim;    /* 64 or 128 */
-  int64_t n_pages; /* 1 .. 2^31 - 1 */
+  int64_t n_pages; /* 1 .. 2^26 */
   void* data;
 } nt_kv4;
 
@@ -442,8 +442,9 @@ nt_status nt_kv4_layout(int head_dim, size_t* page_bytes);
  * set.  A request is refused, with slots of -1 and its length as it was, and the
  * device flag set, when its new length does not fit max_pages, keep[r] is not in
  * 0 .. held[r], or n_new[r] is negative (it then has no rows), and when it and the
- * growing requests before it need more pages than the stack has.  n_req 1..1024;
- * integers 4-byte, slots 8-byte aligned.  One launch without scratch. */
+ * growing requests before it need more pages than the stack has.  n_req 1..1024,
+ * n_pages to 2^26, n_tok below 2^26; integers 4-byte, slots 8-byte aligned.  One launch,
+ * two from n_tok of 4096 on, without scratch. */
 nt_status nt_kv4_pages(nt_ctx* ctx, int n_req, int32_t* table_dev, int64_t max_pages, const int32_t* held_dev,
                        const int32_t* keep_dev, const int32_t* n_new_dev, int32_t* free_dev, int64_t n_pages,
                        const int32_t* n_free_dev, int32_t* held_out_dev, int32_t* n_free_out_dev, int32_t* q_start_dev,

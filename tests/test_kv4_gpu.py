@@ -415,7 +415,7 @@ def test_refusals(ctx):
         f(ctx, cache, fmt, k, v, n, ts, hs, s)
 
     bad = [lambda: attend(cache=desc(fmt=2)), lambda: attend(cache=desc(head_dim=96)), lambda: attend(cache=desc(n_kvh=0)),
-           lambda: attend(cache=desc(n_kvh=65)), lambda: attend(cache=desc(n_pages=0)), lambda: attend(cache=desc(n_pages=1 << 31)),
+           lambda: attend(cache=desc(n_kvh=65)), lambda: attend(cache=desc(n_pages=0)), lambda: attend(cache=desc(n_pages=(1 << 26) + 1)),
            lambda: attend(cache=desc(data=None)), lambda: attend(cache=desc(data=d.data + 8)), lambda: attend(n_qh=3),
            lambda: attend(n_qh=34), lambda: attend(n_qh=0), lambda: attend(n_tok=-1), lambda: attend(n_tok=(1 << 24) + 1),
            lambda: attend(n_req=0), lambda: attend(n_req=1025), lambda: attend(W=0), lambda: attend(W=(1 << 24) + 1),

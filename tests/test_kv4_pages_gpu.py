@@ -97,6 +97,17 @@ def test_pages_given_back_are_taken_in_the_same_step(ctx):
     assert t.n_free == 0
 
 
+@pytest.mark.parametrize("n_tok", [4095, 4096, 4097, 9000])
+def test_few_and_many_rows(ctx, n_tok):
+    """Either side of the number of rows from which a launch of their own writes them; some requests refused, some
+    cut off by n_tok, some giving pages back."""
+    t = Tables(ctx, 40, 60, 300, seed=n_tok)
+    t.step([200] * 20 + [0] * 10 + [64] * 10, n_tok=n_tok, wrong=n_tok < 4640)
+    t.step([1, 500] * 20, keep=[0 if i % 5 == 0 else h for i, h in enumerate(t.held)], n_tok=n_tok, wrong=True)
+    t.step([0] * 40, keep=[h // 2 for h in t.held], n_tok=n_tok)
+    t.step([2] * 39 + [5000], n_tok=n_tok, wrong=True)
+
+
 def test_too_few_pages(ctx):
     """A request that the stack cannot serve, and the growing ones behind it, are refused; one that needs no page is not."""
     t = Tables(ctx, 5, 8, 6)
@@ -176,7 +187,7 @@ def test_refusals(ctx):
     good = dict(n_req=2, table=p.table, max_pages=4, held=p.held, keep=None, n_new=i32, free=p.free, n_pages=9,
                 n_free=p.n_free, held_out=p.held, n_free_out=p.n_free, q_start=i32, slots=s, positions=i32, n_tok=4)
     bad = [dict(n_req=0), dict(n_req=1025), dict(max_pages=0), dict(max_pages=(1 << 24) + 1), dict(n_pages=0),
-           dict(n_pages=1 << 31), dict(n_tok=-1), dict(n_tok=(1 << 28) + 1), dict(slots=s.data_ptr() + 4)]
+           dict(n_pages=(1 << 26) + 1), dict(n_tok=-1), dict(n_tok=1 << 26), dict(slots=s.data_ptr() + 4)]
     bad += [{n: None} for n in good if n not in ("n_req", "max_pages", "keep", "n_pages", "n_tok", "table")]
     bad += [{n: i32.data_ptr() + 2} for n in ("held", "keep", "n_new", "q_start", "positions")]
     for kw in bad:
