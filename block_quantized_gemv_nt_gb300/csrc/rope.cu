@@ -92,9 +92,11 @@ __device__ __forceinline__ void turn_unit(uint4 w[2], const float c[4], const fl
   }
 }
 
-// One thread: one unit of HEADS heads of one row, which its cosines and sines serve.  The angle in turns is the
-// position times the plan's 64-bit fraction of a turn, modulo 2^64: exact, so far
-// positions lose nothing, and its upper 32 bits are within 2^-33 of a turn.
+// One thread: one unit of HEADS heads of one row, which its cosines and sines serve.
+// The angle in turns is the position times the plan's 64-bit fraction of a turn, modulo
+// 2^64: exact, so far positions lose nothing, and its upper 32 bits are within 2^-33 of a
+// turn.  Bound by HBM where rows are many, by a launch and two loads one after the other
+// (position, row) where they are few.
 template <typename T, bool HALVES, int HEADS>
 __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const RopeRowsArgs a, const __grid_constant__ nt_rope_plan plan) {
   __shared__ uint64_t turns[128];
@@ -168,10 +170,12 @@ nt_status launch_rope_rows(Ctx* c, const nt_rope_plan& plan, int fmt, const nt_r
   a.n_tok = n_tok;
   a.units = (a.in_place ? plan.rot_dim : plan.head_dim) / 8;
   a.turned = plan.rot_dim / 8;
-  // One head a thread while all of them run at once (F16: half of that), where latency counts (16 rows of 40
-  // heads 1.8 us, with four heads 2.5; 480 F32 rows 4.75 and 5.2, F16 4.75 and 3.9).  Else as many as keep 128 bytes in flight: the turns' cosines and sines cost as much as
-  // loading three or four heads (16,381 F32 rows of 40 heads 96.6 us, with one head 114; 8191 F16 rows of 72
-  // heads with eight 50, with four 52, with one 100).
+  // One head a thread while all of them run at once (F16: half of that), where latency
+  // counts (16 rows of 40 heads 1.85 us, with four heads 2.5; 480 F32 rows 4.75 and 5.2, F16
+  // 4.75 and 3.9).  Else as many as keep 128 bytes in flight: the turns' cosines and sines
+  // cost as much as loading three or four heads (16,381 F32 rows of 40 heads 96.7 us, 6.9
+  // TB/s, with one head 114; 8191 F16 rows of 72 heads with eight 49.4, 6.1 TB/s, with four
+  // 52, with one 100).
   const bool few = n_tok * a.heads * a.units <= int64_t(c->num_sms) * (fmt == NT_F32 ? 2048 : 1024);
   const int each = few ? 1 : fmt == NT_F32 ? 4 : 8;
   const int64_t threads = n_tok * ((a.heads + each - 1) / each) * a.units;
@@ -209,8 +213,8 @@ extern "C" nt_status nt_rope_plan_init(const nt_rope_desc* d, nt_rope_plan* plan
   if (d->scaling == NT_ROPE_RAMP) {
     const auto pair = [&](double t) { return rot * std::log(L / (t * pi2)) / (2.0 * std::log(d->theta)); };
     from = std::fmax(std::floor(pair(high)), 0.0);
-    to = std::fmin(std::ceil(pair(low)), half - 1.0);
-    if (to == from) to += 0.001;
+    to = std::fmin(std::ceil(pair(low)), rot - 1.0);
+    if (!(to > from)) to = from + 0.001;
   }
   const double base = d->scaling == NT_ROPE_BASE ? d->theta * std::pow(s, rot / (rot - 2.0)) : d->theta;
   *plan = nt_rope_plan{};

@@ -439,6 +439,9 @@ def nt_rope_plan_init(head_dim, rot_dim=None, layout=ROPE_PAIRS, theta=10000.0, 
 
 def nt_rope_rows(ctx, plan: nt_rope_plan, fmt, jobs, n_jobs, n_tok, positions, pos0, stream=None):
     """jobs: a ctypes array of nt_rope_job."""
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(ctx.device)
     return ctx.check(_rope_rows(ctx.handle, plan, fmt, jobs, n_jobs, n_tok, _ptr(positions), pos0, _stream(stream)))
 
 

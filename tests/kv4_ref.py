@@ -134,8 +134,8 @@ def frequencies(rot, theta, scaling, factor=1.0, old_len=0.0, low=0.0, high=0.0,
     elif scaling == "ramp":
         low, high = low or 1.0, high or 32.0
         pair = lambda t: rot * math.log(old_len / (2 * math.pi * t)) / (2 * math.log(theta))  # noqa: E731
-        a, b = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), rot // 2 - 1)
-        b = a + 0.001 if a == b else b
+        a, b = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), rot - 1)
+        b = a + 0.001 if b <= a else b
         k = np.clip((np.arange(rot // 2) - a) / (b - a), 0, 1)
         u = u * (1 - k) + u / s * k
     return u if divisors is None else u / np.asarray(divisors, dtype=np.float64)

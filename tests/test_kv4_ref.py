@@ -95,6 +95,20 @@ def test_plan_turns(name, args, rot):
     assert plan.mag == np.float32(mag)
 
 
+def test_ramp_of_a_length_that_every_pair_turns_often_over():
+    # all pairs turn more than 32 times over the old length: none is slowed down
+    plan = nt.nt_rope_plan_init(64, 64, theta=100.0, scaling=nt.ROPE_RAMP, factor=4.0, old_len=1e9)
+    plain = nt.nt_rope_plan_init(64, 64, theta=100.0)
+    assert list(plan.turns) == list(plain.turns)
+    # the pair that turns once lies behind the last one (64.4 of 64): the ramp is not cut short
+    plan = nt.nt_rope_plan_init(128, 128, theta=10000.0, scaling=nt.ROPE_RAMP, factor=4.0, old_len=65536.0)
+    a, b = 40, 65                                         # 64 ln(L / (2 pi 32)) / ln theta = 40.2, 64.3
+    u = [10000.0 ** (-2.0 * i / 128) for i in range(64)]
+    for i in range(64):
+        k = min(1.0, max(0.0, (i - a) / (b - a)))
+        assert Fraction(plan.turns[i], 2 ** 64) == pytest.approx(u[i] * (1 - 0.75 * k) / (2 * math.pi), rel=1e-13)
+
+
 def test_plan_divisors_and_whole_turns():
     div = [2.0 ** (i - 3) for i in range(8)]
     plan = nt.nt_rope_plan_init(16, 16, theta=10000.0, divisors=div, mag=0.5)
