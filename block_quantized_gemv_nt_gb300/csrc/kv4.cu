@@ -341,8 +341,13 @@ __device__ __forceinline__ float about_inverse(float d) {  // within 2^-23; 0 fo
   return d != 0.f ? r : 0.f;
 }
 
-// One CTA: kRowPasses * 4096 / HD tokens of one head's K or V.  Bound by HBM where rows
-// are many, by two round trips of latency where they are few.
+// One CTA: kRowPasses * 4096 / HD tokens of one head's K or V.  Where rows are few, two
+// round trips of latency (16 rows of 8 heads 1.9 us, a bare launch 1.0); where they are
+// many, HBM: 32,767 F32 rows of 8 heads 48 us, 303 MB, 6.3 TB/s.  Of F16 rows there is
+// half as much to read for the same arithmetic, and instruction issue bounds them: 131,072
+// in 132 us, 671 MB, 5.1 TB/s, the issue slots 82% and the integer pipe 57% busy; with four
+// rows a thread and four CTAs an SM (64 registers), as here, faster than with two rows
+// (134) or one (161).
 template <int FMT, int HD, typename T>
 __global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const Kv4RowsArgs a) {
   using B = Kv4Block<HD>;
@@ -412,6 +417,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const Kv4Row
   }
 }
 
+// The way back: 131,072 F16 rows of 8 heads 105 us, 6.4 TB/s.
 template <int FMT, int HD, typename T>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs a) {
   using B = Kv4Block<HD>;
@@ -492,11 +498,27 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs
 //  - V: the lane reads word w of channels g HD / 8 .. of rows 16 m + 2 c, + 1, + 8, + 9;
 //    channel n of the word is MMA row g or g + 8 of m-tile n % 4 (I4) or n / 2 (E2M1).
 //
-// Work: the steps (a page of one KV head for one chunk of 4 NT query rows) of all requests in one line, the same number to each warp, whatever the
-// requests' lengths.  A warp walks its steps with an online softmax; where it begins or
+// Work: the steps (a page of one KV head for one chunk of 4 NT query rows) of all requests
+// in one line, the same number to each warp, whatever the requests' lengths.  A warp walks its steps with an online softmax; where it begins or
 // ends inside an item (request, head, chunk) it leaves a partial (m, l, o).  The CTA joins
 // its warps' partials of one item, and the last CTA to arrive at an item that several
 // share joins theirs, in the order of the line: nothing depends on who arrives when.
+//
+// A step is a whole page: each warp has the K and the V half of one in shared memory and
+// the next page's halves on their way in the same places as soon as it has used them; with
+// steps of 32 or 16 positions the joins and the copies' round trips cost more than the
+// shorter steps save (4160 positions 17.7 and 22.8 us, whole pages 13.3 then).
+//
+// What bounds it.  Up to 4 rows (a decode step): instruction issue, before HBM.  A page of
+// a head is 9216 bytes and about 1170 warp instructions for E2M1 (hardware conversion and
+// one multiply a pair), 1380 for I4 (shift, mask, fused multiply-add a pair); 1,000,003
+// positions of 8 heads take 185 and 210 us, 6.2 and 5.5 TB/s, the tensor cores 23..26%
+// busy, the integer pipe half.  Two CTAs of 8 warps an SM; 16 warps in one CTA take 178 and
+// 202, but 64 requests of 8000 positions 36.8 and not 34.4.  8 rows (verify passes): one
+// CTA of 8 warps an SM with 255 registers, tensor cores 33%, issue 44%; the dependent
+// products and conversions of 8 warps do not fill more (16 ragged requests of 64 query
+// heads and up to 5 rows 59 us; with 12 warps 67, with 16 rows a step and their spills 87,
+// with unpacked tiles shared by all warps 71).
 constexpr int kMaxCtas = 512;                 // one counter each
 constexpr float kPTop = 8.f, kSlack = 6.f;    // probabilities are up to 2^(kPTop + kSlack), in f16's range
 constexpr float kLowest = -3.402823466e38f;
@@ -647,6 +669,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
       x.len = len_ok ? n : n < 0 ? 0 : int(cap);
       if (!(rows_ok && len_ok) && blockIdx.x == 0) flag_error(a.err, kErrPaged);
       v = ((int64_t(x.rows) * a.G + ROWS - 1) / ROWS) * a.n_kvh * max(1, (x.len + kPg - 1) / kPg);
+      v = min(v, kMaxSteps + 1);  // so that the sums cannot overflow
     }
     return x;
   };
@@ -660,7 +683,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   };
   // Few requests, whose items all find a CTA or a cluster of their own and are not much longer
   // than its warps: then no item is joined through global memory (16 requests of up to 500
-  // positions 6.9 us, in line 9.4; 1088 positions of one 7.4, in line 10.2; 4160 9.4 and 12.4).
+  // positions 7.4 us, in line 9.4; 1088 positions of one 7.7, in line 10.2; 4160 10.4 and 12.5).
   int own_r = -1, own_it = 0;  // the request and item of it that this CTA, or its cluster, has; -1: steps in line
   bool for_cluster = false;    // the cluster has it
   if (a.n_req <= 32) {  // every warp by itself: all write the same
@@ -1396,7 +1419,7 @@ nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, 
   const AttnVariant k = attn_for(kv.fmt, kv.head_dim, NT);
   // Clusters of 8 where no request can be longer than a cluster of its own takes and, by the
   // rows' average, all items find one; else of 2: larger ones do not fill the SMs (1,000,003
-  // positions 209 us in clusters of 2, 330 in such of 4 with as many CTAs).
+  // positions 210 us in clusters of 2, 330 in such of 4: the last of them start when others end).
   const int64_t items = n_req * int64_t(kv.n_kvh) * ((rows + k.rows - 1) / k.rows);
   const bool wide = max_pages <= kSharedSteps * k.warps * kMaxCluster && items <= c->kv4_ctas[NT - 1][1] / kMaxCluster;
   a.cluster_log = wide ? 3 : 1;

@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kPg = NT_KV4_PAGE;
 constexpr int kMaxReq = 1024;
-// From so many rows on a launch of their own writes them, from all SMs, and the tables take a
+// Above so many rows a launch of their own writes them, from all SMs, and the tables take a
 // cluster: the lists' round trips then run side by side (250 mixed requests with 153,000
 // rows: a cluster of 16 writing all 10.0 us, two launches 8.7, with 8 CTAs 9.6, with
 // 2 13.8; 1024 requests with 550,000 rows 16.6, 11.1, 11.8, 14.8).
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kMaxReq) kv4_pages_kernel(const PagesArgs a) {
   if (!ROWS) first = until = have;
   if (need && !refused) until = max(until, want);
   uint32_t u[1] = {uint32_t(max(0, until - first))};
-  const uint32_t all_most[1] = {1u << 26};
+  const uint32_t all_most[1] = {1u << 27};  // above the pages of the pool and of the rows together
   __syncthreads();  // the sums' places are read
   block_sums(u, all_most, sums);
   if (r < a.n_req)

@@ -104,8 +104,7 @@ nt_status nt_ctx_sync(nt_ctx* ctx);
  * host-side poll with a deadline), then report like nt_ctx_sync:
  * NT_ERR_TIMEOUT when the deadline passes first (the work is not
  * cancelled; call again to keep waiting), else the device-side error flag
- * (bounded-wait timeout, position out of range, NaN or infinity written to an
- * 8-bit KV cache), cleared when read. */
+ * (every cause that nt_ctx_sync reports), cleared when read. */
 nt_status nt_stream_sync(nt_ctx* ctx, void* stream, int64_t timeout_us);
 /* Fault injection for the streaming engine's tests ([feat] SLEP streaming;
  * host side only; nothing is ever made to fail on the GPU): the nth following
@@ -119,8 +118,8 @@ nt_status nt_debug_fail_copy(nt_ctx* ctx, int nth);
  * GPU is made to fault or hang): the next n eager launches in this process
  * of the kernels that wait on bulk copies — the quant GEMV (nt_gemv_q,
  * nt_gemv_q_multi, nt_gemv_swiglu), nt_attn_decode, nt_attn_decode_static,
- * nt_attn_kv8, nt_attn_kv8_blocks and nt_attn_kv4 — issue no copies, so their waits run out
- * after a few tries and take the timeout path: the context flag that
+ * nt_attn_kv8, nt_attn_kv8_blocks and nt_attn_kv4 — issue no copies, so their
+ * waits run out after a few tries and take the timeout path: the context flag that
  * nt_ctx_sync reports as NT_ERR_TIMEOUT, or NaN output from
  * nt_attn_decode_static.
  * Launches on a stream being captured are never armed.  n = 0 disarms;
@@ -443,8 +442,8 @@ nt_status nt_kv4_layout(int head_dim, size_t* page_bytes);
  * device flag set, when its new length does not fit max_pages, keep[r] is not in
  * 0 .. held[r], or n_new[r] is negative (it then has no rows), and when it and the
  * growing requests before it need more pages than the stack has.  n_req 1..1024,
- * n_pages to 2^26, n_tok below 2^26; integers 4-byte, slots 8-byte aligned.  One launch,
- * two from n_tok of 4096 on, without scratch. */
+ * n_pages to 2^26, max_pages to 2^24, n_tok below 2^26; integers 4-byte, slots 8-byte
+ * aligned.  One launch, two above 4096 rows (n_tok), without scratch. */
 nt_status nt_kv4_pages(nt_ctx* ctx, int n_req, int32_t* table_dev, int64_t max_pages, const int32_t* held_dev,
                        const int32_t* keep_dev, const int32_t* n_new_dev, int32_t* free_dev, int64_t n_pages,
                        const int32_t* n_free_dev, int32_t* held_out_dev, int32_t* n_free_out_dev, int32_t* q_start_dev,
@@ -453,8 +452,9 @@ nt_status nt_kv4_pages(nt_ctx* ctx, int n_req, int32_t* table_dev, int64_t max_p
 /* Rows of K and V [road], NT_F32 or NT_F16, into the cache's slots: row i of head h
  * at k + i * tok_stride + h * head_stride (elements; multiples of 16 bytes),
  * head_dim values.  A negative slot's row is left out; one behind the cache sets the
- * device flag and is left out.  Two rows of one call with the same slot leave one
- * of their values, group by group.  slots 8-byte aligned. */
+ * device flag and is left out.  The slots of one call differ from one another: two rows
+ * with the same one leave codes of either under the scales of either there.  n_tok to
+ * 2^28; slots 8-byte aligned. */
 nt_status nt_kv4_append(nt_ctx* ctx, const nt_kv4* cache, int src_fmt, const void* k_dev, const void* v_dev,
                         int64_t n_tok, int64_t tok_stride, int64_t head_stride, const int64_t* slots_dev, void* stream);
 
@@ -470,13 +470,15 @@ nt_status nt_kv4_read(nt_ctx* ctx, const nt_kv4* cache, int dst_fmt, void* k_dev
  * that nobody uses) and held[r] positions, the rows' own included; its i-th last row
  * sees all but the last i of them:
  *   out = softmax_j(q . K[j] / sqrt(head_dim)) . V[j],  j < held[r] - i,
- * zeros where that leaves none.  Any number of rows a request; each 4, 8 or 16 of
- * (row, query head) pairs of a KV head read its pages once.  Rows of no request are
- * left as they were.  The device flag is set, and what is wrong taken as absent, where
+ * zeros where that leaves none.  Any number of rows a request; each 8 (row, query head)
+ * pairs of a KV head, or 4 where n_tok / n_req rows have no more, read its pages once.
+ * Rows of no request are left as they were.  The device flag is set, and what is wrong taken as absent, where
  * q_start decreases or leaves 0 .. n_tok (that request has no rows), held[r] is not
  * in 0 .. 64 * max_pages (held to it), or a page is not in 0 .. n_pages - 1 (its
- * positions are not seen).  n_qh 1..16 times n_kvh, n_req 1..1024.  One launch;
- * uses the context scratch. */
+ * positions are not seen); rows that two requests then claim are either's.  So many rows
+ * over so many pages that they make more than 2^28 steps (a page of a KV head for 4 or 8
+ * pairs) set it too, and leave out as it was.  n_qh 1..16 times n_kvh, n_req 1..1024,
+ * n_tok and max_pages to 2^24.  One launch; uses the context scratch. */
 nt_status nt_attn_kv4(nt_ctx* ctx, const float* q_dev, const nt_kv4* cache, float* out_dev, int n_qh, int64_t n_tok,
                       int n_req, const int32_t* q_start_dev, const int32_t* held_dev, const int32_t* table_dev,
                       int64_t max_pages, void* stream);
@@ -494,8 +496,8 @@ nt_status nt_attn_kv4(nt_ctx* ctx, const float* q_dev, const nt_kv4* cache, floa
  *   NT_ROPE_BANDS   w = u k + u / s (1 - k), k = clamp((L u / 2 pi - low) / (high - low), 0, 1)
  *   NT_ROPE_RAMP    w = u (1 - k) + u / s k, k = clamp((i - a) / (b - a), 0, 1), from the pair
  *                   a that turns high times over L (rounded down, at least 0) to the pair b
- *                   that turns low times (rounded up, at most the last; b = a + 0.001 where
- *                   they meet); pair(t) = rot_dim ln(L / (2 pi t)) / (2 ln theta)
+ *                   that turns low times (rounded up, at most rot_dim - 1; b = a + 0.001 where
+ *                   that is not behind a); pair(t) = rot_dim ln(L / (2 pi t)) / (2 ln theta)
  * low and high of 0: 1 and 4 in BANDS, 1 and 32 in RAMP.  mag of 0: 0.1 ln s + 1 in
  * RAMP (s > 1), else 1.  divisors: NULL, or rot_dim / 2 numbers that each w_i is
  * divided by (frequency factors that come with a model). */

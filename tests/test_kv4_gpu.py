@@ -385,6 +385,30 @@ def test_bad_pages_and_lengths(ctx):
     ctx.sync()
 
 
+@pytest.mark.parametrize("n_req", [1, 40])
+def test_more_work_than_the_call_takes(ctx, n_req):
+    """More than 2^28 pages of heads to go through: flagged, and nothing is computed (or read: the table holds -1)."""
+    cache = engine.KV4Cache(ctx, nt.KV4_I4, 64, 64, 1)
+    pages = 2 ** 22 // n_req + 2 ** 16
+    table = torch.full((n_req, pages), -1, dtype=torch.int32, device="cuda")
+    held = torch.full((n_req,), 64 * pages, dtype=torch.int32, device="cuda")
+    q_start = torch.arange(n_req + 1, dtype=torch.int32, device="cuda")
+    q, out = torch.zeros(n_req, 64, 64, device="cuda"), torch.full((n_req, 64, 64), 7.0, device="cuda")
+    cache.attend(q, out, q_start, held, table)
+    with pytest.raises(nt.NtError, match="length"):
+        ctx.sync()
+    assert bool((out == 7.0).all())
+
+
+def test_stale_pages_of_any_bytes(ctx):
+    """Bytes behind a request's positions count for nothing, whatever they are."""
+    for garbage in (0x00, 0x7C, 0x7F, 0xFC):                # huge and NaN scales among them
+        for fmt in FMTS:
+            b = Batch(ctx, fmt, 128, 2, 4, [65, 1, 127, 63], [2, 1, 3, 1], seed=9, garbage=garbage)
+            b.check(b.run())
+    ctx.sync()
+
+
 def test_requests_that_share_pages(ctx):
     """Two requests with a common prefix read the same pages."""
     b = Batch(ctx, nt.KV4_E2M1, 128, 1, 4, [256, 100], [1, 1], seed=8)
