@@ -517,8 +517,11 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs
 // 202, but 64 requests of 8000 positions 36.8 and not 34.4.  8 rows (verify passes): one
 // CTA of 8 warps an SM with 255 registers, tensor cores 33%, issue 44%; the dependent
 // products and conversions of 8 warps do not fill more (16 ragged requests of 64 query
-// heads and up to 5 rows 59 us; with 12 warps 67, with 16 rows a step and their spills 87,
-// with unpacked tiles shared by all warps 71).
+// heads and up to 5 rows 59 us; with 12 warps 67, with 16 rows a step 76, with unpacked
+// tiles shared by all warps 71).  Why not tcgen05: its 128 rows take two pages, unpacked to
+// f16 tiles in shared memory, and scores, probabilities and outputs then pass between warps
+// through TMEM and shared memory; that chain took 2.8 us a step, the ragged requests 122 us,
+// and 2000 rows over 4000 positions 1044 us, where 8 rows a step take 1122.
 constexpr int kMaxCtas = 512;                 // one counter each
 constexpr float kPTop = 8.f, kSlack = 6.f;    // probabilities are up to 2^(kPTop + kSlack), in f16's range
 constexpr float kLowest = -3.402823466e38f;
