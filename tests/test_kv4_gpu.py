@@ -569,6 +569,48 @@ def test_steps_of_several_requests(ctx, fmt, captured):
             at += n
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_pages_past_2_to_32_bytes(ctx, fmt):
+    """A pool of 4.4 GB: written, read back and attended at both of its ends."""
+    rng = np.random.default_rng(13)
+    n, H, hd, n_pages = 150, 8, 128, 60000
+    data = torch.empty(n_pages, H, nt.nt_kv4_layout(hd), dtype=torch.uint8, device="cuda")
+    cache = engine.KV4Cache(ctx, fmt, H, hd, n_pages, data=data)
+    table = np.array([[59999, 0, 58300, -1]], dtype=np.int32)
+    p = np.arange(n)
+    slots = dev(table[0, p // 64].astype(np.int64) * 64 + p % 64)
+    k, v = _rows(rng, n, H, hd), _rows(rng, n, H, hd)
+    cache.append(dev(k), dev(v), slots)
+    ko, vo = torch.empty(n, H, hd, device="cuda"), torch.empty(n, H, hd, device="cuda")
+    cache.read(ko, vo, slots)
+    kq, vq = ref.values(k, fmt), ref.values(v, fmt)
+    assert np.array_equal(host(ko), kq.astype(np.float32)) and np.array_equal(host(vo), vq.astype(np.float32))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for rows in (1, 3):
+        q = rng.standard_normal((rows, 4 * H, hd)).astype(np.float32)
+        out = torch.empty(rows, 4 * H, hd, device="cuda")
+        cache.attend(dev(q), out, i32(0, rows), i32(n), dev(table))
+        want, bound = ref.attend(q, kq, vq, rows)
+        assert (np.abs(host(out) - want) <= bound).all()
+    ctx.sync()
+
+
+def test_first_row_of_the_batch_is_not_the_first_request_s(ctx):
+    """Rows before the first request's are left as they were, and slots read twice come twice."""
+    b = Batch(ctx, nt.KV4_I4, 64, 2, 4, [70, 5], [2, 1], seed=14)
+    q = np.concatenate([np.zeros((3,) + b.q.shape[1:], dtype=np.float32), b.q])
+    out = torch.full(q.shape, 123.0, device="cuda")
+    b.cache.attend(dev(q), out, b.q_start + 3, b.held_dev, b.table)
+    assert (host(out)[:3] == 123.0).all()
+    b.check(out[3:])
+    slot = int(b.table[0, 1]) * 64 + 3
+    ko, vo = torch.empty(3, 2, 64, device="cuda"), torch.empty(3, 2, 64, device="cuda")
+    b.cache.read(ko, vo, torch.full((3,), slot, device="cuda"))
+    for i in range(3):
+        assert np.array_equal(host(ko)[i], ref.values(b.k[0], 0)[67].astype(np.float32))
+    ctx.sync()
+
+
 def test_memory_is_not_allocated(ctx):
     b = Batch(ctx, nt.KV4_I4, 128, 8, 4, [3000, 200], [1, 1], seed=12)
     q, out = dev(b.q), torch.empty(2, 32, 128, device="cuda")

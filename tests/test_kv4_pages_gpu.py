@@ -156,6 +156,35 @@ def test_stack_out_of_range(ctx):
         assert host(room)[[0, 8]].tolist() == [77, 77] and 0 <= int(p.n_free) <= 7
 
 
+def test_captured_with_many_rows(ctx):
+    """The two launches of a step with many rows, captured and replayed."""
+    t = Tables(ctx, 9, 80, 400, seed=6)
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    n_tok = 6000
+    new, keep, q_start, slots, positions = i32(9), i32(9), i32(10), torch.zeros(n_tok, dtype=torch.int64, device="cuda"), i32(n_tok)
+    t.pages.step(new, q_start, slots, positions, keep=keep)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t.pages.step(new, q_start, slots, positions, keep=keep)
+    rng = np.random.default_rng(7)
+    for _ in range(30):
+        ks = [h if rng.random() < 0.7 else int(rng.integers(0, h + 1)) for h in t.held]
+        ns = [int(x) for x in rng.integers(0, 600, 9)]
+        new.copy_(torch.tensor(ns, dtype=torch.int32))
+        keep.copy_(torch.tensor(ks, dtype=torch.int32))
+        graph.replay()
+        t.n_free, *want, wrong = ref.pages_step(t.table, t.held, ks, ns, t.free, t.n_free, 400, n_tok)
+        for got, w in zip((q_start, slots, positions), want):
+            assert host(got).tolist() == w
+        assert host(t.pages.table).tolist() == t.table and host(t.pages.held).tolist() == t.held
+        assert int(t.pages.n_free) == t.n_free
+        if wrong:
+            with pytest.raises(nt.NtError):
+                ctx.sync()
+    ctx.sync()
+
+
 def test_captured(ctx):
     """One captured step, replayed: the lengths are the device's."""
     t = Tables(ctx, 40, 5, 150, seed=3)

@@ -123,6 +123,20 @@ def test_strides_and_rows_between(ctx):
     _check(y, buf.transpose(1, 0, 2).astype(np.float64), np.arange(3, 11), freq, 0, 1.0, False)
 
 
+def test_one_row_for_all(ctx):
+    """An input broadcast over rows and heads (strides of 0), turned at each row's position; no rows at all."""
+    x = np.random.default_rng(5).standard_normal((1, 1, 64)).astype(np.float32)
+    y = torch.empty(7, 3, 64, device="cuda")
+    rope = engine.Rope(ctx, 64, layout=nt.ROPE_HALVES)
+    pos = np.array([0, 5, 5, 1, 70000, -3, 2], dtype=np.int32)
+    rope.rotate((dev(x).expand(7, 3, 64), y), positions=dev(pos))
+    _check(y, np.broadcast_to(x, (7, 3, 64)).astype(np.float64), pos, ref.frequencies(64, 10000.0, "plain"), 1, 1.0, False)
+    with pytest.raises(nt.NtError):               # an output that is broadcast has no place for its rows
+        rope.rotate((y, dev(x).expand(7, 3, 64)), positions=dev(pos))
+    rope.rotate((y[:0], y[:0]), pos0=3)
+    ctx.sync()
+
+
 def test_not_finite_values_stay_in_their_pair(ctx):
     x = np.ones((1, 1, 64), dtype=np.float32)
     x[0, 0, 10], x[0, 0, 20] = np.nan, np.inf
