@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs
 // tiles shared by all warps 71).  Why not tcgen05: its 128 rows take two pages, unpacked to
 // f16 tiles in shared memory, and scores, probabilities and outputs then pass between warps
 // through TMEM and shared memory; that chain took 2.8 us a step, the ragged requests 122 us,
-// and 2000 rows over 4000 positions 1044 us, where 8 rows a step take 1122.
+// and 2000 rows over 4000 positions 1044 us, where 8 rows a step took 1122 (chunks in order).
 constexpr int kMaxCtas = 512;                 // one counter each
 constexpr float kPTop = 8.f, kSlack = 6.f;    // probabilities are up to 2^(kPTop + kSlack), in f16's range
 constexpr float kLowest = -3.402823466e38f;
@@ -780,7 +780,11 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     const unsigned it = divide(off, x.steps), h = divide(it, chunks);
     x.j = int(off - it * x.steps);
     x.h = int(h);
-    x.at = int(it - h * chunks) * ROWS;
+    // a prompt's first chunks see little of it and its last ones all: taken in turn from
+    // either end, so that each warp's share of the line is as much work (4000 rows of 4000
+    // positions 1293 us, in order 2177; 2000 rows of up to 4000 positions 913 and 1123)
+    const unsigned k = it - h * chunks;
+    x.at = int(k & 1 ? chunks - 1 - k / 2 : k / 2) * ROWS;
     x.rows = min(ROWS, q.rows * a.G - x.at);
     return x;
   };

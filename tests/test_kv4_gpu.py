@@ -333,6 +333,16 @@ def test_values_of_very_unequal_size(ctx):
     b.check(b.run())
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hd,H,G,held,rows", [(128, 2, 4, [300], [300]), (64, 1, 3, [1000, 7, 450], [1000, 7, 101]),
+                                              (128, 1, 16, [130, 200], [130, 9])])
+def test_prompts(ctx, fmt, hd, H, G, held, rows):
+    """Prompts of many chunks of rows, from their first position on or behind others."""
+    b = Batch(ctx, fmt, hd, H, G, held, rows, seed=15)
+    b.check(b.run(pad=1))
+    ctx.sync()
+
+
 def test_nan_query_stays_in_its_row(ctx):
     b = Batch(ctx, nt.KV4_I4, 128, 2, 4, [300, 90], [1, 2], seed=5)
     want, bound = b.expect()
