@@ -431,7 +431,8 @@ nt_status nt_kv4_layout(int head_dim, size_t* page_bytes);
  * (free_dev[0 .. *n_free), room for n_pages), in the order of the requests and of
  * their pages; then each request that grows takes its pages from the stack's top, in
  * the order of the requests.  Entries of the table behind a request's pages keep
- * what they held.
+ * what they held.  A page is one request's: tables that share pages (nt_attn_kv4 reads
+ * them) are kept by other means, for each would give the page back.
  *   held_out[r], *n_free_out   the new lengths and stack size (may be held, n_free)
  *   q_start[0 .. n_req]        the first row of each request: sums of n_new
  *   slots[i], positions[i]     row i's slot in the cache and position in its request,
