@@ -484,9 +484,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs
 // Scores and outputs on the tensor cores (mma.sync m16n8k16, f16 products, fp32 sums)
 // with fp32-level operands.  K and V are the A operands: 16 positions by 16 channels of
 // K, 16 channels by 16 positions of V, exact in f16 with their scales.  A column pair
-// (2 r, 2 r + 1) of the B operand holds hi = f16(x) and lo = f16(x - hi) of query row r
-// (or of its probabilities), which together carry 22 bits: a tile of 8 columns is 4 rows
-// (NT tiles: 4 NT rows), and the two parts of a product meet in one thread.
+// (2 r, 2 r + 1) of the B operand holds hi = f16(x) and lo, the rest x - hi, of query row r
+// (or of its probabilities, there times kLo), which together carry 22 bits: of q down to 2^-17
+// of the row's largest value, of probabilities to 2^-22 of the largest.  A tile of 8 columns is
+// 4 rows (NT tiles: 4 NT rows), and the two parts of a product meet in one thread.
 //
 // Fragments come without a transpose in shared memory: the names of MMA rows and k slots
 // are ours.  Lane (g = lane / 4, c = lane % 4), 16 positions 16 m .. of a page:
@@ -569,10 +570,24 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// (hi, lo) f16 parts of x in one register; hi is x with 11 bits, so x - hi is exact
-__device__ __forceinline__ uint32_t hi_lo(float x) {
-  const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
-  return as_u32(__floats2half2_rn(hi, x - hi));
+// A weight's f16 parts: hi to nearest, and what that left, exact in fp32, times 2^11.  So the
+// lower part is as large as hi's own steps allow, and small weights keep theirs: each is off by
+// 2^-22 of itself or by 2^-36, which is 2^-44 of the largest.  (Not scaled, the lower part of
+// weights below 2^-22 of the largest was lost, up to 2^-6 of a tail of equal ones; scaling it
+// costs 0.5 to 1.5% of the time.)
+constexpr float kLo = 0x1p11f;
+// (hi, lo) of x and of y, a register each
+__device__ __forceinline__ void hi_lo(float x, float y, uint32_t& of_x, uint32_t& of_y) {
+  const __half2 hi = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(hi);
+  float2 rest;  // (x - f.x) kLo, (y - f.y) kLo
+  asm("{\n\t.reg .b64 a, b, m, n;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 m, {%6, %6};\n\t"
+      "mov.b64 n, {%7, %7};\n\tmul.rn.f32x2 a, a, m;\n\tfma.rn.f32x2 a, b, n, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(rest.x), "=f"(rest.y)
+      : "f"(x), "f"(y), "f"(f.x), "f"(f.y), "f"(kLo), "f"(-kLo));
+  const __half2 lo = __floats2half2_rn(rest.x, rest.y);
+  of_x = __byte_perm(as_u32(hi), as_u32(lo), 0x5410);
+  of_y = __byte_perm(as_u32(hi), as_u32(lo), 0x7632);
 }
 // 8 bytes at this CTA's shared address `at` in the CTA `rank` of the cluster
 __device__ __forceinline__ float2 ld_cluster(uint32_t at, int rank) {
@@ -995,7 +1010,12 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
           }
           l[t] += sum;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) pf[t][i / 2][i & 1] = transpose8(hi_lo(p[i]));
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a, b;
+            hi_lo(p[2 * i], p[2 * i + 1], a, b);
+            pf[t][i][0] = transpose8(a);
+            pf[t][i][1] = transpose8(b);
+          }
         }
         live = wait(1, nblk != nullptr);
       }
@@ -1062,8 +1082,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-              o[t][8 * w + (FMT == NT_KV4_I4 ? n : 2 * n)] += acc[t][n][0] + acc[t][n][1];
-              o[t][8 * w + (FMT == NT_KV4_I4 ? n + 4 : 2 * n + 1)] += acc[t][n][2] + acc[t][n][3];
+              o[t][8 * w + (FMT == NT_KV4_I4 ? n : 2 * n)] += fmaf(acc[t][n][1], 1.f / kLo, acc[t][n][0]);
+              o[t][8 * w + (FMT == NT_KV4_I4 ? n + 4 : 2 * n + 1)] += fmaf(acc[t][n][3], 1.f / kLo, acc[t][n][2]);
             }
         }
       }
