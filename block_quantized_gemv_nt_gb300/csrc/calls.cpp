@@ -4,7 +4,8 @@
 //
 // Every function returns the entry point's nt_status; a tensor that does not fit raises
 // ValueError and calls nothing.  Streams: None (torch's current one of the device), an
-// address, or an object with cuda_stream.
+// address, or an object with cuda_stream.  Other Python threads run while the library works:
+// a launch waits where the stream's queue is full.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -73,6 +74,12 @@ int row_fmt(const at::Tensor& t, const char* why) {
   return NT_F16;
 }
 
+// the interpreter is let go of while one lives: for the library's call only
+struct Released {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Released() { PyEval_RestoreThread(state); }
+};
+
 template <typename F>
 PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
   if (given != wanted) {
@@ -108,10 +115,12 @@ PyObject* kv4_rows(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int fmt = row_fmt(k, "rows must be float32 or float16");
     nt_ctx* ctx = static_cast<nt_ctx*>(address(a[1]));
     const nt_kv4* cache = static_cast<const nt_kv4*>(address(a[2]));
-    void* stream = stream_of(a[9], index);
-    if (a[0] == Py_True)
-      return nt_kv4_read(ctx, cache, fmt, data<void>(k), data<void>(v), n, k.stride(0), k.stride(1), data<int64_t>(s), stream);
-    return nt_kv4_append(ctx, cache, fmt, data<void>(k), data<void>(v), n, k.stride(0), k.stride(1), data<int64_t>(s), stream);
+    void *kp = data<void>(k), *vp = data<void>(v), *stream = stream_of(a[9], index);
+    const int64_t *slots = data<int64_t>(s), tok = k.stride(0), head = k.stride(1);
+    const bool read = a[0] == Py_True;
+    const Released others;
+    if (read) return nt_kv4_read(ctx, cache, fmt, kp, vp, n, tok, head, slots, stream);
+    return nt_kv4_append(ctx, cache, fmt, kp, vp, n, tok, head, slots, stream);
   });
 }
 
@@ -134,9 +143,15 @@ PyObject* attn_kv4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int32_t* q_start = ints(a[6], n_req + 1, index, "q_start: a contiguous int32 tensor of n_req + 1 on the tables' device");
     const int32_t* held = ints(a[7], n_req, index, "held: a contiguous int32 tensor of n_req on the tables' device");
     need(n_req <= 1 << 20 && q.size(1) <= 1 << 20, "more requests or heads than the library takes");
-    return nt_attn_kv4(static_cast<nt_ctx*>(address(a[0])), data<float>(q), static_cast<const nt_kv4*>(address(a[1])),
-                       data<float>(out), int(q.size(1)), q.size(0), int(n_req), q_start, held, data<int32_t>(table),
-                       table.size(1), stream_of(a[9], index));
+    nt_ctx* ctx = static_cast<nt_ctx*>(address(a[0]));
+    const nt_kv4* cache = static_cast<const nt_kv4*>(address(a[1]));
+    void* stream = stream_of(a[9], index);
+    const float* from = data<float>(q);
+    float* to = data<float>(out);
+    const int32_t* pages = data<int32_t>(table);
+    const int64_t n_tok = q.size(0), n_qh = q.size(1), width = table.size(1);
+    const Released others;
+    return nt_attn_kv4(ctx, from, cache, to, int(n_qh), n_tok, int(n_req), q_start, held, pages, width, stream);
   });
 }
 
@@ -163,10 +178,14 @@ PyObject* kv4_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int32_t* keep = ints_or_null(a[10], R, index, "keep: a contiguous int32 tensor of n_req on the tables' device");
     int32_t* held_out = ints_or_null(a[11], R, index, "held_out: a contiguous int32 tensor of n_req on the tables' device");
     int32_t* n_free_out = ints_or_null(a[12], 1, index, "n_free_out: a contiguous int32 tensor of 1 on the tables' device");
-    return nt_kv4_pages(static_cast<nt_ctx*>(address(a[0])), int(R), data<int32_t>(table), table.size(1), held, keep, n_new,
-                        data<int32_t>(free), free.size(0), n_free, held_out ? held_out : held,
-                        n_free_out ? n_free_out : n_free, q_start, data<int64_t>(slots), positions, slots.size(0),
-                        stream_of(a[13], index));
+    nt_ctx* ctx = static_cast<nt_ctx*>(address(a[0]));
+    void* stream = stream_of(a[13], index);
+    int32_t *entries = data<int32_t>(table), *stack = data<int32_t>(free);
+    int64_t* to = data<int64_t>(slots);
+    const int64_t width = table.size(1), n_pages = free.size(0), n_tok = slots.size(0);
+    const Released others;
+    return nt_kv4_pages(ctx, int(R), entries, width, held, keep, n_new, stack, n_pages, n_free, held_out ? held_out : held,
+                        n_free_out ? n_free_out : n_free, q_start, to, positions, n_tok, stream);
   });
 }
 
@@ -195,8 +214,12 @@ PyObject* rope_rows(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       jobs[i] = {data<void>(x), data<void>(y), int(x.size(1)), x.stride(0), x.stride(1), y.stride(0), y.stride(1)};
     }
     const int32_t* positions = ints_or_null(a[5], n, index, "positions: a contiguous int32 tensor, one for each row");
-    return nt_rope_rows(static_cast<nt_ctx*>(address(a[0])), static_cast<const nt_rope_plan*>(address(a[1])), fmt, jobs, n_jobs,
-                        n, positions, integer(a[6]), stream_of(a[7], index));
+    nt_ctx* ctx = static_cast<nt_ctx*>(address(a[0]));
+    const nt_rope_plan* plan = static_cast<const nt_rope_plan*>(address(a[1]));
+    const int64_t pos0 = integer(a[6]);
+    void* stream = stream_of(a[7], index);
+    const Released others;
+    return nt_rope_rows(ctx, plan, fmt, jobs, n_jobs, n, positions, pos0, stream);
   });
 }
 
