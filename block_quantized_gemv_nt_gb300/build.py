@@ -1,7 +1,8 @@
 """Build libnt.so in-tree (block_quantized_gemv_nt_gb300/_build/) for sm_103a, and
 nt_calls.so beside it: the torch side of some calls, against torch's headers.
 
-Each CUDA translation unit compiles in parallel with nvcc, then one link.
+Each CUDA translation unit compiles in parallel with nvcc, then one link.  libnt.so is
+linked first and needs no torch; without torch it is all there is.
 """
 from __future__ import annotations
 
@@ -31,28 +32,34 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.origin:
-        raise RuntimeError("torch not found")
-    return os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
 def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(SO) or not os.path.exists(CALLS_SO):
+def _older(target: str, sources: list[str]) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(SO), os.path.getmtime(CALLS_SO))
-    deps = sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(HERE, "..", "include", "nt.h"), os.path.abspath(__file__)]
-    return any(os.path.getmtime(d) > t for d in deps)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(s) > t for s in sources + [os.path.join(HERE, "..", "include", "nt.h"), os.path.abspath(__file__)])
 
 
-def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if not force and not _stale():
+def _stale() -> bool:
+    return _older(SO, sources() + glob.glob(os.path.join(CSRC, "*.cuh")))
+
+
+def _calls_stale() -> bool:
+    return _older(CALLS_SO, [CALLS_SRC])
+
+
+def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None, module: bool = True) -> str:
+    """What is not up to date: the library, and with `module` nt_calls.so where torch is installed."""
+    lib, calls = force or _stale(), module and _torch_dir() is not None and (force or _calls_stale())
+    if not lib and not calls:
         return SO
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -79,23 +86,23 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
         return obj
 
+    def run(cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        calls = ex.submit(compile_calls)
-        objs = list(ex.map(compile_one, sources()))
-        calls = calls.result()
-    tmp = SO + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", *objs, "-o", tmp, "-lcudart"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, SO)
-    tmp = CALLS_SO + f".{os.getpid()}.tmp"
-    cmd = ["g++", "-shared", calls, "-o", tmp, "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu",
-           "-lc10", "-lc10_cuda", "-L" + BUILD, "-lnt", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS_SO)
+        calls_obj = ex.submit(compile_calls) if calls else None
+        objs = list(ex.map(compile_one, sources() if lib else []))
+    if lib:
+        tmp = SO + f".{os.getpid()}.tmp"
+        run([nvcc, *ARCH, "-shared", *objs, "-o", tmp, "-lcudart"])
+        os.replace(tmp, SO)
+    if calls:
+        tmp = CALLS_SO + f".{os.getpid()}.tmp"
+        run(["g++", "-shared", calls_obj.result(), "-o", tmp, "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python",
+             "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + BUILD, "-lnt", "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, CALLS_SO)
     return SO
 
 

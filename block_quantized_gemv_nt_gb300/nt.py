@@ -43,7 +43,7 @@ def library_path() -> str:
 def _load():
     path = _build.SO
     if not os.path.exists(path) or _build._stale():
-        _build.build()
+        _build.build(module=False)
     return ctypes.CDLL(path)
 
 
@@ -54,6 +54,8 @@ def load_calls():
     import importlib.util
 
     import torch  # noqa: F401  (its libraries, which the module links against)
+    if _build._calls_stale():
+        _build.build()
     spec = importlib.util.spec_from_file_location("nt_calls", _build.CALLS_SO)
     calls = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(calls)

@@ -1,0 +1,42 @@
+"""The parts of the build: libnt.so needs no torch, and nt_calls.so goes with one torch and one Python (CPU; nvcc)."""
+import importlib.util
+import os
+
+import pytest
+
+from block_quantized_gemv_nt_gb300 import build
+
+
+@pytest.fixture
+def elsewhere(tmp_path, monkeypatch):
+    """A build folder of its own, with one small source in the library's place."""
+    src, out = tmp_path / "csrc", tmp_path / "out"
+    src.mkdir()
+    (src / "one.cu").write_text('extern "C" int one() { return 1; }\n')
+    monkeypatch.setattr(build, "CSRC", str(src))
+    monkeypatch.setattr(build, "BUILD", str(out))
+    monkeypatch.setattr(build, "SO", str(out / "libnt.so"))
+    return monkeypatch
+
+
+def _no_torch(monkeypatch):
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+
+
+def test_the_library_is_built_without_torch(elsewhere):
+    _no_torch(elsewhere)
+    assert build.build() == build.SO and os.path.exists(build.SO)
+    assert sorted(os.listdir(build.BUILD)) == ["libnt.so", "one.o"]
+    built = os.path.getmtime(build.SO)
+    assert build.build() == build.SO and os.path.getmtime(build.SO) == built      # nothing to do
+
+
+def test_the_library_stands_when_the_module_does_not_compile(elsewhere, tmp_path):
+    pytest.importorskip("torch")
+    bad = tmp_path / "calls.cpp"
+    bad.write_text("#error no module\n")
+    elsewhere.setattr(build, "CALLS_SRC", str(bad))
+    with pytest.raises(RuntimeError, match="calls.cpp"):
+        build.build()
+    assert os.path.exists(build.SO)
