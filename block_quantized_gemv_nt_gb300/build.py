@@ -7,8 +7,10 @@ linked first and needs no torch; without torch it is all there is.
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -19,7 +21,6 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 SO = os.path.join(BUILD, "libnt.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
-CALLS_SO = os.path.join(BUILD, "nt_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]
@@ -35,6 +36,18 @@ def _nvcc() -> str:
 def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
     return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
+def _torch_version() -> str:
+    """Of the torch that is installed, which is not imported for it."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        found = re.search(r"^__version__\s*=\s*['\"]([\w.+-]+)['\"]", f.read(), re.M)
+    return found.group(1) if found else importlib.metadata.version("torch")
+
+
+def calls_so() -> str:
+    """The module for this torch and this Python, whose ABIs it holds: another's is another file."""
+    return os.path.join(BUILD, f"nt_calls-torch{_torch_version()}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def sources() -> list[str]:
@@ -53,7 +66,7 @@ def _stale() -> bool:
 
 
 def _calls_stale() -> bool:
-    return _older(CALLS_SO, [CALLS_SRC])
+    return _older(calls_so(), [CALLS_SRC])
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None, module: bool = True) -> str:
@@ -99,10 +112,10 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         run([nvcc, *ARCH, "-shared", *objs, "-o", tmp, "-lcudart"])
         os.replace(tmp, SO)
     if calls:
-        tmp = CALLS_SO + f".{os.getpid()}.tmp"
+        tmp = calls_so() + f".{os.getpid()}.tmp"
         run(["g++", "-shared", calls_obj.result(), "-o", tmp, "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python",
              "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + BUILD, "-lnt", "-Wl,-rpath,$ORIGIN"])
-        os.replace(tmp, CALLS_SO)
+        os.replace(tmp, calls_so())
     return SO
 
 

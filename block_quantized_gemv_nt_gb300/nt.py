@@ -56,7 +56,7 @@ def load_calls():
     import torch  # noqa: F401  (its libraries, which the module links against)
     if _build._calls_stale():
         _build.build()
-    spec = importlib.util.spec_from_file_location("nt_calls", _build.CALLS_SO)
+    spec = importlib.util.spec_from_file_location("nt_calls", _build.calls_so())
     calls = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(calls)
     return calls

@@ -40,3 +40,20 @@ def test_the_library_stands_when_the_module_does_not_compile(elsewhere, tmp_path
     with pytest.raises(RuntimeError, match="calls.cpp"):
         build.build()
     assert os.path.exists(build.SO)
+
+
+def test_the_module_is_of_one_torch_and_one_python(monkeypatch):
+    """nt_calls.so holds torch's inlined accessors and Python's ABI: another version of either has another file."""
+    import sysconfig
+
+    torch = pytest.importorskip("torch")
+    here = build.calls_so()
+    assert torch.__version__ in os.path.basename(here) and sysconfig.get_config_var("EXT_SUFFIX") in here
+    build.build()
+    assert os.path.exists(here) and not build._calls_stale()
+    with monkeypatch.context() as m:
+        m.setattr(build, "_torch_version", lambda: "0.0.1")
+        assert build.calls_so() != here and build._calls_stale()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-other.so")
+        assert build.calls_so() != here and build._calls_stale()
