@@ -167,8 +167,15 @@ class KV8Cache:
         nt.nt_attn_kv8_blocks(self.ctx, q, self.desc, out, n_qh, n_pos, nq, idx, self._list(idx, nq), pos_dev, stream)
 
 
-_calls = nt.load_calls()
-_kv4_rows, _attn_kv4, _kv4_pages, _rope_rows = _calls.kv4_rows, _calls.attn_kv4, _calls.kv4_pages, _calls.rope_rows
+_kv4_rows = _attn_kv4 = _kv4_pages = _rope_rows = None
+
+
+def _need_calls():
+    """nt_calls.so, loaded when the first object that calls it is made."""
+    global _kv4_rows, _attn_kv4, _kv4_pages, _rope_rows
+    if _rope_rows is None:
+        c = nt.load_calls()
+        _kv4_rows, _attn_kv4, _kv4_pages, _rope_rows = c.kv4_rows, c.attn_kv4, c.kv4_pages, c.rope_rows
 
 
 class KV4Cache:
@@ -180,6 +187,7 @@ class KV4Cache:
 
     def __init__(self, ctx: nt.Context, fmt: int, n_kvh: int, head_dim: int, n_pages: int, device: str = "cuda",
                  data=None):
+        _need_calls()
         self.ctx, self.n_kvh, self.head_dim, self.n_pages = ctx, n_kvh, head_dim, n_pages
         shape = (n_pages, n_kvh, nt.nt_kv4_layout(head_dim))
         if data is None:
@@ -221,6 +229,7 @@ class KV4Pages:
 
     def __init__(self, ctx: nt.Context, n_req: int, max_pages: int, n_pages: int, device: str = "cuda",
                  buffers: dict | None = None):
+        _need_calls()
         self.ctx, self.n_req, self.max_pages, self.n_pages = ctx, n_req, max_pages, n_pages
         if buffers is None:
             i32 = {"dtype": torch.int32, "device": device}
@@ -251,6 +260,7 @@ class Rope:
     """Rotary positions of rows: a plan (see nt.nt_rope_plan_init for its arguments) and the call on it."""
 
     def __init__(self, ctx: nt.Context, head_dim: int, rot_dim: int | None = None, layout: int = nt.ROPE_PAIRS, **plan):
+        _need_calls()
         self.ctx, self.head_dim = ctx, head_dim
         self.plan = nt.nt_rope_plan_init(head_dim, rot_dim, layout, **plan)
         self._at = ctypes.addressof(self.plan)

@@ -57,3 +57,31 @@ def test_the_module_is_of_one_torch_and_one_python(monkeypatch):
     with monkeypatch.context() as m:
         m.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-other.so")
         assert build.calls_so() != here and build._calls_stale()
+
+
+def test_only_the_calls_that_need_the_module_load_it():
+    """The model step's and the 8-bit cache's users import the engine without nt_calls.so."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+
+    pytest.importorskip("torch")
+    program = """
+from block_quantized_gemv_nt_gb300 import nt
+def none():
+    raise OSError("no module here")
+nt.load_calls = none
+from block_quantized_gemv_nt_gb300 import engine
+engine.KV8Cache(None, nt.KV8_I8, 1, 64, 64, device="cpu")
+for make in (lambda: engine.KV4Cache(None, nt.KV4_I4, 1, 64, 1, device="cpu"),
+             lambda: engine.KV4Pages(None, 1, 1, 1, device="cpu"), lambda: engine.Rope(None, 64)):
+    try:
+        make()
+    except OSError as e:
+        assert "no module here" in str(e)
+    else:
+        raise SystemExit("loaded without the module")
+"""
+    r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
