@@ -192,14 +192,15 @@ static nt_status take_device_flag(nt_ctx* ctx) {
   if (flag) {
     cudaMemset(ctx->err_flag, 0, sizeof(unsigned));
     // one status, every cause by name: the flag collects what happened since it was last read
-    const char *timeout = "", *range = "", *finite = "", *finite4 = "", *paged = "";
+    const char *timeout = "", *range = "", *finite = "", *finite4 = "", *paged = "", *much = "";
     if (flag & kErrWaitTimeout) timeout = "a device-side bounded wait ran out; ";
     if (flag & kErrPosRange) range = "a device-side position ran past the KV cache; ";
     if (flag & kErrNonFinite) finite = "a NaN or an infinity was written to an 8-bit KV cache; ";
     if (flag & kErrNonFinite4) finite4 = "a NaN or an infinity was written to a 4-bit KV cache; ";
     if (flag & kErrPaged) paged = "a length, page or slot that the paged KV cache or its tables do not have; ";
-    return set_err(ctx, flag & kErrWaitTimeout ? NT_ERR_TIMEOUT : NT_ERR_INVALID_ARG, "%s%s%s%s%s(flag 0x%x)", timeout, range,
-                   finite, finite4, paged, flag);
+    if (flag & kErrTooMuch) much = "more work (rows by lengths) than an attention over the paged KV cache takes in one call; ";
+    return set_err(ctx, flag & kErrWaitTimeout ? NT_ERR_TIMEOUT : NT_ERR_INVALID_ARG, "%s%s%s%s%s%s(flag 0x%x)", timeout, range,
+                   finite, finite4, paged, much, flag);
   }
   return NT_OK;
 }

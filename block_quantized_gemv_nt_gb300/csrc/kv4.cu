@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     }
   }
   if (total64 > kMaxSteps) {
-    if (blockIdx.x == 0 && tid == 0) flag_error(a.err, kErrPaged);
+    if (blockIdx.x == 0 && tid == 0) flag_error(a.err, kErrTooMuch);
     return;
   }
   const int warps = gridDim.x * kWarps;

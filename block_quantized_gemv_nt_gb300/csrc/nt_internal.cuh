@@ -26,6 +26,7 @@ constexpr unsigned kErrPosRange = 2u;  // a device-side position fell outside th
 constexpr unsigned kErrNonFinite = 4u;  // a NaN or an infinity was written to an 8-bit cache
 constexpr unsigned kErrNonFinite4 = 8u;  // the same of a 4-bit cache
 constexpr unsigned kErrPaged = 16u;  // a length, page or slot that a paged cache or its tables do not have
+constexpr unsigned kErrTooMuch = 32u;  // an attention over a paged cache of more steps than a call takes
 
 // a GEMV launch configuration: warps per CTA and stage-size cap (what the
 // tuner chooses), and, for the record, the shape's arithmetic: column parts

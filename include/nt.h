@@ -28,9 +28,10 @@
  *    stream).  Calls only enqueue work.  The device error flag (a bounded
  *    wait inside a kernel that ran out, a device-held position past the KV
  *    cache, a NaN or an infinity written to an 8-bit or a 4-bit KV cache, a
- *    length, page or slot that a paged cache does not have) is read and
- *    cleared by nt_ctx_sync() and nt_stream_sync(); a CUDA fault also fails
- *    the next launch on the context.
+ *    length, page or slot that a paged cache does not have, an attention over
+ *    one of more work than a call takes) is read and cleared by nt_ctx_sync()
+ *    and nt_stream_sync(); a CUDA fault also fails the next launch on the
+ *    context.
  *  - Pointers named *_dev are device (HBM) pointers; pointers named *_host
  *    are host pointers.  The caller owns every weight, activation, KV-cache
  *    and output buffer; the context owns only its scratch, events, side
@@ -97,8 +98,8 @@ nt_status nt_ctx_destroy(nt_ctx* ctx);
  * of an 8-bit cache call) ran past the KV cache — the kernels then wrote
  * nothing outside the caches — or a NaN or an infinity was written to an 8-bit
  * or a 4-bit KV cache, or a paged call met a length, page or slot that its cache
- * or tables do not have.  nt_last_error names every cause since the flag was
- * last read. */
+ * or tables do not have, or more work than it takes.  nt_last_error names every
+ * cause since the flag was last read. */
 nt_status nt_ctx_sync(nt_ctx* ctx);
 /* [road] Wait at most timeout_us for the work enqueued on `stream` to finish (a
  * host-side poll with a deadline), then report like nt_ctx_sync:
@@ -478,8 +479,8 @@ nt_status nt_kv4_read(nt_ctx* ctx, const nt_kv4* cache, int dst_fmt, void* k_dev
  * in 0 .. 64 * max_pages (held to it), or a page is not in 0 .. n_pages - 1 (its
  * positions are not seen); rows that two requests then claim are either's.  So many rows
  * over so many pages that they make more than 2^28 steps (a page of a KV head for 4 or 8
- * pairs) set it too, and leave out as it was.  n_qh 1..16 times n_kvh, n_req 1..1024,
- * n_tok and max_pages to 2^24.  One launch; uses the context scratch. */
+ * pairs; a prompt of 65,536 rows of 32 query heads over 8 KV heads makes 2^28) set it too, and
+ * leave out as it was.  n_qh 1..16 times n_kvh, n_req 1..1024, n_tok and max_pages to 2^24.  One launch; uses the context scratch. */
 nt_status nt_attn_kv4(nt_ctx* ctx, const float* q_dev, const nt_kv4* cache, float* out_dev, int n_qh, int64_t n_tok,
                       int n_req, const int32_t* q_start_dev, const int32_t* held_dev, const int32_t* table_dev,
                       int64_t max_pages, void* stream);
