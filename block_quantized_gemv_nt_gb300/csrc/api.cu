@@ -709,7 +709,7 @@ nt_status nt_attn_kv4(nt_ctx* ctx, const float* q, const nt_kv4* kv, float* out,
   NT_TRY(check_vec(ctx, q, "q"));
   NT_TRY(check_vec(ctx, out, "out"));
   NT_REQUIRE(ctx->scratch_bytes >= kScratchGemm &&
-                 ctx->scratch_bytes - kScratchGemm >= kv4_attn_scratch(ctx, kv->head_dim),
+                 ctx->scratch_bytes - kScratchGemm >= kv4_attn_scratch(kv->head_dim),
              NT_ERR_OOM, "the context scratch has no room for the attention's partials");
   DeviceGuard g(ctx->device);
   return launch_attn_kv4(ctx, *kv, q, out, n_qh, n_tok, n_req, q_start, held, table, max_pages, ctx->scratch + kScratchGemm,

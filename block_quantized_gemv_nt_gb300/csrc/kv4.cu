@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs
 //    channel n of the word is MMA row g or g + 8 of m-tile n % 4 (I4) or n / 2 (E2M1).
 //
 // Work: the steps (a page of one KV head for one chunk of 4 NT query rows) of all requests
-// in one line, the same number to each warp, whatever the requests' lengths.  A warp walks its steps with an online softmax; where it begins or
-// ends inside an item (request, head, chunk) it leaves a partial (m, l, o).  The CTA joins
+// in one line, the same number to each warp, whatever the requests' lengths.  A warp walks
+// its steps with an online softmax; where it begins or ends inside an item (request, head, chunk) it leaves a partial (m, l, o).  The CTA joins
 // its warps' partials of one item, and the last CTA to arrive at an item that several
 // share joins theirs, in the order of the line: nothing depends on who arrives when.
 //
@@ -511,12 +511,14 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowsArgs
 // shorter steps save (4160 positions 17.7 and 22.8 us, whole pages 13.3 then).
 //
 // What bounds it.  Up to 4 rows (a decode step): instruction issue, before HBM.  A page of
-// a head is 9216 bytes and about 1170 warp instructions for E2M1 (hardware conversion and
-// one multiply a pair), 1380 for I4 (shift, mask, fused multiply-add a pair); 1,000,003
-// positions of 8 heads take 185 and 210 us, 6.2 and 5.5 TB/s, the tensor cores 23..26%
-// busy, the integer pipe half.  Two CTAs of 8 warps an SM; 16 warps in one CTA take 178 and
-// 202, but 64 requests of 8000 positions 36.8 and not 34.4.  8 rows (verify passes): one
-// CTA of 8 warps an SM with 255 registers, tensor cores 33%, issue 44%; the dependent
+// a head is 9216 bytes and about 1180 warp instructions for E2M1 (hardware conversion and
+// one multiply a pair), 1390 for I4 (shift, mask, fused multiply-add a pair); 1,000,003
+// positions of 8 heads take 186 and 212 us, 6.2 and 5.4 TB/s, the tensor cores 23..25%
+// busy, the integer pipe half.  Two CTAs of 8 warps an SM; with 16 warps in one CTA these took
+// 178 and 202 where two of 8 took 184 and 209, but 64 requests of up to 8000 positions (107,693
+// in all) 36.8 and not 34.4.  Some 13 us of a call in line are its prologue and the join through
+// global memory (131,071 positions 40.5 us, 22.2 of them bytes).  8 rows (verify passes): one
+// CTA of 8 warps an SM with 255 registers, tensor cores 33%, issue 45%; the dependent
 // products and conversions of 8 warps do not fill more (16 ragged requests of 64 query
 // heads and up to 5 rows 59 us; with 12 warps 67, with 16 rows a step 76, with unpacked
 // tiles shared by all warps 71).  Why not tcgen05: its 128 rows take two pages, unpacked to
@@ -701,7 +703,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
   };
   // Few requests, whose items all find a CTA or a cluster of their own and are not much longer
   // than its warps: then no item is joined through global memory (16 requests of up to 500
-  // positions 7.4 us, in line 9.4; 1088 positions of one 7.7, in line 10.2; 4160 10.4 and 12.5).
+  // positions, 1247 in all, 7.4 us, in line 9.4; 1088 positions of one 7.8 in clusters of 8, 9.3
+  // of 2, in line 10.2; 4160 10.6 and in line 12.8).
   int own_r = -1, own_it = 0;  // the request and item of it that this CTA, or its cluster, has; -1: steps in line
   bool for_cluster = false;    // the cluster has it
   if (a.n_req <= 32) {  // every warp by itself: all write the same
@@ -797,7 +800,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) attn_kv4_kernel(const AttnK
     x.h = int(h);
     // a prompt's first chunks see little of it and its last ones all: taken in turn from
     // either end, so that each warp's share of the line is as much work (4000 rows of 4000
-    // positions 1293 us, in order 2177; 2000 rows of up to 4000 positions 913 and 1123)
+    // positions 1313 us, in order 2177; 2000 rows of up to 4000 positions 924 and 1123)
     const unsigned k = it - h * chunks;
     x.at = int(k & 1 ? chunks - 1 - k / 2 : k / 2) * ROWS;
     x.rows = min(ROWS, q.rows * a.G - x.at);
@@ -1414,9 +1417,8 @@ nt_status launch_kv4_read(Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v, i
                     "4-bit cache read launch");
 }
 
-size_t kv4_attn_scratch(const Ctx* c, int head_dim) {
+size_t kv4_attn_scratch(int head_dim) {
   // at most 4096 rows of CTAs, two partials each
-  (void)c;
   return size_t(4096) * 2 * (head_dim * sizeof(float) + sizeof(float2));
 }
 
@@ -1441,12 +1443,18 @@ nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, 
   a.G = n_qh / kv.n_kvh;
   a.inv_g = ((uint64_t(1) << 32) + a.G - 1) / a.G;
   a.stall = take_stall(st);
+  // By the rows that there is room for; the lengths are the device's.  8 rows a step where the
+  // requests have one each cost a second product and leave one CTA an SM (room for five: 16 requests
+  // of 1900 positions, 32/8 heads, 22.1 us and not 14.7, of 8000 49.6 and not 40.3); 4 rows a
+  // step where they have more read the pages again for each 4.
   const int64_t rows = (n_tok + n_req - 1) / n_req * a.G;
   const int NT = rows <= 4 ? 1 : 2;
   const AttnVariant k = attn_for(kv.fmt, kv.head_dim, NT);
   // Clusters of 8 where no request can be longer than a cluster of its own takes and, by the
   // rows' average, all items find one; else of 2: larger ones do not fill the SMs (1,000,003
-  // positions 210 us in clusters of 2, 330 in such of 4: the last of them start when others end).
+  // positions 212 us in clusters of 2, 330 in such of 4: the last of them start when others end).
+  // What a request may hold is the tables' width, so a short one in a wide table has clusters of 2
+  // or stands in line (256 pages: 1088 positions 9.2 us and not 7.8, 4160 12.8 and not 10.6).
   const int64_t items = n_req * int64_t(kv.n_kvh) * ((rows + k.rows - 1) / k.rows);
   const bool wide = max_pages <= kSharedSteps * k.warps * kMaxCluster && items <= c->kv4_ctas[NT - 1][1] / kMaxCluster;
   a.cluster_log = wide ? 3 : 1;

@@ -84,7 +84,7 @@ nt_status launch_kv4_append(Ctx* c, const nt_kv4& kv, int fmt, const void* k, co
                             int64_t head_stride, const int64_t* slots, cudaStream_t st);
 nt_status launch_kv4_read(Ctx* c, const nt_kv4& kv, int fmt, void* k, void* v, int64_t n, int64_t tok_stride,
                           int64_t head_stride, const int64_t* slots, cudaStream_t st);
-size_t kv4_attn_scratch(const Ctx* c, int head_dim);
+size_t kv4_attn_scratch(int head_dim);
 // counters: kAttnCounterBytes, zero at rest (the launch leaves them so)
 nt_status launch_attn_kv4(Ctx* c, const nt_kv4& kv, const float* q, float* out, int n_qh, int64_t n_tok, int n_req,
                           const int32_t* q_start, const int32_t* held, const int32_t* table, int64_t max_pages, char* scratch,

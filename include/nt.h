@@ -397,8 +397,9 @@ nt_status nt_attn_kv8_blocks(nt_ctx* ctx, const float* q_dev, const nt_kv8* cach
  * Slot s of the cache is position s % 64 of page s / 64.
  *
  * A row's channels share a scale by 32: d, an f16 number of at most 8
- * significant bits and at most 2720.  Every value, code times d, is exact in fp32, and
- * in f16 too (but for halves of E2M1 scales below 2^-22, which end in 2^-25).
+ * significant bits (rounded to those first, then to f16) and at most 2720.  Every
+ * value, code times d, is exact in fp32, and in f16 too (but for halves of E2M1
+ * scales below 2^-22, which end in 2^-25).
  *   NT_KV4_I4    codes -8 .. 7; d the nearest to x / -8, x the value of the largest
  *                magnitude (the positive one of two that tie): x itself is -8 d
  *   NT_KV4_E2M1  codes 0 0.5 1 1.5 2 3 4 6 and their negatives; d the nearest to
@@ -473,14 +474,20 @@ nt_status nt_kv4_read(nt_ctx* ctx, const nt_kv4* cache, int dst_fmt, void* k_dev
  * sees all but the last i of them:
  *   out = softmax_j(q . K[j] / sqrt(head_dim)) . V[j],  j < held[r] - i,
  * zeros where that leaves none.  Any number of rows a request; each 8 (row, query head)
- * pairs of a KV head, or 4 where n_tok / n_req rows have no more, read its pages once.
- * Rows of no request are left as they were.  The device flag is set, and what is wrong taken as absent, where
- * q_start decreases or leaves 0 .. n_tok (that request has no rows), held[r] is not
- * in 0 .. 64 * max_pages (held to it), or a page is not in 0 .. n_pages - 1 (its
- * positions are not seen); rows that two requests then claim are either's.  So many rows
- * over so many pages that they make more than 2^28 steps (a page of a KV head for 4 or 8
- * pairs; a prompt of 65,536 rows of 32 query heads over 8 KV heads makes 2^28) set it too, and
- * leave out as it was.  n_qh 1..16 times n_kvh, n_req 1..1024, n_tok and max_pages to 2^24.  One launch; uses the context scratch. */
+ * pairs of a KV head, or 4 where n_tok / n_req rows (those that there is room for, not
+ * those that q_start gives) have no more, read its pages once.  Few short requests are
+ * fastest in tables of at most 192 pages a request.
+ * Scores and sums are fp32: a score is off by some 2^-18 of sum_d |q_d K[j]_d| /
+ * sqrt(head_dim) at most, and the products with V leave out at most 2^-22 of a weight,
+ * or 2^-44 of the request's largest where that is more.
+ * Rows of no request are left as they were.  The device flag is set, and what is wrong
+ * taken as absent, where q_start decreases or leaves 0 .. n_tok (that request has no
+ * rows), held[r] is not in 0 .. 64 * max_pages (held to it), or a page is not in 0 ..
+ * n_pages - 1 (its positions are not seen); rows that two requests then claim are
+ * either's.  So many rows over so many pages that they make more than 2^28 steps (a page
+ * of a KV head for 4 or 8 pairs; a prompt of 65,536 rows of 32 query heads over 8 KV
+ * heads makes 2^28) set it too, and leave out as it was.  n_qh 1..16 times n_kvh, n_req
+ * 1..1024, n_tok and max_pages to 2^24.  One launch; uses the context scratch. */
 nt_status nt_attn_kv4(nt_ctx* ctx, const float* q_dev, const nt_kv4* cache, float* out_dev, int n_qh, int64_t n_tok,
                       int n_req, const int32_t* q_start_dev, const int32_t* held_dev, const int32_t* table_dev,
                       int64_t max_pages, void* stream);
